@@ -356,6 +356,74 @@ int msa_qkv_project_insert(const msa_cache* cache, const void* x, const void* w,
  * rounded to fp32 (base > 1, e.g. 10,000). */
 int msa_rope_table(float* cos_sin, int32_t max_pos, double base, msa_stream_t stream);
 
+/* Element types of rows that the calls below take or return. */
+#define MSA_DTYPE_F32 0
+#define MSA_DTYPE_BF16 1
+#define MSA_DTYPE_F16 2
+
+/* Projected rows of new tokens, in one element type: channels and heads
+ * contiguous (head h of token t at pointer + t * stride + 128 h, strides in
+ * elements), so that slices of one projection's output can be passed as they
+ * are.  Pointers and strides * element size are multiples of 16 bytes. */
+typedef struct msa_rows {
+  const void* q;      /* [n_tokens][16][128] */
+  const void* k;      /* [n_tokens][4][128] */
+  const void* v;      /* [n_tokens][4][128] */
+  const void* idx_k;  /* [n_tokens][128] */
+  const void* q_idx;  /* [n_tokens][8][128], or NULL: no index queries */
+  int64_t q_stride, k_stride, v_stride, idx_k_stride, q_idx_stride;
+  int32_t dtype;      /* MSA_DTYPE_* */
+} msa_rows;
+
+/*
+ * Rotary positions on projected rows, FP8 queries and index queries, and cache
+ * insertion (the part of msa_qkv_project_insert behind its projection and norm,
+ * for models that turn their heads in another way or project elsewhere).
+ *
+ *   rot_dim      channels 0 .. rot_dim - 1 of every query, key, index-key and
+ *                index-query head are turned; a multiple of 16, 0 .. 128 (0:
+ *                nothing is turned, cos_sin may be NULL).
+ *   interleaved  0: pairs (i, i + rot_dim / 2); 1: pairs (2 i, 2 i + 1).
+ *   cos_sin      fp32 [max_pos][rot_dim]: cos of the rot_dim / 2 pairs, then
+ *                their sin (msa_rope_table for rot_dim 128, msa_rope_table_freqs
+ *                for any), 16-byte aligned; positions int32 [n_tokens] index it
+ *                (a position outside [0, max_pos) leaves the token unturned and
+ *                sets MSA_STATUS_BAD_SEQ).
+ *   slot_mapping int64 [n_tokens] as msa_quantize_kv_insert (negative: the
+ *                token's cache entry is not written, its queries are).
+ *   q8, q_idx8   uint8 [n_tokens][16][128] and [n_tokens][8][128] out: E4M3
+ *                (RNE, satfinite, zeros as 0x00), 16-byte aligned; q_idx8 is
+ *                used with rows->q_idx only.
+ * A pair (a, b) becomes (fl(fl(a c) - fl(b s)), fl(fl(b c) + fl(a s))) in fp32,
+ * every product and sum rounded on its own.  Keys and values -> NVFP4 and index
+ * keys -> E4M3 in the slot, exactly as msa_quantize_kv_insert writes them.
+ * Slots written by one call must be distinct.
+ */
+int msa_rotary_insert(const msa_cache* cache, const msa_rows* rows, int32_t n_tokens, const float* cos_sin,
+                      int32_t max_pos, int32_t rot_dim, int32_t interleaved, const int32_t* positions,
+                      const int64_t* slot_mapping, uint8_t* q8, uint8_t* q_idx8, msa_stream_t stream);
+/* RoPE table of given frequencies: cos_sin[pos][i] = amplitude * cos(pos * freq[i])
+ * and cos_sin[pos][rot_dim / 2 + i] = amplitude * sin(pos * freq[i]), computed in
+ * double precision and rounded to fp32.  freq is a HOST array of rot_dim / 2
+ * finite doubles (rot_dim a multiple of 16, 0 .. 128); amplitude is finite. */
+int msa_rope_table_freqs(float* cos_sin, int32_t max_pos, const double* freq, int32_t rot_dim, double amplitude,
+                         msa_stream_t stream);
+
+/*
+ * Read-back of cache slots (a prefill that goes on with the values later steps
+ * will see; hand-over to an engine with a 16-bit cache).
+ *
+ *   slot_mapping int64 [n_tokens]: page * 128 + offset; a negative entry leaves
+ *                the token's rows as they are, a page >= n_pages too and sets
+ *                MSA_STATUS_BAD_SLOT.  A slot may be listed more than once.
+ *   k, v         [n_tokens][4][128] out, idx_k [n_tokens][128] out, in the type
+ *                `dtype` (MSA_DTYPE_*), 16-byte aligned; NULL: not wanted.
+ * K and V elements are e2m1(code) * fl(sb * fl(1 / s_enc)), the product rounded
+ * to fp32 and then to the output type; index keys are their E4M3 values.
+ */
+int msa_read_kv(const msa_cache* cache, const int64_t* slot_mapping, int32_t n_tokens, int32_t dtype, void* k,
+                void* v, void* idx_k, msa_stream_t stream);
+
 /*
  * Block-outer transfer rows (blog, "AMD uses different conversion and
  * communication mechanisms": a KV block kept as one contiguous row is moved in

@@ -33,6 +33,10 @@ cudaError_t launch_qkv_fused(const msa_cache*, const void*, const void*, int, in
                              const float*, const float*, int, const int*, const int64_t*, float, uint8_t*,
                              float*, cudaStream_t);
 cudaError_t launch_block_rows(const msa_cache*, int, const int*, int, uint8_t*, bool, cudaStream_t);
+cudaError_t launch_rotary_insert(const msa_cache*, const msa_rows*, int, const float*, int, int, int, const int*,
+                                 const int64_t*, uint8_t*, uint8_t*, cudaStream_t);
+cudaError_t launch_rope_table_freqs(float*, int, const double*, int, double, cudaStream_t);
+cudaError_t launch_read_kv(const msa_cache*, const int64_t*, int, int, void*, void*, void*, cudaStream_t);
 
 namespace {
 std::atomic<unsigned long long> g_wait_ns{kDefaultWaitLimitNs};
@@ -292,6 +296,55 @@ int msa_qkv_project_insert(const msa_cache* cache, const void* x, const void* w,
   return launched(msa::launch_qkv_fused(cache, x, w, n_tokens, d_model, gamma_q, gamma_k, gamma_idx, cos_sin,
                                         max_pos, positions, slot_mapping, eps, q8, y_out,
                                         reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int msa_rotary_insert(const msa_cache* cache, const msa_rows* rows, int32_t n_tokens, const float* cos_sin,
+                      int32_t max_pos, int32_t rot_dim, int32_t interleaved, const int32_t* positions,
+                      const int64_t* slot_mapping, uint8_t* q8, uint8_t* q_idx8, msa_stream_t stream) {
+  if (int rc = check_cache(cache)) return rc;
+  if (!rows || n_tokens < 0 || max_pos < 0 || (interleaved != 0 && interleaved != 1)) return MSA_ERR_INVALID_ARG;
+  if (rows->dtype != MSA_DTYPE_F32 && rows->dtype != MSA_DTYPE_BF16 && rows->dtype != MSA_DTYPE_F16)
+    return MSA_ERR_INVALID_ARG;
+  if (rot_dim < 0 || rot_dim > msa::kHeadDim || rot_dim % 16 != 0) return MSA_ERR_UNSUPPORTED_SHAPE;
+  if (n_tokens > 0 && (!rows->q || !rows->k || !rows->v || !rows->idx_k || !positions || !slot_mapping || !q8 ||
+                       (rows->q_idx && !q_idx8) || (rot_dim > 0 && (!cos_sin || max_pos == 0))))
+    return MSA_ERR_INVALID_ARG;
+  const int64_t size = rows->dtype == MSA_DTYPE_F32 ? 4 : 2;
+  const int64_t strides[5] = {rows->q_stride, rows->k_stride, rows->v_stride, rows->idx_k_stride,
+                              rows->q_idx ? rows->q_idx_stride : 0};
+  uintptr_t bits = reinterpret_cast<uintptr_t>(rows->q) | reinterpret_cast<uintptr_t>(rows->k) |
+                   reinterpret_cast<uintptr_t>(rows->v) | reinterpret_cast<uintptr_t>(rows->idx_k) |
+                   reinterpret_cast<uintptr_t>(rows->q_idx) | reinterpret_cast<uintptr_t>(cos_sin) |
+                   reinterpret_cast<uintptr_t>(q8) | reinterpret_cast<uintptr_t>(q_idx8);
+  for (int64_t s : strides) {
+    if (s < 0) return MSA_ERR_INVALID_ARG;
+    bits |= (uintptr_t)(s * size);
+  }
+  if (bits & 15) return MSA_ERR_INVALID_ARG;
+  return launched(msa::launch_rotary_insert(cache, rows, n_tokens, cos_sin, max_pos, rot_dim, interleaved, positions,
+                                            slot_mapping, q8, q_idx8, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int msa_rope_table_freqs(float* cos_sin, int32_t max_pos, const double* freq, int32_t rot_dim, double amplitude,
+                         msa_stream_t stream) {
+  if (max_pos < 0 || !isfinite(amplitude)) return MSA_ERR_INVALID_ARG;
+  if (rot_dim < 0 || rot_dim > msa::kHeadDim || rot_dim % 16 != 0) return MSA_ERR_UNSUPPORTED_SHAPE;
+  if (rot_dim > 0 && (!freq || (max_pos > 0 && !cos_sin))) return MSA_ERR_INVALID_ARG;
+  for (int i = 0; i < rot_dim / 2; ++i)
+    if (!isfinite(freq[i])) return MSA_ERR_INVALID_ARG;
+  return launched(msa::launch_rope_table_freqs(cos_sin, max_pos, freq, rot_dim, amplitude,
+                                               reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int msa_read_kv(const msa_cache* cache, const int64_t* slot_mapping, int32_t n_tokens, int32_t dtype, void* k,
+                void* v, void* idx_k, msa_stream_t stream) {
+  if (int rc = check_cache(cache)) return rc;
+  if (n_tokens < 0 || (n_tokens > 0 && !slot_mapping)) return MSA_ERR_INVALID_ARG;
+  if (dtype != MSA_DTYPE_F32 && dtype != MSA_DTYPE_BF16 && dtype != MSA_DTYPE_F16) return MSA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) | reinterpret_cast<uintptr_t>(idx_k)) & 15)
+    return MSA_ERR_INVALID_ARG;
+  return launched(msa::launch_read_kv(cache, slot_mapping, n_tokens, dtype, k, v, idx_k,
+                                      reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t msa_block_row_bytes(int32_t n_layers) {

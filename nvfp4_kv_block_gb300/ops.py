@@ -55,6 +55,22 @@ class _Cache(ctypes.Structure):
     ]
 
 
+class _Rows(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("idx_k", ctypes.c_void_p),
+        ("q_idx", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("idx_k_stride", ctypes.c_int64),
+        ("q_idx_stride", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
@@ -83,6 +99,9 @@ _SIGS = {
     "msa_qkv_project_insert": (ctypes.c_int, [_P, _P, _P, _I32, _I32, _P, _P, _P, _P, _I32, _P, _P,
                                               ctypes.c_float, _P, _P, _P]),
     "msa_rope_table": (ctypes.c_int, [_P, _I32, ctypes.c_double, _P]),
+    "msa_rotary_insert": (ctypes.c_int, [_P, _P, _I32, _P, _I32, _I32, _I32, _P, _P, _P, _P, _P]),
+    "msa_rope_table_freqs": (ctypes.c_int, [_P, _I32, _P, _I32, ctypes.c_double, _P]),
+    "msa_read_kv": (ctypes.c_int, [_P, _P, _I32, _I32, _P, _P, _P, _P]),
     "msa_absmax": (ctypes.c_int, [_P, _I64, _P, _P]),
     "msa_encode_scale": (ctypes.c_float, [ctypes.c_float]),
     "msa_debug_fp8_page": (ctypes.c_int, [_P, _I64, _P, _P, _P]),
@@ -146,6 +165,26 @@ class KVCache:
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
         self.s_enc_k = float(s_enc_k)
         self.s_enc_v = float(s_enc_v)
+
+    @classmethod
+    def from_pools(cls, kv_pool, idx_pool, s_enc_k, s_enc_v, status=None):
+        """A cache over pools that the caller holds already: uint8 [n_pages, 73,728]
+        and [n_pages, 16,384] in the page format, and an int32 [1] status word (a
+        new one if None)."""
+        _ptr(kv_pool, torch.uint8, "kv_pool", 2)
+        _ptr(idx_pool, torch.uint8, "idx_pool", 2)
+        n = kv_pool.shape[0]
+        if tuple(kv_pool.shape) != (n, KV_PAGE_BYTES) or tuple(idx_pool.shape) != (n, IDX_PAGE_BYTES):
+            raise ValueError("kv_pool must be [n, 73728] and idx_pool [n, 16384]")
+        if status is None:
+            status = torch.zeros(1, dtype=torch.int32, device=kv_pool.device)
+        _ptr(status, torch.int32, "status", 1)
+        if not (kv_pool.device == idx_pool.device == status.device):
+            raise ValueError("the pools and the status word must be on one device")
+        self = cls.__new__(cls)
+        self.n_pages, self.kv_pool, self.idx_pool, self.status = n, kv_pool, idx_pool, status
+        self.s_enc_k, self.s_enc_v = float(s_enc_k), float(s_enc_v)
+        return self
 
     def struct(self):
         return _Cache(self.kv_pool.data_ptr(), self.idx_pool.data_ptr(), self.n_pages, PAGE_TOKENS,
@@ -367,6 +406,157 @@ def qkv_project_insert(cache, x, w, gamma_q, gamma_k, gamma_idx, cos_sin, positi
         cos_sin.shape[0], _ptr(positions, torch.int32, "positions"), _ptr(slot_mapping, torch.int64, "slot_mapping"),
         float(eps), _ptr(q8, torch.uint8, "q8"), yp, _stream()))
     return q8
+
+
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}  # MSA_DTYPE_*
+
+
+def _on_device(dev, *tensors):
+    """Raises unless every tensor is on CUDA device ``dev`` and that device is current."""
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"all tensors must be on the cache's device {dev}, got {t.device}")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the cache is on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_max_pos=None, beta_fast=32.0,
+                     beta_slow=1.0):
+    """(frequencies of the rot_dim / 2 pairs, amplitude) of a rotary embedding.
+
+    Unscaled: base^(-2i / rot_dim).  ``scaling`` stretches a model trained on
+    ``original_max_pos`` positions to ``factor`` times as many:
+      "linear"  every position divided by the factor;
+      "ntk"     base * factor^(rot_dim / (rot_dim - 2)): the slowest pair is
+                stretched by the factor, the fastest not at all;
+      "yarn"    pairs that turn more than ``beta_fast`` times over the original
+                length keep their frequency, pairs below ``beta_slow`` turns are
+                divided by the factor, a linear ramp over the pair index between;
+                amplitude 0.1 ln(factor) + 1.
+    """
+    if rot_dim % 16 or not 0 <= rot_dim <= HEAD_DIM:
+        raise ValueError("rot_dim must be a multiple of 16 from 0 to 128")
+    if not base > 1.0 or not math.isfinite(base):
+        raise ValueError("base must be above 1")
+    if scaling not in (None, "linear", "ntk", "yarn"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if not factor >= 1.0 or not math.isfinite(factor):
+        raise ValueError("factor must be at least 1")
+    if scaling == "ntk" and rot_dim > 2:
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    freq = [base ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)]
+    if scaling == "linear":
+        return [f / factor for f in freq], 1.0
+    if scaling != "yarn":
+        return freq, 1.0
+    if original_max_pos is None or original_max_pos <= 0 or not beta_fast > beta_slow > 0:
+        raise ValueError("yarn needs original_max_pos > 0 and beta_fast > beta_slow > 0")
+
+    def pair(turns):  # the (fractional) pair that turns so often over the original length
+        return rot_dim * math.log(original_max_pos / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
+
+    lo = max(math.floor(pair(beta_fast)), 0)
+    hi = min(math.ceil(pair(beta_slow)), rot_dim - 1)
+    out = []
+    for i, f in enumerate(freq):
+        slow = min(max((i - lo) / max(hi - lo, 1e-3), 0.0), 1.0)
+        out.append(f * (1.0 - slow) + f / factor * slow)
+    return out, 0.1 * math.log(factor) + 1.0
+
+
+def rope_table_scaled(max_pos, rot_dim=HEAD_DIM, base=10000.0, scaling=None, factor=1.0, original_max_pos=None,
+                      device="cuda", **betas):
+    """fp32 [max_pos, rot_dim] cos / sin table of ``rope_frequencies`` for rotary_insert
+    (msa_rope_table_freqs); a table of rot_dim 128 also serves qkv_project_insert."""
+    freq, amplitude = rope_frequencies(rot_dim, base, scaling, factor, original_max_pos, **betas)
+    t = torch.empty((max_pos, rot_dim), dtype=torch.float32, device=device)
+    arr = (ctypes.c_double * max(len(freq), 1))(*freq)
+    _on_device(t.device)
+    _check(lib().msa_rope_table_freqs(_ptr(t, torch.float32, "cos_sin"), int(max_pos), arr, int(rot_dim), amplitude,
+                                      _stream()))
+    return t
+
+
+def _rows(t, name, heads, n, dtype):
+    """(pointer, token stride) of projected rows [n, heads, 128] ([n, 128] for heads 0)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} like q, got {t.dtype}")
+    shape = (n, heads, HEAD_DIM) if heads else (n, HEAD_DIM)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    st = t.stride()
+    if st[-1] != 1 or (heads > 1 and st[1] != HEAD_DIM):
+        raise ValueError(f"{name} must have contiguous channels and heads")
+    stride = st[0] if n > 1 else 0
+    if t.data_ptr() % 16 or stride * t.element_size() % 16:
+        raise ValueError(f"{name} and its token stride must be aligned to 16 bytes")
+    return t.data_ptr(), stride
+
+
+def rotary_insert(cache, q, k, v, idx_k, cos_sin, positions, slot_mapping, q_idx=None, interleaved=False, q8=None,
+                  qi8=None):
+    """Rotary positions on projected rows, FP8 queries and index queries (returned:
+    uint8 [n, 16, 128] and [n, 8, 128], or None without ``q_idx``), and NVFP4 / FP8
+    cache insertion at ``slot_mapping`` (negative: not inserted).
+
+    Rows are fp32, bf16 or fp16, [n, heads, 128] ([n, 128] index keys), contiguous
+    within a token; slices of one projection's output will do.  ``cos_sin`` is fp32
+    [max_pos, rot_dim]: the first rot_dim channels of each head are turned, in pairs
+    (i, i + rot_dim / 2), or (2i, 2i + 1) when ``interleaved``.
+    """
+    n = q.shape[0]
+    dtype = q.dtype
+    if dtype not in _DTYPES:
+        raise TypeError(f"q must be float32, bfloat16 or float16, got {dtype}")
+    rows = [_rows(q, "q", Q_HEADS, n, dtype), _rows(k, "k", KV_HEADS, n, dtype), _rows(v, "v", KV_HEADS, n, dtype),
+            _rows(idx_k, "idx_k", 0, n, dtype), (None, 0) if q_idx is None else _rows(q_idx, "q_idx", IDX_HEADS, n, dtype)]
+    dev = cache.kv_pool.device
+    if q8 is None:
+        q8 = torch.empty((n, Q_HEADS, HEAD_DIM), dtype=torch.uint8, device=dev)
+    if qi8 is None and q_idx is not None:
+        qi8 = torch.empty((n, IDX_HEADS, IDX_DIM), dtype=torch.uint8, device=dev)
+    if tuple(q8.shape) != (n, Q_HEADS, HEAD_DIM) or (q_idx is not None and tuple(qi8.shape) != (n, IDX_HEADS, IDX_DIM)):
+        raise ValueError("q8 must be [n, 16, 128] and qi8 [n, 8, 128]")
+    if tuple(positions.shape) != (n,) or tuple(slot_mapping.shape) != (n,):
+        raise ValueError("positions and slot_mapping must be [n]")
+    _on_device(dev, q, k, v, idx_k, q_idx, cos_sin, positions, slot_mapping, q8, qi8)
+    r = _Rows(*(p for p, _ in rows), *(s for _, s in rows), _DTYPES[dtype])
+    c = cache.struct()
+    _check(lib().msa_rotary_insert(
+        ctypes.byref(c), ctypes.byref(r), n, _ptr(cos_sin, torch.float32, "cos_sin", 2), cos_sin.shape[0],
+        cos_sin.shape[1], int(bool(interleaved)), _ptr(positions, torch.int32, "positions"),
+        _ptr(slot_mapping, torch.int64, "slot_mapping"), _ptr(q8, torch.uint8, "q8"),
+        None if q_idx is None else _ptr(qi8, torch.uint8, "qi8"), _stream()))
+    return q8, (None if q_idx is None else qi8)
+
+
+def read_kv(cache, slot_mapping, dtype=torch.bfloat16, k=None, v=None, idx_k=None):
+    """The values the cache holds at ``slot_mapping`` (int64 [n]): K [n, 4, 128],
+    V [n, 4, 128] and index keys [n, 128].  Rows go into the given tensors (of one
+    type: fp32, bf16 or fp16), or, when none is given, into new ones of ``dtype``;
+    the others are not read and come back as None.  Rows of negative slots are left
+    as they were (zeros in new tensors)."""
+    n = slot_mapping.shape[0]
+    given = [t for t in (k, v, idx_k) if t is not None]
+    dev = cache.kv_pool.device
+    if given:
+        dtype = given[0].dtype
+    if dtype not in _DTYPES:
+        raise TypeError(f"values are float32, bfloat16 or float16, not {dtype}")
+    if not given:
+        k, v = (torch.zeros((n, KV_HEADS, HEAD_DIM), dtype=dtype, device=dev) for _ in range(2))
+        idx_k = torch.zeros((n, IDX_DIM), dtype=dtype, device=dev)
+    for t, name, shape in ((k, "k", (n, KV_HEADS, HEAD_DIM)), (v, "v", (n, KV_HEADS, HEAD_DIM)), (idx_k, "idx_k", (n, IDX_DIM))):
+        if t is not None and tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    _on_device(dev, slot_mapping, k, v, idx_k)
+    c = cache.struct()
+    _check(lib().msa_read_kv(
+        ctypes.byref(c), _ptr(slot_mapping, torch.int64, "slot_mapping", 1), n, _DTYPES[dtype],
+        *(None if t is None else _ptr(t, dtype, name) for t, name in ((k, "k"), (v, "v"), (idx_k, "idx_k"))), _stream()))
+    return k, v, idx_k
 
 
 def set_fault_injection(flags=0, wait_limit_ns=0):
