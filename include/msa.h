@@ -425,6 +425,55 @@ int msa_read_kv(const msa_cache* cache, const int64_t* slot_mapping, int32_t n_t
                 void* v, void* idx_k, msa_stream_t stream);
 
 /*
+ * Attention of drafted tokens over the whole cached context: a tree of drafts
+ * per sequence (speculative verification), a plain causal run of up to 64 new
+ * tokens, or one token of a layer without block selection.
+ *
+ *   q           E4M3 [n_q_total][n_q_heads = 16][128] queries; the drafts' keys and
+ *               values are in the cache already (draft i of a sequence at position
+ *               ctx + i, ctx = seq_lens[b] - n_q; its rotary position is its depth's,
+ *               msa_rotary_insert).
+ *   block_table, max_pages, seq_lens, q_start_loc, n_seqs, n_q_total as
+ *               msa_sparse_attn_decode; a sequence has at most MSA_TREE_MAX_DRAFTS
+ *               query tokens (more, like any inconsistent sequence, sets
+ *               MSA_STATUS_BAD_SEQ and leaves the sequence's rows as they were).
+ *   tree_mask   uint64 [n_q_total] or NULL: bit i of a draft's word = it sees draft
+ *               i of its sequence (its own bit included only if set; bits of drafts
+ *               that do not exist are ignored).  NULL: draft j sees drafts 0 .. j.
+ *               The ctx tokens before the drafts are visible to every draft.
+ *   sel, n_sel  int32 [n_seqs][17] and [n_seqs], or both NULL (every block): one list
+ *               of block ids per sequence, strictly ascending, shared by its drafts,
+ *               as msa_indexer_topk writes it for one query token.  Visited are the
+ *               listed blocks below ctx / 128 and the blocks from ctx / 128 on (those
+ *               that can hold drafts).  An entry that is not above the ones before
+ *               it, or behind the sequence, is left out and sets
+ *               MSA_STATUS_BAD_SELECTION.
+ *   dtype       MSA_DTYPE_BF16 or MSA_DTYPE_F16: type of out.
+ *   out         [n_q_total][16][128], 16-byte aligned; zeros where a row sees nothing.
+ *   lse         fp32 [n_q_total][16] out or NULL: natural-log sum of exp of the row's
+ *               logits (-inf where it sees nothing).
+ *   ws, ws_bytes scratch of at least msa_tree_attn_workspace_bytes(n_q_total) bytes,
+ *               16-byte aligned, ZEROED before its first use (every call that does
+ *               not time out leaves the words that have to be zero so).  Calls
+ *               sharing a workspace must not overlap on the GPU.
+ * Rows behind the last sequence (q_start_loc[n_seqs] .. n_q_total - 1) are left as
+ * they were.  Operands as msa_sparse_attn_decode; the weights 2^x are rounded to f16
+ * (2^-12 relative) before they meet the values, everything else is fp32; rows are
+ * summed in an order that depends on the call's sizes only.  A physical page outside
+ * the pool sets MSA_STATUS_BAD_PAGE and its tokens are not seen.  A cache scale byte
+ * of 0x7F or 0xFF (no number, never written by the library) counts as zero.
+ * Limits: n_seqs <= 4096, n_q_total <= 65535.  Two launches, both programmatic
+ * dependents of the kernel before them.
+ */
+#define MSA_TREE_MAX_DRAFTS 64
+int msa_tree_attn(const msa_cache* cache, const uint8_t* q, int32_t n_q_heads, float softmax_scale,
+                  const int32_t* block_table, int32_t max_pages, const int32_t* seq_lens,
+                  const int32_t* q_start_loc, int32_t n_seqs, int32_t n_q_total, const uint64_t* tree_mask,
+                  const int32_t* sel, const int32_t* n_sel, int32_t dtype, void* out, float* lse, void* ws,
+                  size_t ws_bytes, msa_stream_t stream);
+size_t msa_tree_attn_workspace_bytes(int32_t n_q_total);
+
+/*
  * Block-outer transfer rows (blog, "AMD uses different conversion and
  * communication mechanisms": a KV block kept as one contiguous row is moved in
  * one read instead of one read per page).  The row of a block holds, for every

@@ -36,6 +36,9 @@ cudaError_t launch_block_rows(const msa_cache*, int, const int*, int, uint8_t*, 
 cudaError_t launch_rotary_insert(const msa_cache*, const msa_rows*, int, const float*, int, int, int, const int*,
                                  const int64_t*, uint8_t*, uint8_t*, cudaStream_t);
 cudaError_t launch_rope_table_freqs(float*, int, const double*, int, double, cudaStream_t);
+size_t tree_attn_workspace_bytes(int);
+cudaError_t launch_tree_attn(const msa_cache*, const uint8_t*, float, const int*, int, const int*, const int*, int, int,
+                             const uint64_t*, const int*, const int*, int, void*, float*, void*, cudaStream_t);
 cudaError_t launch_read_kv(const msa_cache*, const int64_t*, int, int, void*, void*, void*, cudaStream_t);
 
 namespace {
@@ -345,6 +348,32 @@ int msa_read_kv(const msa_cache* cache, const int64_t* slot_mapping, int32_t n_t
     return MSA_ERR_INVALID_ARG;
   return launched(msa::launch_read_kv(cache, slot_mapping, n_tokens, dtype, k, v, idx_k,
                                       reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t msa_tree_attn_workspace_bytes(int32_t n_q_total) {
+  return n_q_total > 0 ? msa::tree_attn_workspace_bytes(n_q_total) : 256;
+}
+
+int msa_tree_attn(const msa_cache* cache, const uint8_t* q, int32_t n_q_heads, float softmax_scale,
+                  const int32_t* block_table, int32_t max_pages, const int32_t* seq_lens,
+                  const int32_t* q_start_loc, int32_t n_seqs, int32_t n_q_total, const uint64_t* tree_mask,
+                  const int32_t* sel, const int32_t* n_sel, int32_t dtype, void* out, float* lse, void* ws,
+                  size_t ws_bytes, msa_stream_t stream) {
+  if (int rc = check_cache(cache)) return rc;
+  if (n_q_heads != msa::kQHeads) return MSA_ERR_UNSUPPORTED_SHAPE;
+  if (n_q_total < 0 || n_seqs < 0 || max_pages <= 0 || !(softmax_scale > 0.f) || !isfinite(softmax_scale) ||
+      (dtype != MSA_DTYPE_BF16 && dtype != MSA_DTYPE_F16) || (sel == nullptr) != (n_sel == nullptr))
+    return MSA_ERR_INVALID_ARG;
+  if (n_q_total > 65535 || n_seqs > msa::kMaxSeqs || max_pages > kMaxPagesPerSeq) return MSA_ERR_UNSUPPORTED_SHAPE;
+  if (n_q_total > 0 && (!q || !block_table || !seq_lens || !q_start_loc || !out || !ws || n_seqs == 0))
+    return MSA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(ws) |
+       reinterpret_cast<uintptr_t>(cache->kv_pool)) & 15)
+    return MSA_ERR_INVALID_ARG;
+  if (ws_bytes < msa_tree_attn_workspace_bytes(n_q_total)) return MSA_ERR_WORKSPACE_TOO_SMALL;
+  return launched(msa::launch_tree_attn(cache, q, softmax_scale, block_table, max_pages, seq_lens, q_start_loc, n_seqs,
+                                        n_q_total, tree_mask, sel, n_sel, dtype, out, lse, ws,
+                                        reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t msa_block_row_bytes(int32_t n_layers) {

@@ -1,0 +1,874 @@
+// Attention of drafted tokens over a paged NVFP4 cache: every draft sees its
+// sequence's committed context (all of it, or one block selection shared by the
+// sequence's drafts) and the drafts that its mask names (its ancestors in a tree
+// of drafts and itself).
+//
+// Mathematics.  For a row (draft, query head) with FP8 query q and keys k8_t, the
+// NVFP4 operands dequantised to FP8 as in the sparse decode path,
+//   x_t = (q . k8_t) scale / s_enc_k log2(e),  out = sum_t 2^x_t v8_t / sum_t 2^x_t / s_enc_v
+// over the visible t, in one pass with a reference m per row that follows the
+// running maximum: weights 2^(x_t - m + 8) are summed in fp32 (l) and multiply V
+// in f16.  m moves only when a page's maximum exceeds it by 7 (log2), so the
+// weights stay below 2^15 and the accumulator is rescaled a few times per row;
+// they keep full f16 precision down to 2^-22 of the largest (an E4M3 weight, with
+// its 17 binades, would lose the bulk of a long context behind one large key).
+// V8 is an f16 value by moving its seven magnitude bits: E4M3 bits << 7 is
+// v8 2^-8 exactly, subnormals included.
+//
+// One persistent CTA per SM; rows of one (sequence, KV head) are row 4 i + h of
+// one tile of 128 (up to 32 drafts) or two, so K and V are converted once for all
+// drafts.  The (sequence, KV head, page) units are cut into equal weighted ranges,
+// one per CTA; a (sequence, KV head) cut across CTAs leaves fp32 partial rows in
+// the workspace, merged by a second kernel.  Roles, all hand-offs mbarriers with
+// bounded waits:
+//   warp 0        segment records and one 18,432-byte bulk copy per page;
+//   warp 1        MMA issuer: S = Q K8^T (kind::f8f6f4, 128 x 128 x 128), then
+//                 O += P V (kind::f16, P from tensor memory over S's own columns,
+//                 V MN-major), in the order QK(j + 2) behind PV(j);
+//   warp 2        query rows of the next segment (cp.async);
+//   warp 3        tensor-memory allocation;
+//   warps 4-11    two softmax sets, thread = row: with one row tile a set takes
+//                 every other page (its own reference, sum and accumulator, joined
+//                 at the segment's end), with two tiles a set takes a tile;
+//   warps 12-15   K conversion, thread = token; warps 16-23 V conversion, thread =
+//                 token and half of the channels.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace msa {
+namespace {
+
+constexpr int kTreeThreads = 768;
+constexpr int kTreeMaxDrafts = 64;  // per sequence: one 64-bit mask word, two row tiles
+constexpr int kTreeCtas = 152;      // most CTAs of a launch (the workspace is sized for them)
+constexpr int kRaw = 4;             // raw page stages
+constexpr int kSlot = 2;            // converted pages in flight
+constexpr int kRecs = 4;
+constexpr int kInfo = 16;
+constexpr int kKTabCopies = 4, kVTabCopies = 8;
+
+constexpr int kOffQ = 0;                                      // 2 tiles [128 rows][128 B]
+constexpr int kOffK8 = kOffQ + 2 * 16384;                     // kSlot x [128 tokens][128 B]
+constexpr int kOffV16 = kOffK8 + kSlot * 16384;               // kSlot x 2 halves x [128 tokens][64 f16]
+constexpr int kOffRaw = kOffV16 + kSlot * 32768;              // kRaw x 18,432
+constexpr int kOffKTab = kOffRaw + kRaw * kHeadBytes;         // uint2 [128][copies]
+constexpr int kOffVTab = kOffKTab + 128 * 8 * kKTabCopies;    // uint4 [128][copies]
+constexpr int kOffMl = kOffVTab + 128 * 16 * kVTabCopies;     // float2 [2 parities][2 sets][128]
+constexpr int kOffRecs = kOffMl + 2 * 2 * 128 * 8;            // kRecs x 64 B
+constexpr int kOffInfo = kOffRecs + kRecs * 64;               // int2 [kInfo]: first position, valid tokens
+constexpr int kOffScan = kOffInfo + kInfo * 8;                // long long [32] and the start
+constexpr int kOffTreeBars = kOffScan + 32 * 8 + 64;
+constexpr int kBRawFull = 0, kBRawEmpty = kBRawFull + kRaw, kBKFull = kBRawEmpty + kRaw, kBKEmpty = kBKFull + kSlot,
+              kBVFull = kBKEmpty + kSlot, kBVEmpty = kBVFull + kSlot, kBSFull = kBVEmpty + kSlot, kBPFull = kBSFull + 2,
+              kBPvDone = kBPFull + 2, kBOFree = kBPvDone + 2, kBMl = kBOFree + 1, kBQFull = kBMl + 1,
+              kBQEmpty = kBQFull + 1, kBRecFull = kBQEmpty + 1, kBRecEmpty = kBRecFull + kRecs,
+              kBDone = kBRecEmpty + kRecs, kTreeBars = kBDone + 1;
+constexpr int kOffTreeMisc = kOffTreeBars + 8 * ((kTreeBars + 1) & ~1);  // tmem, abort, copies issued
+constexpr int kTreeSmem = 1024 + kOffTreeMisc + 16;
+static_assert(kTreeSmem <= 232448, "shared memory of one CTA");
+static_assert(kOffRaw % 16 == 0 && kOffVTab % 16 == 0 && kOffTreeBars % 8 == 0, "alignment");
+constexpr uint32_t kTmemS = 0, kTmemO = 256;  // S of set s at 128 s, O of set s at 256 + 128 s
+constexpr float kTreeGrowth = 7.0f, kTreeBias = 8.0f;
+constexpr float kTreeLog2e = 1.4426950408889634f, kTreeLn2 = 0.6931471805599453f;
+
+// Weights of the partition: a page of a one-tile sequence, of a two-tile one,
+// the fixed part of a (sequence, KV head), and the least share of a CTA (at
+// least a page's weight, so that every CTA between a sequence's first and last
+// has pages of it).
+constexpr int kPageWeight1 = 2, kPageWeight2 = 4, kFixedWeight = 6, kLeastShare = 4;
+static_assert(kLeastShare >= kPageWeight2, "a share holds a page");
+
+struct SegRec {
+  int n_pg;      // pages of the segment; -1: no more segments
+  int g, q0, n_q;
+  int ctx;       // tokens before the drafts
+  int slot;      // partial slot, or -1: the segment is the whole (sequence, KV head)
+};
+static_assert(sizeof(SegRec) <= 64, "record slot");
+
+struct TreeParams {
+  const uint8_t* kv_pool;
+  int64_t n_pages;
+  const uint8_t* q;  // [T][16][128]
+  const int* block_table;
+  int max_pages;
+  const int* seq_lens;
+  const int* q_start_loc;
+  int n_seqs;
+  int n_q_total;
+  const unsigned long long* tree_mask;  // [T] or null (draft j sees drafts 0 .. j)
+  const int* sel;                       // [n_seqs][17] or null (all blocks)
+  const int* n_sel;
+  float scale_log2;
+  float out_scale;  // 2^8 / s_enc_v
+  int out_f16;
+  uint16_t* out;    // [T][16][128] bf16 or f16
+  float* lse;       // [T][16] or null
+  int* row_desc;    // [T][4] workspace: first CTA | parts << 8 | draft << 20, 0 = nothing to merge
+  float* part_o;    // [2 kTreeCtas][rows][128]
+  float2* part_ml;  // [2 kTreeCtas][rows]
+  int part_rows;
+  int* status;
+  unsigned long long wait_ns;
+};
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0;
+}
+__device__ __forceinline__ bool twait(uint32_t bar, uint32_t parity, const WaitCtl& w) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, w));
+}
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// kind::f16 with A in tensor memory (row m in lane m, two f16 per column), B in shared memory.
+__device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Blocks a sequence's drafts visit: `chosen` of the selection, then those that can
+// hold drafts; and the units' weight.
+struct SeqWork {
+  SeqInfo s;
+  int ctx, first, chosen, n_vis, pw;
+};
+__device__ __forceinline__ SeqWork seq_work(const TreeParams& p, int b) {
+  SeqWork w;
+  w.s = load_seq(b, p.seq_lens, p.q_start_loc, p.max_pages, p.n_q_total);
+  if (w.s.n_q > kTreeMaxDrafts) w.s.ok = false;
+  w.ctx = w.s.seq_len - w.s.n_q;
+  w.first = w.ctx / kPageTokens;
+  w.chosen = w.first;
+  w.n_vis = 0;
+  w.pw = w.s.n_q > 32 ? kPageWeight2 : kPageWeight1;
+  if (!w.s.ok || w.s.n_q == 0) return w;
+  if (p.sel) {
+    const int n = min(max(p.n_sel[b], 0), kSelStride);
+    int top = -1;
+    w.chosen = 0;
+    for (int i = 0; i < n; ++i) {
+      const int id = p.sel[(size_t)b * kSelStride + i];
+      w.chosen += id > top && id < w.first;
+      top = max(top, id);
+    }
+  }
+  w.n_vis = w.chosen + (w.s.seq_len - 1) / kPageTokens - w.first + 1;
+  return w;
+}
+
+// One code word (8 channels) -> 8 f16 values v8 2^-8, through the scale's table:
+// hi = E4M3 magnitude bits >> 1, lo = their last bit << 7, per E2M1 magnitude.
+__device__ __forceinline__ uint4 dequant8_f16(uint32_t w, uint4 t) {
+  const uint32_t m = w & 0x77777777u, m2 = m >> 16;
+  const uint32_t h0 = prmt(t.x, t.y, m) | (w & 0x80808080u);
+  const uint32_t h1 = prmt(t.x, t.y, m2) | ((w << 4) & 0x80808080u);
+  const uint32_t l0 = prmt(t.z, t.w, m), l1 = prmt(t.z, t.w, m2);
+  return make_uint4(prmt(l0, h0, 0x5140u), prmt(l0, h0, 0x7362u), prmt(l1, h1, 0x5140u), prmt(l1, h1, 0x7362u));
+}
+
+// The 32 drafts' bits of the positions pos .. pos + 31 for a row with mask word tm
+// (bits of drafts that exist only): context tokens are visible.
+__device__ __forceinline__ uint32_t visible_bits(unsigned long long tm, int pos, int ctx) {
+  const int sh = pos - ctx;
+  if (sh >= 64) return 0u;
+  if (sh >= 0) return (uint32_t)(tm >> sh);
+  if (sh <= -32) return 0xFFFFFFFFu;
+  return ((uint32_t)tm << -sh) | ((1u << -sh) - 1u);
+}
+
+__device__ __forceinline__ uint32_t pack16(float a, float b, bool f16) {
+  if (f16) return cvt_f16x2_f32(b, a);
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid_constant__ TreeParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  auto bar = [&](int i) { return sbase + kOffTreeBars + 8 * i; };
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffTreeMisc);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kOffTreeMisc + 4);
+  int* s_issued = reinterpret_cast<int*>(smem + kOffTreeMisc + 8);
+  const WaitCtl wc{s_abort, p.wait_ns};
+  auto rec = [&](int k) { return reinterpret_cast<SegRec*>(smem + kOffRecs + 64 * (k % kRecs)); };
+  int2* s_info = reinterpret_cast<int2*>(smem + kOffInfo);
+  long long* s_scan = reinterpret_cast<long long*>(smem + kOffScan);  // [24] warp sums, then total, start b, its offset
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  // ---- prologue ------------------------------------------------------------------
+  {
+    uint2* kt = reinterpret_cast<uint2*>(smem + kOffKTab);
+    uint4* vt = reinterpret_cast<uint4*>(smem + kOffVTab);
+    if (tid < 128) {
+      const float mags[8] = {0.f, 0.5f, 1.f, 1.5f, 2.f, 3.f, 4.f, 6.f};
+      // (0x7F is no number and never written: it counts as zero)
+      const float s = tid == 127 ? 0.f : e4m3_to_f32((uint32_t)tid);
+      uint32_t k[2] = {0, 0}, hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+      for (int m = 0; m < 8; ++m) {
+        const uint32_t e = f32_to_e4m3(mags[m] * s);
+        k[m >> 2] |= e << (8 * (m & 3));
+        hi[m >> 2] |= (e >> 1) << (8 * (m & 3));
+        lo[m >> 2] |= ((e & 1) << 7) << (8 * (m & 3));
+      }
+#pragma unroll
+      for (int c = 0; c < kKTabCopies; ++c) kt[tid * kKTabCopies + c] = make_uint2(k[0], k[1]);
+#pragma unroll
+      for (int c = 0; c < kVTabCopies; ++c) vt[tid * kVTabCopies + c] = make_uint4(hi[0], hi[1], lo[0], lo[1]);
+    }
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kRaw; ++i) {
+      mbar_init(bar(kBRawFull + i), 1);
+      mbar_init(bar(kBRawEmpty + i), 12);
+    }
+    for (int i = 0; i < kSlot; ++i) {
+      mbar_init(bar(kBKFull + i), 4);
+      mbar_init(bar(kBKEmpty + i), 1);
+      mbar_init(bar(kBVFull + i), 8);
+      mbar_init(bar(kBVEmpty + i), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(kBSFull + s), 1);
+      mbar_init(bar(kBPFull + s), 4);
+      mbar_init(bar(kBPvDone + s), 1);
+    }
+    mbar_init(bar(kBOFree), 8);
+    mbar_init(bar(kBMl), 8);
+    mbar_init(bar(kBQFull), 1);
+    mbar_init(bar(kBQEmpty), 1);
+    for (int i = 0; i < kRecs; ++i) {
+      mbar_init(bar(kBRecFull + i), 1);
+      mbar_init(bar(kBRecEmpty + i), 1 + 1 + 8 + 4 + 8);  // MMA, queries, softmax, K and V conversion
+    }
+    mbar_init(bar(kBDone), 1);
+    *s_abort = 0;
+    *s_issued = 0;
+    fence_barrier_init();
+  }
+  if (warp == 3) tmem_alloc(smem_u32(s_tmem), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  pdl_wait();  // everything below may come from the previous kernel
+  pdl_trigger();
+
+  // ---- this CTA's range of the weighted units ------------------------------------------
+  // thread i sums the sequences i * per .. of its share, then a scan over the CTA
+  const int per = (p.n_seqs + kTreeThreads - 1) / kTreeThreads;
+  {
+    long long mine = 0;
+    const int b0 = min(tid * per, p.n_seqs), b1 = min(b0 + per, p.n_seqs);
+    for (int b = b0; b < b1; ++b) {
+      const SeqWork w = seq_work(p, b);
+      if (!w.s.ok && blockIdx.x == 0) set_status(p.status, MSA_STATUS_BAD_SEQ);
+      if (w.n_vis > 0) mine += (long long)kKvHeads * (w.pw * w.n_vis + kFixedWeight);
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    long long before = 0, total = 0;
+    for (int i = 0; i < kTreeThreads / 32; ++i) {
+      if (i < warp) before += s_scan[i];
+      total += s_scan[i];
+    }
+    const int G = (int)min((long long)gridDim.x, max(1ll, total / kLeastShare));
+    const long long lo = blockIdx.x < G ? total * blockIdx.x / G : total;
+    const long long mine0 = before + incl - mine;
+    if (mine > 0 && lo >= mine0 && lo < mine0 + mine) {  // the first sequence of the range is in this share
+      s_scan[25] = b0;
+      s_scan[26] = mine0;
+    }
+    if (tid == 0) s_scan[24] = total;
+    __syncthreads();
+  }
+  const long long total = s_scan[24];
+  const int G = (int)min((long long)gridDim.x, max(1ll, total / kLeastShare));
+  const bool idle = (int)blockIdx.x >= G || total == 0;
+
+  if (warp == 0) {
+    // ---------------- segment records and page copies -------------------------------------
+    int e = 0, k = 0;
+    bool ok = true;
+    if (!idle) {
+      const long long lo = total * blockIdx.x / G, hi = total * (blockIdx.x + 1) / G;
+      long long off = s_scan[26];
+      for (int b = (int)s_scan[25]; ok && b < p.n_seqs && off < hi; ++b) {
+        const SeqWork w = seq_work(p, b);
+        if (w.n_vis == 0) continue;
+        const long long wg = (long long)w.pw * w.n_vis + kFixedWeight;
+        // the selection, one entry per lane: its place among the chosen ones
+        int my_blk = -1;
+        if (p.sel && off + kKvHeads * wg > lo) {
+          const int n = min(max(p.n_sel[b], 0), kSelStride);
+          const int id = lane < n ? p.sel[(size_t)b * kSelStride + lane] : -1;
+          int top = id;  // the largest entry so far, this one included
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, top, o);
+            if (lane >= o) top = max(top, v);
+          }
+          const int prev = __shfl_up_sync(0xffffffffu, top, 1);
+          const bool up = lane < n && id > (lane ? max(prev, -1) : -1);
+          if (lane < n && (!up || id > (w.s.seq_len - 1) / kPageTokens)) set_status(p.status, MSA_STATUS_BAD_SELECTION);
+          const unsigned chosen = __ballot_sync(0xffffffffu, up && id < w.first);
+          // lane i takes the i-th chosen entry
+          int src = 0;
+          for (int i = 0, c = 0; i < kSelStride; ++i)
+            if (chosen >> i & 1) {
+              if (c == lane) src = i;
+              ++c;
+            }
+          my_blk = __shfl_sync(0xffffffffu, id, src);
+        }
+        for (int g = 0; ok && g < kKvHeads; ++g, off += wg) {
+          // page i starts at weight off + kFixedWeight + i pw; it belongs to the range that holds its start
+          const long long base = off + kFixedWeight;
+          const int p_lo = (int)min((long long)w.n_vis, max(0ll, (lo - base + w.pw - 1) / w.pw));
+          const int p_hi = (int)min((long long)w.n_vis, max(0ll, (hi - base + w.pw - 1) / w.pw));
+          const int a = lo <= base ? 0 : p_lo;
+          const int z = hi <= base ? 0 : p_hi;
+          if (a >= z) continue;
+          if (!twait(bar(kBRecEmpty + k % kRecs), ((k / kRecs) & 1) ^ 1, wc)) {
+            ok = false;
+            break;
+          }
+          const bool whole = a == 0 && z == w.n_vis;
+          if (lane == 0) {
+            SegRec* r = rec(k);
+            r->n_pg = z - a;
+            r->g = g;
+            r->q0 = w.s.q0;
+            r->n_q = w.s.n_q;
+            r->ctx = w.ctx;
+            r->slot = whole ? -1 : 2 * (int)blockIdx.x + (a > 0 ? 0 : 1);
+          }
+          if (!whole && a == 0) {
+            // the first part tells the merge who has the others
+            const long long last = base + (long long)(w.n_vis - 1) * w.pw;
+            const int c_last = (int)(((last + 1) * G - 1) / total);
+            const int parts = c_last - (int)blockIdx.x + 1;
+            for (int i = lane; i < w.s.n_q; i += 32)
+              p.row_desc[(size_t)(w.s.q0 + i) * kKvHeads + g] = (int)blockIdx.x | parts << 8 | i << 20;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBRecFull + k % kRecs));
+          ++k;
+          const uint8_t* head = p.kv_pool + (size_t)g * kHeadBytes;
+          for (int i0 = a; ok && i0 < z; i0 += 32) {
+            const int i = i0 + lane, cnt = min(32, z - i0);
+            int blk = i;
+            if (p.sel) {
+              const int from = __shfl_sync(0xffffffffu, my_blk, i & 31);
+              blk = i < w.chosen ? from : w.first + i - w.chosen;
+            }
+            int phys = -1;
+            if (lane < cnt) {
+              phys = p.block_table[(size_t)b * p.max_pages + blk];
+              if (phys < 0 || phys >= p.n_pages) {
+                set_status(p.status, MSA_STATUS_BAD_PAGE);
+                phys = -1;
+              }
+            }
+            for (int j = 0; j < cnt; ++j, ++e) {
+              const int ph = __shfl_sync(0xffffffffu, phys, j), bl = __shfl_sync(0xffffffffu, blk, j);
+              const int st = e % kRaw;
+              if (!twait(bar(kBRawEmpty + st), ((e / kRaw) & 1) ^ 1, wc)) {
+                ok = false;
+                break;
+              }
+              if (lane == 0) {
+                const int pos = bl * kPageTokens;
+                s_info[e % kInfo] = make_int2(pos, ph < 0 ? 0 : min(kPageTokens, w.s.seq_len - pos));
+                if (ph < 0) {
+                  mbar_arrive(bar(kBRawFull + st));  // nothing to copy: no token of the page is valid
+                } else {
+                  mbar_arrive_expect_tx(bar(kBRawFull + st), kHeadBytes);
+                  bulk_g2s(sbase + kOffRaw + st * kHeadBytes, head + (size_t)ph * kKvPageBytes, kHeadBytes,
+                           bar(kBRawFull + st));
+                }
+                *s_issued = e + 1;
+              }
+              __syncwarp();
+            }
+          }
+        }
+      }
+    }
+    // no more segments
+    if (ok && twait(bar(kBRecEmpty + k % kRecs), ((k / kRecs) & 1) ^ 1, wc) && lane == 0) {
+      rec(k)->n_pg = -1;
+      mbar_arrive(bar(kBRecFull + k % kRecs));
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer ---------------------------------------------------------------
+    const uint32_t idesc_qk = umma_idesc_e4m3(128, 128);
+    // D fp32, A and B f16, A K-major, B MN-major
+    const uint32_t idesc_pv = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+    int e0 = 0, cnt[2] = {0, 0};
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      if (!twait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc)) break;
+      const int n_pg = rec(k)->n_pg;
+      if (n_pg < 0) break;
+      const int two = rec(k)->n_q > 32 ? 1 : 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
+      const int n_jobs = n_pg << two;
+      if (!twait(bar(kBQFull), k & 1, wc)) break;
+      auto qk = [&](int j) -> bool {
+        const int s = j & 1, e = e0 + (j >> two), sl = e % kSlot;
+        if (!twait(bar(kBKFull + sl), (e / kSlot) & 1, wc)) return false;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t a = umma_desc_sw128(sbase + kOffQ + (two ? s : 0) * 16384);
+          const uint64_t b = umma_desc_sw128(sbase + kOffK8 + sl * 16384);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) umma_e4m3(tmem + kTmemS + 128 * s, a + 2 * kk, b + 2 * kk, idesc_qk, kk > 0);
+          if (!two || (j & 1)) umma_commit(bar(kBKEmpty + sl));
+          if (j == n_jobs - 1) umma_commit(bar(kBQEmpty));
+          umma_commit(bar(kBSFull + s));
+        }
+        __syncwarp();
+        return true;
+      };
+      ok = qk(0) && (n_jobs < 2 || qk(1));
+      for (int j = 0; ok && j < n_jobs; ++j) {
+        const int s = j & 1, e = e0 + (j >> two), sl = e % kSlot;
+        if (j < 2 && k > 0 && !twait(bar(kBOFree), (k - 1) & 1, wc)) { ok = false; break; }
+        if (!twait(bar(kBVFull + sl), (e / kSlot) & 1, wc) || !twait(bar(kBPFull + s), cnt[s] & 1, wc)) {
+          ok = false;
+          break;
+        }
+        ++cnt[s];
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t v = sbase + kOffV16 + sl * 32768;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)  // 16 tokens each: 8 columns of P inside S's 32-column chunks
+            umma_f16_ts(tmem + kTmemO + 128 * s, tmem + kTmemS + 128 * s + 32 * (kk >> 1) + 8 * (kk & 1),
+                        umma_desc_sw128_lbo_sbo(v + kk * 2048, 16384, 1024), idesc_pv, (j >= 2 || kk > 0) ? 1u : 0u);
+          if (!two || (j & 1)) umma_commit(bar(kBVEmpty + sl));
+          umma_commit(bar(kBPvDone + s));
+        }
+        __syncwarp();
+        if (j + 2 < n_jobs) ok = qk(j + 2);
+      }
+      e0 += n_pg;
+    }
+    __syncwarp();
+    if (elect_one()) umma_commit(bar(kBDone));
+    __syncwarp();
+  } else if (warp == 2) {
+    // ---------------- query rows of a segment: row 4 i + h of draft i, head 4 g + h -----------------
+    for (int k = 0;; ++k) {
+      if (!twait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc)) break;
+      const SegRec r = *rec(k);
+      __syncwarp();
+      if (r.n_pg < 0) break;
+      if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
+      if (k > 0 && !twait(bar(kBQEmpty), (k - 1) & 1, wc)) break;
+      for (int x = lane; x < r.n_q * 32; x += 32) {
+        const int row = x >> 3, c = x & 7;
+        cp_async16(sbase + kOffQ + row * 128 + ((c ^ (row & 7)) << 4),
+                   p.q + ((size_t)(r.q0 + (row >> 2)) * kQHeads + kGqa * r.g + (row & 3)) * kHeadDim + 16 * c);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBQFull));
+    }
+  } else if (warp >= 16) {
+    // ---------------- V conversion: token tok, channels 64 half .. 64 half + 63 ----------------------
+    const int half = (warp - 16) >> 2, tok = 32 * (warp & 3) + lane;
+    const uint4* tab = reinterpret_cast<const uint4*>(smem + kOffVTab) + (lane & (kVTabCopies - 1));
+    int e = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      if (!twait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc)) break;
+      const int n_pg = rec(k)->n_pg;
+      __syncwarp();
+      if (n_pg < 0) break;
+      if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
+      for (int i = 0; i < n_pg; ++i, ++e) {
+        const int st = e % kRaw, sl = e % kSlot;
+        if (!twait(bar(kBRawFull + st), (e / kRaw) & 1, wc) || !twait(bar(kBVEmpty + sl), ((e / kSlot) & 1) ^ 1, wc)) {
+          ok = false;
+          break;
+        }
+        const uint8_t* raw = smem + kOffRaw + st * kHeadBytes + kOffVc;
+        const bool live = tok < s_info[e % kInfo].y;  // rows behind the sequence become zeros
+        uint8_t* dst = smem + kOffV16 + sl * 32768 + half * 16384 + tok * 128;
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) {
+          const int c = 2 * half + cc;
+          const uint4 w = *reinterpret_cast<const uint4*>(raw + tok * 64 + 16 * code_chunk_pos(c, tok));
+          const uint8_t* sc = raw + (kOffKs - kOffKc) + 2 * c * kPageTokens + tok;
+          uint4 t0 = tab[(sc[0] & 127) * kVTabCopies], t1 = tab[(sc[kPageTokens] & 127) * kVTabCopies];
+          uint4 o[4] = {dequant8_f16(w.x, t0), dequant8_f16(w.y, t0), dequant8_f16(w.z, t1), dequant8_f16(w.w, t1)};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            if (!live) o[u] = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(dst + (((4 * cc + u) ^ (tok & 7)) << 4)) = o[u];
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(kBVFull + sl));
+          mbar_arrive(bar(kBRawEmpty + st));
+        }
+      }
+    }
+  } else if (warp >= 12) {
+    // ---------------- K conversion: token tok ----------------------------------------------------------
+    const int tok = 32 * (warp & 3) + lane;
+    const uint2* tab = reinterpret_cast<const uint2*>(smem + kOffKTab) + (lane & (kKTabCopies - 1));
+    int e = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      if (!twait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc)) break;
+      const int n_pg = rec(k)->n_pg;
+      __syncwarp();
+      if (n_pg < 0) break;
+      if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
+      for (int i = 0; i < n_pg; ++i, ++e) {
+        const int st = e % kRaw, sl = e % kSlot;
+        if (!twait(bar(kBRawFull + st), (e / kRaw) & 1, wc) || !twait(bar(kBKEmpty + sl), ((e / kSlot) & 1) ^ 1, wc)) {
+          ok = false;
+          break;
+        }
+        const uint8_t* raw = smem + kOffRaw + st * kHeadBytes + kOffKc;
+        uint8_t* dst = smem + kOffK8 + sl * 16384 + tok * 128;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint4 w = *reinterpret_cast<const uint4*>(raw + tok * 64 + 16 * code_chunk_pos(c, tok));
+          const uint8_t* sc = raw + (kOffKs - kOffKc) + 2 * c * kPageTokens + tok;
+          const uint2 t0 = tab[(sc[0] & 127) * kKTabCopies], t1 = tab[(sc[kPageTokens] & 127) * kKTabCopies];
+          const uint2 a = dequant8(w.x, t0), b = dequant8(w.y, t0), d = dequant8(w.z, t1), f = dequant8(w.w, t1);
+          *reinterpret_cast<uint4*>(dst + (((2 * c) ^ (tok & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
+          *reinterpret_cast<uint4*>(dst + (((2 * c + 1) ^ (tok & 7)) << 4)) = make_uint4(d.x, d.y, f.x, f.y);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(kBKFull + sl));
+          mbar_arrive(bar(kBRawEmpty + st));
+        }
+      }
+    }
+  } else if (warp >= 4) {
+    // ---------------- softmax: set = (warp - 4) / 4, row = TMEM lane ------------------------------------
+    const int set = (warp - 4) >> 2, quad = warp & 3, lrow = 32 * quad + lane;
+    const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16);
+    const uint32_t t_s = tl + kTmemS + 128 * set;
+    int e0 = 0, cnt[2] = {0, 0};  // pages so far, jobs of each set so far
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      if (!twait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc)) break;
+      const SegRec r = *rec(k);
+      __syncwarp();
+      if (r.n_pg < 0) break;
+      if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
+      const int two = r.n_q > 32 ? 1 : 0;
+      const int n_jobs = r.n_pg << two;
+      const int n_rows = kGqa * r.n_q;
+      const int row = (two ? 128 * set : 0) + lrow;
+      const bool busy = (two ? 128 * set : 0) + 32 * quad < n_rows;  // some lane of the warp has a row
+      const bool mine = row < n_rows;
+      const int draft = row >> 2;
+      unsigned long long tm = 0;
+      if (mine) {
+        tm = p.tree_mask ? p.tree_mask[r.q0 + draft] : (2ull << draft) - 1;
+        if (r.n_q < 64) tm &= (1ull << r.n_q) - 1;
+      }
+      float m_ref = -INFINITY, l = 0.f;
+      for (int j = set; j < n_jobs; j += 2) {
+        if (!twait(bar(kBSFull + set), cnt[set] & 1, wc)) {
+          ok = false;
+          break;
+        }
+        ++cnt[set];
+        if (busy) {
+          const int2 info = s_info[(e0 + (j >> two)) % kInfo];
+          const bool edge = info.y < kPageTokens || info.x + kPageTokens > r.ctx;  // warp-uniform
+          tc_fence_after();
+          // pass 1: the page's maximum
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[32];
+            tmem_ld32x32b_x32(t_s + 32 * c, v);
+            tmem_wait_ld();
+            if (edge) {
+              const uint32_t vis = info.y > 0 ? visible_bits(tm, info.x + 32 * c, r.ctx) : 0u;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (vis >> i & 1) top = fmaxf(top, __uint_as_float(v[i]));
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(v[i]));
+            }
+          }
+          const float x_top = top * p.scale_log2;
+          const bool grow = x_top > m_ref + kTreeGrowth || (m_ref == -INFINITY && top > -INFINITY);
+          if (__any_sync(0xffffffffu, grow && mine)) {
+            const float m_new = grow ? x_top : m_ref;
+            const float f = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m_new);
+            m_ref = m_new;
+            l *= f;
+            if (j >= 2) {
+              // earlier pages' sums: the PVs before this S are done
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                uint32_t v[32];
+                const uint32_t t_o = tl + kTmemO + 128 * set + 32 * c;
+                tmem_ld32x32b_x32(t_o, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+                tmem_st32(t_o, v);
+              }
+            }
+          }
+          // pass 2: weights, as f16 pairs over the first half of each chunk's own columns
+          const float shift = m_ref == -INFINITY ? 0.f : kTreeBias - m_ref;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[32];
+            tmem_ld32x32b_x32(t_s + 32 * c, v);
+            tmem_wait_ld();
+            const uint32_t vis = !edge ? 0xFFFFFFFFu : info.y > 0 ? visible_bits(tm, info.x + 32 * c, r.ctx) : 0u;
+            uint32_t o[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float a = fast_exp2(fmaf(__uint_as_float(v[2 * i]), p.scale_log2, shift));
+              float b = fast_exp2(fmaf(__uint_as_float(v[2 * i + 1]), p.scale_log2, shift));
+              if (edge) {
+                a = vis >> (2 * i) & 1 ? a : 0.f;
+                b = vis >> (2 * i + 1) & 1 ? b : 0.f;
+              }
+              l += a + b;
+              o[i] = cvt_f16x2_f32(b, a);
+            }
+            tmem_st_x16(t_s + 32 * c, o);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBPFull + set));
+      }
+      if (!ok) break;
+      // ---- end of the segment: both accumulators are final ---------------------------------------------
+      cnt[set ^ 1] += two ? r.n_pg : (r.n_pg + (set ? 1 : 0)) >> 1;
+      const bool any0 = n_jobs > 0, any1 = n_jobs > 1;
+      ok = (set ? !any1 : !any0) || twait(bar(kBPvDone + set), (cnt[set] - 1) & 1, wc);
+      ok = ok && ((set ? !any0 : !any1) || twait(bar(kBPvDone + (set ^ 1)), (cnt[set ^ 1] - 1) & 1, wc));
+      float2* ml = reinterpret_cast<float2*>(smem + kOffMl) + (k & 1) * 256;
+      ml[128 * set + lrow] = make_float2(m_ref, l);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBMl));
+      if (!ok || !twait(bar(kBMl), k & 1, wc)) break;
+      float w0 = 1.f, w1 = 0.f, m = m_ref, L = l;
+      if (!two) {
+        const float2 a = ml[lrow], b = ml[128 + lrow];
+        m = fmaxf(a.x, b.x);
+        w0 = a.y > 0.f ? fast_exp2(a.x - m) : 0.f;
+        w1 = b.y > 0.f ? fast_exp2(b.x - m) : 0.f;
+        L = a.y * w0 + b.y * w1;
+      }
+      if (busy) {
+        tc_fence_after();
+        const size_t at = (size_t)(r.q0 + draft) * kQHeads + kGqa * r.g + (row & 3);
+        const float inv = L > 0.f ? p.out_scale / L : 0.f;
+        // one tile: set s writes channels 64 s .. of both accumulators' sum; two tiles: all of its own
+        const int c0 = two ? 0 : 2 * set, c1 = two ? 4 : 2 * set + 2;
+        for (int c = c0; c < c1; ++c) {
+          uint32_t v[32];
+          if (two) {
+            tmem_ld32x32b_x32(tl + kTmemO + 128 * set + 32 * c, v);
+            tmem_wait_ld();
+          } else {
+            tmem_ld32x32b_x32(tl + kTmemO + 32 * c, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(w0 > 0.f ? __uint_as_float(v[i]) * w0 : 0.f);
+            if (any1) {
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh) {
+                uint32_t u[16];
+                tmem_ld32x32b_x16(tl + kTmemO + 128 + 32 * c + 16 * hh, u);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  if (w1 > 0.f) v[16 * hh + i] = __float_as_uint(fmaf(__uint_as_float(u[i]), w1, __uint_as_float(v[16 * hh + i])));
+              }
+            }
+          }
+          if (mine) {
+            if (r.slot < 0) {
+              uint4* dst = reinterpret_cast<uint4*>(p.out + at * kHeadDim + 32 * c);
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                uint32_t x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  x[i] = L > 0.f ? pack16(__uint_as_float(v[8 * u + 2 * i]) * inv, __uint_as_float(v[8 * u + 2 * i + 1]) * inv, p.out_f16) : 0u;
+                dst[u] = make_uint4(x[0], x[1], x[2], x[3]);
+              }
+            } else {
+              float4* dst = reinterpret_cast<float4*>(p.part_o + ((size_t)r.slot * p.part_rows + row) * kHeadDim + 32 * c);
+#pragma unroll
+              for (int u = 0; u < 8; ++u)
+                dst[u] = L > 0.f ? make_float4(__uint_as_float(v[4 * u]), __uint_as_float(v[4 * u + 1]),
+                                               __uint_as_float(v[4 * u + 2]), __uint_as_float(v[4 * u + 3]))
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+          }
+        }
+        if (mine && (two || set == 0)) {
+          if (r.slot >= 0) p.part_ml[(size_t)r.slot * p.part_rows + row] = make_float2(m, L);
+          else if (p.lse) p.lse[at] = L > 0.f ? (m - kTreeBias + log2f(L)) * kTreeLn2 : -INFINITY;
+        }
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBOFree));
+      e0 += r.n_pg;
+    }
+  }
+
+  // ---- teardown -------------------------------------------------------------------------
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0) {
+    mbar_wait_drain(bar(kBDone), 0, p.wait_ns);  // every tcgen05.mma is done
+    if (*s_abort) {
+      set_status(p.status, MSA_STATUS_TIMEOUT);
+      for (int e = max(0, *s_issued - kRaw); e < *s_issued; ++e)  // copies that may still be landing
+        mbar_wait_drain(bar(kBRawFull + e % kRaw), (e / kRaw) & 1, p.wait_ns);
+    }
+  }
+  __syncthreads();
+  if (warp == 3) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Rows whose pages were cut across CTAs: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
+// One warp per (draft, KV head, query head), lane = 4 channels; parts in CTA order.
+__global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeParams p) {
+  const int lane = threadIdx.x & 31, h = (threadIdx.x >> 5) & 3;
+  const long long tg = (long long)blockIdx.x * 2 + (threadIdx.x >> 7);  // (token, KV head)
+  pdl_wait();
+  int desc = 0;
+  if (tg < (long long)p.n_q_total * kKvHeads) desc = p.row_desc[tg];
+  __syncthreads();
+  if (desc == 0) return;
+  if (h == 0 && lane == 0) p.row_desc[tg] = 0;  // at rest for the next call
+  const int c0 = desc & 255, parts = (desc >> 8) & 4095, row = 4 * (desc >> 20) + h;
+  float M = -INFINITY;
+  for (int i = lane; i < parts; i += 32) {
+    const float2 ml = p.part_ml[(size_t)(2 * (c0 + i) + (i == 0)) * p.part_rows + row];
+    if (ml.y > 0.f) M = fmaxf(M, ml.x);
+  }
+  M = warp_max_f32(M);
+  float L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < parts; ++i) {
+    const size_t at = (size_t)(2 * (c0 + i) + (i == 0)) * p.part_rows + row;
+    const float2 ml = p.part_ml[at];
+    const float4 x = reinterpret_cast<const float4*>(p.part_o + at * kHeadDim)[lane];
+    const float w = ml.y > 0.f ? fast_exp2(ml.x - M) : 0.f;
+    L = fmaf(ml.y, w, L);
+    o.x = fmaf(x.x, w, o.x);
+    o.y = fmaf(x.y, w, o.y);
+    o.z = fmaf(x.z, w, o.z);
+    o.w = fmaf(x.w, w, o.w);
+  }
+  const float inv = L > 0.f ? p.out_scale / L : 0.f;
+  const size_t at = (size_t)(tg >> 2) * kQHeads + kGqa * (tg & 3) + h;
+  *reinterpret_cast<uint2*>(p.out + at * kHeadDim + 4 * lane) =
+      make_uint2(pack16(o.x * inv, o.y * inv, p.out_f16), pack16(o.z * inv, o.w * inv, p.out_f16));
+  if (p.lse && lane == 0) p.lse[at] = L > 0.f ? (M - kTreeBias + log2f(L)) * kTreeLn2 : -INFINITY;
+}
+
+int tree_rows(int n_q_total) { return n_q_total < kTreeMaxDrafts ? kGqa * n_q_total : kGqa * kTreeMaxDrafts; }
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+
+size_t tree_attn_workspace_bytes(int n_q_total) {
+  const size_t rows = tree_rows(n_q_total);
+  return round256((size_t)n_q_total * kKvHeads * 4) + round256(2 * kTreeCtas * rows * 8) + 2 * kTreeCtas * rows * kHeadDim * 4;
+}
+
+cudaError_t launch_tree_attn(const msa_cache* c, const uint8_t* q, float softmax_scale, const int* block_table,
+                             int max_pages, const int* seq_lens, const int* q_start_loc, int n_seqs, int n_q_total,
+                             const uint64_t* tree_mask, const int* sel, const int* n_sel, int dtype, void* out,
+                             float* lse, void* ws, cudaStream_t stream) {
+  if (n_q_total == 0 || n_seqs == 0) return cudaSuccess;
+  static DeviceSetup setup;
+  int dev = 0, n_sm = 0;
+  cudaError_t e = setup.get(&dev, &n_sm, [](int) {
+    return cudaFuncSetAttribute(tree_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTreeSmem);
+  });
+  if (e != cudaSuccess) return e;
+  TreeParams tp{};
+  tp.kv_pool = static_cast<const uint8_t*>(c->kv_pool);
+  tp.n_pages = c->n_pages;
+  tp.q = q;
+  tp.block_table = block_table;
+  tp.max_pages = max_pages;
+  tp.seq_lens = seq_lens;
+  tp.q_start_loc = q_start_loc;
+  tp.n_seqs = n_seqs;
+  tp.n_q_total = n_q_total;
+  tp.tree_mask = reinterpret_cast<const unsigned long long*>(tree_mask);
+  tp.sel = sel;
+  tp.n_sel = n_sel;
+  tp.scale_log2 = softmax_scale / c->s_enc_k * kTreeLog2e;
+  tp.out_scale = 256.0f / c->s_enc_v;
+  tp.out_f16 = dtype == MSA_DTYPE_F16;
+  tp.out = static_cast<uint16_t*>(out);
+  tp.lse = lse;
+  tp.part_rows = tree_rows(n_q_total);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  tp.row_desc = reinterpret_cast<int*>(w);
+  w += round256((size_t)n_q_total * kKvHeads * 4);
+  tp.part_ml = reinterpret_cast<float2*>(w);
+  w += round256((size_t)2 * kTreeCtas * tp.part_rows * 8);
+  tp.part_o = reinterpret_cast<float*>(w);
+  tp.status = c->status;
+  tp.wait_ns = launch_settings().wait_ns;
+  const int most = n_sm < kTreeCtas ? n_sm : kTreeCtas;
+  e = launch_pdl(tree_attn_kernel, dim3(most), dim3(kTreeThreads), kTreeSmem, stream, tp);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(tree_merge_kernel, dim3((unsigned)(((long long)n_q_total * kKvHeads + 1) / 2)), dim3(256), 0, stream, tp);
+}
+
+}  // namespace msa

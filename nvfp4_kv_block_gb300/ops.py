@@ -102,6 +102,9 @@ _SIGS = {
     "msa_rotary_insert": (ctypes.c_int, [_P, _P, _I32, _P, _I32, _I32, _I32, _P, _P, _P, _P, _P]),
     "msa_rope_table_freqs": (ctypes.c_int, [_P, _I32, _P, _I32, ctypes.c_double, _P]),
     "msa_read_kv": (ctypes.c_int, [_P, _P, _I32, _I32, _P, _P, _P, _P]),
+    "msa_tree_attn": (ctypes.c_int, [_P, _P, _I32, ctypes.c_float, _P, _I32, _P, _P, _I32, _I32, _P, _P, _P, _I32, _P,
+                                     _P, _P, ctypes.c_size_t, _P]),
+    "msa_tree_attn_workspace_bytes": (ctypes.c_size_t, [_I32]),
     "msa_absmax": (ctypes.c_int, [_P, _I64, _P, _P]),
     "msa_encode_scale": (ctypes.c_float, [ctypes.c_float]),
     "msa_debug_fp8_page": (ctypes.c_int, [_P, _I64, _P, _P, _P]),
@@ -557,6 +560,62 @@ def read_kv(cache, slot_mapping, dtype=torch.bfloat16, k=None, v=None, idx_k=Non
         ctypes.byref(c), _ptr(slot_mapping, torch.int64, "slot_mapping", 1), n, _DTYPES[dtype],
         *(None if t is None else _ptr(t, dtype, name) for t, name in ((k, "k"), (v, "v"), (idx_k, "idx_k"))), _stream()))
     return k, v, idx_k
+
+
+TREE_MAX_DRAFTS = 64  # MSA_TREE_MAX_DRAFTS: query tokens of one sequence in tree_attn
+
+
+class TreeBuffers:
+    """Outputs and scratch of tree_attn for up to n_q_total query tokens of up to
+    n_seqs sequences (reused across steps): out [n_q_total, 16, 128] in ``dtype``
+    (bf16 or fp16), lse [n_q_total, 16]."""
+
+    def __init__(self, n_q_total, n_seqs, dtype=torch.bfloat16, device="cuda"):
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError(f"tree_attn's output is bfloat16 or float16, not {dtype}")
+        self.T, self.n_seqs = int(n_q_total), int(n_seqs)
+        nbytes = lib().msa_tree_attn_workspace_bytes(self.T)
+        self.ws = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+        self.out = torch.zeros((self.T, Q_HEADS, HEAD_DIM), dtype=dtype, device=device)
+        self.lse = torch.zeros((self.T, Q_HEADS), dtype=torch.float32, device=device)
+
+
+def tree_attn(cache, q, block_table, seq_lens, q_start_loc, bufs, tree_mask=None, sel=None, n_sel=None,
+              softmax_scale=None):
+    """Attention of each sequence's query tokens (drafts, up to 64, already in the
+    cache) over its whole cached context and over the drafts that ``tree_mask``
+    names (int64 [T], bit i of a draft's word: it sees draft i of its sequence;
+    None: drafts 0 .. itself).  With ``sel`` [B, 17] and ``n_sel`` [B] (ascending block
+    ids, e.g. of indexer_topk for one token per sequence) only those blocks of the
+    context are visited, and the blocks that hold drafts.  Returns bufs.out
+    [T, 16, 128]; bufs.lse [T, 16] has the log-sum-exp of the logits."""
+    T = q.shape[0]
+    n_seqs, max_pages = block_table.shape
+    if tuple(q.shape) != (T, Q_HEADS, HEAD_DIM):
+        raise ValueError("q must be [T, 16, 128] uint8 (E4M3)")
+    if tuple(seq_lens.shape) != (n_seqs,) or tuple(q_start_loc.shape) != (n_seqs + 1,):
+        raise ValueError("seq_lens must be [B], q_start_loc [B+1]")
+    if T != bufs.T or n_seqs > bufs.n_seqs:
+        raise ValueError(f"bufs are for {bufs.T} query tokens of up to {bufs.n_seqs} sequences")
+    if tree_mask is not None and tuple(tree_mask.shape) != (T,):
+        raise ValueError("tree_mask must be [T]")
+    if (sel is None) != (n_sel is None):
+        raise ValueError("sel and n_sel come together")
+    if sel is not None and (tuple(sel.shape) != (n_seqs, TOPK + 1) or tuple(n_sel.shape) != (n_seqs,)):
+        raise ValueError("sel must be [B, 17] and n_sel [B]")
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(HEAD_DIM)
+    _on_device(cache.kv_pool.device, q, block_table, seq_lens, q_start_loc, tree_mask, sel, n_sel, bufs.out)
+    c = cache.struct()
+    _check(lib().msa_tree_attn(
+        ctypes.byref(c), _ptr(q, torch.uint8, "q"), Q_HEADS, float(softmax_scale),
+        _ptr(block_table, torch.int32, "block_table"), max_pages, _ptr(seq_lens, torch.int32, "seq_lens"),
+        _ptr(q_start_loc, torch.int32, "q_start_loc"), n_seqs, T,
+        None if tree_mask is None else _ptr(tree_mask, torch.int64, "tree_mask"),
+        None if sel is None else _ptr(sel, torch.int32, "sel"),
+        None if n_sel is None else _ptr(n_sel, torch.int32, "n_sel"), _DTYPES[bufs.out.dtype],
+        bufs.out.data_ptr(), bufs.lse.data_ptr(), bufs.ws.data_ptr(), bufs.ws.numel(), _stream()))
+    return bufs.out
 
 
 def set_fault_injection(flags=0, wait_limit_ns=0):
