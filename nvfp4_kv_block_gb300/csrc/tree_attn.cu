@@ -58,7 +58,8 @@ constexpr int kOffVTab = kOffKTab + 128 * 8 * kKTabCopies;    // uint4 [128][cop
 constexpr int kOffMl = kOffVTab + 128 * 16 * kVTabCopies;     // float2 [2 parities][2 sets][128]
 constexpr int kOffRecs = kOffMl + 2 * 2 * 128 * 8;            // kRecs x 64 B
 constexpr int kOffInfo = kOffRecs + kRecs * 64;               // int2 [kInfo]: first position, valid tokens
-constexpr int kOffScan = kOffInfo + kInfo * 8;                // long long [32] and the start
+constexpr int kOffRow = kOffInfo + kInfo * 8;                 // float2 [2 sets][64]: a row's reference and sum
+constexpr int kOffScan = kOffRow + 2 * 64 * 8;                // long long [32] and the start
 constexpr int kOffTreeBars = kOffScan + 32 * 8 + 64;
 constexpr int kBRawFull = 0, kBRawEmpty = kBRawFull + kRaw, kBKFull = kBRawEmpty + kRaw, kBKEmpty = kBKFull + kSlot,
               kBVFull = kBKEmpty + kSlot, kBVEmpty = kBVFull + kSlot, kBSFull = kBVEmpty + kSlot, kBPFull = kBSFull + 2,
@@ -79,6 +80,11 @@ constexpr float kTreeLog2e = 1.4426950408889634f, kTreeLn2 = 0.6931471805599453f
 // has pages of it).
 constexpr int kPageWeight1 = 2, kPageWeight2 = 4, kFixedWeight = 6, kLeastShare = 4;
 static_assert(kLeastShare >= kPageWeight2, "a share holds a page");
+
+// Copies of the query rows in a one-tile segment's 128 rows: with few rows every
+// warp quad (32 lanes of tensor memory) gets the same rows and its own share of a
+// page's tokens, so that no softmax warp is idle.
+__host__ __device__ __forceinline__ int tree_copies(int n_q) { return n_q <= 8 ? 4 : n_q <= 16 ? 2 : 1; }
 
 struct SegRec {
   int n_pg;      // pages of the segment; -1: no more segments
@@ -136,6 +142,41 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, 
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+__device__ __forceinline__ uint64_t pair64(uint32_t a, uint32_t b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint2 split64(uint64_t x) {
+  uint2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(r.x), "=r"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// OR of a predicate over the threads of a named barrier (all of them wait).
+__device__ __forceinline__ bool barrier_or(int id, int nthreads, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, %2, %3, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"((uint32_t)pred), "r"(id), "r"(nthreads)
+      : "memory");
+  return r != 0;
 }
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -199,7 +240,8 @@ __device__ __forceinline__ uint32_t pack16(float a, float b, bool f16) {
 
 __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid_constant__ TreeParams p) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (pointer arithmetic, no integer cast: the accesses stay shared-memory instructions)
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t sbase = smem_u32(smem);
   auto bar = [&](int i) { return sbase + kOffTreeBars + 8 * i; };
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffTreeMisc);
@@ -308,6 +350,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
   const int G = (int)min((long long)gridDim.x, max(1ll, total / kLeastShare));
   const bool idle = (int)blockIdx.x >= G || total == 0;
 
+  // registers: 128 threads x 64 + 256 x 120 + 384 x 56 of the launch's 768 x 80
+  if (warp < 4) {
+    regs_dec<64>();
   if (warp == 0) {
     // ---------------- segment records and page copies -------------------------------------
     int e = 0, k = 0;
@@ -490,17 +535,286 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       if (r.n_pg < 0) break;
       if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
       if (k > 0 && !twait(bar(kBQEmpty), (k - 1) & 1, wc)) break;
+      // the second tile is also the exchange buffer of a segment with row copies
+      if (k > 0 && r.n_q > 32 && !twait(bar(kBOFree), (k - 1) & 1, wc)) break;
+      const int copies = tree_copies(r.n_q), gap = 128 / copies;
       for (int x = lane; x < r.n_q * 32; x += 32) {
         const int row = x >> 3, c = x & 7;
-        cp_async16(sbase + kOffQ + row * 128 + ((c ^ (row & 7)) << 4),
-                   p.q + ((size_t)(r.q0 + (row >> 2)) * kQHeads + kGqa * r.g + (row & 3)) * kHeadDim + 16 * c);
+        const uint8_t* src = p.q + ((size_t)(r.q0 + (row >> 2)) * kQHeads + kGqa * r.g + (row & 3)) * kHeadDim + 16 * c;
+        for (int i = 0; i < copies; ++i)
+          cp_async16(sbase + kOffQ + (row + i * gap) * 128 + ((c ^ (row & 7)) << 4), src);
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBQFull));
     }
-  } else if (warp >= 16) {
+  }
+  } else if (warp < 12) {
+    regs_inc<120>();
+    // ---------------- softmax: set = (warp - 4) / 4, row = TMEM lane ------------------------------------
+    const int set = (warp - 4) >> 2, quad = warp & 3, lrow = 32 * quad + lane;
+    const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16);
+    const uint32_t t_s = tl + kTmemS + 128 * set;
+    const uint64_t scale2 = pair64(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
+    int e0 = 0, cnt[2] = {0, 0};  // pages so far, jobs of each set so far
+    bool ok = true;
+    for (int k = 0;; ++k) {
+      // (the set's warps leave together: they meet at named barriers below)
+      if (barrier_or(1 + set, 128, !twait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc))) break;
+      const SegRec r = *rec(k);
+      __syncwarp();
+      if (r.n_pg < 0) break;
+      if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
+      const int two = r.n_q > 32 ? 1 : 0;
+      const int n_jobs = r.n_pg << two;
+      const int n_rows = kGqa * r.n_q;
+      const int copies = tree_copies(r.n_q), gap = 128 / copies;  // (one copy with two tiles)
+      const int row = two ? 128 * set + lrow : lrow & (gap - 1);
+      const int copy = lrow / gap;
+      const bool busy = row - lane < n_rows;  // some lane of the warp has a row
+      const bool mine = row < n_rows;
+      const int draft = row >> 2;
+      // this warp's token chunks of a page: 32-column chunks c0 .. c1 - 1
+      const int c0 = copy * 4 / copies, c1 = c0 + 4 / copies;
+      unsigned long long tm = 0;
+      if (mine) {
+        tm = p.tree_mask ? p.tree_mask[r.q0 + draft] : (2ull << draft) - 1;
+        if (r.n_q < 64) tm &= (1ull << r.n_q) - 1;
+      }
+      float m_ref = -INFINITY, l = 0.f;
+      for (int j = set; j < n_jobs; j += 2) {
+        if (!twait(bar(kBSFull + set), cnt[set] & 1, wc)) {
+          ok = false;
+          break;
+        }
+        ++cnt[set];
+        if (busy) {
+          const int2 info = s_info[(e0 + (j >> two)) % kInfo];
+          const bool edge = info.y < kPageTokens || info.x + kPageTokens > r.ctx;  // warp-uniform
+          // logits of chunk c, -inf where the row does not see the token
+          auto load = [&](int c, uint32_t* v) { tmem_ld32x32b_x32(t_s + 32 * c, v); };
+          auto mask = [&](int c, uint32_t* v) {
+            const uint32_t vis = info.y > 0 ? visible_bits(tm, info.x + 32 * c, r.ctx) : 0u;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = vis >> i & 1 ? v[i] : 0xFF800000u;
+          };
+          auto most = [&](const uint32_t* v, float top) {
+            float t[4] = {top, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                t[u] = fmaxf(fmaxf(t[u], __uint_as_float(v[i + 2 * u])), __uint_as_float(v[i + 2 * u + 1]));
+            return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+          };
+          tc_fence_after();
+          // the page's maximum over this warp's tokens (a warp with one chunk keeps its logits)
+          float top = -INFINITY;
+          uint32_t v[32];
+          if (copies == 4) {
+            load(c0, v);
+            tmem_wait_ld();
+            if (edge) mask(c0, v);
+            top = most(v, top);
+          } else {
+#pragma unroll 1
+            for (int c = c0; c < c1; c += 2) {
+              uint32_t u[32];
+              load(c, v);
+              load(c + 1, u);
+              tmem_wait_ld();
+              if (edge) {
+                mask(c, v);
+                mask(c + 1, u);
+              }
+              top = most(u, most(v, top));
+            }
+          }
+          const float x_top = top * p.scale_log2;
+          const bool grow = x_top > m_ref + kTreeGrowth || (m_ref == -INFINITY && top > -INFINITY);
+          if (__any_sync(0xffffffffu, grow && mine)) {
+            const float m_new = grow ? x_top : m_ref;
+            const float f = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m_new);
+            m_ref = m_new;
+            l *= f;
+            if (j >= 2) {
+              // earlier pages' sums: the PVs before this S are done
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                uint32_t u[32];
+                const uint32_t t_o = tl + kTmemO + 128 * set + 32 * c;
+                tmem_ld32x32b_x32(t_o, u);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * f);
+                tmem_st32(t_o, u);
+              }
+            }
+          }
+          // weights, as f16 pairs over the first half of each chunk's own columns
+          const float shift = m_ref == -INFINITY ? 0.f : kTreeBias - m_ref;
+          const uint64_t shift2 = pair64(__float_as_uint(shift), __float_as_uint(shift));
+          uint64_t sums[2] = {0, 0};
+          auto weigh = [&](int c, const uint32_t* v) {
+            uint32_t o[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint2 x = split64(fma_f32x2(pair64(v[2 * i], v[2 * i + 1]), scale2, shift2));
+              const float a = fast_exp2(__uint_as_float(x.x)), b = fast_exp2(__uint_as_float(x.y));
+              sums[i & 1] = add_f32x2(sums[i & 1], pair64(__float_as_uint(a), __float_as_uint(b)));
+              o[i] = cvt_f16x2_f32(b, a);
+            }
+            tmem_st_x16(t_s + 32 * c, o);
+          };
+          if (copies == 4) {
+            weigh(c0, v);
+          } else {
+#pragma unroll 1
+            for (int c = c0; c < c1; c += 2) {
+              uint32_t u[32];
+              load(c, v);
+              load(c + 1, u);
+              tmem_wait_ld();
+              if (edge) {
+                mask(c, v);
+                mask(c + 1, u);
+              }
+              weigh(c, v);
+              weigh(c + 1, u);
+            }
+          }
+          if (copies > 1) {  // the other warps' tokens
+            uint32_t zero[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) zero[i] = 0;
+            for (int c = 0; c < 4; ++c)
+              if (c < c0 || c >= c1) tmem_st_x16(t_s + 32 * c, zero);
+          }
+          const uint2 sum = split64(add_f32x2(sums[0], sums[1]));
+          l += __uint_as_float(sum.x) + __uint_as_float(sum.y);
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBPFull + set));
+      }
+      // ---- end of the segment: both accumulators are final ---------------------------------------------
+      const bool any0 = n_jobs > 0, any1 = n_jobs > 1;
+      if (ok) {
+        cnt[set ^ 1] += two ? r.n_pg : (r.n_pg + (set ? 1 : 0)) >> 1;
+        ok = (set ? !any1 : !any0) || twait(bar(kBPvDone + set), (cnt[set] - 1) & 1, wc);
+        ok = ok && ((set ? !any0 : !any1) || twait(bar(kBPvDone + (set ^ 1)), (cnt[set ^ 1] - 1) & 1, wc));
+      }
+      float2* ml = reinterpret_cast<float2*>(smem + kOffMl) + (k & 1) * 256;
+      ml[128 * set + lrow] = make_float2(m_ref, l);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBMl));
+      ok = ok && twait(bar(kBMl), k & 1, wc);
+      if (barrier_or(1 + set, 128, !ok)) break;
+      // the row's parts (one per set and copy): the joint reference and sum, the weights of this lane's
+      float w0 = 1.f, w1 = 0.f, m = m_ref, L = l;
+      if (!two) {
+        m = -INFINITY;
+        for (int i = 0; i < copies; ++i) m = fmaxf(m, fmaxf(ml[row + i * gap].x, ml[128 + row + i * gap].x));
+        L = 0.f;
+        for (int i = 0; i < copies; ++i) {
+          const float2 a = ml[row + i * gap], b = ml[128 + row + i * gap];
+          const float wa = a.y > 0.f ? fast_exp2(a.x - m) : 0.f, wb = b.y > 0.f ? fast_exp2(b.x - m) : 0.f;
+          L = fmaf(a.y, wa, fmaf(b.y, wb, L));
+          if (i == copy) {
+            w0 = wa;
+            w1 = wb;
+          }
+        }
+      }
+      const size_t at0 = (size_t)r.q0 * kQHeads + kGqa * r.g;  // row i of the segment: + 16 (i / 4) + i % 4
+      auto store4 = [&](int i, int ch, float Li, float a, float b, float c, float d) {
+        if (r.slot < 0) {
+          const float inv = Li > 0.f ? p.out_scale / Li : 0.f;
+          uint2 x = make_uint2(pack16(a * inv, b * inv, p.out_f16), pack16(c * inv, d * inv, p.out_f16));
+          if (!(Li > 0.f)) x = make_uint2(0u, 0u);
+          *reinterpret_cast<uint2*>(p.out + (at0 + (size_t)(i >> 2) * kQHeads + (i & 3)) * kHeadDim + ch) = x;
+        } else {
+          *reinterpret_cast<float4*>(p.part_o + ((size_t)r.slot * p.part_rows + i) * kHeadDim + ch) =
+              Li > 0.f ? make_float4(a, b, c, d) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      };
+      tc_fence_after();
+      if (copies > 1) {
+        // set s joins channels 64 s .. of both accumulators, 16 at a time, across the warps' copies
+        float* xb = reinterpret_cast<float*>(smem + kOffQ + 16384 + 8192 * set);  // [128 lanes][16], chunks swizzled
+        float2* rows = reinterpret_cast<float2*>(smem + kOffRow) + 64 * set;
+        if (copy == 0) rows[row] = make_float2(m, L);
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          const int ch = 64 * set + 16 * q;
+          uint32_t u[16], v[16];
+          tmem_ld32x32b_x16(tl + kTmemO + ch, u);
+          if (any1) tmem_ld32x32b_x16(tl + kTmemO + 128 + ch, v);
+          tmem_wait_ld();
+          float x[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            x[i] = w0 > 0.f ? __uint_as_float(u[i]) * w0 : 0.f;
+            if (any1 && w1 > 0.f) x[i] = fmaf(__uint_as_float(v[i]), w1, x[i]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float4*>(xb + 16 * lrow + 4 * (i ^ (lrow >> 1 & 3))) =
+                make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+          named_barrier_sync(1 + set, 128);
+          for (int i = lrow; i < 4 * n_rows; i += 128) {
+            const int ri = i >> 2, c = i & 3;
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int cp = 0; cp < copies; ++cp) {
+              const int ln = ri + cp * gap;
+              const float4 z = *reinterpret_cast<const float4*>(xb + 16 * ln + 4 * (c ^ (ln >> 1 & 3)));
+              y.x += z.x;
+              y.y += z.y;
+              y.z += z.z;
+              y.w += z.w;
+            }
+            store4(ri, ch + 4 * c, rows[ri].y, y.x, y.y, y.z, y.w);
+          }
+          named_barrier_sync(1 + set, 128);
+        }
+      } else if (busy) {
+        // one tile: set s writes channels 64 s .. of both accumulators' sum; two tiles: all of its own
+        const int ca = two ? 0 : 2 * set, cz = two ? 4 : 2 * set + 2;
+#pragma unroll 1
+        for (int c = ca; c < cz; ++c) {
+          uint32_t v[32];
+          tmem_ld32x32b_x32(tl + kTmemO + (two ? 128 * set : 0) + 32 * c, v);
+          if (!two && any1) {
+            uint32_t u[32];
+            tmem_ld32x32b_x32(tl + kTmemO + 128 + 32 * c, u);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              v[i] = __float_as_uint((w0 > 0.f ? __uint_as_float(v[i]) * w0 : 0.f) + (w1 > 0.f ? __uint_as_float(u[i]) * w1 : 0.f));
+          } else {
+            tmem_wait_ld();
+          }
+          if (mine)
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              store4(row, 32 * c + 4 * u, L, __uint_as_float(v[4 * u]), __uint_as_float(v[4 * u + 1]),
+                     __uint_as_float(v[4 * u + 2]), __uint_as_float(v[4 * u + 3]));
+        }
+      }
+      if (mine && copy == 0 && (two || set == 0)) {
+        if (r.slot >= 0) p.part_ml[(size_t)r.slot * p.part_rows + row] = make_float2(m, L);
+        else if (p.lse) p.lse[at0 + (size_t)(row >> 2) * kQHeads + (row & 3)] = L > 0.f ? (m - kTreeBias + log2f(L)) * kTreeLn2 : -INFINITY;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBOFree));
+      e0 += r.n_pg;
+    }
+  } else {
+    regs_dec<56>();
+  if (warp >= 16) {
     // ---------------- V conversion: token tok, channels 64 half .. 64 half + 63 ----------------------
     const int half = (warp - 16) >> 2, tok = 32 * (warp & 3) + lane;
     const uint4* tab = reinterpret_cast<const uint4*>(smem + kOffVTab) + (lane & (kVTabCopies - 1));
@@ -521,13 +835,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
         const uint8_t* raw = smem + kOffRaw + st * kHeadBytes + kOffVc;
         const bool live = tok < s_info[e % kInfo].y;  // rows behind the sequence become zeros
         uint8_t* dst = smem + kOffV16 + sl * 32768 + half * 16384 + tok * 128;
+        // every load before the first store: the compiler must not assume that they are apart
+        uint4 w[2], t[4];
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc)
+          w[cc] = *reinterpret_cast<const uint4*>(raw + tok * 64 + 16 * code_chunk_pos(2 * half + cc, tok));
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          t[u] = tab[(raw[(kOffKs - kOffKc) + (4 * half + u) * kPageTokens + tok] & 127) * kVTabCopies];
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
-          const int c = 2 * half + cc;
-          const uint4 w = *reinterpret_cast<const uint4*>(raw + tok * 64 + 16 * code_chunk_pos(c, tok));
-          const uint8_t* sc = raw + (kOffKs - kOffKc) + 2 * c * kPageTokens + tok;
-          uint4 t0 = tab[(sc[0] & 127) * kVTabCopies], t1 = tab[(sc[kPageTokens] & 127) * kVTabCopies];
-          uint4 o[4] = {dequant8_f16(w.x, t0), dequant8_f16(w.y, t0), dequant8_f16(w.z, t1), dequant8_f16(w.w, t1)};
+          uint4 o[4] = {dequant8_f16(w[cc].x, t[2 * cc]), dequant8_f16(w[cc].y, t[2 * cc]),
+                        dequant8_f16(w[cc].z, t[2 * cc + 1]), dequant8_f16(w[cc].w, t[2 * cc + 1])};
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             if (!live) o[u] = make_uint4(0, 0, 0, 0);
@@ -542,7 +861,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
         }
       }
     }
-  } else if (warp >= 12) {
+  } else {
     // ---------------- K conversion: token tok ----------------------------------------------------------
     const int tok = 32 * (warp & 3) + lane;
     const uint2* tab = reinterpret_cast<const uint2*>(smem + kOffKTab) + (lane & (kKTabCopies - 1));
@@ -562,12 +881,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
         }
         const uint8_t* raw = smem + kOffRaw + st * kHeadBytes + kOffKc;
         uint8_t* dst = smem + kOffK8 + sl * 16384 + tok * 128;
+        uint4 w[4];
+        uint2 t[8];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) w[c] = *reinterpret_cast<const uint4*>(raw + tok * 64 + 16 * code_chunk_pos(c, tok));
+#pragma unroll
+        for (int u = 0; u < 8; ++u) t[u] = tab[(raw[(kOffKs - kOffKc) + u * kPageTokens + tok] & 127) * kKTabCopies];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const uint4 w = *reinterpret_cast<const uint4*>(raw + tok * 64 + 16 * code_chunk_pos(c, tok));
-          const uint8_t* sc = raw + (kOffKs - kOffKc) + 2 * c * kPageTokens + tok;
-          const uint2 t0 = tab[(sc[0] & 127) * kKTabCopies], t1 = tab[(sc[kPageTokens] & 127) * kKTabCopies];
-          const uint2 a = dequant8(w.x, t0), b = dequant8(w.y, t0), d = dequant8(w.z, t1), f = dequant8(w.w, t1);
+          const uint2 a = dequant8(w[c].x, t[2 * c]), b = dequant8(w[c].y, t[2 * c]);
+          const uint2 d = dequant8(w[c].z, t[2 * c + 1]), f = dequant8(w[c].w, t[2 * c + 1]);
           *reinterpret_cast<uint4*>(dst + (((2 * c) ^ (tok & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
           *reinterpret_cast<uint4*>(dst + (((2 * c + 1) ^ (tok & 7)) << 4)) = make_uint4(d.x, d.y, f.x, f.y);
         }
@@ -579,186 +902,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
         }
       }
     }
-  } else if (warp >= 4) {
-    // ---------------- softmax: set = (warp - 4) / 4, row = TMEM lane ------------------------------------
-    const int set = (warp - 4) >> 2, quad = warp & 3, lrow = 32 * quad + lane;
-    const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16);
-    const uint32_t t_s = tl + kTmemS + 128 * set;
-    int e0 = 0, cnt[2] = {0, 0};  // pages so far, jobs of each set so far
-    bool ok = true;
-    for (int k = 0; ok; ++k) {
-      if (!twait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc)) break;
-      const SegRec r = *rec(k);
-      __syncwarp();
-      if (r.n_pg < 0) break;
-      if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
-      const int two = r.n_q > 32 ? 1 : 0;
-      const int n_jobs = r.n_pg << two;
-      const int n_rows = kGqa * r.n_q;
-      const int row = (two ? 128 * set : 0) + lrow;
-      const bool busy = (two ? 128 * set : 0) + 32 * quad < n_rows;  // some lane of the warp has a row
-      const bool mine = row < n_rows;
-      const int draft = row >> 2;
-      unsigned long long tm = 0;
-      if (mine) {
-        tm = p.tree_mask ? p.tree_mask[r.q0 + draft] : (2ull << draft) - 1;
-        if (r.n_q < 64) tm &= (1ull << r.n_q) - 1;
-      }
-      float m_ref = -INFINITY, l = 0.f;
-      for (int j = set; j < n_jobs; j += 2) {
-        if (!twait(bar(kBSFull + set), cnt[set] & 1, wc)) {
-          ok = false;
-          break;
-        }
-        ++cnt[set];
-        if (busy) {
-          const int2 info = s_info[(e0 + (j >> two)) % kInfo];
-          const bool edge = info.y < kPageTokens || info.x + kPageTokens > r.ctx;  // warp-uniform
-          tc_fence_after();
-          // pass 1: the page's maximum
-          float top = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[32];
-            tmem_ld32x32b_x32(t_s + 32 * c, v);
-            tmem_wait_ld();
-            if (edge) {
-              const uint32_t vis = info.y > 0 ? visible_bits(tm, info.x + 32 * c, r.ctx) : 0u;
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (vis >> i & 1) top = fmaxf(top, __uint_as_float(v[i]));
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(v[i]));
-            }
-          }
-          const float x_top = top * p.scale_log2;
-          const bool grow = x_top > m_ref + kTreeGrowth || (m_ref == -INFINITY && top > -INFINITY);
-          if (__any_sync(0xffffffffu, grow && mine)) {
-            const float m_new = grow ? x_top : m_ref;
-            const float f = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m_new);
-            m_ref = m_new;
-            l *= f;
-            if (j >= 2) {
-              // earlier pages' sums: the PVs before this S are done
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                uint32_t v[32];
-                const uint32_t t_o = tl + kTmemO + 128 * set + 32 * c;
-                tmem_ld32x32b_x32(t_o, v);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-                tmem_st32(t_o, v);
-              }
-            }
-          }
-          // pass 2: weights, as f16 pairs over the first half of each chunk's own columns
-          const float shift = m_ref == -INFINITY ? 0.f : kTreeBias - m_ref;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[32];
-            tmem_ld32x32b_x32(t_s + 32 * c, v);
-            tmem_wait_ld();
-            const uint32_t vis = !edge ? 0xFFFFFFFFu : info.y > 0 ? visible_bits(tm, info.x + 32 * c, r.ctx) : 0u;
-            uint32_t o[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float a = fast_exp2(fmaf(__uint_as_float(v[2 * i]), p.scale_log2, shift));
-              float b = fast_exp2(fmaf(__uint_as_float(v[2 * i + 1]), p.scale_log2, shift));
-              if (edge) {
-                a = vis >> (2 * i) & 1 ? a : 0.f;
-                b = vis >> (2 * i + 1) & 1 ? b : 0.f;
-              }
-              l += a + b;
-              o[i] = cvt_f16x2_f32(b, a);
-            }
-            tmem_st_x16(t_s + 32 * c, o);
-          }
-          tmem_wait_st();
-          tc_fence_before();
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBPFull + set));
-      }
-      if (!ok) break;
-      // ---- end of the segment: both accumulators are final ---------------------------------------------
-      cnt[set ^ 1] += two ? r.n_pg : (r.n_pg + (set ? 1 : 0)) >> 1;
-      const bool any0 = n_jobs > 0, any1 = n_jobs > 1;
-      ok = (set ? !any1 : !any0) || twait(bar(kBPvDone + set), (cnt[set] - 1) & 1, wc);
-      ok = ok && ((set ? !any0 : !any1) || twait(bar(kBPvDone + (set ^ 1)), (cnt[set ^ 1] - 1) & 1, wc));
-      float2* ml = reinterpret_cast<float2*>(smem + kOffMl) + (k & 1) * 256;
-      ml[128 * set + lrow] = make_float2(m_ref, l);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBMl));
-      if (!ok || !twait(bar(kBMl), k & 1, wc)) break;
-      float w0 = 1.f, w1 = 0.f, m = m_ref, L = l;
-      if (!two) {
-        const float2 a = ml[lrow], b = ml[128 + lrow];
-        m = fmaxf(a.x, b.x);
-        w0 = a.y > 0.f ? fast_exp2(a.x - m) : 0.f;
-        w1 = b.y > 0.f ? fast_exp2(b.x - m) : 0.f;
-        L = a.y * w0 + b.y * w1;
-      }
-      if (busy) {
-        tc_fence_after();
-        const size_t at = (size_t)(r.q0 + draft) * kQHeads + kGqa * r.g + (row & 3);
-        const float inv = L > 0.f ? p.out_scale / L : 0.f;
-        // one tile: set s writes channels 64 s .. of both accumulators' sum; two tiles: all of its own
-        const int c0 = two ? 0 : 2 * set, c1 = two ? 4 : 2 * set + 2;
-        for (int c = c0; c < c1; ++c) {
-          uint32_t v[32];
-          if (two) {
-            tmem_ld32x32b_x32(tl + kTmemO + 128 * set + 32 * c, v);
-            tmem_wait_ld();
-          } else {
-            tmem_ld32x32b_x32(tl + kTmemO + 32 * c, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(w0 > 0.f ? __uint_as_float(v[i]) * w0 : 0.f);
-            if (any1) {
-#pragma unroll
-              for (int hh = 0; hh < 2; ++hh) {
-                uint32_t u[16];
-                tmem_ld32x32b_x16(tl + kTmemO + 128 + 32 * c + 16 * hh, u);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  if (w1 > 0.f) v[16 * hh + i] = __float_as_uint(fmaf(__uint_as_float(u[i]), w1, __uint_as_float(v[16 * hh + i])));
-              }
-            }
-          }
-          if (mine) {
-            if (r.slot < 0) {
-              uint4* dst = reinterpret_cast<uint4*>(p.out + at * kHeadDim + 32 * c);
-#pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                uint32_t x[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  x[i] = L > 0.f ? pack16(__uint_as_float(v[8 * u + 2 * i]) * inv, __uint_as_float(v[8 * u + 2 * i + 1]) * inv, p.out_f16) : 0u;
-                dst[u] = make_uint4(x[0], x[1], x[2], x[3]);
-              }
-            } else {
-              float4* dst = reinterpret_cast<float4*>(p.part_o + ((size_t)r.slot * p.part_rows + row) * kHeadDim + 32 * c);
-#pragma unroll
-              for (int u = 0; u < 8; ++u)
-                dst[u] = L > 0.f ? make_float4(__uint_as_float(v[4 * u]), __uint_as_float(v[4 * u + 1]),
-                                               __uint_as_float(v[4 * u + 2]), __uint_as_float(v[4 * u + 3]))
-                                 : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-          }
-        }
-        if (mine && (two || set == 0)) {
-          if (r.slot >= 0) p.part_ml[(size_t)r.slot * p.part_rows + row] = make_float2(m, L);
-          else if (p.lse) p.lse[at] = L > 0.f ? (m - kTreeBias + log2f(L)) * kTreeLn2 : -INFINITY;
-        }
-        tc_fence_before();
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBOFree));
-      e0 += r.n_pg;
-    }
+  }
   }
 
   // ---- teardown -------------------------------------------------------------------------
