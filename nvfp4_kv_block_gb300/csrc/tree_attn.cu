@@ -24,9 +24,8 @@
 //   warp 0        segment records and one 18,432-byte bulk copy per page;
 //   warp 1        MMA issuer: S = Q K8^T (kind::f8f6f4, 128 x 128 x 128), then
 //                 O += P V (kind::f16, P from tensor memory over S's own columns,
-//                 V MN-major), in the order QK(j + 2) behind PV(j);
+//                 V MN-major), the set's next QK behind it;
 //   warp 2        query rows of the next segment (cp.async);
-//   warp 3        tensor-memory allocation;
 //   warps 4-11    two softmax sets, thread = row: with one row tile a set takes
 //                 every other page (its own reference, sum and accumulator, joined
 //                 at the segment's end), with two tiles a set takes a tile;
@@ -34,6 +33,8 @@
 //                 token and half of the channels.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -44,7 +45,7 @@ constexpr int kTreeThreads = 768;
 constexpr int kTreeMaxDrafts = 64;  // per sequence: one 64-bit mask word, two row tiles
 constexpr int kTreeCtas = 152;      // most CTAs of a launch (the workspace is sized for them)
 constexpr int kRaw = 4;             // raw page stages
-constexpr int kSlot = 2;            // converted pages in flight
+constexpr int kSlot = 2;            // converted pages in flight (page e in slot e & 1)
 constexpr int kRecs = 4;
 constexpr int kInfo = 16;
 constexpr int kKTabCopies = 4, kVTabCopies = 8;
@@ -62,8 +63,8 @@ constexpr int kOffRow = kOffInfo + kInfo * 8;                 // float2 [2 sets]
 constexpr int kOffScan = kOffRow + 2 * 64 * 8;                // long long [32] and the start
 constexpr int kOffTreeBars = kOffScan + 32 * 8 + 64;
 constexpr int kBRawFull = 0, kBRawEmpty = kBRawFull + kRaw, kBKFull = kBRawEmpty + kRaw, kBKEmpty = kBKFull + kSlot,
-              kBVFull = kBKEmpty + kSlot, kBVEmpty = kBVFull + kSlot, kBSFull = kBVEmpty + kSlot, kBPFull = kBSFull + 2,
-              kBPvDone = kBPFull + 2, kBOFree = kBPvDone + 2, kBMl = kBOFree + 1, kBQFull = kBMl + 1,
+              kBVEmpty = kBKEmpty + kSlot, kBSFull = kBVEmpty + kSlot, kBPFull = kBSFull + 2,  // P: [set][slot]
+              kBPvDone = kBPFull + 2 * kSlot, kBOFree = kBPvDone + 2, kBMl = kBOFree + 1, kBQFull = kBMl + 1,
               kBQEmpty = kBQFull + 1, kBRecFull = kBQEmpty + 1, kBRecEmpty = kBRecFull + kRecs,
               kBDone = kBRecEmpty + kRecs, kTreeBars = kBDone + 1;
 constexpr int kOffTreeMisc = kOffTreeBars + 8 * ((kTreeBars + 1) & ~1);  // tmem, abort, copies issued
@@ -283,12 +284,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
     for (int i = 0; i < kSlot; ++i) {
       mbar_init(bar(kBKFull + i), 4);
       mbar_init(bar(kBKEmpty + i), 1);
-      mbar_init(bar(kBVFull + i), 8);
       mbar_init(bar(kBVEmpty + i), 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(kBSFull + s), 1);
-      mbar_init(bar(kBPFull + s), 4);
+      mbar_init(bar(kBPFull + 2 * s), 4 + 8);  // the set's softmax warps and the V conversion
+      mbar_init(bar(kBPFull + 2 * s + 1), 4 + 8);
       mbar_init(bar(kBPvDone + s), 1);
     }
     mbar_init(bar(kBOFree), 8);
@@ -468,58 +469,83 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       mbar_arrive(bar(kBRecFull + k % kRecs));
     }
   } else if (warp == 1) {
-    // ---------------- MMA issuer ---------------------------------------------------------------
+    // ---------------- MMA issuer ---------------------------------------------------------------------
+    // Job j of a segment belongs to set j & 1: page j with one row tile, tile j & 1 of page j / 2
+    // with two.  In turn: PV(j), then QK(j + 2) into the same columns.  The two sets' jobs
+    // alternate on one issuer, so that one set's products run under the other's softmax (an
+    // issuer per set lets two tiles fall into step: 603 against 482 us on 8 x 128K x 64 drafts).
+    // The warp stays together and elects a lane for the MMAs only: in a loop that one lane runs
+    // alone nothing is warp-uniform, and an MMA then takes three times as long to issue.
     const uint32_t idesc_qk = umma_idesc_e4m3(128, 128);
     // D fp32, A and B f16, A K-major, B MN-major
     const uint32_t idesc_pv = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
-    int e0 = 0, cnt[2] = {0, 0};
+    int e0 = 0;
+    uint32_t phases = 0;  // of the four P barriers
     bool ok = true;
     for (int k = 0; ok; ++k) {
       if (!twait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc)) break;
-      const int n_pg = rec(k)->n_pg;
+      const int n_pg = __shfl_sync(0xffffffffu, rec(k)->n_pg, 0);
       if (n_pg < 0) break;
-      const int two = rec(k)->n_q > 32 ? 1 : 0;
-      __syncwarp();
+      const bool two = __shfl_sync(0xffffffffu, rec(k)->n_q, 0) > 32;
       if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
-      const int n_jobs = n_pg << two;
+      const int n_jobs = two ? 2 * n_pg : n_pg;
       if (!twait(bar(kBQFull), k & 1, wc)) break;
-      auto qk = [&](int j) -> bool {
-        const int s = j & 1, e = e0 + (j >> two), sl = e % kSlot;
-        if (!twait(bar(kBKFull + sl), (e / kSlot) & 1, wc)) return false;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t a = umma_desc_sw128(sbase + kOffQ + (two ? s : 0) * 16384);
-          const uint64_t b = umma_desc_sw128(sbase + kOffK8 + sl * 16384);
+      auto k_ready = [&](int e) { return twait(bar(kBKFull + (e & 1)), (e >> 1) & 1, wc); };
+      // QK of page e for set S (inside an elected lane); `free_k`: the last reader of the K tile
+      auto issue_qk = [&](auto set, int e, bool free_k, bool free_q) {
+        constexpr int S = decltype(set)::value;
+        const uint64_t qdesc = umma_desc_sw128(sbase + kOffQ + (two ? S : 0) * 16384);
+        const uint64_t kdesc = umma_desc_sw128(sbase + kOffK8 + (e & 1) * 16384);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) umma_e4m3(tmem + kTmemS + 128 * s, a + 2 * kk, b + 2 * kk, idesc_qk, kk > 0);
-          if (!two || (j & 1)) umma_commit(bar(kBKEmpty + sl));
-          if (j == n_jobs - 1) umma_commit(bar(kBQEmpty));
-          umma_commit(bar(kBSFull + s));
+        for (int kk = 0; kk < 4; ++kk) umma_e4m3(tmem + kTmemS + 128 * S, qdesc + 2 * kk, kdesc + 2 * kk, idesc_qk, kk > 0);
+        umma_commit(bar(kBSFull + S));
+        if (free_k) umma_commit(bar(kBKEmpty + (e & 1)));
+        if (free_q) umma_commit(bar(kBQEmpty));
+      };
+      // job j of set S
+      auto step = [&](auto set, int j) -> bool {
+        constexpr int S = decltype(set)::value;
+        const int e = e0 + (two ? j >> 1 : j), en = e + (two ? 1 : 2);
+        const bool next = j + 2 < n_jobs;
+        if (next && (!two || S == 0) && !k_ready(en)) return false;
+        const int pb = 2 * S + (e & 1);
+        if (!twait(bar(kBPFull + pb), phases >> pb & 1, wc)) return false;
+        phases ^= 1u << pb;
+        tc_fence_after();
+        const uint64_t vdesc = umma_desc_sw128_lbo_sbo(sbase + kOffV16 + (e & 1) * 32768, 16384, 1024);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)  // 16 tokens each: 8 columns of P inside S's 32-column chunks
+            umma_f16_ts(tmem + kTmemO + 128 * S, tmem + kTmemS + 128 * S + 32 * (kk >> 1) + 8 * (kk & 1),
+                        vdesc + kk * (2048 >> 4), idesc_pv, (j >= 2 || kk > 0) ? 1u : 0u);
+          if (!two || S == 1) umma_commit(bar(kBVEmpty + (e & 1)));
+          if (next) issue_qk(set, en, !two || S == 1, j + 3 == n_jobs);
+          else umma_commit(bar(kBPvDone + S));  // the set's accumulator is final
         }
         __syncwarp();
         return true;
       };
-      ok = qk(0) && (n_jobs < 2 || qk(1));
-      for (int j = 0; ok && j < n_jobs; ++j) {
-        const int s = j & 1, e = e0 + (j >> two), sl = e % kSlot;
-        if (j < 2 && k > 0 && !twait(bar(kBOFree), (k - 1) & 1, wc)) { ok = false; break; }
-        if (!twait(bar(kBVFull + sl), (e / kSlot) & 1, wc) || !twait(bar(kBPFull + s), cnt[s] & 1, wc)) {
-          ok = false;
-          break;
-        }
-        ++cnt[s];
+      using Set0 = std::integral_constant<int, 0>;
+      using Set1 = std::integral_constant<int, 1>;
+      ok = k_ready(e0);
+      if (ok) {
         tc_fence_after();
-        if (elect_one()) {
-          const uint32_t v = sbase + kOffV16 + sl * 32768;
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)  // 16 tokens each: 8 columns of P inside S's 32-column chunks
-            umma_f16_ts(tmem + kTmemO + 128 * s, tmem + kTmemS + 128 * s + 32 * (kk >> 1) + 8 * (kk & 1),
-                        umma_desc_sw128_lbo_sbo(v + kk * 2048, 16384, 1024), idesc_pv, (j >= 2 || kk > 0) ? 1u : 0u);
-          if (!two || (j & 1)) umma_commit(bar(kBVEmpty + sl));
-          umma_commit(bar(kBPvDone + s));
-        }
+        if (elect_one()) issue_qk(Set0{}, e0, !two, n_jobs == 1);
         __syncwarp();
-        if (j + 2 < n_jobs) ok = qk(j + 2);
+      }
+      if (ok && n_jobs > 1) {
+        ok = two || k_ready(e0 + 1);
+        tc_fence_after();
+        if (ok && elect_one()) issue_qk(Set1{}, two ? e0 : e0 + 1, true, n_jobs == 2);
+        __syncwarp();
+      } else if (lane == 0) {
+        mbar_arrive(bar(kBPvDone + 1));
+      }
+      // both accumulators are read
+      ok = ok && (k == 0 || twait(bar(kBOFree), (k - 1) & 1, wc));
+      for (int j = 0; ok && j < n_jobs; j += 2) {
+        ok = step(Set0{}, j);
+        if (ok && j + 1 < n_jobs) ok = step(Set1{}, j + 1);
       }
       e0 += n_pg;
     }
@@ -536,6 +562,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
       if (k > 0 && !twait(bar(kBQEmpty), (k - 1) & 1, wc)) break;
       // the second tile is also the exchange buffer of a segment with row copies
+      // (the earlier phase first: every phase is seen in turn)
+      if (k > 1 && !twait(bar(kBOFree), k & 1, wc)) break;
       if (k > 0 && r.n_q > 32 && !twait(bar(kBOFree), (k - 1) & 1, wc)) break;
       const int copies = tree_copies(r.n_q), gap = 128 / copies;
       for (int x = lane; x < r.n_q * 32; x += 32) {
@@ -557,7 +585,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
     const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16);
     const uint32_t t_s = tl + kTmemS + 128 * set;
     const uint64_t scale2 = pair64(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
-    int e0 = 0, cnt[2] = {0, 0};  // pages so far, jobs of each set so far
+    int e0 = 0, jobs = 0;  // pages so far, jobs of this set so far
     bool ok = true;
     for (int k = 0;; ++k) {
       // (the set's warps leave together: they meet at named barriers below)
@@ -584,11 +612,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       }
       float m_ref = -INFINITY, l = 0.f;
       for (int j = set; j < n_jobs; j += 2) {
-        if (!twait(bar(kBSFull + set), cnt[set] & 1, wc)) {
+        if (!twait(bar(kBSFull + set), jobs & 1, wc)) {
           ok = false;
           break;
         }
-        ++cnt[set];
+        ++jobs;
         if (busy) {
           const int2 info = s_info[(e0 + (j >> two)) % kInfo];
           const bool edge = info.y < kPageTokens || info.x + kPageTokens > r.ctx;  // warp-uniform
@@ -697,15 +725,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
           tc_fence_before();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBPFull + set));
+        if (lane == 0) mbar_arrive(bar(kBPFull + 2 * set + ((e0 + (j >> two)) & 1)));
       }
       // ---- end of the segment: both accumulators are final ---------------------------------------------
-      const bool any0 = n_jobs > 0, any1 = n_jobs > 1;
+      const bool any1 = n_jobs > 1;
       if (ok) {
-        cnt[set ^ 1] += two ? r.n_pg : (r.n_pg + (set ? 1 : 0)) >> 1;
-        ok = (set ? !any1 : !any0) || twait(bar(kBPvDone + set), (cnt[set] - 1) & 1, wc);
-        ok = ok && ((set ? !any0 : !any1) || twait(bar(kBPvDone + (set ^ 1)), (cnt[set ^ 1] - 1) & 1, wc));
+        ok = twait(bar(kBPvDone + set), k & 1, wc);
       }
+      tc_fence_before();  // (a set's accumulator is read by both sets, behind kBMl)
       float2* ml = reinterpret_cast<float2*>(smem + kOffMl) + (k & 1) * 256;
       ml[128 * set + lrow] = make_float2(m_ref, l);
       __syncwarp();
@@ -823,6 +850,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
     for (int k = 0; ok; ++k) {
       if (!twait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc)) break;
       const int n_pg = rec(k)->n_pg;
+      const bool two = rec(k)->n_q > 32;
       __syncwarp();
       if (n_pg < 0) break;
       if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
@@ -856,7 +884,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(bar(kBVFull + sl));
+          if (two || (i & 1) == 0) mbar_arrive(bar(kBPFull + sl));
+          if (two || (i & 1) == 1) mbar_arrive(bar(kBPFull + 2 + sl));
           mbar_arrive(bar(kBRawEmpty + st));
         }
       }
