@@ -8,9 +8,9 @@
 //   x_t = (q . k8_t) scale / s_enc_k log2(e),  out = sum_t 2^x_t v8_t / sum_t 2^x_t / s_enc_v
 // over the visible t, in one pass with a reference m per row that follows the
 // running maximum: weights 2^(x_t - m + 8) are summed in fp32 (l) and multiply V
-// in f16.  m moves only when a page's maximum exceeds it by 7 (log2), so the
-// weights stay below 2^15 and the accumulator is rescaled a few times per row;
-// they keep full f16 precision down to 2^-22 of the largest (an E4M3 weight, with
+// in f16.  m moves only when 32 weights sum to more than 49,152, so that they stay
+// below f16's end and the accumulator is rescaled a few times per row;
+// they keep full f16 precision down to 2^-22 of the reference's (an E4M3 weight, with
 // its 17 binades, would lose the bulk of a long context behind one large key).
 // V8 is an f16 value by moving its seven magnitude bits: E4M3 bits << 7 is
 // v8 2^-8 exactly, subnormals included.
@@ -29,12 +29,10 @@
 //   warps 4-11    two softmax sets, thread = row: with one row tile a set takes
 //                 every other page (its own reference, sum and accumulator, joined
 //                 at the segment's end), with two tiles a set takes a tile;
-//   warps 12-15   K conversion, thread = token; warps 16-23 V conversion, thread =
-//                 token and half of the channels.
+//   warps 12-23   K conversion (four warps, thread = token) and V conversion (eight,
+//                 thread = token and half of the channels).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-
-#include <type_traits>
 
 #include "common.cuh"
 
@@ -72,7 +70,9 @@ constexpr int kTreeSmem = 1024 + kOffTreeMisc + 16;
 static_assert(kTreeSmem <= 232448, "shared memory of one CTA");
 static_assert(kOffRaw % 16 == 0 && kOffVTab % 16 == 0 && kOffTreeBars % 8 == 0, "alignment");
 constexpr uint32_t kTmemS = 0, kTmemO = 256;  // S of set s at 128 s, O of set s at 256 + 128 s
-constexpr float kTreeGrowth = 7.0f, kTreeBias = 8.0f;
+constexpr float kTreeBias = 8.0f;
+constexpr float kTreeMost = 49152.0f;  // largest sum of a chunk's weights, and so largest weight (f16 ends at 65,504)
+constexpr float kTreeUnset = 3e38f;    // shift of a row without a reference: a visible token's weight is infinite
 constexpr float kTreeLog2e = 1.4426950408889634f, kTreeLn2 = 0.6931471805599453f;
 
 // Weights of the partition: a page of a one-tile sequence, of a two-tile one,
@@ -126,8 +126,18 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
   return r != 0;
 }
+// Waits (the whole warp) for the phase with the given parity: as mbar_wait, bounded in
+// time and given up when another role has, but short in code (there are thirty of them).
 __device__ __forceinline__ bool twait(uint32_t bar, uint32_t parity, const WaitCtl& w) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, w));
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  for (;;) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, *w.abort || globaltimer_ns() - t0 > w.limit_ns)) {
+      *w.abort = 1;
+      return false;
+    }
+  }
 }
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
@@ -491,61 +501,53 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       const int n_jobs = two ? 2 * n_pg : n_pg;
       if (!twait(bar(kBQFull), k & 1, wc)) break;
       auto k_ready = [&](int e) { return twait(bar(kBKFull + (e & 1)), (e >> 1) & 1, wc); };
-      // QK of page e for set S (inside an elected lane); `free_k`: the last reader of the K tile
-      auto issue_qk = [&](auto set, int e, bool free_k, bool free_q) {
-        constexpr int S = decltype(set)::value;
-        const uint64_t qdesc = umma_desc_sw128(sbase + kOffQ + (two ? S : 0) * 16384);
+      // QK of page e for a set (inside an elected lane); free_k: the last reader of the K tile.
+      // (The loops stay short: straight-line MMAs are long, and a long way round the warp's
+      // code misses the instruction cache.)
+      auto issue_qk = [&](int set, int e, bool free_k, bool free_q) {
+        const uint64_t qdesc = umma_desc_sw128(sbase + kOffQ + (two ? set : 0) * 16384);
         const uint64_t kdesc = umma_desc_sw128(sbase + kOffK8 + (e & 1) * 16384);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) umma_e4m3(tmem + kTmemS + 128 * S, qdesc + 2 * kk, kdesc + 2 * kk, idesc_qk, kk > 0);
-        umma_commit(bar(kBSFull + S));
+#pragma unroll 2
+        for (int kk = 0; kk < 4; ++kk) umma_e4m3(tmem + kTmemS + 128 * set, qdesc + 2 * kk, kdesc + 2 * kk, idesc_qk, kk > 0);
+        umma_commit(bar(kBSFull + set));
         if (free_k) umma_commit(bar(kBKEmpty + (e & 1)));
         if (free_q) umma_commit(bar(kBQEmpty));
       };
-      // job j of set S
-      auto step = [&](auto set, int j) -> bool {
-        constexpr int S = decltype(set)::value;
+      // first QKs of both sets, then job after job
+      for (int j = -2; ok && j < n_jobs; ++j) {
+        const int set = j & 1;
         const int e = e0 + (two ? j >> 1 : j), en = e + (two ? 1 : 2);
         const bool next = j + 2 < n_jobs;
-        if (next && (!two || S == 0) && !k_ready(en)) return false;
-        const int pb = 2 * S + (e & 1);
-        if (!twait(bar(kBPFull + pb), phases >> pb & 1, wc)) return false;
-        phases ^= 1u << pb;
+        if (next && !(two && set) && !k_ready(en)) {
+          ok = false;
+          break;
+        }
+        if (j == 0 && k > 0 && !twait(bar(kBOFree), (k - 1) & 1, wc)) {  // both accumulators are read
+          ok = false;
+          break;
+        }
+        const int pb = kSlot * set + (e & 1);
+        if (j >= 0) {
+          if (!twait(bar(kBPFull + pb), phases >> pb & 1, wc)) {
+            ok = false;
+            break;
+          }
+          phases ^= 1u << pb;
+        }
         tc_fence_after();
         const uint64_t vdesc = umma_desc_sw128_lbo_sbo(sbase + kOffV16 + (e & 1) * 32768, 16384, 1024);
         if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)  // 16 tokens each: 8 columns of P inside S's 32-column chunks
-            umma_f16_ts(tmem + kTmemO + 128 * S, tmem + kTmemS + 128 * S + 32 * (kk >> 1) + 8 * (kk & 1),
-                        vdesc + kk * (2048 >> 4), idesc_pv, (j >= 2 || kk > 0) ? 1u : 0u);
-          if (!two || S == 1) umma_commit(bar(kBVEmpty + (e & 1)));
-          if (next) issue_qk(set, en, !two || S == 1, j + 3 == n_jobs);
-          else umma_commit(bar(kBPvDone + S));  // the set's accumulator is final
+          if (j >= 0) {
+#pragma unroll 4
+            for (int kk = 0; kk < 8; ++kk)  // 16 tokens each: 8 columns of P inside S's 32-column chunks
+              umma_f16_ts(tmem + kTmemO + 128 * set, tmem + kTmemS + 128 * set + 32 * (kk >> 1) + 8 * (kk & 1),
+                          vdesc + kk * (2048 >> 4), idesc_pv, (j >= 2 || kk > 0) ? 1u : 0u);
+            if (!(two && set == 0)) umma_commit(bar(kBVEmpty + (e & 1)));
+          }
+          if (next) issue_qk(set, en, !(two && set == 0), j + 3 == n_jobs);
+          else umma_commit(bar(kBPvDone + set));  // the set's accumulator is final (or it has no job)
         }
         __syncwarp();
-        return true;
-      };
-      using Set0 = std::integral_constant<int, 0>;
-      using Set1 = std::integral_constant<int, 1>;
-      ok = k_ready(e0);
-      if (ok) {
-        tc_fence_after();
-        if (elect_one()) issue_qk(Set0{}, e0, !two, n_jobs == 1);
-        __syncwarp();
-      }
-      if (ok && n_jobs > 1) {
-        ok = two || k_ready(e0 + 1);
-        tc_fence_after();
-        if (ok && elect_one()) issue_qk(Set1{}, two ? e0 : e0 + 1, true, n_jobs == 2);
-        __syncwarp();
-      } else if (lane == 0) {
-        mbar_arrive(bar(kBPvDone + 1));
-      }
-      // both accumulators are read
-      ok = ok && (k == 0 || twait(bar(kBOFree), (k - 1) & 1, wc));
-      for (int j = 0; ok && j < n_jobs; j += 2) {
-        ok = step(Set0{}, j);
-        if (ok && j + 1 < n_jobs) ok = step(Set1{}, j + 1);
       }
       e0 += n_pg;
     }
@@ -585,6 +587,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
     const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16);
     const uint32_t t_s = tl + kTmemS + 128 * set;
     const uint64_t scale2 = pair64(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
+    uint32_t zero[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) asm volatile("mov.u32 %0, 0;" : "=r"(zero[i]));
     int e0 = 0, jobs = 0;  // pages so far, jobs of this set so far
     bool ok = true;
     for (int k = 0;; ++k) {
@@ -610,7 +615,35 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
         tm = p.tree_mask ? p.tree_mask[r.q0 + draft] : (2ull << draft) - 1;
         if (r.n_q < 64) tm &= (1ull << r.n_q) - 1;
       }
-      float m_ref = -INFINITY, l = 0.f;
+      float shift = kTreeUnset, l = 0.f;  // kTreeBias less the reference, and the sum of weights
+      // Multiplies what the row has so far by f: the earlier pages' sums (the PVs before this S
+      // are done) and this page's weights of the chunks before c.
+      auto rescale = [&](int c, bool sums, float f) {
+        if (sums)
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            uint32_t u[32];
+            const uint32_t t_o = tl + kTmemO + 128 * set + 32 * i;
+            tmem_ld32x32b_x32(t_o, u);
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 32; ++x) u[x] = __float_as_uint(__uint_as_float(u[x]) * f);
+            tmem_st32(t_o, u);
+          }
+        tmem_wait_st();
+#pragma unroll 1
+        for (int i = c0; i < c; ++i) {
+          uint32_t u[16];
+          tmem_ld32x32b_x16(t_s + 32 * i, u);
+          tmem_wait_ld();
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&u[x]));
+            u[x] = cvt_f16x2_f32(w.y * f, w.x * f);
+          }
+          tmem_st_x16(t_s + 32 * i, u);
+        }
+      };
       for (int j = set; j < n_jobs; j += 2) {
         if (!twait(bar(kBSFull + set), jobs & 1, wc)) {
           ok = false;
@@ -620,107 +653,58 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
         if (busy) {
           const int2 info = s_info[(e0 + (j >> two)) % kInfo];
           const bool edge = info.y < kPageTokens || info.x + kPageTokens > r.ctx;  // warp-uniform
-          // logits of chunk c, -inf where the row does not see the token
-          auto load = [&](int c, uint32_t* v) { tmem_ld32x32b_x32(t_s + 32 * c, v); };
-          auto mask = [&](int c, uint32_t* v) {
-            const uint32_t vis = info.y > 0 ? visible_bits(tm, info.x + 32 * c, r.ctx) : 0u;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = vis >> i & 1 ? v[i] : 0xFF800000u;
-          };
-          auto most = [&](const uint32_t* v, float top) {
-            float t[4] = {top, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int i = 0; i < 32; i += 8)
-#pragma unroll
-              for (int u = 0; u < 4; ++u)
-                t[u] = fmaxf(fmaxf(t[u], __uint_as_float(v[i + 2 * u])), __uint_as_float(v[i + 2 * u + 1]));
-            return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-          };
           tc_fence_after();
-          // the page's maximum over this warp's tokens (a warp with one chunk keeps its logits)
-          float top = -INFINITY;
-          uint32_t v[32];
-          if (copies == 4) {
-            load(c0, v);
+          // One chunk of 32 tokens at a time, in a loop that stays rolled (as the issuer's): weights
+          // relative to the row's reference as f16 pairs over the first half of the chunk's own
+          // columns.  There is no pass for the maximum: a chunk whose weights sum to kTreeMost
+          // or less has no weight above it, and any other (a row's first one: its shift is
+          // kTreeUnset) moves the reference to its maximum and is weighed again.
+#pragma unroll 1
+          for (int c = c0; c < c1; ++c) {
+            uint32_t v[32], o[16];
+            tmem_ld32x32b_x32(t_s + 32 * c, v);
             tmem_wait_ld();
-            if (edge) mask(c0, v);
-            top = most(v, top);
-          } else {
-#pragma unroll 1
-            for (int c = c0; c < c1; c += 2) {
-              uint32_t u[32];
-              load(c, v);
-              load(c + 1, u);
-              tmem_wait_ld();
-              if (edge) {
-                mask(c, v);
-                mask(c + 1, u);
-              }
-              top = most(u, most(v, top));
-            }
-          }
-          const float x_top = top * p.scale_log2;
-          const bool grow = x_top > m_ref + kTreeGrowth || (m_ref == -INFINITY && top > -INFINITY);
-          if (__any_sync(0xffffffffu, grow && mine)) {
-            const float m_new = grow ? x_top : m_ref;
-            const float f = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m_new);
-            m_ref = m_new;
-            l *= f;
-            if (j >= 2) {
-              // earlier pages' sums: the PVs before this S are done
-#pragma unroll 1
-              for (int c = 0; c < 4; ++c) {
-                uint32_t u[32];
-                const uint32_t t_o = tl + kTmemO + 128 * set + 32 * c;
-                tmem_ld32x32b_x32(t_o, u);
-                tmem_wait_ld();
+            if (edge) {  // -inf where the row does not see the token
+              const uint32_t vis = info.y > 0 ? visible_bits(tm, info.x + 32 * c, r.ctx) : 0u;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * f);
-                tmem_st32(t_o, u);
-              }
+              for (int i = 0; i < 32; ++i) v[i] = vis >> i & 1 ? v[i] : 0xFF800000u;
             }
-          }
-          // weights, as f16 pairs over the first half of each chunk's own columns
-          const float shift = m_ref == -INFINITY ? 0.f : kTreeBias - m_ref;
-          const uint64_t shift2 = pair64(__float_as_uint(shift), __float_as_uint(shift));
-          uint64_t sums[2] = {0, 0};
-          auto weigh = [&](int c, const uint32_t* v) {
-            uint32_t o[16];
+            for (;;) {
+              const uint64_t shift2 = pair64(__float_as_uint(shift), __float_as_uint(shift));
+              uint64_t sums[2] = {0, 0};
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const uint2 x = split64(fma_f32x2(pair64(v[2 * i], v[2 * i + 1]), scale2, shift2));
-              const float a = fast_exp2(__uint_as_float(x.x)), b = fast_exp2(__uint_as_float(x.y));
-              sums[i & 1] = add_f32x2(sums[i & 1], pair64(__float_as_uint(a), __float_as_uint(b)));
-              o[i] = cvt_f16x2_f32(b, a);
+              for (int i = 0; i < 16; ++i) {
+                const uint2 x = split64(fma_f32x2(pair64(v[2 * i], v[2 * i + 1]), scale2, shift2));
+                const float a = fast_exp2(__uint_as_float(x.x)), b = fast_exp2(__uint_as_float(x.y));
+                sums[i & 1] = add_f32x2(sums[i & 1], pair64(__float_as_uint(a), __float_as_uint(b)));
+                o[i] = cvt_f16x2_f32(b, a);
+              }
+              const uint2 sum2 = split64(add_f32x2(sums[0], sums[1]));
+              const float sum = __uint_as_float(sum2.x) + __uint_as_float(sum2.y);
+              const bool over = mine && sum > kTreeMost;
+              if (!__any_sync(0xffffffffu, over)) {
+                l += sum;
+                break;
+              }
+              float f = 1.f;
+              if (over) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(v[i]));
+                const float next = kTreeBias - top * p.scale_log2;
+                f = fast_exp2(next - shift);  // (0 for the first: shift is kTreeUnset)
+                shift = next;
+                l *= f;
+              }
+              rescale(c, j >= 2, f);
             }
             tmem_st_x16(t_s + 32 * c, o);
-          };
-          if (copies == 4) {
-            weigh(c0, v);
-          } else {
-#pragma unroll 1
-            for (int c = c0; c < c1; c += 2) {
-              uint32_t u[32];
-              load(c, v);
-              load(c + 1, u);
-              tmem_wait_ld();
-              if (edge) {
-                mask(c, v);
-                mask(c + 1, u);
-              }
-              weigh(c, v);
-              weigh(c + 1, u);
-            }
           }
-          if (copies > 1) {  // the other warps' tokens
-            uint32_t zero[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) zero[i] = 0;
+          if (copies > 1) {  // the other copies' tokens
+#pragma unroll 1
             for (int c = 0; c < 4; ++c)
               if (c < c0 || c >= c1) tmem_st_x16(t_s + 32 * c, zero);
           }
-          const uint2 sum = split64(add_f32x2(sums[0], sums[1]));
-          l += __uint_as_float(sum.x) + __uint_as_float(sum.y);
           tmem_wait_st();
           tc_fence_before();
         }
@@ -734,6 +718,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       }
       tc_fence_before();  // (a set's accumulator is read by both sets, behind kBMl)
       float2* ml = reinterpret_cast<float2*>(smem + kOffMl) + (k & 1) * 256;
+      const float m_ref = kTreeBias - shift;
       ml[128 * set + lrow] = make_float2(m_ref, l);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBMl));
@@ -841,9 +826,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
     }
   } else {
     regs_dec<56>();
-  if (warp >= 16) {
+    // A scheduler (warp % 4) runs one of the two conversions, as far as the counts allow: the
+    // fewer roles it has, the less its instruction cache is fought over.  V: warps 12, 16, 20,
+    // 13, 17, 21, 14, 18; K: warps 15, 19, 23, 22.
+    const int sched = warp & 3, turn = (warp - 12) >> 2;
+    const bool is_v = sched < 2 || (sched == 2 && turn < 2);
+    const int part = is_v ? 3 * sched + turn : sched == 3 ? turn : 3;
+  if (is_v) {
     // ---------------- V conversion: token tok, channels 64 half .. 64 half + 63 ----------------------
-    const int half = (warp - 16) >> 2, tok = 32 * (warp & 3) + lane;
+    const int half = part >> 2, tok = 32 * (part & 3) + lane;
     const uint4* tab = reinterpret_cast<const uint4*>(smem + kOffVTab) + (lane & (kVTabCopies - 1));
     int e = 0;
     bool ok = true;
@@ -861,7 +852,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
           break;
         }
         const uint8_t* raw = smem + kOffRaw + st * kHeadBytes + kOffVc;
-        const bool live = tok < s_info[e % kInfo].y;  // rows behind the sequence become zeros
+        const int valid = s_info[e % kInfo].y;
         uint8_t* dst = smem + kOffV16 + sl * 32768 + half * 16384 + tok * 128;
         // every load before the first store: the compiler must not assume that they are apart
         uint4 w[2], t[4];
@@ -871,15 +862,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
 #pragma unroll
         for (int u = 0; u < 4; ++u)
           t[u] = tab[(raw[(kOffKs - kOffKc) + (4 * half + u) * kPageTokens + tok] & 127) * kVTabCopies];
+        if (valid < kPageTokens && tok >= valid) {  // rows behind the sequence become zeros: a scale of zero
+#pragma unroll
+          for (int u = 0; u < 4; ++u) t[u] = make_uint4(0, 0, 0, 0);
+          w[0] = w[1] = make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
-          uint4 o[4] = {dequant8_f16(w[cc].x, t[2 * cc]), dequant8_f16(w[cc].y, t[2 * cc]),
-                        dequant8_f16(w[cc].z, t[2 * cc + 1]), dequant8_f16(w[cc].w, t[2 * cc + 1])};
+          const uint4 o[4] = {dequant8_f16(w[cc].x, t[2 * cc]), dequant8_f16(w[cc].y, t[2 * cc]),
+                              dequant8_f16(w[cc].z, t[2 * cc + 1]), dequant8_f16(w[cc].w, t[2 * cc + 1])};
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            if (!live) o[u] = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(dst + (((4 * cc + u) ^ (tok & 7)) << 4)) = o[u];
-          }
+          for (int u = 0; u < 4; ++u) *reinterpret_cast<uint4*>(dst + (((4 * cc + u) ^ (tok & 7)) << 4)) = o[u];
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -892,7 +885,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
     }
   } else {
     // ---------------- K conversion: token tok ----------------------------------------------------------
-    const int tok = 32 * (warp & 3) + lane;
+    const int tok = 32 * part + lane;
     const uint2* tab = reinterpret_cast<const uint2*>(smem + kOffKTab) + (lane & (kKTabCopies - 1));
     int e = 0;
     bool ok = true;
@@ -910,18 +903,24 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
         }
         const uint8_t* raw = smem + kOffRaw + st * kHeadBytes + kOffKc;
         uint8_t* dst = smem + kOffK8 + sl * 16384 + tok * 128;
-        uint4 w[4];
-        uint2 t[8];
+        // half of the channels at a time, every load before the first store
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint4 w[2];
+          uint2 t[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) w[c] = *reinterpret_cast<const uint4*>(raw + tok * 64 + 16 * code_chunk_pos(c, tok));
+          for (int c = 0; c < 2; ++c)
+            w[c] = *reinterpret_cast<const uint4*>(raw + tok * 64 + 16 * code_chunk_pos(2 * h + c, tok));
 #pragma unroll
-        for (int u = 0; u < 8; ++u) t[u] = tab[(raw[(kOffKs - kOffKc) + u * kPageTokens + tok] & 127) * kKTabCopies];
+          for (int u = 0; u < 4; ++u)
+            t[u] = tab[(raw[(kOffKs - kOffKc) + (4 * h + u) * kPageTokens + tok] & 127) * kKTabCopies];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint2 a = dequant8(w[c].x, t[2 * c]), b = dequant8(w[c].y, t[2 * c]);
-          const uint2 d = dequant8(w[c].z, t[2 * c + 1]), f = dequant8(w[c].w, t[2 * c + 1]);
-          *reinterpret_cast<uint4*>(dst + (((2 * c) ^ (tok & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
-          *reinterpret_cast<uint4*>(dst + (((2 * c + 1) ^ (tok & 7)) << 4)) = make_uint4(d.x, d.y, f.x, f.y);
+          for (int c = 0; c < 2; ++c) {
+            const uint2 a = dequant8(w[c].x, t[2 * c]), b = dequant8(w[c].y, t[2 * c]);
+            const uint2 d = dequant8(w[c].z, t[2 * c + 1]), f = dequant8(w[c].w, t[2 * c + 1]);
+            *reinterpret_cast<uint4*>(dst + (((4 * h + 2 * c) ^ (tok & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
+            *reinterpret_cast<uint4*>(dst + (((4 * h + 2 * c + 1) ^ (tok & 7)) << 4)) = make_uint4(d.x, d.y, f.x, f.y);
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
