@@ -49,8 +49,8 @@ constexpr int kInfo = 16;
 constexpr int kKTabCopies = 4, kVTabCopies = 8;
 
 constexpr int kOffQ = 0;                                      // 2 tiles [128 rows][128 B]
-constexpr int kOffK8 = kOffQ + 2 * 16384;                     // kSlot x [128 tokens][128 B]
-constexpr int kOffV16 = kOffK8 + kSlot * 16384;               // kSlot x 2 halves x [128 tokens][64 f16]
+constexpr int kOffK8 = kOffQ + 2 * 16384;                     // kSlot x [8 groups of 16 channels][128 tokens][16 B]
+constexpr int kOffV16 = kOffK8 + kSlot * 16384;               // kSlot x [16 groups of 8 channels][128 tokens][16 B]
 constexpr int kOffRaw = kOffV16 + kSlot * 32768;              // kRaw x 18,432
 constexpr int kOffKTab = kOffRaw + kRaw * kHeadBytes;         // uint2 [128][copies]
 constexpr int kOffVTab = kOffKTab + 128 * 8 * kKTabCopies;    // uint4 [128][copies]
@@ -132,7 +132,9 @@ __device__ __forceinline__ bool twait(uint32_t bar, uint32_t parity, const WaitC
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   const unsigned long long t0 = globaltimer_ns();
   for (;;) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i)
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     if (__any_sync(0xffffffffu, *w.abort || globaltimer_ns() - t0 > w.limit_ns)) {
       *w.abort = 1;
       return false;
@@ -153,6 +155,25 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, 
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
+}
+// Shared memory by 32-bit address (every access in program order).
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -506,9 +527,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       // code misses the instruction cache.)
       auto issue_qk = [&](int set, int e, bool free_k, bool free_q) {
         const uint64_t qdesc = umma_desc_sw128(sbase + kOffQ + (two ? set : 0) * 16384);
-        const uint64_t kdesc = umma_desc_sw128(sbase + kOffK8 + (e & 1) * 16384);
+        // K-major without swizzle: 8 tokens x 16 channels are 128 contiguous bytes, the next 16
+        // channels 2,048 further (so that a converting thread's stores are at fixed offsets)
+        const uint64_t kdesc = umma_desc_noswz_lbo_sbo(sbase + kOffK8 + (e & 1) * 16384, 2048, 128);
 #pragma unroll 2
-        for (int kk = 0; kk < 4; ++kk) umma_e4m3(tmem + kTmemS + 128 * set, qdesc + 2 * kk, kdesc + 2 * kk, idesc_qk, kk > 0);
+        for (int kk = 0; kk < 4; ++kk)  // 32 channels each
+          umma_e4m3(tmem + kTmemS + 128 * set, qdesc + 2 * kk, kdesc + kk * (4096 >> 4), idesc_qk, kk > 0);
         umma_commit(bar(kBSFull + set));
         if (free_k) umma_commit(bar(kBKEmpty + (e & 1)));
         if (free_q) umma_commit(bar(kBQEmpty));
@@ -535,13 +559,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
           phases ^= 1u << pb;
         }
         tc_fence_after();
-        const uint64_t vdesc = umma_desc_sw128_lbo_sbo(sbase + kOffV16 + (e & 1) * 32768, 16384, 1024);
+        // MN-major without swizzle: 8 tokens x 8 channels are 128 contiguous bytes, the next 8 tokens
+        // follow, the next 8 channels are 2,048 further
+        const uint64_t vdesc = umma_desc_noswz_lbo_sbo(sbase + kOffV16 + (e & 1) * 32768, 128, 2048);
         if (elect_one()) {
           if (j >= 0) {
 #pragma unroll 4
             for (int kk = 0; kk < 8; ++kk)  // 16 tokens each: 8 columns of P inside S's 32-column chunks
               umma_f16_ts(tmem + kTmemO + 128 * set, tmem + kTmemS + 128 * set + 32 * (kk >> 1) + 8 * (kk & 1),
-                          vdesc + kk * (2048 >> 4), idesc_pv, (j >= 2 || kk > 0) ? 1u : 0u);
+                          vdesc + kk * (256 >> 4), idesc_pv, (j >= 2 || kk > 0) ? 1u : 0u);
             if (!(two && set == 0)) umma_commit(bar(kBVEmpty + (e & 1)));
           }
           if (next) issue_qk(set, en, !(two && set == 0), j + 3 == n_jobs);
@@ -835,7 +861,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
   if (is_v) {
     // ---------------- V conversion: token tok, channels 64 half .. 64 half + 63 ----------------------
     const int half = part >> 2, tok = 32 * (part & 3) + lane;
-    const uint4* tab = reinterpret_cast<const uint4*>(smem + kOffVTab) + (lane & (kVTabCopies - 1));
+    const uint32_t tab = sbase + kOffVTab + 16 * (lane & (kVTabCopies - 1));
+    const uint32_t raw0 = sbase + kOffRaw + kOffVc, out0 = sbase + kOffV16 + half * 16384 + tok * 16;
+    const uint32_t code0 = tok * 64 + 16 * code_chunk_pos(2 * half, tok), code1 = tok * 64 + 16 * code_chunk_pos(2 * half + 1, tok);
+    const uint32_t scale0 = (kOffKs - kOffKc) + 4 * half * kPageTokens + tok;
     int e = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -851,28 +880,26 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
           ok = false;
           break;
         }
-        const uint8_t* raw = smem + kOffRaw + st * kHeadBytes + kOffVc;
+        const uint32_t raw = raw0 + st * kHeadBytes, dst = out0 + sl * 32768;
         const int valid = s_info[e % kInfo].y;
-        uint8_t* dst = smem + kOffV16 + sl * 32768 + half * 16384 + tok * 128;
-        // every load before the first store: the compiler must not assume that they are apart
-        uint4 w[2], t[4];
+        uint4 w[2] = {lds128(raw + code0), lds128(raw + code1)}, t[4];
+        uint32_t sb[4];
 #pragma unroll
-        for (int cc = 0; cc < 2; ++cc)
-          w[cc] = *reinterpret_cast<const uint4*>(raw + tok * 64 + 16 * code_chunk_pos(2 * half + cc, tok));
+        for (int u = 0; u < 4; ++u) sb[u] = lds_u8(raw + scale0 + u * kPageTokens) & 127;
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          t[u] = tab[(raw[(kOffKs - kOffKc) + (4 * half + u) * kPageTokens + tok] & 127) * kVTabCopies];
+        for (int u = 0; u < 4; ++u) t[u] = lds128(tab + sb[u] * (16 * kVTabCopies));
         if (valid < kPageTokens && tok >= valid) {  // rows behind the sequence become zeros: a scale of zero
 #pragma unroll
           for (int u = 0; u < 4; ++u) t[u] = make_uint4(0, 0, 0, 0);
           w[0] = w[1] = make_uint4(0, 0, 0, 0);
         }
+        // 8 channels of 128 tokens are 2,048 contiguous bytes
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
-          const uint4 o[4] = {dequant8_f16(w[cc].x, t[2 * cc]), dequant8_f16(w[cc].y, t[2 * cc]),
-                              dequant8_f16(w[cc].z, t[2 * cc + 1]), dequant8_f16(w[cc].w, t[2 * cc + 1])};
-#pragma unroll
-          for (int u = 0; u < 4; ++u) *reinterpret_cast<uint4*>(dst + (((4 * cc + u) ^ (tok & 7)) << 4)) = o[u];
+          sts128(dst + (4 * cc) * 2048, dequant8_f16(w[cc].x, t[2 * cc]));
+          sts128(dst + (4 * cc + 1) * 2048, dequant8_f16(w[cc].y, t[2 * cc]));
+          sts128(dst + (4 * cc + 2) * 2048, dequant8_f16(w[cc].z, t[2 * cc + 1]));
+          sts128(dst + (4 * cc + 3) * 2048, dequant8_f16(w[cc].w, t[2 * cc + 1]));
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -886,7 +913,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
   } else {
     // ---------------- K conversion: token tok ----------------------------------------------------------
     const int tok = 32 * part + lane;
-    const uint2* tab = reinterpret_cast<const uint2*>(smem + kOffKTab) + (lane & (kKTabCopies - 1));
+    const uint32_t tab = sbase + kOffKTab + 8 * (lane & (kKTabCopies - 1));
+    const uint32_t raw0 = sbase + kOffRaw + kOffKc, out0 = sbase + kOffK8 + tok * 16;
+    const uint32_t code0 = tok * 64 + 16 * code_chunk_pos(0, tok), scale0 = (kOffKs - kOffKc) + tok;
     int e = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -901,25 +930,25 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
           ok = false;
           break;
         }
-        const uint8_t* raw = smem + kOffRaw + st * kHeadBytes + kOffKc;
-        uint8_t* dst = smem + kOffK8 + sl * 16384 + tok * 128;
-        // half of the channels at a time, every load before the first store
+        const uint32_t raw = raw0 + st * kHeadBytes, dst = out0 + sl * 16384;
+        // half of the channels at a time; 16 channels of 128 tokens are 2,048 contiguous bytes
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
-          uint4 w[2];
+          // (code chunk c is at chunk c ^ x of the row: (code0 ^ 16 c) for the offset of chunk 0)
+          const uint32_t ch = raw + (code0 ^ (32 * h)), ch1 = raw + (code0 ^ (32 * h + 16));
+          const uint4 w[2] = {lds128(ch), lds128(ch1)};
+          uint32_t sb[4];
           uint2 t[4];
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-            w[c] = *reinterpret_cast<const uint4*>(raw + tok * 64 + 16 * code_chunk_pos(2 * h + c, tok));
+          for (int u = 0; u < 4; ++u) sb[u] = lds_u8(raw + scale0 + (4 * h + u) * kPageTokens) & 127;
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
-            t[u] = tab[(raw[(kOffKs - kOffKc) + (4 * h + u) * kPageTokens + tok] & 127) * kKTabCopies];
+          for (int u = 0; u < 4; ++u) t[u] = lds64(tab + sb[u] * (8 * kKTabCopies));
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const uint2 a = dequant8(w[c].x, t[2 * c]), b = dequant8(w[c].y, t[2 * c]);
             const uint2 d = dequant8(w[c].z, t[2 * c + 1]), f = dequant8(w[c].w, t[2 * c + 1]);
-            *reinterpret_cast<uint4*>(dst + (((4 * h + 2 * c) ^ (tok & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
-            *reinterpret_cast<uint4*>(dst + (((4 * h + 2 * c + 1) ^ (tok & 7)) << 4)) = make_uint4(d.x, d.y, f.x, f.y);
+            sts128(dst + (4 * h + 2 * c) * 2048, make_uint4(a.x, a.y, b.x, b.y));
+            sts128(dst + (4 * h + 2 * c + 1) * 2048, make_uint4(d.x, d.y, f.x, f.y));
           }
         }
         fence_proxy_async_smem();
