@@ -347,6 +347,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
   // ---- this CTA's range of the weighted units ------------------------------------------
   // thread i sums the sequences i * per .. of its share, then a scan over the CTA
   const int per = (p.n_seqs + kTreeThreads - 1) / kTreeThreads;
+  bool wide = false;  // some sequence has two row tiles
   {
     long long mine = 0;
     const int b0 = min(tid * per, p.n_seqs), b1 = min(b0 + per, p.n_seqs);
@@ -354,6 +355,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       const SeqWork w = seq_work(p, b);
       if (!w.s.ok && blockIdx.x == 0) set_status(p.status, MSA_STATUS_BAD_SEQ);
       if (w.n_vis > 0) mine += (long long)kKvHeads * (w.pw * w.n_vis + kFixedWeight);
+      wide |= w.n_vis > 0 && w.s.n_q > 32;
     }
     long long incl = mine;
 #pragma unroll
@@ -376,7 +378,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       s_scan[26] = mine0;
     }
     if (tid == 0) s_scan[24] = total;
-    __syncthreads();
+    wide = __syncthreads_or(wide);
   }
   const long long total = s_scan[24];
   const int G = (int)min((long long)gridDim.x, max(1ll, total / kLeastShare));
@@ -589,10 +591,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       if (r.n_pg < 0) break;
       if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
       if (k > 0 && !twait(bar(kBQEmpty), (k - 1) & 1, wc)) break;
-      // the second tile is also the exchange buffer of a segment with row copies
-      // (the earlier phase first: every phase is seen in turn)
-      if (k > 1 && !twait(bar(kBOFree), k & 1, wc)) break;
-      if (k > 0 && r.n_q > 32 && !twait(bar(kBOFree), (k - 1) & 1, wc)) break;
+      // the second tile is also the exchange buffer of a segment with row copies (all segments or
+      // none wait: a parity does not tell phase k - 1 from k - 3, so every phase is seen in turn)
+      if (wide && k > 0 && !twait(bar(kBOFree), (k - 1) & 1, wc)) break;
       const int copies = tree_copies(r.n_q), gap = 128 / copies;
       for (int x = lane; x < r.n_q * 32; x += 32) {
         const int row = x >> 3, c = x & 7;
