@@ -414,13 +414,35 @@ def qkv_project_insert(cache, x, w, gamma_q, gamma_k, gamma_idx, cos_sin, positi
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}  # MSA_DTYPE_*
 
 
-def _on_device(dev, *tensors):
-    """Raises unless every tensor is on CUDA device ``dev`` and that device is current."""
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"all tensors must be on the cache's device {dev}, got {t.device}")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"the cache is on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
+def _raw_stream(dev):
+    """The current stream of CUDA device ``dev`` (an index), as an integer."""
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):  # the same without a Stream object
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _device_of(cache):
+    """Index of the cache's CUDA device, which has to be the current one."""
+    dev = cache.kv_pool.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"the cache is on {cache.kv_pool.device}, not on the current CUDA device")
+    return dev
+
+
+def _arg(t, dtype, shape, dev, name):
+    """Pointer of a contiguous tensor of this type and shape on CUDA device ``dev`` (raises
+    otherwise).  A call has a dozen of them: the checks are one line when they hold."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _ptr(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    raise ValueError(f"{name} must be on the cache's device cuda:{dev}, got {t.device}")
 
 
 def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_max_pos=None, beta_fast=32.0,
@@ -474,28 +496,29 @@ def rope_table_scaled(max_pos, rot_dim=HEAD_DIM, base=10000.0, scaling=None, fac
     freq, amplitude = rope_frequencies(rot_dim, base, scaling, factor, original_max_pos, **betas)
     t = torch.empty((max_pos, rot_dim), dtype=torch.float32, device=device)
     arr = (ctypes.c_double * max(len(freq), 1))(*freq)
-    _on_device(t.device)
-    _check(lib().msa_rope_table_freqs(_ptr(t, torch.float32, "cos_sin"), int(max_pos), arr, int(rot_dim), amplitude,
-                                      _stream()))
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{t.device} is not the current CUDA device")
+    _check(lib().msa_rope_table_freqs(t.data_ptr(), int(max_pos), arr, int(rot_dim), amplitude, _stream()))
     return t
 
 
-def _rows(t, name, heads, n, dtype):
-    """(pointer, token stride) of projected rows [n, heads, 128] ([n, 128] for heads 0)."""
+def _rows(t, name, shape, dtype, dev):
+    """(pointer, token stride) of projected rows [n, heads, 128] or [n, 128]."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype} like q, got {t.dtype}")
-    shape = (n, heads, HEAD_DIM) if heads else (n, HEAD_DIM)
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the cache's device cuda:{dev}, got {t.device}")
     st = t.stride()
-    if st[-1] != 1 or (heads > 1 and st[1] != HEAD_DIM):
+    if st[-1] != 1 or (len(st) == 3 and st[1] != HEAD_DIM):
         raise ValueError(f"{name} must have contiguous channels and heads")
-    stride = st[0] if n > 1 else 0
-    if t.data_ptr() % 16 or stride * t.element_size() % 16:
+    ptr, stride = t.data_ptr(), st[0] if shape[0] > 1 else 0
+    if ptr & 15 or stride * (4 if dtype is torch.float32 else 2) & 15:
         raise ValueError(f"{name} and its token stride must be aligned to 16 bytes")
-    return t.data_ptr(), stride
+    return ptr, stride
 
 
 def rotary_insert(cache, q, k, v, idx_k, cos_sin, positions, slot_mapping, q_idx=None, interleaved=False, q8=None,
@@ -509,30 +532,34 @@ def rotary_insert(cache, q, k, v, idx_k, cos_sin, positions, slot_mapping, q_idx
     [max_pos, rot_dim]: the first rot_dim channels of each head are turned, in pairs
     (i, i + rot_dim / 2), or (2i, 2i + 1) when ``interleaved``.
     """
-    n = q.shape[0]
-    dtype = q.dtype
-    if dtype not in _DTYPES:
+    n, dtype = q.shape[0], q.dtype
+    code = _DTYPES.get(dtype)
+    if code is None:
         raise TypeError(f"q must be float32, bfloat16 or float16, got {dtype}")
-    rows = [_rows(q, "q", Q_HEADS, n, dtype), _rows(k, "k", KV_HEADS, n, dtype), _rows(v, "v", KV_HEADS, n, dtype),
-            _rows(idx_k, "idx_k", 0, n, dtype), (None, 0) if q_idx is None else _rows(q_idx, "q_idx", IDX_HEADS, n, dtype)]
-    dev = cache.kv_pool.device
+    dev = _device_of(cache)
+    qp, qs = _rows(q, "q", (n, Q_HEADS, HEAD_DIM), dtype, dev)
+    kp, ks = _rows(k, "k", (n, KV_HEADS, HEAD_DIM), dtype, dev)
+    vp, vs = _rows(v, "v", (n, KV_HEADS, HEAD_DIM), dtype, dev)
+    ip, i_s = _rows(idx_k, "idx_k", (n, IDX_DIM), dtype, dev)
     if q8 is None:
-        q8 = torch.empty((n, Q_HEADS, HEAD_DIM), dtype=torch.uint8, device=dev)
-    if qi8 is None and q_idx is not None:
-        qi8 = torch.empty((n, IDX_HEADS, IDX_DIM), dtype=torch.uint8, device=dev)
-    if tuple(q8.shape) != (n, Q_HEADS, HEAD_DIM) or (q_idx is not None and tuple(qi8.shape) != (n, IDX_HEADS, IDX_DIM)):
-        raise ValueError("q8 must be [n, 16, 128] and qi8 [n, 8, 128]")
-    if tuple(positions.shape) != (n,) or tuple(slot_mapping.shape) != (n,):
-        raise ValueError("positions and slot_mapping must be [n]")
-    _on_device(dev, q, k, v, idx_k, q_idx, cos_sin, positions, slot_mapping, q8, qi8)
-    r = _Rows(*(p for p, _ in rows), *(s for _, s in rows), _DTYPES[dtype])
+        q8 = torch.empty((n, Q_HEADS, HEAD_DIM), dtype=torch.uint8, device=q.device)
+    if q_idx is None:
+        qi8 = qip = qi8p = None
+        qis = 0
+    else:
+        qip, qis = _rows(q_idx, "q_idx", (n, IDX_HEADS, IDX_DIM), dtype, dev)
+        if qi8 is None:
+            qi8 = torch.empty((n, IDX_HEADS, IDX_DIM), dtype=torch.uint8, device=q.device)
+        qi8p = _arg(qi8, torch.uint8, (n, IDX_HEADS, IDX_DIM), dev, "qi8")
+    rows = _Rows(qp, kp, vp, ip, qip, qs, ks, vs, i_s, qis, code)
+    max_pos, rot_dim = cos_sin.shape
     c = cache.struct()
     _check(lib().msa_rotary_insert(
-        ctypes.byref(c), ctypes.byref(r), n, _ptr(cos_sin, torch.float32, "cos_sin", 2), cos_sin.shape[0],
-        cos_sin.shape[1], int(bool(interleaved)), _ptr(positions, torch.int32, "positions"),
-        _ptr(slot_mapping, torch.int64, "slot_mapping"), _ptr(q8, torch.uint8, "q8"),
-        None if q_idx is None else _ptr(qi8, torch.uint8, "qi8"), _stream()))
-    return q8, (None if q_idx is None else qi8)
+        ctypes.byref(c), ctypes.byref(rows), n, _arg(cos_sin, torch.float32, (max_pos, rot_dim), dev, "cos_sin"), max_pos,
+        rot_dim, 1 if interleaved else 0, _arg(positions, torch.int32, (n,), dev, "positions"),
+        _arg(slot_mapping, torch.int64, (n,), dev, "slot_mapping"),
+        _arg(q8, torch.uint8, (n, Q_HEADS, HEAD_DIM), dev, "q8"), qi8p, _raw_stream(dev)))
+    return q8, qi8
 
 
 def read_kv(cache, slot_mapping, dtype=torch.bfloat16, k=None, v=None, idx_k=None):
@@ -542,23 +569,22 @@ def read_kv(cache, slot_mapping, dtype=torch.bfloat16, k=None, v=None, idx_k=Non
     the others are not read and come back as None.  Rows of negative slots are left
     as they were (zeros in new tensors)."""
     n = slot_mapping.shape[0]
-    given = [t for t in (k, v, idx_k) if t is not None]
-    dev = cache.kv_pool.device
-    if given:
-        dtype = given[0].dtype
-    if dtype not in _DTYPES:
+    first = k if k is not None else v if v is not None else idx_k
+    if first is not None:
+        dtype = first.dtype
+    code = _DTYPES.get(dtype)
+    if code is None:
         raise TypeError(f"values are float32, bfloat16 or float16, not {dtype}")
-    if not given:
-        k, v = (torch.zeros((n, KV_HEADS, HEAD_DIM), dtype=dtype, device=dev) for _ in range(2))
-        idx_k = torch.zeros((n, IDX_DIM), dtype=dtype, device=dev)
-    for t, name, shape in ((k, "k", (n, KV_HEADS, HEAD_DIM)), (v, "v", (n, KV_HEADS, HEAD_DIM)), (idx_k, "idx_k", (n, IDX_DIM))):
-        if t is not None and tuple(t.shape) != shape:
-            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    _on_device(dev, slot_mapping, k, v, idx_k)
+    dev = _device_of(cache)
+    if first is None:
+        k, v = (torch.zeros((n, KV_HEADS, HEAD_DIM), dtype=dtype, device=cache.kv_pool.device) for _ in range(2))
+        idx_k = torch.zeros((n, IDX_DIM), dtype=dtype, device=cache.kv_pool.device)
     c = cache.struct()
     _check(lib().msa_read_kv(
-        ctypes.byref(c), _ptr(slot_mapping, torch.int64, "slot_mapping", 1), n, _DTYPES[dtype],
-        *(None if t is None else _ptr(t, dtype, name) for t, name in ((k, "k"), (v, "v"), (idx_k, "idx_k"))), _stream()))
+        ctypes.byref(c), _arg(slot_mapping, torch.int64, (n,), dev, "slot_mapping"), n, code,
+        None if k is None else _arg(k, dtype, (n, KV_HEADS, HEAD_DIM), dev, "k"),
+        None if v is None else _arg(v, dtype, (n, KV_HEADS, HEAD_DIM), dev, "v"),
+        None if idx_k is None else _arg(idx_k, dtype, (n, IDX_DIM), dev, "idx_k"), _raw_stream(dev)))
     return k, v, idx_k
 
 
@@ -589,32 +615,26 @@ def tree_attn(cache, q, block_table, seq_lens, q_start_loc, bufs, tree_mask=None
     ids, e.g. of indexer_topk for one token per sequence) only those blocks of the
     context are visited, and the blocks that hold drafts.  Returns bufs.out
     [T, 16, 128]; bufs.lse [T, 16] has the log-sum-exp of the logits."""
-    T = q.shape[0]
+    T = bufs.T
     n_seqs, max_pages = block_table.shape
-    if tuple(q.shape) != (T, Q_HEADS, HEAD_DIM):
-        raise ValueError("q must be [T, 16, 128] uint8 (E4M3)")
-    if tuple(seq_lens.shape) != (n_seqs,) or tuple(q_start_loc.shape) != (n_seqs + 1,):
-        raise ValueError("seq_lens must be [B], q_start_loc [B+1]")
-    if T != bufs.T or n_seqs > bufs.n_seqs:
-        raise ValueError(f"bufs are for {bufs.T} query tokens of up to {bufs.n_seqs} sequences")
-    if tree_mask is not None and tuple(tree_mask.shape) != (T,):
-        raise ValueError("tree_mask must be [T]")
+    if n_seqs > bufs.n_seqs:
+        raise ValueError(f"bufs are for up to {bufs.n_seqs} sequences")
     if (sel is None) != (n_sel is None):
         raise ValueError("sel and n_sel come together")
-    if sel is not None and (tuple(sel.shape) != (n_seqs, TOPK + 1) or tuple(n_sel.shape) != (n_seqs,)):
-        raise ValueError("sel must be [B, 17] and n_sel [B]")
-    if softmax_scale is None:
-        softmax_scale = 1.0 / math.sqrt(HEAD_DIM)
-    _on_device(cache.kv_pool.device, q, block_table, seq_lens, q_start_loc, tree_mask, sel, n_sel, bufs.out)
+    dev = _device_of(cache)
     c = cache.struct()
     _check(lib().msa_tree_attn(
-        ctypes.byref(c), _ptr(q, torch.uint8, "q"), Q_HEADS, float(softmax_scale),
-        _ptr(block_table, torch.int32, "block_table"), max_pages, _ptr(seq_lens, torch.int32, "seq_lens"),
-        _ptr(q_start_loc, torch.int32, "q_start_loc"), n_seqs, T,
-        None if tree_mask is None else _ptr(tree_mask, torch.int64, "tree_mask"),
-        None if sel is None else _ptr(sel, torch.int32, "sel"),
-        None if n_sel is None else _ptr(n_sel, torch.int32, "n_sel"), _DTYPES[bufs.out.dtype],
-        bufs.out.data_ptr(), bufs.lse.data_ptr(), bufs.ws.data_ptr(), bufs.ws.numel(), _stream()))
+        ctypes.byref(c), _arg(q, torch.uint8, (T, Q_HEADS, HEAD_DIM), dev, "q"), Q_HEADS,
+        HEAD_DIM ** -0.5 if softmax_scale is None else float(softmax_scale),
+        _arg(block_table, torch.int32, (n_seqs, max_pages), dev, "block_table"), max_pages,
+        _arg(seq_lens, torch.int32, (n_seqs,), dev, "seq_lens"),
+        _arg(q_start_loc, torch.int32, (n_seqs + 1,), dev, "q_start_loc"), n_seqs, T,
+        None if tree_mask is None else _arg(tree_mask, torch.int64, (T,), dev, "tree_mask"),
+        None if sel is None else _arg(sel, torch.int32, (n_seqs, TOPK + 1), dev, "sel"),
+        None if sel is None else _arg(n_sel, torch.int32, (n_seqs,), dev, "n_sel"), _DTYPES[bufs.out.dtype],
+        _arg(bufs.out, bufs.out.dtype, (T, Q_HEADS, HEAD_DIM), dev, "bufs.out"),
+        _arg(bufs.lse, torch.float32, (T, Q_HEADS), dev, "bufs.lse"), bufs.ws.data_ptr(), bufs.ws.numel(),
+        _raw_stream(dev)))
     return bufs.out
 
 

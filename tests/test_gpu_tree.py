@@ -355,4 +355,15 @@ def test_refusals():
         ops.tree_attn(cache, q, bt, lens, qsl, ops.TreeBuffers(3, 1))
     with pytest.raises(ops.MsaError):
         ops.tree_attn(cache, q, bt, lens, qsl, bufs, softmax_scale=-1.0)
+    i32 = torch.int32
+    for at, bad in ((1, q[:1]), (1, q[:, :8]), (3, lens.repeat(2)), (4, qsl[:1]), (2, bt.t())):
+        args = [cache, q, bt, lens, qsl, bufs]
+        args[at] = bad
+        with pytest.raises(ValueError):
+            ops.tree_attn(*args)
+    with pytest.raises(ValueError):
+        ops.tree_attn(cache, q, bt, lens, qsl, bufs, tree_mask=torch.zeros(3, dtype=torch.int64, device=DEV))
+    with pytest.raises(ValueError):
+        ops.tree_attn(cache, q, bt, lens, qsl, bufs, sel=torch.zeros((1, 16), dtype=i32, device=DEV),
+                      n_sel=torch.zeros(1, dtype=i32, device=DEV))
     assert cache.read_status() == 0

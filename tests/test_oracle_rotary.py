@@ -158,19 +158,33 @@ def test_read_kv_validation_needs_no_gpu(lib):  # noqa: F811
 
 
 def test_row_checks_of_the_binding():
-    n = 3
+    n, f32, cpu = 3, torch.float32, -1  # (get_device() of a CPU tensor)
     x = torch.zeros(n, 33, 128)
-    assert ops._rows(x[:, 16:20], "k", 4, n, torch.float32) == (x.data_ptr() + 16 * 512, 33 * 128)
-    assert ops._rows(x[:, 24], "idx_k", 0, n, torch.float32)[1] == 33 * 128
+    shape = (n, 4, 128)
+    assert ops._rows(x[:, 16:20], "k", shape, f32, cpu) == (x.data_ptr() + 16 * 512, 33 * 128)
+    assert ops._rows(x[:, 24], "idx_k", (n, 128), f32, cpu)[1] == 33 * 128
     with pytest.raises(TypeError):
-        ops._rows(x[:, :4].half(), "k", 4, n, torch.float32)
+        ops._rows(x[:, :4].half(), "k", shape, f32, cpu)
+    with pytest.raises(TypeError):
+        ops._rows(x[:, :4].numpy(), "k", shape, f32, cpu)
     with pytest.raises(ValueError):
-        ops._rows(x[:, :5], "k", 4, n, torch.float32)
+        ops._rows(x[:, :5], "k", shape, f32, cpu)
+    with pytest.raises(ValueError):  # another device
+        ops._rows(x[:, :4], "k", shape, f32, 0)
     with pytest.raises(ValueError):  # heads not contiguous
-        ops._rows(x[:, :8:2], "k", 4, n, torch.float32)
+        ops._rows(x[:, :8:2], "k", shape, f32, cpu)
     with pytest.raises(ValueError):  # channels not contiguous
-        ops._rows(torch.zeros(n, 4, 256)[:, :, ::2], "k", 4, n, torch.float32)
+        ops._rows(torch.zeros(n, 4, 256)[:, :, ::2], "k", shape, f32, cpu)
     with pytest.raises(ValueError):  # token stride off 16 bytes
-        ops._rows(torch.zeros(n * 514).as_strided((n, 4, 128), (514, 128, 1)), "k", 4, n, torch.float32)
+        ops._rows(torch.zeros(n * 514).as_strided((n, 4, 128), (514, 128, 1)), "k", shape, f32, cpu)
     with pytest.raises(ValueError):  # base off 16 bytes
-        ops._rows(torch.zeros(n * 512 + 1)[1:].view(n, 4, 128), "k", 4, n, torch.float32)
+        ops._rows(torch.zeros(n * 512 + 1)[1:].view(n, 4, 128), "k", shape, f32, cpu)
+
+
+def test_argument_checks_of_the_binding():
+    x = torch.zeros(4, 6, dtype=torch.int32)
+    for t, dtype, shape, dev, error in ((x, torch.int64, (4, 6), -1, TypeError), ([1, 2], torch.int32, (2,), -1, TypeError),
+                                        (x, torch.int32, (4, 6), 0, ValueError), (x, torch.int32, (6, 4), -1, ValueError),
+                                        (x.t(), torch.int32, (6, 4), -1, ValueError)):
+        with pytest.raises(error):
+            ops._arg(t, dtype, shape, dev, "x")

@@ -84,12 +84,9 @@ def test_binding_checks():
     i32 = torch.int32
     args = [None, torch.zeros(4, 16, 128, dtype=torch.uint8), torch.zeros(1, 4, dtype=i32), torch.zeros(1, dtype=i32),
             torch.zeros(2, dtype=i32), bufs]
-    for at, bad in ((1, args[1][:3]), (1, args[1][:, :8]), (2, torch.zeros(2, 4, dtype=i32)), (3, torch.zeros(2, dtype=i32))):
-        with pytest.raises(ValueError):
-            ops.tree_attn(*(args[:at] + [bad] + args[at + 1:]))
-    with pytest.raises(ValueError):
-        ops.tree_attn(*args, tree_mask=torch.zeros(3, dtype=torch.int64))
+    with pytest.raises(ValueError):  # more sequences than the buffers are for
+        ops.tree_attn(*args[:2], torch.zeros(2, 4, dtype=i32), *args[3:])
     with pytest.raises(ValueError):
         ops.tree_attn(*args, sel=torch.zeros(1, 17, dtype=i32))
     with pytest.raises(ValueError):
-        ops.tree_attn(*args, sel=torch.zeros(1, 16, dtype=i32), n_sel=torch.zeros(1, dtype=i32))
+        ops.tree_attn(*args, n_sel=torch.zeros(1, dtype=i32))
