@@ -12,10 +12,14 @@
 // of msa_quantize_kv_insert), index keys -> E4M3.
 //
 // Bound by memory: a bf16 token of 33 heads reads 8,448 bytes and writes 3,776.
-// One half-warp takes one head row, lane l its channels 8l .. 8l + 7: one or two
-// 16-byte loads, one 8-byte FP8 store or one 32-bit code word, a 16-channel
-// group is two lanes, and the partner channels of a half pair sit in one lane
-// a fixed distance away.
+// Eight lanes take one head row, each two chunks of 8 channels: with half pairs
+// lane l < rot / 16 the chunks l and l + rot / 16, partners of each other, with
+// interleaved pairs and unturned channels the chunks 2 l and 2 l + 1; so a
+// rotation needs no other lane and each cos and sin is loaded once for both
+// chunks.  A warp takes one head of a tile of tokens, four at a time, and keeps
+// the tile's scale bytes in shared memory: a group's scales of consecutive tokens
+// are consecutive bytes of the page, so a tile of tokens in page order leaves as
+// whole sectors and not byte by byte.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -30,7 +34,8 @@ struct RopeParams {
   const void* rows[5];     // q, k, v, idx_k, q_idx (may be null)
   long long stride[5];     // elements from one token's rows to the next
   int n_tokens;
-  int n_pairs;             // half-warp jobs come in pairs: 17 per token, 13 without index queries
+  int n_rows;              // head rows of a token: 33, 25 without index queries
+  int tile;                // tokens of a warp's tile (a multiple of 4, at most 32)
   const float* cos_sin;    // [max_pos][rot]: cos of the rot / 2 pairs, then their sin
   int max_pos;
   int rot;
@@ -51,18 +56,34 @@ __device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
   x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
   x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 v = ld_stream_v4(p);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// Eight channels as they lie in memory (loaded ahead of their turn) and as floats.
+template <typename T>
+struct Chunk {
+  uint4 v[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = ld_stream_v4(reinterpret_cast<const uint4*>(p) + i);
+  }
+};
+__device__ __forceinline__ void to_floats(const Chunk<float>& c, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    x[4 * i] = __uint_as_float(c.v[i].x);
+    x[4 * i + 1] = __uint_as_float(c.v[i].y);
+    x[4 * i + 2] = __uint_as_float(c.v[i].z);
+    x[4 * i + 3] = __uint_as_float(c.v[i].w);
+  }
+}
+__device__ __forceinline__ void to_floats(const Chunk<__nv_bfloat16>& c, float (&x)[8]) {
+  const uint32_t w[4] = {c.v[0].x, c.v[0].y, c.v[0].z, c.v[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     x[2 * i] = __uint_as_float(w[i] << 16);
     x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
 }
-__device__ __forceinline__ void load8(const __half* p, float (&x)[8]) {
-  const uint4 v = ld_stream_v4(p);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void to_floats(const Chunk<__half>& c, float (&x)[8]) {
+  const uint32_t w[4] = {c.v[0].x, c.v[0].y, c.v[0].z, c.v[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
@@ -71,117 +92,160 @@ __device__ __forceinline__ void load8(const __half* p, float (&x)[8]) {
   }
 }
 
-// Eight E4M3 bytes (RNE, satfinite, zeros as 0x00), channel order.
+// Eight E4M3 bytes (RNE, satfinite, zeros as 0x00: a byte's sign stays where its
+// seven magnitude bits carry into bit 7), channel order.
 __device__ __forceinline__ uint2 to_fp8x8(const float (&x)[8]) {
   uint32_t w[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint32_t lo = f32x2_to_e4m3x2(x[4 * h], x[4 * h + 1]), hi = f32x2_to_e4m3x2(x[4 * h + 2], x[4 * h + 3]);
-    w[h] = canon_zero(lo & 0xFF) | (canon_zero(lo >> 8) << 8) | (canon_zero(hi & 0xFF) << 16) | (canon_zero(hi >> 8) << 24);
+    const uint32_t b = f32x2_to_e4m3x2(x[4 * h], x[4 * h + 1]) | (f32x2_to_e4m3x2(x[4 * h + 2], x[4 * h + 3]) << 16);
+    w[h] = b & (((b & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) | 0x7F7F7F7Fu);
   }
   return make_uint2(w[0], w[1]);
 }
 
+// Code word (8 channels) of x under the scale sb.
+__device__ __forceinline__ uint32_t code_word(const float (&x)[8], float s_enc, float sb) {
+  uint32_t word = 0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float v = x[4 * h + i];
+      c[i] = e2m1_code(__fmul_rn(fabsf(v), s_enc), sb);
+      c[i] |= (v < 0.f && c[i]) ? 8u : 0u;
+    }
+    word |= code_word_part(c, h);
+  }
+  return word;
+}
+__device__ __forceinline__ float max_abs(const float (&x)[8]) {
+  float a = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(x[i]));
+  return a;
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kRopeThreads) rotary_insert_kernel(RopeParams p) {
-  const int lane = threadIdx.x & 31, l = lane & 15;
-  const long long n_jobs = (long long)p.n_tokens * p.n_pairs;
+__global__ void __launch_bounds__(kRopeThreads, 4) rotary_insert_kernel(const __grid_constant__ RopeParams p) {
+  __shared__ __align__(8) uint8_t s_scales[kRopeThreads / 32][32 * 8];  // [warp][token][group]
+  const int lane = threadIdx.x & 31, l = lane & 7, sub = lane >> 3;
+  uint8_t* scales = s_scales[threadIdx.x >> 5];
+  const long long n_jobs = (long long)((p.n_tokens + p.tile - 1) / p.tile) * p.n_rows;
   const long long warp0 = ((long long)blockIdx.x * kRopeThreads + threadIdx.x) >> 5;
   const long long n_warps = ((long long)gridDim.x * kRopeThreads) >> 5;
+  const int half = p.rot >> 1;
   for (long long job = warp0; job < n_jobs; job += n_warps) {
-    const int t = (int)(job / p.n_pairs);
-    // rows of a token in job order: 16 q, 4 k, 4 v, 8 q_idx, idx_k (and one idle half)
-    int row = 2 * (int)(job % p.n_pairs) + (lane >> 4);
-    if (p.n_pairs == 13 && row >= 24) row += 8;
-    const int kind = row < 16 ? 0 : row < 20 ? 1 : row < 24 ? 2 : row < 32 ? 4 : 3;
-    const int head = kind == 0 ? row : kind == 1 ? row - 16 : kind == 2 ? row - 20 : kind == 4 ? row - 24 : 0;
-    const bool live = row <= 32;
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (live)
-      load8(static_cast<const T*>(p.rows[kind]) + (size_t)t * p.stride[kind] + head * kHeadDim + 8 * l, x);
-    // rotation (values stay as they are)
-    const int pos = p.positions[t];
-    const bool turn = pos >= 0 && pos < p.max_pos;
-    if (p.rot > 0 && !turn && lane == 0 && row == 0) set_status(p.status, MSA_STATUS_BAD_SEQ);
-    if (turn && p.rot > 0) {
-      const float* cs = p.cos_sin + (size_t)pos * p.rot;
-      const int half = p.rot >> 1;
-      const bool mine = kind != 2 && 8 * l < p.rot;
-      if (p.interleaved) {
-        if (mine) {
-          const float4 c = __ldg(reinterpret_cast<const float4*>(cs + 4 * l));
-          const float4 s = __ldg(reinterpret_cast<const float4*>(cs + half + 4 * l));
-          const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+    // rows of a token in job order: 16 q, 4 k, 4 v, idx_k, 8 q_idx
+    const int t0 = (int)(job / p.n_rows) * p.tile, cnt = min(p.tile, p.n_tokens - t0), row = (int)(job % p.n_rows);
+    const int kind = row < 16 ? 0 : row < 20 ? 1 : row < 24 ? 2 : row == 24 ? 3 : 4;
+    const int head = kind == 0 ? row : kind == 1 ? row - 16 : kind == 2 ? row - 20 : kind == 4 ? row - 25 : 0;
+    const bool cached = kind >= 1 && kind <= 3;
+    const int my_pos = lane < cnt && p.rot > 0 ? p.positions[t0 + lane] : 0;
+    int64_t my_slot = lane < cnt && cached ? p.slot_mapping[t0 + lane] : -1;
+    if (my_slot >= 0 && (my_slot >> 7) >= p.n_pages) {
+      set_status(p.status, MSA_STATUS_BAD_SLOT);
+      my_slot = -1;
+    }
+    if (row == 0 && p.rot > 0 && (my_pos < 0 || my_pos >= p.max_pos)) set_status(p.status, MSA_STATUS_BAD_SEQ);
+    // half pairs: lanes below h have partner chunks h apart (values are not turned)
+    const int h = p.interleaved || kind == 2 ? 0 : p.rot >> 4;
+    const int ca = l < h ? l : 2 * l, cb = l < h ? l + h : 2 * l + 1;
+    const bool turns = kind != 2 && (p.interleaved ? 16 * l < p.rot : l < h);
+    const T* src = static_cast<const T*>(p.rows[kind]) + (size_t)t0 * p.stride[kind] + head * kHeadDim;
+    const size_t stride = p.stride[kind];
+    Chunk<T> na = {}, nb = {};  // of the next four tokens
+    if (sub < cnt) {
+      na.load(src + sub * stride + 8 * ca);
+      nb.load(src + sub * stride + 8 * cb);
+    }
+    for (int i0 = 0; i0 < cnt; i0 += 4) {
+      const int i = i0 + sub, t = t0 + i;
+      const int pos = __shfl_sync(0xffffffffu, my_pos, i & 31);
+      const int64_t slot = __shfl_sync(0xffffffffu, my_slot, i & 31);
+      const bool live = i < cnt;
+      float a[8], b[8];
+      to_floats(na, a);
+      to_floats(nb, b);
+      if (i + 4 < cnt) {
+        na.load(src + (i + 4) * stride + 8 * ca);
+        nb.load(src + (i + 4) * stride + 8 * cb);
+      }
+      if (live && turns && pos >= 0 && pos < p.max_pos) {
+        const float* cs = p.cos_sin + (size_t)pos * p.rot + 8 * l;
+        float c[8], s[8];
+        load8(cs, c);
+        load8(cs + half, s);
+        if (h) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float a = x[2 * i], b = x[2 * i + 1];
-            x[2 * i] = __fsub_rn(__fmul_rn(a, cc[i]), __fmul_rn(b, ss[i]));
-            x[2 * i + 1] = __fadd_rn(__fmul_rn(b, cc[i]), __fmul_rn(a, ss[i]));
+          for (int u = 0; u < 8; ++u) {
+            const float x = a[u], y = b[u];
+            a[u] = __fsub_rn(__fmul_rn(x, c[u]), __fmul_rn(y, s[u]));
+            b[u] = __fadd_rn(__fmul_rn(y, c[u]), __fmul_rn(x, s[u]));
           }
-        }
-      } else {
-        // channel c < half pairs with c + half: half / 8 lanes further on
-        const int step = half >> 3;
-        const bool first = l < step;
-        const int src = (lane & 16) | ((first ? l + step : l - step) & 15);
-        float o[8];
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(0xffffffffu, x[i], src);
-        if (mine) {
-          const int at = 8 * (first ? l : l - step);
-          float c[8], s[8];
-          load8(cs + at, c);
-          load8(cs + half + at, s);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float u = __fmul_rn(x[i], c[i]), w = __fmul_rn(o[i], s[i]);
-            x[i] = first ? __fsub_rn(u, w) : __fadd_rn(u, w);
+          for (int u = 0; u < 8; u += 2) {
+            float x = a[u], y = a[u + 1];
+            a[u] = __fsub_rn(__fmul_rn(x, c[u >> 1]), __fmul_rn(y, s[u >> 1]));
+            a[u + 1] = __fadd_rn(__fmul_rn(y, c[u >> 1]), __fmul_rn(x, s[u >> 1]));
+            x = b[u], y = b[u + 1];
+            b[u] = __fsub_rn(__fmul_rn(x, c[4 + (u >> 1)]), __fmul_rn(y, s[4 + (u >> 1)]));
+            b[u + 1] = __fadd_rn(__fmul_rn(y, c[4 + (u >> 1)]), __fmul_rn(x, s[4 + (u >> 1)]));
           }
         }
       }
-    }
-    if (kind == 0 || kind == 4) {
-      uint8_t* dst = kind == 0 ? p.q8 + ((size_t)t * kQHeads + head) * kHeadDim
-                               : p.qi8 + ((size_t)t * kIdxHeads + head) * kIdxDim;
-      *reinterpret_cast<uint2*>(dst + 8 * l) = to_fp8x8(x);
-    }
-    // NVFP4 scale of the 16-channel group: this lane and its neighbour
-    float a = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(x[i]));
-    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-    const int64_t slot = p.slot_mapping[t];
-    const int64_t page = slot >> 7;
-    const int off = (int)(slot & 127);
-    if (!live || slot < 0 || kind == 0 || kind == 4) continue;
-    if (page >= p.n_pages) {
-      if (l == 0) set_status(p.status, MSA_STATUS_BAD_SLOT);
-      continue;
-    }
-    if (kind == 3) {
-      uint8_t* dst = p.idx_pool + (size_t)page * kIdxPageBytes + off * kIdxDim;
-      *reinterpret_cast<uint2*>(dst + (((l >> 1) ^ (off & 7)) << 4) + 8 * (l & 1)) = to_fp8x8(x);
-      continue;
-    }
-    const float s_enc = kind == 1 ? p.s_enc_k : p.s_enc_v;
-    const uint32_t sb_byte = f32_to_e4m3(__fmul_rn(__fdiv_rn(a, 6.0f), s_enc));
-    const float sb = e4m3_to_f32(sb_byte);
-    uint32_t word = 0;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t c[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float v = x[4 * h + i];
-        c[i] = e2m1_code(__fmul_rn(fabsf(v), s_enc), sb);
-        c[i] |= (v < 0.f && c[i]) ? 8u : 0u;
+      if (!cached) {
+        if (live) {
+          uint8_t* dst = kind == 0 ? p.q8 + ((size_t)t * kQHeads + head) * kHeadDim
+                                   : p.qi8 + ((size_t)t * kIdxHeads + head) * kIdxDim;
+          *reinterpret_cast<uint2*>(dst + 8 * ca) = to_fp8x8(a);
+          *reinterpret_cast<uint2*>(dst + 8 * cb) = to_fp8x8(b);
+        }
+        continue;
       }
-      word |= code_word_part(c, h);
+      // maxima of the two 16-channel groups: the other chunk of group c / 2 is c ^ 1
+      const float ma = max_abs(a), mb = max_abs(b);
+      float ga = fmaxf(ma, mb), gb = ga;
+      if (h) {
+        const int xa = ca ^ 1, xb = cb ^ 1;  // (of lanes below h: held by lane c or c - h)
+        const int la = l < h ? (lane & 24) | (xa < h ? xa : xa - h) : lane, lb = l < h ? (lane & 24) | (xb < h ? xb : xb - h) : lane;
+        const float a1 = __shfl_sync(0xffffffffu, ma, la), a2 = __shfl_sync(0xffffffffu, mb, la);
+        const float b1 = __shfl_sync(0xffffffffu, ma, lb), b2 = __shfl_sync(0xffffffffu, mb, lb);
+        if (l < h) {
+          ga = fmaxf(ma, xa < h ? a1 : a2);
+          gb = fmaxf(mb, xb < h ? b1 : b2);
+        }
+      }
+      if (!live || slot < 0) continue;
+      const int off = (int)(slot & 127);
+      if (kind == 3) {
+        uint8_t* dst = p.idx_pool + (size_t)(slot >> 7) * kIdxPageBytes + off * kIdxDim;
+        *reinterpret_cast<uint2*>(dst + (((ca >> 1) ^ (off & 7)) << 4) + 8 * (ca & 1)) = to_fp8x8(a);
+        *reinterpret_cast<uint2*>(dst + (((cb >> 1) ^ (off & 7)) << 4) + 8 * (cb & 1)) = to_fp8x8(b);
+        continue;
+      }
+      const float s_enc = kind == 1 ? p.s_enc_k : p.s_enc_v;
+      const uint32_t sa = f32_to_e4m3(__fmul_rn(__fdiv_rn(ga, 6.0f), s_enc));
+      const uint32_t sb = f32_to_e4m3(__fmul_rn(__fdiv_rn(gb, 6.0f), s_enc));
+      uint8_t* codes = p.kv_pool + (size_t)(slot >> 7) * kKvPageBytes + head * kHeadBytes + (kind == 1 ? kOffKc : kOffVc) + off * 64;
+      *reinterpret_cast<uint32_t*>(codes + (code_chunk_pos(ca >> 2, off) << 4) + 4 * (ca & 3)) = code_word(a, s_enc, e4m3_to_f32(sa));
+      *reinterpret_cast<uint32_t*>(codes + (code_chunk_pos(cb >> 2, off) << 4) + 4 * (cb & 3)) = code_word(b, s_enc, e4m3_to_f32(sb));
+      if ((ca & 1) == 0) scales[i * 8 + (ca >> 1)] = (uint8_t)sa;
+      if ((cb & 1) == 0) scales[i * 8 + (cb >> 1)] = (uint8_t)sb;
     }
-    uint8_t* hb = p.kv_pool + (size_t)page * kKvPageBytes + head * kHeadBytes;
-    const int off_c = kind == 1 ? kOffKc : kOffVc, off_s = kind == 1 ? kOffKs : kOffVs;
-    *reinterpret_cast<uint32_t*>(hb + off_c + off * 64 + (code_chunk_pos(l >> 2, off) << 4) + 4 * (l & 3)) = word;
-    if ((l & 1) == 0) hb[off_s + (l >> 1) * kPageTokens + off] = (uint8_t)sb_byte;
+    if (kind == 1 || kind == 2) {  // lane = token: its eight scale bytes
+      __syncwarp();
+      if (my_slot >= 0) {
+        const uint2 sc = *reinterpret_cast<const uint2*>(scales + 8 * lane);
+        uint8_t* dst = p.kv_pool + (size_t)(my_slot >> 7) * kKvPageBytes + head * kHeadBytes +
+                       (kind == 1 ? kOffKs : kOffVs) + (my_slot & 127);
+#pragma unroll
+        for (int g = 0; g < 8; ++g) dst[g * kPageTokens] = (uint8_t)((g < 4 ? sc.x : sc.y) >> (8 * (g & 3)));
+      }
+      __syncwarp();
+    }
   }
 }
 
@@ -217,7 +281,7 @@ cudaError_t launch_rotary_insert(const msa_cache* c, const msa_rows* r, int n_to
     rp.stride[i] = strides[i];
   }
   rp.n_tokens = n_tokens;
-  rp.n_pairs = r->q_idx ? 17 : 13;
+  rp.n_rows = r->q_idx ? 33 : 25;
   rp.cos_sin = cos_sin;
   rp.max_pos = max_pos;
   rp.rot = rot;
@@ -232,9 +296,12 @@ cudaError_t launch_rotary_insert(const msa_cache* c, const msa_rows* r, int n_to
   rp.q8 = q8;
   rp.qi8 = qi8;
   rp.status = c->status;
-  const long long warps = (long long)n_tokens * rp.n_pairs;
+  // the largest tile that still makes 48 warps per SM
+  rp.tile = 32;
+  while (rp.tile > 4 && (long long)n_tokens / rp.tile * rp.n_rows < 48ll * n_sm) rp.tile >>= 1;
+  const long long warps = ((long long)n_tokens + rp.tile - 1) / rp.tile * rp.n_rows;
   long long blocks = (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
-  if (blocks > 8ll * n_sm) blocks = 8ll * n_sm;
+  if (blocks > 64ll * n_sm) blocks = 64ll * n_sm;
   const dim3 grid((unsigned)blocks), block(kRopeThreads);
   if (r->dtype == MSA_DTYPE_F32) rotary_insert_kernel<float><<<grid, block, 0, stream>>>(rp);
   else if (r->dtype == MSA_DTYPE_BF16) rotary_insert_kernel<__nv_bfloat16><<<grid, block, 0, stream>>>(rp);
