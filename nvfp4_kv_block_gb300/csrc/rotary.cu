@@ -104,31 +104,63 @@ __device__ __forceinline__ uint2 to_fp8x8(const float (&x)[8]) {
   return make_uint2(w[0], w[1]);
 }
 
-// Code word (8 channels) of x under the scale sb.
-__device__ __forceinline__ uint32_t code_word(const float (&x)[8], float s_enc, float sb) {
-  uint32_t word = 0;
+// Code word (8 channels) of finite x under the scale sb.  A code is the E2M1
+// rounding (to nearest even, saturating) of y / sb, y = fl(x s_enc), and the
+// hardware rounds an fp32 quotient.  The quotient must only not move onto or off a
+// midpoint: y = mid sb (exact in fp32) has to give mid, and any other y lies at
+// least an ulp of y away, more than half an ulp of mid, so the correctly rounded
+// quotient is on the same side.  It is q + r (y - q sb) with q = y r, r the rounded
+// reciprocal of sb (P. Markstein, 1990); a remainder that underflows belongs to a
+// quotient far below the first midpoint.  inv: r, 0 for sb = 0.  The insert kernel
+// compares y with every midpoint: five times the instructions.
+__device__ __forceinline__ uint32_t code_word(const float (&x)[8], float s_enc, float sb, float inv) {
+  float q[8];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t c[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float v = x[4 * h + i];
-      c[i] = e2m1_code(__fmul_rn(fabsf(v), s_enc), sb);
-      c[i] |= (v < 0.f && c[i]) ? 8u : 0u;
-    }
-    word |= code_word_part(c, h);
+  for (int i = 0; i < 8; ++i) {
+    const float y = __fmul_rn(x[i], s_enc), q0 = __fmul_rn(y, inv);
+    q[i] = __fmaf_rn(__fmaf_rn(-q0, sb, y), inv, q0);
   }
-  return word;
+  uint32_t n;  // nibble i: code of channel i
+  asm("{\n .reg .b8 a, b, c, d;\n cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n mov.b32 %0, {a, b, c, d};\n}"
+      : "=r"(n)
+      : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+  const uint32_t m = n & 0x77777777u;
+  const uint32_t sg = (n & (m + 0x77777777u) & 0x88888888u) >> 3;  // signs of codes that are not zero, at bit 4 i
+  // sign of channel i < 4 to bit 8 i + 7, of channel 4 + i to bit 8 i + 3
+  uint32_t lo = sg & 0x1111u, hi = sg >> 16;
+  lo = (lo | (lo << 8)) & 0x00110011u;
+  lo = (lo | (lo << 4)) & 0x01010101u;
+  hi = (hi | (hi << 8)) & 0x00110011u;
+  hi = (hi | (hi << 4)) & 0x01010101u;
+  return m | (lo << 7) | (hi << 3);
 }
-__device__ __forceinline__ float max_abs(const float (&x)[8]) {
-  float a = 0.f;
+// Values that are none, for code_word: NaN has the code 0, what is beyond `most` the largest.
+__device__ __forceinline__ void make_finite(float (&x)[8], float most) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(x[i]));
+  for (int i = 0; i < 8; ++i) x[i] = x[i] == x[i] ? fminf(fmaxf(x[i], -most), most) : 0.f;
+}
+// Largest magnitude (fmaxf drops NaN, as the insert kernel's does); `all` keeps NaN.
+__device__ __forceinline__ float max_abs(const float (&x)[8], float& all) {
+  float a = 0.f, n = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    a = fmaxf(a, fabsf(x[i]));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(n) : "f"(fabsf(x[i])));
+  }
+  all = n;
   return a;
+}
+// (a, b) turned by c and s: two products and a sum, each rounded on its own.  (Not as packed
+// pairs: the compiler joins a packed product and sum to one rounding.)
+__device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
+  const float x = a, y = b;
+  a = __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
+  b = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kRopeThreads, 4) rotary_insert_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 3) rotary_insert_kernel(const __grid_constant__ RopeParams p) {
   __shared__ __align__(8) uint8_t s_scales[kRopeThreads / 32][32 * 8];  // [warp][token][group]
   const int lane = threadIdx.x & 31, l = lane & 7, sub = lane >> 3;
   uint8_t* scales = s_scales[threadIdx.x >> 5];
@@ -179,20 +211,12 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rotary_insert_kernel(const __
         load8(cs + half, s);
         if (h) {
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const float x = a[u], y = b[u];
-            a[u] = __fsub_rn(__fmul_rn(x, c[u]), __fmul_rn(y, s[u]));
-            b[u] = __fadd_rn(__fmul_rn(y, c[u]), __fmul_rn(x, s[u]));
-          }
+          for (int u = 0; u < 8; ++u) turn(a[u], b[u], c[u], s[u]);
         } else {
 #pragma unroll
-          for (int u = 0; u < 8; u += 2) {
-            float x = a[u], y = a[u + 1];
-            a[u] = __fsub_rn(__fmul_rn(x, c[u >> 1]), __fmul_rn(y, s[u >> 1]));
-            a[u + 1] = __fadd_rn(__fmul_rn(y, c[u >> 1]), __fmul_rn(x, s[u >> 1]));
-            x = b[u], y = b[u + 1];
-            b[u] = __fsub_rn(__fmul_rn(x, c[4 + (u >> 1)]), __fmul_rn(y, s[4 + (u >> 1)]));
-            b[u + 1] = __fadd_rn(__fmul_rn(y, c[4 + (u >> 1)]), __fmul_rn(x, s[4 + (u >> 1)]));
+          for (int u = 0; u < 4; ++u) {
+            turn(a[2 * u], a[2 * u + 1], c[u], s[u]);
+            turn(b[2 * u], b[2 * u + 1], c[4 + u], s[4 + u]);
           }
         }
       }
@@ -206,7 +230,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rotary_insert_kernel(const __
         continue;
       }
       // maxima of the two 16-channel groups: the other chunk of group c / 2 is c ^ 1
-      const float ma = max_abs(a), mb = max_abs(b);
+      float all_a, all_b;
+      const float ma = max_abs(a, all_a), mb = max_abs(b, all_b);
       float ga = fmaxf(ma, mb), gb = ga;
       if (h) {
         const int xa = ca ^ 1, xb = cb ^ 1;  // (of lanes below h: held by lane c or c - h)
@@ -230,8 +255,16 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rotary_insert_kernel(const __
       const uint32_t sa = f32_to_e4m3(__fmul_rn(__fdiv_rn(ga, 6.0f), s_enc));
       const uint32_t sb = f32_to_e4m3(__fmul_rn(__fdiv_rn(gb, 6.0f), s_enc));
       uint8_t* codes = p.kv_pool + (size_t)(slot >> 7) * kKvPageBytes + head * kHeadBytes + (kind == 1 ? kOffKc : kOffVc) + off * 64;
-      *reinterpret_cast<uint32_t*>(codes + (code_chunk_pos(ca >> 2, off) << 4) + 4 * (ca & 3)) = code_word(a, s_enc, e4m3_to_f32(sa));
-      *reinterpret_cast<uint32_t*>(codes + (code_chunk_pos(cb >> 2, off) << 4) + 4 * (cb & 3)) = code_word(b, s_enc, e4m3_to_f32(sb));
+      const float fa = e4m3_to_f32(sa), fb = e4m3_to_f32(sb);
+      if (!(fmaxf(all_a, all_b) * s_enc < 1e30f) || all_a != all_a || all_b != all_b) {
+        const float most = fminf(1e30f / s_enc, 3e38f);
+        make_finite(a, most);
+        make_finite(b, most);
+      }
+      const uint32_t wa = code_word(a, s_enc, fa, fa > 0.f ? __frcp_rn(fa) : 0.f);
+      const uint32_t wb = code_word(b, s_enc, fb, fb > 0.f ? __frcp_rn(fb) : 0.f);
+      *reinterpret_cast<uint32_t*>(codes + (code_chunk_pos(ca >> 2, off) << 4) + 4 * (ca & 3)) = wa;
+      *reinterpret_cast<uint32_t*>(codes + (code_chunk_pos(cb >> 2, off) << 4) + 4 * (cb & 3)) = wb;
       if ((ca & 1) == 0) scales[i * 8 + (ca >> 1)] = (uint8_t)sa;
       if ((cb & 1) == 0) scales[i * 8 + (cb >> 1)] = (uint8_t)sb;
     }

@@ -142,6 +142,31 @@ def test_large_values_saturate_and_infinities_stay_finite():
     assert torch.isfinite(k).all() and torch.count_nonzero(v[2, 1]) == 0
 
 
+def test_codes_at_and_next_to_every_midpoint_and_of_values_that_are_none():
+    """Values on, one ulp below and one ulp above each E2M1 midpoint under every scale, of both
+    signs, and NaN and infinities: the bytes of quantize_kv_insert."""
+    scales = np.arange(1, 127, dtype=np.uint8)
+    sb = formats.decode_e4m3(scales).astype(np.float32)
+    mids = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], np.float32)
+    n = len(sb)
+    x = np.zeros((n, 4, 8, 16), np.float32)
+    # with s_enc = 1 the group's scale is E4M3(max / 6): one value 6 sb sets it
+    t = (mids[None] * sb[:, None]).astype(np.float32)
+    x[..., 0] = 6 * sb[:, None, None]
+    for g, y in enumerate((t, np.nextafter(t, np.float32(0)), np.nextafter(t, np.float32(1e9)), 0.5 * t)):
+        x[:, :, g, 1:8], x[:, :, g, 8:15] = y[:, None], -y[:, None]
+    x[:, 1, 4, 3], x[:, 1, 5, 4], x[:, 2, 6, 5], x[:, 3, 7, 6] = np.nan, np.inf, -np.inf, 1e38
+    k = torch.from_numpy(x.reshape(n, 4, 128)).to(DEV)
+    ik = torch.zeros((n, 128), device=DEV)
+    slots = torch.arange(n, device=DEV)
+    for s_enc in (1.0, 1e3):
+        a, b = (ops.KVCache(1, s_enc, 1.0, DEV) for _ in range(2))
+        ops.quantize_kv_insert(a, k, k.neg(), ik, slots)
+        ops.rotary_insert(b, torch.zeros((n, 16, 128), device=DEV), k, k.neg(), ik, torch.zeros((1, 0), device=DEV),
+                          torch.zeros(n, dtype=torch.int32, device=DEV), slots)
+        assert torch.equal(a.kv_pool, b.kv_pool)
+
+
 def test_table_of_given_frequencies():
     for rot, scaling, factor in ((128, None, 1.0), (64, "yarn", 8.0), (96, "ntk", 2.0), (16, "linear", 4.0)):
         t = ops.rope_table_scaled(3000, rot, 500000.0, scaling, factor, 1000, device=DEV).cpu().numpy()
