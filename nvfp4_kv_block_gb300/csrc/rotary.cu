@@ -12,14 +12,15 @@
 // of msa_quantize_kv_insert), index keys -> E4M3.
 //
 // Bound by memory: a bf16 token of 33 heads reads 8,448 bytes and writes 3,776.
-// Eight lanes take one head row, each two chunks of 8 channels: with half pairs
-// lane l < rot / 16 the chunks l and l + rot / 16, partners of each other, with
-// interleaved pairs and unturned channels the chunks 2 l and 2 l + 1; so a
-// rotation needs no other lane and each cos and sin is loaded once for both
-// chunks.  A warp takes one head of a tile of tokens, four at a time, and keeps
-// the tile's scale bytes in shared memory: a group's scales of consecutive tokens
-// are consecutive bytes of the page, so a tile of tokens in page order leaves as
-// whole sectors and not byte by byte.
+// A warp takes a part (four heads, or the index key) of four tokens: one bulk copy
+// per token brings its 1,024 bytes to shared memory, so that 4 KB per warp are on
+// their way without a register for them.  Eight lanes take one head row, each two
+// chunks of 8 channels: with half pairs lane l < rot / 16 the chunks l and l + rot / 16,
+// partners of each other, with interleaved pairs and unturned channels the chunks 2 l
+// and 2 l + 1; so a rotation needs no other lane, and a token's cos and sin are
+// loaded once for the part's heads.  The scale bytes of the four tokens wait in
+// shared memory: a group's scales of consecutive tokens are consecutive bytes of the
+// page, and leave together.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -28,14 +29,16 @@
 namespace msa {
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
+constexpr int kPartHeads = 4;  // heads of a warp's part
+constexpr int kTile = 4;       // its tokens
+static_assert(kPartHeads == kKvHeads && kTile == 4, "the parts of a token, and a lane per (head, group)");
 
 struct RopeParams {
   const void* rows[5];     // q, k, v, idx_k, q_idx (may be null)
   long long stride[5];     // elements from one token's rows to the next
   int n_tokens;
-  int n_rows;              // head rows of a token: 33, 25 without index queries
-  int tile;                // tokens of a warp's tile (a multiple of 4, at most 32)
+  unsigned long long wait_ns;
   const float* cos_sin;    // [max_pos][rot]: cos of the rot / 2 pairs, then their sin
   int max_pos;
   int rot;
@@ -56,13 +59,13 @@ __device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
   x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
   x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
 }
-// Eight channels as they lie in memory (loaded ahead of their turn) and as floats.
+// Eight channels as they lie in memory and as floats.
 template <typename T>
 struct Chunk {
   uint4 v[sizeof(T) / 2];
-  __device__ __forceinline__ void load(const T* p) {
+  __device__ __forceinline__ Chunk(const uint8_t* p) {
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = ld_stream_v4(reinterpret_cast<const uint4*>(p) + i);
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
   }
 };
 __device__ __forceinline__ void to_floats(const Chunk<float>& c, float (&x)[8]) {
@@ -140,16 +143,26 @@ __device__ __forceinline__ void make_finite(float (&x)[8], float most) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) x[i] = x[i] == x[i] ? fminf(fmaxf(x[i], -most), most) : 0.f;
 }
-// Largest magnitude (fmaxf drops NaN, as the insert kernel's does); `all` keeps NaN.
-__device__ __forceinline__ float max_abs(const float (&x)[8], float& all) {
-  float a = 0.f, n = 0.f;
+// Largest magnitude without NaN, as the insert kernel takes it; `fine` if all values
+// are finite and their products with s_enc far from overflow.
+__device__ __forceinline__ float max_abs(const float (&x)[8], float s_enc, bool& fine) {
+  float n = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    a = fmaxf(a, fabsf(x[i]));
-    asm("max.NaN.f32 %0, %0, %1;" : "+f"(n) : "f"(fabsf(x[i])));
-  }
-  all = n;
+  for (int i = 0; i < 8; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(n) : "f"(fabsf(x[i])));
+  fine = n * s_enc < 1e30f;
+  if (fine) return n;
+  float a = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(x[i]));
   return a;
+}
+// fl(a / 6): q + r (a - 6 q), q = a r, r = fl(1 / 6) (P. Markstein, 1990), away from the
+// ends of the range.
+__device__ __forceinline__ float sixth(float a) {
+  if (!(a > 1e-30f && a < 1e36f)) return __fdiv_rn(a, 6.0f);
+  constexpr float r = 1.0f / 6.0f;
+  const float q = __fmul_rn(a, r);
+  return __fmaf_rn(__fmaf_rn(-q, 6.0f, a), r, q);
 }
 // (a, b) turned by c and s: two products and a sum, each rounded on its own.  (Not as packed
 // pairs: the compiler joins a packed product and sum to one rounding.)
@@ -160,124 +173,153 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kRopeThreads, 3) rotary_insert_kernel(const __grid_constant__ RopeParams p) {
-  __shared__ __align__(8) uint8_t s_scales[kRopeThreads / 32][32 * 8];  // [warp][token][group]
-  const int lane = threadIdx.x & 31, l = lane & 7, sub = lane >> 3;
-  uint8_t* scales = s_scales[threadIdx.x >> 5];
-  const long long n_jobs = (long long)((p.n_tokens + p.tile - 1) / p.tile) * p.n_rows;
-  const long long warp0 = ((long long)blockIdx.x * kRopeThreads + threadIdx.x) >> 5;
-  const long long n_warps = ((long long)gridDim.x * kRopeThreads) >> 5;
-  const int half = p.rot >> 1;
-  for (long long job = warp0; job < n_jobs; job += n_warps) {
-    // rows of a token in job order: 16 q, 4 k, 4 v, idx_k, 8 q_idx
-    const int t0 = (int)(job / p.n_rows) * p.tile, cnt = min(p.tile, p.n_tokens - t0), row = (int)(job % p.n_rows);
-    const int kind = row < 16 ? 0 : row < 20 ? 1 : row < 24 ? 2 : row == 24 ? 3 : 4;
-    const int head = kind == 0 ? row : kind == 1 ? row - 16 : kind == 2 ? row - 20 : kind == 4 ? row - 25 : 0;
-    const bool cached = kind >= 1 && kind <= 3;
-    const int my_pos = lane < cnt && p.rot > 0 ? p.positions[t0 + lane] : 0;
-    int64_t my_slot = lane < cnt && cached ? p.slot_mapping[t0 + lane] : -1;
-    if (my_slot >= 0 && (my_slot >> 7) >= p.n_pages) {
-      set_status(p.status, MSA_STATUS_BAD_SLOT);
-      my_slot = -1;
+__global__ void __launch_bounds__(kRopeThreads, 6) rotary_insert_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int kPart = kPartHeads * kHeadDim * sizeof(T);  // bytes of a token's part
+  constexpr int kWarps = kRopeThreads / 32;
+  __shared__ __align__(128) uint8_t s_rows[kWarps][kTile * kPart];
+  __shared__ __align__(4) uint8_t s_scales[kWarps][kPartHeads * 8 * kTile];  // [warp][head][group][token]
+  __shared__ float s_inv[128];  // fl(1 / sb) of a scale byte, 0 for the scale 0
+  __shared__ __align__(8) uint64_t s_bar[kWarps];
+  __shared__ int s_abort;
+  const int lane = threadIdx.x & 31, l = lane & 7, sub = lane >> 3, warp = threadIdx.x >> 5;
+  const uint32_t bar = smem_u32(&s_bar[warp]);
+  // part: 0 keys, 1 values, 2-5 queries, 6 index key, 7-8 index queries (the longest first)
+  const int part = blockIdx.y, kind = part == 0 ? 1 : part == 1 ? 2 : part < 6 ? 0 : part == 6 ? 3 : 4;
+  const bool cached = kind >= 1 && kind <= 3;
+  if (threadIdx.x < 128) s_inv[threadIdx.x] = threadIdx.x ? __frcp_rn(e4m3_to_f32(threadIdx.x)) : 0.f;
+  if (lane == 0) {
+    mbar_init(bar, 1);
+    s_abort = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  const int t0 = ((int)blockIdx.x * kWarps + warp) * kTile, cnt = min(kTile, p.n_tokens - t0);
+  if (cnt <= 0) return;
+  const int head0 = kind == 0 ? 4 * (part - 2) : kind == 4 ? 4 * (part - 7) : 0, heads = kind == 3 ? 1 : kPartHeads;
+  const uint32_t bytes = heads * kHeadDim * sizeof(T);
+  if (lane == 0) mbar_arrive_expect_tx(bar, cnt * bytes);
+  __syncwarp();
+  if (lane < cnt)
+    bulk_g2s(smem_u32(s_rows[warp]) + lane * kPart,
+             static_cast<const T*>(p.rows[kind]) + (size_t)(t0 + lane) * p.stride[kind] + head0 * kHeadDim, bytes, bar);
+  // lane = (token sub, part l of its rows)
+  const bool live = sub < cnt;
+  const int t = t0 + sub;
+  const int pos = live && p.rot > 0 ? p.positions[t] : 0;
+  int64_t slot = live && cached ? p.slot_mapping[t] : -1;
+  if (slot >= 0 && (slot >> 7) >= p.n_pages) {
+    set_status(p.status, MSA_STATUS_BAD_SLOT);
+    slot = -1;
+  }
+  const bool known = pos >= 0 && pos < p.max_pos;
+  if (part == 2 && p.rot > 0 && live && !known) set_status(p.status, MSA_STATUS_BAD_SEQ);
+  // half pairs: lanes below h have partner chunks h apart (values are not turned)
+  const int h = p.interleaved || kind == 2 ? 0 : p.rot >> 4;
+  const int ca = l < h ? l : 2 * l, cb = l < h ? l + h : 2 * l + 1;
+  const bool turned = live && known && kind != 2 && (p.interleaved ? 16 * l < p.rot : l < h);
+  float c[8], s[8];
+  if (turned) {
+    const float* cs = p.cos_sin + (size_t)pos * p.rot + 8 * l;
+    load8(cs, c);
+    load8(cs + (p.rot >> 1), s);
+  }
+  if (!__all_sync(0xffffffffu, mbar_wait(bar, 0, WaitCtl{&s_abort, p.wait_ns}))) {
+    // nothing of the tile is written, and the copies in flight are waited for
+    if (lane == 0) set_status(p.status, MSA_STATUS_TIMEOUT);
+    mbar_wait_drain(bar, 0, p.wait_ns);
+    return;
+  }
+  const uint8_t* ra = s_rows[warp] + sub * kPart + 8 * ca * sizeof(T);
+  const uint8_t* rb = s_rows[warp] + sub * kPart + 8 * cb * sizeof(T);
+  auto rows = [&](int hd, float (&a)[8], float (&b)[8]) {
+    to_floats(Chunk<T>(ra + hd * kHeadDim * sizeof(T)), a);
+    to_floats(Chunk<T>(rb + hd * kHeadDim * sizeof(T)), b);
+    if (!turned) return;
+    if (h) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) turn(a[u], b[u], c[u], s[u]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        turn(a[2 * u], a[2 * u + 1], c[u], s[u]);
+        turn(b[2 * u], b[2 * u + 1], c[4 + u], s[4 + u]);
+      }
     }
-    if (row == 0 && p.rot > 0 && (my_pos < 0 || my_pos >= p.max_pos)) set_status(p.status, MSA_STATUS_BAD_SEQ);
-    // half pairs: lanes below h have partner chunks h apart (values are not turned)
-    const int h = p.interleaved || kind == 2 ? 0 : p.rot >> 4;
-    const int ca = l < h ? l : 2 * l, cb = l < h ? l + h : 2 * l + 1;
-    const bool turns = kind != 2 && (p.interleaved ? 16 * l < p.rot : l < h);
-    const T* src = static_cast<const T*>(p.rows[kind]) + (size_t)t0 * p.stride[kind] + head * kHeadDim;
-    const size_t stride = p.stride[kind];
-    Chunk<T> na = {}, nb = {};  // of the next four tokens
-    if (sub < cnt) {
-      na.load(src + sub * stride + 8 * ca);
-      nb.load(src + sub * stride + 8 * cb);
-    }
-    for (int i0 = 0; i0 < cnt; i0 += 4) {
-      const int i = i0 + sub, t = t0 + i;
-      const int pos = __shfl_sync(0xffffffffu, my_pos, i & 31);
-      const int64_t slot = __shfl_sync(0xffffffffu, my_slot, i & 31);
-      const bool live = i < cnt;
+  };
+  if (!cached) {
+    uint8_t* dst = (kind == 0 ? p.q8 + (size_t)t * kQHeads * kHeadDim : p.qi8 + (size_t)t * kIdxHeads * kIdxDim) + head0 * kHeadDim;
+#pragma unroll 1
+    for (int hd = 0; hd < kPartHeads; ++hd, dst += kHeadDim) {
       float a[8], b[8];
-      to_floats(na, a);
-      to_floats(nb, b);
-      if (i + 4 < cnt) {
-        na.load(src + (i + 4) * stride + 8 * ca);
-        nb.load(src + (i + 4) * stride + 8 * cb);
+      rows(hd, a, b);
+      if (live) {
+        *reinterpret_cast<uint2*>(dst + 8 * ca) = to_fp8x8(a);
+        *reinterpret_cast<uint2*>(dst + 8 * cb) = to_fp8x8(b);
       }
-      if (live && turns && pos >= 0 && pos < p.max_pos) {
-        const float* cs = p.cos_sin + (size_t)pos * p.rot + 8 * l;
-        float c[8], s[8];
-        load8(cs, c);
-        load8(cs + half, s);
-        if (h) {
-#pragma unroll
-          for (int u = 0; u < 8; ++u) turn(a[u], b[u], c[u], s[u]);
-        } else {
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            turn(a[2 * u], a[2 * u + 1], c[u], s[u]);
-            turn(b[2 * u], b[2 * u + 1], c[4 + u], s[4 + u]);
-          }
-        }
-      }
-      if (!cached) {
-        if (live) {
-          uint8_t* dst = kind == 0 ? p.q8 + ((size_t)t * kQHeads + head) * kHeadDim
-                                   : p.qi8 + ((size_t)t * kIdxHeads + head) * kIdxDim;
-          *reinterpret_cast<uint2*>(dst + 8 * ca) = to_fp8x8(a);
-          *reinterpret_cast<uint2*>(dst + 8 * cb) = to_fp8x8(b);
-        }
-        continue;
-      }
-      // maxima of the two 16-channel groups: the other chunk of group c / 2 is c ^ 1
-      float all_a, all_b;
-      const float ma = max_abs(a, all_a), mb = max_abs(b, all_b);
-      float ga = fmaxf(ma, mb), gb = ga;
-      if (h) {
-        const int xa = ca ^ 1, xb = cb ^ 1;  // (of lanes below h: held by lane c or c - h)
-        const int la = l < h ? (lane & 24) | (xa < h ? xa : xa - h) : lane, lb = l < h ? (lane & 24) | (xb < h ? xb : xb - h) : lane;
-        const float a1 = __shfl_sync(0xffffffffu, ma, la), a2 = __shfl_sync(0xffffffffu, mb, la);
-        const float b1 = __shfl_sync(0xffffffffu, ma, lb), b2 = __shfl_sync(0xffffffffu, mb, lb);
-        if (l < h) {
-          ga = fmaxf(ma, xa < h ? a1 : a2);
-          gb = fmaxf(mb, xb < h ? b1 : b2);
-        }
-      }
-      if (!live || slot < 0) continue;
-      const int off = (int)(slot & 127);
-      if (kind == 3) {
-        uint8_t* dst = p.idx_pool + (size_t)(slot >> 7) * kIdxPageBytes + off * kIdxDim;
-        *reinterpret_cast<uint2*>(dst + (((ca >> 1) ^ (off & 7)) << 4) + 8 * (ca & 1)) = to_fp8x8(a);
-        *reinterpret_cast<uint2*>(dst + (((cb >> 1) ^ (off & 7)) << 4) + 8 * (cb & 1)) = to_fp8x8(b);
-        continue;
-      }
-      const float s_enc = kind == 1 ? p.s_enc_k : p.s_enc_v;
-      const uint32_t sa = f32_to_e4m3(__fmul_rn(__fdiv_rn(ga, 6.0f), s_enc));
-      const uint32_t sb = f32_to_e4m3(__fmul_rn(__fdiv_rn(gb, 6.0f), s_enc));
-      uint8_t* codes = p.kv_pool + (size_t)(slot >> 7) * kKvPageBytes + head * kHeadBytes + (kind == 1 ? kOffKc : kOffVc) + off * 64;
-      const float fa = e4m3_to_f32(sa), fb = e4m3_to_f32(sb);
-      if (!(fmaxf(all_a, all_b) * s_enc < 1e30f) || all_a != all_a || all_b != all_b) {
-        const float most = fminf(1e30f / s_enc, 3e38f);
-        make_finite(a, most);
-        make_finite(b, most);
-      }
-      const uint32_t wa = code_word(a, s_enc, fa, fa > 0.f ? __frcp_rn(fa) : 0.f);
-      const uint32_t wb = code_word(b, s_enc, fb, fb > 0.f ? __frcp_rn(fb) : 0.f);
-      *reinterpret_cast<uint32_t*>(codes + (code_chunk_pos(ca >> 2, off) << 4) + 4 * (ca & 3)) = wa;
-      *reinterpret_cast<uint32_t*>(codes + (code_chunk_pos(cb >> 2, off) << 4) + 4 * (cb & 3)) = wb;
-      if ((ca & 1) == 0) scales[i * 8 + (ca >> 1)] = (uint8_t)sa;
-      if ((cb & 1) == 0) scales[i * 8 + (cb >> 1)] = (uint8_t)sb;
     }
-    if (kind == 1 || kind == 2) {  // lane = token: its eight scale bytes
-      __syncwarp();
-      if (my_slot >= 0) {
-        const uint2 sc = *reinterpret_cast<const uint2*>(scales + 8 * lane);
-        uint8_t* dst = p.kv_pool + (size_t)(my_slot >> 7) * kKvPageBytes + head * kHeadBytes +
-                       (kind == 1 ? kOffKs : kOffVs) + (my_slot & 127);
-#pragma unroll
-        for (int g = 0; g < 8; ++g) dst[g * kPageTokens] = (uint8_t)((g < 4 ? sc.x : sc.y) >> (8 * (g & 3)));
+    return;
+  }
+  const int off = (int)(slot & 127);
+  if (kind == 3) {
+    float a[8], b[8];
+    rows(0, a, b);
+    if (slot >= 0) {
+      uint8_t* dst = p.idx_pool + (size_t)(slot >> 7) * kIdxPageBytes + off * kIdxDim;
+      *reinterpret_cast<uint2*>(dst + (((ca >> 1) ^ (off & 7)) << 4) + 8 * (ca & 1)) = to_fp8x8(a);
+      *reinterpret_cast<uint2*>(dst + (((cb >> 1) ^ (off & 7)) << 4) + 8 * (cb & 1)) = to_fp8x8(b);
+    }
+    return;
+  }
+  const float s_enc = kind == 1 ? p.s_enc_k : p.s_enc_v;
+  uint8_t* head = p.kv_pool + (size_t)(slot >= 0 ? slot >> 7 : 0) * kKvPageBytes + (kind == 1 ? kOffKc : kOffVc);
+  const int wa = off * 64 + (code_chunk_pos(ca >> 2, off) << 4) + 4 * (ca & 3);
+  const int wb = off * 64 + (code_chunk_pos(cb >> 2, off) << 4) + 4 * (cb & 3);
+  // the other chunk of a 16-channel group is c ^ 1; of lanes below h lane c or c - h has it
+  const int xa = ca ^ 1, xb = cb ^ 1;
+  const int la = (lane & 24) | (l >= h ? l : xa < h ? xa : xa - h), lb = (lane & 24) | (l >= h ? l : xb < h ? xb : xb - h);
+  uint8_t* scales = s_scales[warp] + sub;
+#pragma unroll 1
+  for (int hd = 0; hd < kPartHeads; ++hd, head += kHeadBytes) {
+    float a[8], b[8];
+    rows(hd, a, b);
+    bool fine_a, fine_b;
+    const float ma = max_abs(a, s_enc, fine_a), mb = max_abs(b, s_enc, fine_b);
+    float ga = fmaxf(ma, mb), gb = ga;
+    if (h) {
+      const float a1 = __shfl_sync(0xffffffffu, ma, la), a2 = __shfl_sync(0xffffffffu, mb, la);
+      const float b1 = __shfl_sync(0xffffffffu, ma, lb), b2 = __shfl_sync(0xffffffffu, mb, lb);
+      if (l < h) {
+        ga = fmaxf(ma, xa < h ? a1 : a2);
+        gb = fmaxf(mb, xb < h ? b1 : b2);
       }
-      __syncwarp();
+    }
+    if (!(fine_a && fine_b)) {
+      const float most = fminf(1e30f / s_enc, 3e38f);
+      make_finite(a, most);
+      make_finite(b, most);
+    }
+    const uint32_t sa = f32_to_e4m3(__fmul_rn(sixth(ga), s_enc)), sb = f32_to_e4m3(__fmul_rn(sixth(gb), s_enc));
+    const uint32_t va = code_word(a, s_enc, e4m3_to_f32(sa), s_inv[sa]), vb = code_word(b, s_enc, e4m3_to_f32(sb), s_inv[sb]);
+    if (slot >= 0) {
+      *reinterpret_cast<uint32_t*>(head + wa) = va;
+      *reinterpret_cast<uint32_t*>(head + wb) = vb;
+    }
+    if ((ca & 1) == 0) scales[(hd * 8 + (ca >> 1)) * kTile] = (uint8_t)sa;
+    if ((cb & 1) == 0) scales[(hd * 8 + (cb >> 1)) * kTile] = (uint8_t)sb;
+  }
+  // the scale bytes: lane = (head, group) of the four tokens, as one word where they are consecutive
+  __syncwarp();
+  const uint32_t word = reinterpret_cast<const uint32_t*>(s_scales[warp])[lane];
+  const int64_t slot0 = __shfl_sync(0xffffffffu, slot, 0);
+  const bool run = __all_sync(0xffffffffu, slot == slot0 + sub && (slot0 & 3) == 0);
+  const size_t place = (size_t)(lane >> 3) * kHeadBytes + (kind == 1 ? kOffKs : kOffVs) + (lane & 7) * kPageTokens;
+  if (run) {
+    if (slot0 >= 0) *reinterpret_cast<uint32_t*>(p.kv_pool + (size_t)(slot0 >> 7) * kKvPageBytes + place + (slot0 & 127)) = word;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kTile; ++i) {
+      const int64_t si = __shfl_sync(0xffffffffu, slot, 8 * i);
+      if (si >= 0) p.kv_pool[(size_t)(si >> 7) * kKvPageBytes + place + (si & 127)] = (uint8_t)(word >> (8 * i));
     }
   }
 }
@@ -314,7 +356,6 @@ cudaError_t launch_rotary_insert(const msa_cache* c, const msa_rows* r, int n_to
     rp.stride[i] = strides[i];
   }
   rp.n_tokens = n_tokens;
-  rp.n_rows = r->q_idx ? 33 : 25;
   rp.cos_sin = cos_sin;
   rp.max_pos = max_pos;
   rp.rot = rot;
@@ -329,13 +370,9 @@ cudaError_t launch_rotary_insert(const msa_cache* c, const msa_rows* r, int n_to
   rp.q8 = q8;
   rp.qi8 = qi8;
   rp.status = c->status;
-  // the largest tile that still makes 48 warps per SM
-  rp.tile = 32;
-  while (rp.tile > 4 && (long long)n_tokens / rp.tile * rp.n_rows < 48ll * n_sm) rp.tile >>= 1;
-  const long long warps = ((long long)n_tokens + rp.tile - 1) / rp.tile * rp.n_rows;
-  long long blocks = (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
-  if (blocks > 64ll * n_sm) blocks = 64ll * n_sm;
-  const dim3 grid((unsigned)blocks), block(kRopeThreads);
+  rp.wait_ns = launch_settings().wait_ns;
+  const int per_block = kRopeThreads / 32 * kTile;
+  const dim3 grid((unsigned)((n_tokens + (long long)per_block - 1) / per_block), r->q_idx ? 9 : 7), block(kRopeThreads);
   if (r->dtype == MSA_DTYPE_F32) rotary_insert_kernel<float><<<grid, block, 0, stream>>>(rp);
   else if (r->dtype == MSA_DTYPE_BF16) rotary_insert_kernel<__nv_bfloat16><<<grid, block, 0, stream>>>(rp);
   else rotary_insert_kernel<__half><<<grid, block, 0, stream>>>(rp);
