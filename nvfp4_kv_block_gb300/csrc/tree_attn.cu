@@ -75,12 +75,12 @@ constexpr float kTreeMost = 49152.0f;  // largest sum of a chunk's weights, and 
 constexpr float kTreeUnset = 3e38f;    // shift of a row without a reference: a visible token's weight is infinite
 constexpr float kTreeLog2e = 1.4426950408889634f, kTreeLn2 = 0.6931471805599453f;
 
-// Weights of the partition: a page of a one-tile sequence, of a two-tile one,
-// the fixed part of a (sequence, KV head), and the least share of a CTA (at
-// least a page's weight, so that every CTA between a sequence's first and last
-// has pages of it).
-constexpr int kPageWeight1 = 2, kPageWeight2 = 4, kFixedWeight = 6, kLeastShare = 4;
-static_assert(kLeastShare >= kPageWeight2, "a share holds a page");
+// Weights of the partition, in units of 0.2 us: a page of a sequence with up to 8, 16,
+// 32 and 64 drafts (0.81, 1.01, 1.27 and 2.24 us per page of a CTA on 32K contexts), and
+// the fixed part of a (sequence, KV head).  The least share of a CTA is a page's
+// weight, so that every CTA between a sequence's first and last has pages of it.
+__host__ __device__ __forceinline__ int tree_page_weight(int n_q) { return n_q <= 8 ? 4 : n_q <= 16 ? 5 : n_q <= 32 ? 6 : 11; }
+constexpr int kFixedWeight = 10, kLeastShare1 = 6, kLeastShare2 = 11;
 
 // Copies of the query rows in a one-tile segment's 128 rows: with few rows every
 // warp quad (32 lanes of tensor memory) gets the same rows and its own share of a
@@ -228,7 +228,7 @@ __device__ __forceinline__ SeqWork seq_work(const TreeParams& p, int b) {
   w.first = w.ctx / kPageTokens;
   w.chosen = w.first;
   w.n_vis = 0;
-  w.pw = w.s.n_q > 32 ? kPageWeight2 : kPageWeight1;
+  w.pw = tree_page_weight(w.s.n_q);
   if (!w.s.ok || w.s.n_q == 0) return w;
   if (p.sel) {
     const int n = min(max(p.n_sel[b], 0), kSelStride);
@@ -243,6 +243,8 @@ __device__ __forceinline__ SeqWork seq_work(const TreeParams& p, int b) {
   w.n_vis = w.chosen + (w.s.seq_len - 1) / kPageTokens - w.first + 1;
   return w;
 }
+
+static_assert(sizeof(SeqWork) <= 64, "beside the scan");
 
 // One code word (8 channels) -> 8 f16 values v8 2^-8, through the scale's table:
 // hi = E4M3 magnitude bits >> 1, lo = their last bit << 7, per E2M1 magnitude.
@@ -283,6 +285,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
   auto rec = [&](int k) { return reinterpret_cast<SegRec*>(smem + kOffRecs + 64 * (k % kRecs)); };
   int2* s_info = reinterpret_cast<int2*>(smem + kOffInfo);
   long long* s_scan = reinterpret_cast<long long*>(smem + kOffScan);  // [24] warp sums, then total, start b, its offset
+  SeqWork* s_first = reinterpret_cast<SeqWork*>(smem + kOffScan + 32 * 8);  // the first sequence of the range
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   // ---- prologue ------------------------------------------------------------------
@@ -350,9 +353,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
   bool wide = false;  // some sequence has two row tiles
   {
     long long mine = 0;
+    SeqWork last{};
     const int b0 = min(tid * per, p.n_seqs), b1 = min(b0 + per, p.n_seqs);
     for (int b = b0; b < b1; ++b) {
       const SeqWork w = seq_work(p, b);
+      last = w;
       if (!w.s.ok && blockIdx.x == 0) set_status(p.status, MSA_STATUS_BAD_SEQ);
       if (w.n_vis > 0) mine += (long long)kKvHeads * (w.pw * w.n_vis + kFixedWeight);
       wide |= w.n_vis > 0 && w.s.n_q > 32;
@@ -364,24 +369,25 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       if (lane >= o) incl += v;
     }
     if (lane == 31) s_scan[warp] = incl;
-    __syncthreads();
+    wide = __syncthreads_or(wide);
     long long before = 0, total = 0;
     for (int i = 0; i < kTreeThreads / 32; ++i) {
       if (i < warp) before += s_scan[i];
       total += s_scan[i];
     }
-    const int G = (int)min((long long)gridDim.x, max(1ll, total / kLeastShare));
+    const int G = (int)min((long long)gridDim.x, max(1ll, total / (wide ? kLeastShare2 : kLeastShare1)));
     const long long lo = blockIdx.x < G ? total * blockIdx.x / G : total;
     const long long mine0 = before + incl - mine;
     if (mine > 0 && lo >= mine0 && lo < mine0 + mine) {  // the first sequence of the range is in this share
       s_scan[25] = b0;
       s_scan[26] = mine0;
+      *s_first = last;  // (of use if the share is this sequence alone)
     }
     if (tid == 0) s_scan[24] = total;
-    wide = __syncthreads_or(wide);
+    __syncthreads();
   }
   const long long total = s_scan[24];
-  const int G = (int)min((long long)gridDim.x, max(1ll, total / kLeastShare));
+  const int G = (int)min((long long)gridDim.x, max(1ll, total / (wide ? kLeastShare2 : kLeastShare1)));
   const bool idle = (int)blockIdx.x >= G || total == 0;
 
   // registers: 128 threads x 64 + 256 x 120 + 384 x 56 of the launch's 768 x 80
@@ -395,7 +401,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       const long long lo = total * blockIdx.x / G, hi = total * (blockIdx.x + 1) / G;
       long long off = s_scan[26];
       for (int b = (int)s_scan[25]; ok && b < p.n_seqs && off < hi; ++b) {
-        const SeqWork w = seq_work(p, b);
+        const SeqWork w = per == 1 && b == (int)s_scan[25] ? *s_first : seq_work(p, b);
         if (w.n_vis == 0) continue;
         const long long wg = (long long)w.pw * w.n_vis + kFixedWeight;
         // the selection, one entry per lane: its place among the chosen ones
@@ -993,24 +999,36 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
   if (desc == 0) return;
   if (h == 0 && lane == 0) p.row_desc[tg] = 0;  // at rest for the next call
   const int c0 = desc & 255, parts = (desc >> 8) & 4095, row = 4 * (desc >> 20) + h;
+  auto slot = [&](int i) { return (size_t)(2 * (c0 + i) + (i == 0)) * p.part_rows + row; };
   float M = -INFINITY;
   for (int i = lane; i < parts; i += 32) {
-    const float2 ml = p.part_ml[(size_t)(2 * (c0 + i) + (i == 0)) * p.part_rows + row];
+    const float2 ml = p.part_ml[slot(i)];
     if (ml.y > 0.f) M = fmaxf(M, ml.x);
   }
   M = warp_max_f32(M);
   float L = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = 0; i < parts; ++i) {
-    const size_t at = (size_t)(2 * (c0 + i) + (i == 0)) * p.part_rows + row;
-    const float2 ml = p.part_ml[at];
-    const float4 x = reinterpret_cast<const float4*>(p.part_o + at * kHeadDim)[lane];
-    const float w = ml.y > 0.f ? fast_exp2(ml.x - M) : 0.f;
-    L = fmaf(ml.y, w, L);
-    o.x = fmaf(x.x, w, o.x);
-    o.y = fmaf(x.y, w, o.y);
-    o.z = fmaf(x.z, w, o.z);
-    o.w = fmaf(x.w, w, o.w);
+  for (int i0 = 0; i0 < parts; i0 += 8) {  // eight parts' loads at a time
+    float4 x[8];
+    float w[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      w[u] = 0.f;
+      if (i0 + u < parts) {
+        const float2 ml = p.part_ml[slot(i0 + u)];
+        x[u] = reinterpret_cast<const float4*>(p.part_o + slot(i0 + u) * kHeadDim)[lane];
+        w[u] = ml.y > 0.f ? fast_exp2(ml.x - M) : 0.f;
+        L = fmaf(ml.y, w[u], L);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      o.x = fmaf(x[u].x, w[u], o.x);
+      o.y = fmaf(x[u].y, w[u], o.y);
+      o.z = fmaf(x[u].z, w[u], o.z);
+      o.w = fmaf(x[u].w, w[u], o.w);
+    }
   }
   const float inv = L > 0.f ? p.out_scale / L : 0.f;
   const size_t at = (size_t)(tg >> 2) * kQHeads + kGqa * (tg & 3) + h;
