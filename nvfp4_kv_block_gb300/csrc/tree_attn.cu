@@ -245,6 +245,8 @@ __device__ __forceinline__ SeqWork seq_work(const TreeParams& p, int b) {
 }
 
 static_assert(sizeof(SeqWork) <= 64, "beside the scan");
+// Start of CTA c's range of total = G quota + extra units.
+__device__ __forceinline__ long long range_start(long long quota, int extra, int c) { return c * quota + min(c, extra); }
 
 // One code word (8 channels) -> 8 f16 values v8 2^-8, through the scale's table:
 // hi = E4M3 magnitude bits >> 1, lo = their last bit << 7, per E2M1 magnitude.
@@ -376,7 +378,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       total += s_scan[i];
     }
     const int G = (int)min((long long)gridDim.x, max(1ll, total / (wide ? kLeastShare2 : kLeastShare1)));
-    const long long lo = blockIdx.x < G ? total * blockIdx.x / G : total;
+    const long long lo = (int)blockIdx.x < G ? range_start(total / G, (int)(total % G), blockIdx.x) : total;
     const long long mine0 = before + incl - mine;
     if (mine > 0 && lo >= mine0 && lo < mine0 + mine) {  // the first sequence of the range is in this share
       s_scan[25] = b0;
@@ -398,7 +400,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
     int e = 0, k = 0;
     bool ok = true;
     if (!idle) {
-      const long long lo = total * blockIdx.x / G, hi = total * (blockIdx.x + 1) / G;
+      const long long quota = total / G;
+      const int extra = (int)(total - quota * G);
+      const long long lo = range_start(quota, extra, blockIdx.x), hi = range_start(quota, extra, blockIdx.x + 1);
       long long off = s_scan[26];
       for (int b = (int)s_scan[25]; ok && b < p.n_seqs && off < hi; ++b) {
         const SeqWork w = per == 1 && b == (int)s_scan[25] ? *s_first : seq_work(p, b);
@@ -431,10 +435,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
         for (int g = 0; ok && g < kKvHeads; ++g, off += wg) {
           // page i starts at weight off + kFixedWeight + i pw; it belongs to the range that holds its start
           const long long base = off + kFixedWeight;
-          const int p_lo = (int)min((long long)w.n_vis, max(0ll, (lo - base + w.pw - 1) / w.pw));
-          const int p_hi = (int)min((long long)w.n_vis, max(0ll, (hi - base + w.pw - 1) / w.pw));
-          const int a = lo <= base ? 0 : p_lo;
-          const int z = hi <= base ? 0 : p_hi;
+          auto page_at = [&](long long x) {  // the first page that starts at weight x or behind it
+            if (x <= base) return 0;
+            return x - base > (long long)w.n_vis * w.pw ? w.n_vis : ((int)(x - base) + w.pw - 1) / w.pw;
+          };
+          const int a = page_at(lo), z = page_at(hi);
           if (a >= z) continue;
           if (!twait(bar(kBRecEmpty + k % kRecs), ((k / kRecs) & 1) ^ 1, wc)) {
             ok = false;
@@ -453,7 +458,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
           if (!whole && a == 0) {
             // the first part tells the merge who has the others
             const long long last = base + (long long)(w.n_vis - 1) * w.pw;
-            const int c_last = (int)(((last + 1) * G - 1) / total);
+            const long long big = extra * (quota + 1);  // the first `extra` CTAs have one unit more
+            const int c_last = last < big ? (int)(last / (quota + 1)) : extra + (int)((last - big) / quota);
             const int parts = c_last - (int)blockIdx.x + 1;
             for (int i = lane; i < w.s.n_q; i += 32)
               p.row_desc[(size_t)(w.s.q0 + i) * kKvHeads + g] = (int)blockIdx.x | parts << 8 | i << 20;
@@ -988,53 +994,65 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
 }
 
 // Rows whose pages were cut across CTAs: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
-// One warp per (draft, KV head, query head), lane = 4 channels; parts in CTA order.
+// One CTA per (draft, KV head): two warps per query head, each with every other part, lane =
+// 4 channels.  A latency chain: a descriptor, then up to 12 parts' loads of a warp at once
+// (relative to their own maximum; the two warps' halves join in shared memory).
+constexpr int kMergeParts = 12;
 __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeParams p) {
-  const int lane = threadIdx.x & 31, h = (threadIdx.x >> 5) & 3;
-  const long long tg = (long long)blockIdx.x * 2 + (threadIdx.x >> 7);  // (token, KV head)
+  __shared__ float4 s_o[4][32];
+  __shared__ float2 s_ml[4];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = warp & 3, half = warp >> 2;
+  const int tg = blockIdx.x;  // (token, KV head)
   pdl_wait();
-  int desc = 0;
-  if (tg < (long long)p.n_q_total * kKvHeads) desc = p.row_desc[tg];
+  const int desc = p.row_desc[tg];
   __syncthreads();
   if (desc == 0) return;
-  if (h == 0 && lane == 0) p.row_desc[tg] = 0;  // at rest for the next call
+  if (threadIdx.x == 0) p.row_desc[tg] = 0;  // at rest for the next call
   const int c0 = desc & 255, parts = (desc >> 8) & 4095, row = 4 * (desc >> 20) + h;
-  auto slot = [&](int i) { return (size_t)(2 * (c0 + i) + (i == 0)) * p.part_rows + row; };
-  float M = -INFINITY;
-  for (int i = lane; i < parts; i += 32) {
-    const float2 ml = p.part_ml[slot(i)];
-    if (ml.y > 0.f) M = fmaxf(M, ml.x);
-  }
-  M = warp_max_f32(M);
-  float L = 0.f;
+  float M = -INFINITY, L = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < parts; i0 += 8) {  // eight parts' loads at a time
-    float4 x[8];
-    float w[8];
+  for (int i0 = half; i0 < parts; i0 += 2 * kMergeParts) {
+    float4 x[kMergeParts];
+    float2 ml = make_float2(-INFINITY, 0.f);  // lane u: part i0 + 2 u
+    auto slot = [&](int u) { return (size_t)(2 * (c0 + i0 + 2 * u) + (i0 + 2 * u == 0)) * p.part_rows + row; };
+    if (lane < kMergeParts && i0 + 2 * lane < parts) ml = p.part_ml[slot(lane)];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
+    for (int u = 0; u < kMergeParts; ++u) {
       x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      w[u] = 0.f;
-      if (i0 + u < parts) {
-        const float2 ml = p.part_ml[slot(i0 + u)];
-        x[u] = reinterpret_cast<const float4*>(p.part_o + slot(i0 + u) * kHeadDim)[lane];
-        w[u] = ml.y > 0.f ? fast_exp2(ml.x - M) : 0.f;
-        L = fmaf(ml.y, w[u], L);
-      }
+      if (i0 + 2 * u < parts) x[u] = reinterpret_cast<const float4*>(p.part_o + slot(u) * kHeadDim)[lane];
     }
+    const float top = fmaxf(M, warp_max_f32(ml.y > 0.f ? ml.x : -INFINITY));
+    const float f = M > -INFINITY ? fast_exp2(M - top) : 0.f, w = ml.y > 0.f ? fast_exp2(ml.x - top) : 0.f;
+    M = top;
+    L *= f;
+    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      o.x = fmaf(x[u].x, w[u], o.x);
-      o.y = fmaf(x[u].y, w[u], o.y);
-      o.z = fmaf(x[u].z, w[u], o.z);
-      o.w = fmaf(x[u].w, w[u], o.w);
+    for (int u = 0; u < kMergeParts; ++u) {
+      const float wu = __shfl_sync(0xffffffffu, w, u);
+      L = fmaf(__shfl_sync(0xffffffffu, ml.y, u), wu, L);
+      o.x = fmaf(x[u].x, wu, o.x);
+      o.y = fmaf(x[u].y, wu, o.y);
+      o.z = fmaf(x[u].z, wu, o.z);
+      o.w = fmaf(x[u].w, wu, o.w);
     }
   }
+  if (half == 1) {
+    s_o[h][lane] = o;
+    if (lane == 0) s_ml[h] = make_float2(M, L);
+  }
+  __syncthreads();
+  if (half == 1) return;
+  const float2 b = s_ml[h];
+  const float4 y = s_o[h][lane];
+  const float top = fmaxf(M, b.x);
+  const float wa = L > 0.f ? fast_exp2(M - top) : 0.f, wb = b.y > 0.f ? fast_exp2(b.x - top) : 0.f;
+  L = L * wa + b.y * wb;
+  o = make_float4(o.x * wa + y.x * wb, o.y * wa + y.y * wb, o.z * wa + y.z * wb, o.w * wa + y.w * wb);
   const float inv = L > 0.f ? p.out_scale / L : 0.f;
   const size_t at = (size_t)(tg >> 2) * kQHeads + kGqa * (tg & 3) + h;
   *reinterpret_cast<uint2*>(p.out + at * kHeadDim + 4 * lane) =
       make_uint2(pack16(o.x * inv, o.y * inv, p.out_f16), pack16(o.z * inv, o.w * inv, p.out_f16));
-  if (p.lse && lane == 0) p.lse[at] = L > 0.f ? (M - kTreeBias + log2f(L)) * kTreeLn2 : -INFINITY;
+  if (p.lse && lane == 0) p.lse[at] = L > 0.f ? (top - kTreeBias + log2f(L)) * kTreeLn2 : -INFINITY;
 }
 
 int tree_rows(int n_q_total) { return n_q_total < kTreeMaxDrafts ? kGqa * n_q_total : kGqa * kTreeMaxDrafts; }
@@ -1088,7 +1106,7 @@ cudaError_t launch_tree_attn(const msa_cache* c, const uint8_t* q, float softmax
   const int most = n_sm < kTreeCtas ? n_sm : kTreeCtas;
   e = launch_pdl(tree_attn_kernel, dim3(most), dim3(kTreeThreads), kTreeSmem, stream, tp);
   if (e != cudaSuccess) return e;
-  return launch_pdl(tree_merge_kernel, dim3((unsigned)(((long long)n_q_total * kKvHeads + 1) / 2)), dim3(256), 0, stream, tp);
+  return launch_pdl(tree_merge_kernel, dim3((unsigned)(n_q_total * kKvHeads)), dim3(256), 0, stream, tp);
 }
 
 }  // namespace msa
