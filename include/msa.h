@@ -453,15 +453,18 @@ int msa_read_kv(const msa_cache* cache, const int64_t* slot_mapping, int32_t n_t
  *   lse         fp32 [n_q_total][16] out or NULL: natural-log sum of exp of the row's
  *               logits (-inf where it sees nothing).
  *   ws, ws_bytes scratch of at least msa_tree_attn_workspace_bytes(n_q_total) bytes,
- *               16-byte aligned, ZEROED before its first use (every call that does
- *               not time out leaves the words that have to be zero so).  Calls
- *               sharing a workspace must not overlap on the GPU.
+ *               16-byte aligned, ZEROED before its first use (every call leaves the
+ *               words that have to be zero so; calls of different sizes may share
+ *               one).  Calls sharing a workspace must not overlap on the GPU.
  * Rows behind the last sequence (q_start_loc[n_seqs] .. n_q_total - 1) are left as
  * they were.  Operands as msa_sparse_attn_decode; the weights 2^x are rounded to f16
  * (2^-12 relative) before they meet the values, everything else is fp32; rows are
  * summed in an order that depends on the call's sizes only.  A physical page outside
  * the pool sets MSA_STATUS_BAD_PAGE and its tokens are not seen.  A cache scale byte
  * of 0x7F or 0xFF (no number, never written by the library) counts as zero.
+ * A query byte of 0x7F or 0xFF makes its row's out and lse NaN.  Rows that two
+ * sequences claim (q_start_loc not ascending) hold numbers of no meaning.
+ * softmax_scale > 0, and softmax_scale / s_enc_k times 2^26 finite.
  * Limits: n_seqs <= 4096, n_q_total <= 65535.  Two launches, both programmatic
  * dependents of the kernel before them.
  */

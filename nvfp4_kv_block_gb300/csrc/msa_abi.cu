@@ -370,6 +370,8 @@ int msa_tree_attn(const msa_cache* cache, const uint8_t* q, int32_t n_q_heads, f
   if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(ws) |
        reinterpret_cast<uintptr_t>(cache->kv_pool)) & 15)
     return MSA_ERR_INVALID_ARG;
+  // (the largest score, 128 products of 448 x 448, has to be a finite number)
+  if (!isfinite(softmax_scale / cache->s_enc_k * 128.f * 448.f * 448.f * 2.f)) return MSA_ERR_INVALID_ARG;
   if (ws_bytes < msa_tree_attn_workspace_bytes(n_q_total)) return MSA_ERR_WORKSPACE_TOO_SMALL;
   return launched(msa::launch_tree_attn(cache, q, softmax_scale, block_table, max_pages, seq_lens, q_start_loc, n_seqs,
                                         n_q_total, tree_mask, sel, n_sel, dtype, out, lse, ws,

@@ -708,8 +708,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = vis >> i & 1 ? v[i] : 0xFF800000u;
             }
+            float sh = shift;
             for (;;) {
-              const uint64_t shift2 = pair64(__float_as_uint(shift), __float_as_uint(shift));
+              const uint64_t shift2 = pair64(__float_as_uint(sh), __float_as_uint(sh));
               uint64_t sums[2] = {0, 0};
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
@@ -734,6 +735,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
                 f = fast_exp2(next - shift);  // (0 for the first: shift is kTreeUnset)
                 shift = next;
                 l *= f;
+                // weighed again as differences from the maximum: no weight above 2^kTreeBias
+                // whatever the product's rounding, so that a chunk is weighed twice at most
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) - top);
+                sh = kTreeBias;
               }
               rescale(c, j >= 2, f);
             }
@@ -771,7 +777,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
         L = 0.f;
         for (int i = 0; i < copies; ++i) {
           const float2 a = ml[row + i * gap], b = ml[128 + row + i * gap];
-          const float wa = a.y > 0.f ? fast_exp2(a.x - m) : 0.f, wb = b.y > 0.f ? fast_exp2(b.x - m) : 0.f;
+          const float wa = a.y != 0.f ? fast_exp2(a.x - m) : 0.f, wb = b.y != 0.f ? fast_exp2(b.x - m) : 0.f;
           L = fmaf(a.y, wa, fmaf(b.y, wb, L));
           if (i == copy) {
             w0 = wa;
@@ -782,53 +788,60 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       const size_t at0 = (size_t)r.q0 * kQHeads + kGqa * r.g;  // row i of the segment: + 16 (i / 4) + i % 4
       auto store4 = [&](int i, int ch, float Li, float a, float b, float c, float d) {
         if (r.slot < 0) {
-          const float inv = Li > 0.f ? p.out_scale / Li : 0.f;
+          const float inv = p.out_scale / Li;  // (a NaN of the query stays one)
           uint2 x = make_uint2(pack16(a * inv, b * inv, p.out_f16), pack16(c * inv, d * inv, p.out_f16));
-          if (!(Li > 0.f)) x = make_uint2(0u, 0u);
+          if (Li == 0.f) x = make_uint2(0u, 0u);
           *reinterpret_cast<uint2*>(p.out + (at0 + (size_t)(i >> 2) * kQHeads + (i & 3)) * kHeadDim + ch) = x;
         } else {
           *reinterpret_cast<float4*>(p.part_o + ((size_t)r.slot * p.part_rows + i) * kHeadDim + ch) =
-              Li > 0.f ? make_float4(a, b, c, d) : make_float4(0.f, 0.f, 0.f, 0.f);
+              Li != 0.f ? make_float4(a, b, c, d) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
       };
       tc_fence_after();
       if (copies > 1) {
-        // set s joins channels 64 s .. of both accumulators, 16 at a time, across the warps' copies
-        float* xb = reinterpret_cast<float*>(smem + kOffQ + 16384 + 8192 * set);  // [128 lanes][16], chunks swizzled
+        // set s joins channels 64 s .. of both accumulators across the warps' copies: as many groups
+        // of 16 channels at a time as the set's 8 KB hold (all four up to two drafts)
+        const int parts = n_rows * copies, ush = parts <= 32 ? 2 : parts <= 64 ? 1 : 0, units = 1 << ush;
+        const int me = copy * n_rows + row;  // (with a row)
+        float* xb = reinterpret_cast<float*>(smem + kOffQ + 16384 + 8192 * set);  // [units][parts][16], chunks swizzled
         float2* rows = reinterpret_cast<float2*>(smem + kOffRow) + 64 * set;
-        if (copy == 0) rows[row] = make_float2(m, L);
+        if (copy == 0 && mine) rows[row] = make_float2(m, L);
 #pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          const int ch = 64 * set + 16 * q;
-          uint32_t u[16], v[16];
-          tmem_ld32x32b_x16(tl + kTmemO + ch, u);
-          if (any1) tmem_ld32x32b_x16(tl + kTmemO + 128 + ch, v);
-          tmem_wait_ld();
-          float x[16];
+        for (int q = 0; q < 4; q += units) {
+          if (q > 0) named_barrier_sync(1 + set, 128);
+          if (busy)
+#pragma unroll 1
+            for (int un = 0; un < units; ++un) {
+              uint32_t u[16], v[16];
+              tmem_ld32x32b_x16(tl + kTmemO + 64 * set + 16 * (q + un), u);
+              if (any1) tmem_ld32x32b_x16(tl + kTmemO + 128 + 64 * set + 16 * (q + un), v);
+              tmem_wait_ld();
+              if (!mine) continue;
+              float x[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            x[i] = w0 > 0.f ? __uint_as_float(u[i]) * w0 : 0.f;
-            if (any1 && w1 > 0.f) x[i] = fmaf(__uint_as_float(v[i]), w1, x[i]);
-          }
+              for (int i = 0; i < 16; ++i) {
+                x[i] = w0 > 0.f ? __uint_as_float(u[i]) * w0 : 0.f;
+                if (any1 && w1 > 0.f) x[i] = fmaf(__uint_as_float(v[i]), w1, x[i]);
+              }
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<float4*>(xb + 16 * lrow + 4 * (i ^ (lrow >> 1 & 3))) =
-                make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<float4*>(xb + 16 * (un * parts + me) + 4 * (i ^ (me >> 1 & 3))) =
+                    make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            }
+          __syncwarp();
           named_barrier_sync(1 + set, 128);
-          for (int i = lrow; i < 4 * n_rows; i += 128) {
-            const int ri = i >> 2, c = i & 3;
+          for (int i = lrow; i < 4 * units * n_rows; i += 128) {  // (row, unit, chunk)
+            const int c = i & (4 * units - 1), ri = i >> (2 + ush), un = c >> 2;
             float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int cp = 0; cp < copies; ++cp) {
-              const int ln = ri + cp * gap;
-              const float4 z = *reinterpret_cast<const float4*>(xb + 16 * ln + 4 * (c ^ (ln >> 1 & 3)));
+            for (int ln = ri; ln < parts; ln += n_rows) {
+              const float4 z = *reinterpret_cast<const float4*>(xb + 16 * (un * parts + ln) + 4 * ((c & 3) ^ (ln >> 1 & 3)));
               y.x += z.x;
               y.y += z.y;
               y.z += z.z;
               y.w += z.w;
             }
-            store4(ri, ch + 4 * c, rows[ri].y, y.x, y.y, y.z, y.w);
+            store4(ri, 64 * set + 16 * q + 4 * c, rows[ri].y, y.x, y.y, y.z, y.w);
           }
-          named_barrier_sync(1 + set, 128);
         }
       } else if (busy) {
         // one tile: set s writes channels 64 s .. of both accumulators' sum; two tiles: all of its own
@@ -856,7 +869,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       }
       if (mine && copy == 0 && (two || set == 0)) {
         if (r.slot >= 0) p.part_ml[(size_t)r.slot * p.part_rows + row] = make_float2(m, L);
-        else if (p.lse) p.lse[at0 + (size_t)(row >> 2) * kQHeads + (row & 3)] = L > 0.f ? (m - kTreeBias + log2f(L)) * kTreeLn2 : -INFINITY;
+        else if (p.lse) p.lse[at0 + (size_t)(row >> 2) * kQHeads + (row & 3)] = L != 0.f ? (m - kTreeBias + log2f(L)) * kTreeLn2 : -INFINITY;
       }
       tc_fence_before();
       __syncwarp();
@@ -1021,8 +1034,8 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
       x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i0 + 2 * u < parts) x[u] = reinterpret_cast<const float4*>(p.part_o + slot(u) * kHeadDim)[lane];
     }
-    const float top = fmaxf(M, warp_max_f32(ml.y > 0.f ? ml.x : -INFINITY));
-    const float f = M > -INFINITY ? fast_exp2(M - top) : 0.f, w = ml.y > 0.f ? fast_exp2(ml.x - top) : 0.f;
+    const float top = fmaxf(M, warp_max_f32(ml.y != 0.f ? ml.x : -INFINITY));
+    const float f = M > -INFINITY ? fast_exp2(M - top) : 0.f, w = ml.y != 0.f ? fast_exp2(ml.x - top) : 0.f;
     M = top;
     L *= f;
     o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
@@ -1045,24 +1058,27 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
   const float2 b = s_ml[h];
   const float4 y = s_o[h][lane];
   const float top = fmaxf(M, b.x);
-  const float wa = L > 0.f ? fast_exp2(M - top) : 0.f, wb = b.y > 0.f ? fast_exp2(b.x - top) : 0.f;
+  const float wa = L != 0.f ? fast_exp2(M - top) : 0.f, wb = b.y != 0.f ? fast_exp2(b.x - top) : 0.f;
   L = L * wa + b.y * wb;
   o = make_float4(o.x * wa + y.x * wb, o.y * wa + y.y * wb, o.z * wa + y.z * wb, o.w * wa + y.w * wb);
-  const float inv = L > 0.f ? p.out_scale / L : 0.f;
+  const float inv = L != 0.f ? p.out_scale / L : 0.f;  // (a NaN of the query stays one)
   const size_t at = (size_t)(tg >> 2) * kQHeads + kGqa * (tg & 3) + h;
   *reinterpret_cast<uint2*>(p.out + at * kHeadDim + 4 * lane) =
       make_uint2(pack16(o.x * inv, o.y * inv, p.out_f16), pack16(o.z * inv, o.w * inv, p.out_f16));
-  if (p.lse && lane == 0) p.lse[at] = L > 0.f ? (top - kTreeBias + log2f(L)) * kTreeLn2 : -INFINITY;
+  if (p.lse && lane == 0) p.lse[at] = L != 0.f ? (top - kTreeBias + log2f(L)) * kTreeLn2 : -INFINITY;
 }
 
 int tree_rows(int n_q_total) { return n_q_total < kTreeMaxDrafts ? kGqa * n_q_total : kGqa * kTreeMaxDrafts; }
-size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+// The descriptors first, at a size of their own: the words that have to be zero between
+// calls are in one place whatever the sizes of the calls that share a workspace.
+constexpr size_t kDescBytes = (size_t)65536 * kKvHeads * sizeof(int);
+size_t ml_bytes(size_t rows) { return (2 * kTreeCtas * rows * sizeof(float2) + 255) / 256 * 256; }
 
 }  // namespace
 
 size_t tree_attn_workspace_bytes(int n_q_total) {
   const size_t rows = tree_rows(n_q_total);
-  return round256((size_t)n_q_total * kKvHeads * 4) + round256(2 * kTreeCtas * rows * 8) + 2 * kTreeCtas * rows * kHeadDim * 4;
+  return kDescBytes + ml_bytes(rows) + 2 * kTreeCtas * rows * kHeadDim * sizeof(float);
 }
 
 cudaError_t launch_tree_attn(const msa_cache* c, const uint8_t* q, float softmax_scale, const int* block_table,
@@ -1097,9 +1113,9 @@ cudaError_t launch_tree_attn(const msa_cache* c, const uint8_t* q, float softmax
   tp.part_rows = tree_rows(n_q_total);
   uint8_t* w = static_cast<uint8_t*>(ws);
   tp.row_desc = reinterpret_cast<int*>(w);
-  w += round256((size_t)n_q_total * kKvHeads * 4);
+  w += kDescBytes;
   tp.part_ml = reinterpret_cast<float2*>(w);
-  w += round256((size_t)2 * kTreeCtas * tp.part_rows * 8);
+  w += ml_bytes(tp.part_rows);
   tp.part_o = reinterpret_cast<float*>(w);
   tp.status = c->status;
   tp.wait_ns = launch_settings().wait_ns;

@@ -341,6 +341,103 @@ def test_drafts_written_selected_attended_and_read_back():
     assert cache.read_status() == 0
 
 
+@pytest.mark.parametrize("scale", [1e6, 1e9, 1e25])
+def test_scores_far_beyond_fp32_steps(scale):
+    """Scores whose rounding alone exceeds f16's range of weights: the largest key takes all."""
+    seqs = [(3000, 1), (700, 9), (500, 40)]
+    b = Batch(seqs, 18)
+    cache, q, bt, lens, qsl = b.device()
+    bufs = ops.TreeBuffers(b.T, len(seqs), F16)
+    ops.tree_attn(cache, q, bt, lens, qsl, bufs, softmax_scale=scale)
+    torch.cuda.synchronize()
+    out, sure = bufs.out.double().cpu().numpy(), 0
+    qv = formats.decode_e4m3(b.q8)
+    for s, (ctx, n) in enumerate(seqs):
+        k8, v8 = zip(*(tree.page_operands(b.pool[b.bt[s, i]]) for i in range(-(-(ctx + n) // 128))))
+        k, v = (formats.decode_e4m3(np.concatenate(x)) for x in (k8, v8))
+        for j in range(n):
+            for h in range(16):
+                row, keys = qv[b.qsl[s] + j, h], k[: ctx + j + 1, h // 4]
+                z = keys @ row
+                first, second = np.sort(z)[[-1, -2]]
+                # the scores' own rounding, and then the gap has to leave the second nothing (2^-30)
+                if (first - second - 260 * 2.0**-24 * (np.abs(keys) @ np.abs(row)).max()) * scale / S_ENC_K < 21:
+                    continue
+                sure += 1
+                want = v[np.argmax(z), h // 4] / float(np.float32(S_ENC_V))
+                got = out[b.qsl[s] + j, h]
+                # the weight 2^8 is exact; its sum and the scale 256 / s_enc round once each, then the type
+                assert np.all(np.abs(got - want) <= np.abs(want) * (2.0**-11 + 2.0**-21) + 2.0**-24), (s, j, h)
+    assert sure > 100 and torch.isfinite(bufs.lse).all() and cache.read_status() == 0
+
+
+def test_scores_near_zero_are_a_mean():
+    b = Batch([(1000, 3)], 19)
+    cache, q, bt, lens, qsl = b.device()
+    bufs = ops.TreeBuffers(3, 1, F16)
+    ops.tree_attn(cache, q, bt, lens, qsl, bufs, softmax_scale=1e-30)
+    torch.cuda.synchronize()
+    _, v8 = zip(*(tree.page_operands(b.pool[b.bt[0, i]]) for i in range(8)))
+    v = formats.decode_e4m3(np.concatenate(v8)) / float(np.float32(S_ENC_V))
+    for j in range(3):
+        m, size = v[: 1001 + j].mean(0), np.abs(v[: 1001 + j]).mean(0)
+        tol = (2.0**-11 + 2004 * 2.0**-24) * size + 2.0**-11 * np.abs(m) + 2.0**-24
+        assert np.all(np.abs(bufs.out[j].double().cpu().numpy() - m.repeat(4, 0)) <= tol.repeat(4, 0))
+
+
+def test_a_query_that_is_no_number_stays_so():
+    b = Batch([(2500, 3), (90, 2), (400, 40)], 20)
+    b.q8[1, 5, 17] = 0x7F
+    b.q8[4, 0, 0] = 0xFF
+    b.q8[20, 15, 127] = 0x7F
+    dev = b.device()
+    out, lse, cache = b.run(F16, cache_dev=dev)
+    bad = torch.zeros((b.T, 16), dtype=torch.bool, device=DEV)
+    bad[1, 5] = bad[4, 0] = bad[20, 15] = True
+    assert torch.equal(out.isnan().all(-1), bad) and torch.equal(out.isnan().any(-1), bad)
+    assert torch.equal(lse.isnan(), bad) and cache.read_status() == 0
+
+
+def test_calls_of_different_sizes_share_a_workspace():
+    small, large = Batch([(5000, 2)], 21), Batch([(4000, 40), (3000, 30)], 22)
+    bufs = [ops.TreeBuffers(x.T, len(x.seqs), F16) for x in (small, large)]
+    bufs[0].ws = bufs[1].ws
+    for x, y in ((small, bufs[0]), (large, bufs[1]), (small, bufs[0]), (large, bufs[1])):
+        out, lse, _ = x.run(F16, bufs=y)
+        x.check(out, lse)
+
+
+def test_another_stream_than_the_tensors_own():
+    b = Batch([(2000, 4), (100, 60)], 23)
+    dev = b.device()
+    bufs = ops.TreeBuffers(b.T, 2, F16)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        ops.tree_attn(*dev, bufs)
+    torch.cuda.current_stream().wait_stream(side)
+    b.dtype = F16
+    b.check(bufs.out, bufs.lse)
+
+
+def test_two_calls_at_once_with_a_workspace_each():
+    """Both kernels want every SM: their CTAs take turns, and neither waits for the other's."""
+    batches = [Batch([(9000, 20), (50, 3)], 24), Batch([(7000, 1), (300, 64), (2000, 10)], 25)]
+    devs = [b.device() for b in batches]
+    bufs = [ops.TreeBuffers(b.T, len(b.seqs), F16) for b in batches]
+    streams = [torch.cuda.Stream() for _ in batches]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for d, u, s in zip(devs, bufs, streams):
+            with torch.cuda.stream(s):
+                ops.tree_attn(*d, u)
+    torch.cuda.synchronize()
+    for b, d, u in zip(batches, devs, bufs):
+        b.dtype = F16
+        b.check(u.out, u.lse)
+        assert d[0].read_status() == 0
+
+
 def test_refusals():
     b = Batch([(300, 2)], 17)
     cache, q, bt, lens, qsl = b.device()
@@ -355,6 +452,8 @@ def test_refusals():
         ops.tree_attn(cache, q, bt, lens, qsl, ops.TreeBuffers(3, 1))
     with pytest.raises(ops.MsaError):
         ops.tree_attn(cache, q, bt, lens, qsl, bufs, softmax_scale=-1.0)
+    with pytest.raises(ops.MsaError):
+        ops.tree_attn(cache, q, bt, lens, qsl, bufs, softmax_scale=3e38)
     i32 = torch.int32
     for at, bad in ((1, q[:1]), (1, q[:, :8]), (3, lens.repeat(2)), (4, qsl[:1]), (2, bt.t())):
         args = [cache, q, bt, lens, qsl, bufs]

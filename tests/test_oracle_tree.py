@@ -72,9 +72,10 @@ def test_validation_needs_no_gpu(lib):  # noqa: F811
     assert call(q=ctypes.c_void_p(8)) == -1 and call(out=ctypes.c_void_p(8)) == -1 and call(ws=ctypes.c_void_p(8)) == -1
     assert call(out=None) == -1 and call(bt=None) == -1
     assert call(ws_bytes=lib.msa_tree_attn_workspace_bytes(1) - 1) == -3
-    # 64 drafts fill two row tiles: more tokens only add their words
+    assert call(scale=3e38) == -1
+    # 64 drafts fill two row tiles: more tokens need no more
     a, b = lib.msa_tree_attn_workspace_bytes(64), lib.msa_tree_attn_workspace_bytes(128)
-    assert b - a == 64 * 16 and lib.msa_tree_attn_workspace_bytes(0) == 256
+    assert a == b and lib.msa_tree_attn_workspace_bytes(0) == 256
 
 
 def test_binding_checks():
