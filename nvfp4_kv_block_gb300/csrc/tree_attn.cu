@@ -31,6 +31,15 @@
 //                 at the segment's end), with two tiles a set takes a tile;
 //   warps 12-23   K conversion (four warps, thread = token) and V conversion (eight,
 //                 thread = token and half of the channels).
+//
+// What bounds it.  A page of 18,432 bytes takes a CTA 0.81 us with up to 8 drafts, 1.01 us
+// up to 16, 1.27 us up to 32 and 2.24 us with two tiles; its products take the tensor pipe
+// 0.39 us per tile.  The rest is instruction issue and hand-offs: 1,958 warp instructions
+// of conversion a page (K 763, V 1,195), 911 (one draft) to 2,550 (32) of softmax, about
+// 1,450 of waits.  32 sequences of 32,768 tokens, one draft each: 188 us, 3.2 TB/s;
+// 8 of 131,072 with 64 drafts: 462 us, 1.13 PFLOP/s; one of 4,096: 15.4 us, a
+// chain of latencies (lengths and ranges 2.6, first page 2.4, its scores 1.4, joining
+// the row copies 1.7, the merge kernel 4).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -222,6 +231,13 @@ struct SeqWork {
 };
 __device__ __forceinline__ SeqWork seq_work(const TreeParams& p, int b) {
   SeqWork w;
+  // (all loads at once: a sequence's start is a chain of them)
+  int id[kSelStride], n = 0;
+  if (p.sel) {
+    n = p.n_sel[b];
+#pragma unroll
+    for (int i = 0; i < kSelStride; ++i) id[i] = p.sel[(size_t)b * kSelStride + i];
+  }
   w.s = load_seq(b, p.seq_lens, p.q_start_loc, p.max_pages, p.n_q_total);
   if (w.s.n_q > kTreeMaxDrafts) w.s.ok = false;
   w.ctx = w.s.seq_len - w.s.n_q;
@@ -231,14 +247,14 @@ __device__ __forceinline__ SeqWork seq_work(const TreeParams& p, int b) {
   w.pw = tree_page_weight(w.s.n_q);
   if (!w.s.ok || w.s.n_q == 0) return w;
   if (p.sel) {
-    const int n = min(max(p.n_sel[b], 0), kSelStride);
     int top = -1;
     w.chosen = 0;
-    for (int i = 0; i < n; ++i) {
-      const int id = p.sel[(size_t)b * kSelStride + i];
-      w.chosen += id > top && id < w.first;
-      top = max(top, id);
-    }
+#pragma unroll
+    for (int i = 0; i < kSelStride; ++i)
+      if (i < n) {
+        w.chosen += id[i] > top && id[i] < w.first;
+        top = max(top, id[i]);
+      }
   }
   w.n_vis = w.chosen + (w.s.seq_len - 1) / kPageTokens - w.first + 1;
   return w;
@@ -395,230 +411,230 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
   // registers: 128 threads x 64 + 256 x 120 + 384 x 56 of the launch's 768 x 80
   if (warp < 4) {
     regs_dec<64>();
-  if (warp == 0) {
-    // ---------------- segment records and page copies -------------------------------------
-    int e = 0, k = 0;
-    bool ok = true;
-    if (!idle) {
-      const long long quota = total / G;
-      const int extra = (int)(total - quota * G);
-      const long long lo = range_start(quota, extra, blockIdx.x), hi = range_start(quota, extra, blockIdx.x + 1);
-      long long off = s_scan[26];
-      for (int b = (int)s_scan[25]; ok && b < p.n_seqs && off < hi; ++b) {
-        const SeqWork w = per == 1 && b == (int)s_scan[25] ? *s_first : seq_work(p, b);
-        if (w.n_vis == 0) continue;
-        const long long wg = (long long)w.pw * w.n_vis + kFixedWeight;
-        // the selection, one entry per lane: its place among the chosen ones
-        int my_blk = -1;
-        if (p.sel && off + kKvHeads * wg > lo) {
-          const int n = min(max(p.n_sel[b], 0), kSelStride);
-          const int id = lane < n ? p.sel[(size_t)b * kSelStride + lane] : -1;
-          int top = id;  // the largest entry so far, this one included
+    if (warp == 0) {
+      // ---------------- segment records and page copies -------------------------------------
+      int e = 0, k = 0;
+      bool ok = true;
+      if (!idle) {
+        const long long quota = total / G;
+        const int extra = (int)(total - quota * G);
+        const long long lo = range_start(quota, extra, blockIdx.x), hi = range_start(quota, extra, blockIdx.x + 1);
+        long long off = s_scan[26];
+        for (int b = (int)s_scan[25]; ok && b < p.n_seqs && off < hi; ++b) {
+          const SeqWork w = per == 1 && b == (int)s_scan[25] ? *s_first : seq_work(p, b);
+          if (w.n_vis == 0) continue;
+          const long long wg = (long long)w.pw * w.n_vis + kFixedWeight;
+          // the selection, one entry per lane: its place among the chosen ones
+          int my_blk = -1;
+          if (p.sel && off + kKvHeads * wg > lo) {
+            const int n = min(max(p.n_sel[b], 0), kSelStride);
+            const int id = lane < n ? p.sel[(size_t)b * kSelStride + lane] : -1;
+            int top = id;  // the largest entry so far, this one included
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, top, o);
-            if (lane >= o) top = max(top, v);
-          }
-          const int prev = __shfl_up_sync(0xffffffffu, top, 1);
-          const bool up = lane < n && id > (lane ? max(prev, -1) : -1);
-          if (lane < n && (!up || id > (w.s.seq_len - 1) / kPageTokens)) set_status(p.status, MSA_STATUS_BAD_SELECTION);
-          const unsigned chosen = __ballot_sync(0xffffffffu, up && id < w.first);
-          // lane i takes the i-th chosen entry
-          int src = 0;
-          for (int i = 0, c = 0; i < kSelStride; ++i)
-            if (chosen >> i & 1) {
-              if (c == lane) src = i;
-              ++c;
+            for (int o = 1; o < 32; o <<= 1) {
+              const int v = __shfl_up_sync(0xffffffffu, top, o);
+              if (lane >= o) top = max(top, v);
             }
-          my_blk = __shfl_sync(0xffffffffu, id, src);
+            const int prev = __shfl_up_sync(0xffffffffu, top, 1);
+            const bool up = lane < n && id > (lane ? max(prev, -1) : -1);
+            if (lane < n && (!up || id > (w.s.seq_len - 1) / kPageTokens)) set_status(p.status, MSA_STATUS_BAD_SELECTION);
+            const unsigned chosen = __ballot_sync(0xffffffffu, up && id < w.first);
+            // lane i takes the i-th chosen entry
+            int src = 0;
+            for (int i = 0, c = 0; i < kSelStride; ++i)
+              if (chosen >> i & 1) {
+                if (c == lane) src = i;
+                ++c;
+              }
+            my_blk = __shfl_sync(0xffffffffu, id, src);
+          }
+          for (int g = 0; ok && g < kKvHeads; ++g, off += wg) {
+            // page i starts at weight off + kFixedWeight + i pw; it belongs to the range that holds its start
+            const long long base = off + kFixedWeight;
+            auto page_at = [&](long long x) {  // the first page that starts at weight x or behind it
+              if (x <= base) return 0;
+              return x - base > (long long)w.n_vis * w.pw ? w.n_vis : ((int)(x - base) + w.pw - 1) / w.pw;
+            };
+            const int a = page_at(lo), z = page_at(hi);
+            if (a >= z) continue;
+            if (!twait(bar(kBRecEmpty + k % kRecs), ((k / kRecs) & 1) ^ 1, wc)) {
+              ok = false;
+              break;
+            }
+            const bool whole = a == 0 && z == w.n_vis;
+            if (lane == 0) {
+              SegRec* r = rec(k);
+              r->n_pg = z - a;
+              r->g = g;
+              r->q0 = w.s.q0;
+              r->n_q = w.s.n_q;
+              r->ctx = w.ctx;
+              r->slot = whole ? -1 : 2 * (int)blockIdx.x + (a > 0 ? 0 : 1);
+            }
+            if (!whole && a == 0) {
+              // the first part tells the merge who has the others
+              const long long last = base + (long long)(w.n_vis - 1) * w.pw;
+              const long long big = extra * (quota + 1);  // the first `extra` CTAs have one unit more
+              const int c_last = last < big ? (int)(last / (quota + 1)) : extra + (int)((last - big) / quota);
+              const int parts = c_last - (int)blockIdx.x + 1;
+              for (int i = lane; i < w.s.n_q; i += 32)
+                p.row_desc[(size_t)(w.s.q0 + i) * kKvHeads + g] = (int)blockIdx.x | parts << 8 | i << 20;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBRecFull + k % kRecs));
+            ++k;
+            const uint8_t* head = p.kv_pool + (size_t)g * kHeadBytes;
+            for (int i0 = a; ok && i0 < z; i0 += 32) {
+              const int i = i0 + lane, cnt = min(32, z - i0);
+              int blk = i;
+              if (p.sel) {
+                const int from = __shfl_sync(0xffffffffu, my_blk, i & 31);
+                blk = i < w.chosen ? from : w.first + i - w.chosen;
+              }
+              int phys = -1;
+              if (lane < cnt) {
+                phys = p.block_table[(size_t)b * p.max_pages + blk];
+                if (phys < 0 || phys >= p.n_pages) {
+                  set_status(p.status, MSA_STATUS_BAD_PAGE);
+                  phys = -1;
+                }
+              }
+              for (int j = 0; j < cnt; ++j, ++e) {
+                const int ph = __shfl_sync(0xffffffffu, phys, j), bl = __shfl_sync(0xffffffffu, blk, j);
+                const int st = e % kRaw;
+                if (!twait(bar(kBRawEmpty + st), ((e / kRaw) & 1) ^ 1, wc)) {
+                  ok = false;
+                  break;
+                }
+                if (lane == 0) {
+                  const int pos = bl * kPageTokens;
+                  s_info[e % kInfo] = make_int2(pos, ph < 0 ? 0 : min(kPageTokens, w.s.seq_len - pos));
+                  if (ph < 0) {
+                    mbar_arrive(bar(kBRawFull + st));  // nothing to copy: no token of the page is valid
+                  } else {
+                    mbar_arrive_expect_tx(bar(kBRawFull + st), kHeadBytes);
+                    bulk_g2s(sbase + kOffRaw + st * kHeadBytes, head + (size_t)ph * kKvPageBytes, kHeadBytes,
+                             bar(kBRawFull + st));
+                  }
+                  *s_issued = e + 1;
+                }
+                __syncwarp();
+              }
+            }
+          }
         }
-        for (int g = 0; ok && g < kKvHeads; ++g, off += wg) {
-          // page i starts at weight off + kFixedWeight + i pw; it belongs to the range that holds its start
-          const long long base = off + kFixedWeight;
-          auto page_at = [&](long long x) {  // the first page that starts at weight x or behind it
-            if (x <= base) return 0;
-            return x - base > (long long)w.n_vis * w.pw ? w.n_vis : ((int)(x - base) + w.pw - 1) / w.pw;
-          };
-          const int a = page_at(lo), z = page_at(hi);
-          if (a >= z) continue;
-          if (!twait(bar(kBRecEmpty + k % kRecs), ((k / kRecs) & 1) ^ 1, wc)) {
+      }
+      // no more segments
+      if (ok && twait(bar(kBRecEmpty + k % kRecs), ((k / kRecs) & 1) ^ 1, wc) && lane == 0) {
+        rec(k)->n_pg = -1;
+        mbar_arrive(bar(kBRecFull + k % kRecs));
+      }
+    } else if (warp == 1) {
+      // ---------------- MMA issuer ---------------------------------------------------------------------
+      // Job j of a segment belongs to set j & 1: page j with one row tile, tile j & 1 of page j / 2
+      // with two.  In turn: PV(j), then QK(j + 2) into the same columns.  The two sets' jobs
+      // alternate on one issuer, so that one set's products run under the other's softmax (an
+      // issuer per set lets two tiles fall into step: 603 against 482 us on 8 x 128K x 64 drafts).
+      // The warp stays together and elects a lane for the MMAs only: in a loop that one lane runs
+      // alone nothing is warp-uniform, and an MMA then takes three times as long to issue.
+      const uint32_t idesc_qk = umma_idesc_e4m3(128, 128);
+      // D fp32, A and B f16, A K-major, B MN-major
+      const uint32_t idesc_pv = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+      int e0 = 0;
+      uint32_t phases = 0;  // of the four P barriers
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        if (!twait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc)) break;
+        const int n_pg = __shfl_sync(0xffffffffu, rec(k)->n_pg, 0);
+        if (n_pg < 0) break;
+        const bool two = __shfl_sync(0xffffffffu, rec(k)->n_q, 0) > 32;
+        if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
+        const int n_jobs = two ? 2 * n_pg : n_pg;
+        if (!twait(bar(kBQFull), k & 1, wc)) break;
+        auto k_ready = [&](int e) { return twait(bar(kBKFull + (e & 1)), (e >> 1) & 1, wc); };
+        // QK of page e for a set (inside an elected lane); free_k: the last reader of the K tile.
+        // (The loops stay short: straight-line MMAs are long, and a long way round the warp's
+        // code misses the instruction cache.)
+        auto issue_qk = [&](int set, int e, bool free_k, bool free_q) {
+          const uint64_t qdesc = umma_desc_sw128(sbase + kOffQ + (two ? set : 0) * 16384);
+          // K-major without swizzle: 8 tokens x 16 channels are 128 contiguous bytes, the next 16
+          // channels 2,048 further (so that a converting thread's stores are at fixed offsets)
+          const uint64_t kdesc = umma_desc_noswz_lbo_sbo(sbase + kOffK8 + (e & 1) * 16384, 2048, 128);
+#pragma unroll 2
+          for (int kk = 0; kk < 4; ++kk)  // 32 channels each
+            umma_e4m3(tmem + kTmemS + 128 * set, qdesc + 2 * kk, kdesc + kk * (4096 >> 4), idesc_qk, kk > 0);
+          umma_commit(bar(kBSFull + set));
+          if (free_k) umma_commit(bar(kBKEmpty + (e & 1)));
+          if (free_q) umma_commit(bar(kBQEmpty));
+        };
+        // first QKs of both sets, then job after job
+        for (int j = -2; ok && j < n_jobs; ++j) {
+          const int set = j & 1;
+          const int e = e0 + (two ? j >> 1 : j), en = e + (two ? 1 : 2);
+          const bool next = j + 2 < n_jobs;
+          if (next && !(two && set) && !k_ready(en)) {
             ok = false;
             break;
           }
-          const bool whole = a == 0 && z == w.n_vis;
-          if (lane == 0) {
-            SegRec* r = rec(k);
-            r->n_pg = z - a;
-            r->g = g;
-            r->q0 = w.s.q0;
-            r->n_q = w.s.n_q;
-            r->ctx = w.ctx;
-            r->slot = whole ? -1 : 2 * (int)blockIdx.x + (a > 0 ? 0 : 1);
+          if (j == 0 && k > 0 && !twait(bar(kBOFree), (k - 1) & 1, wc)) {  // both accumulators are read
+            ok = false;
+            break;
           }
-          if (!whole && a == 0) {
-            // the first part tells the merge who has the others
-            const long long last = base + (long long)(w.n_vis - 1) * w.pw;
-            const long long big = extra * (quota + 1);  // the first `extra` CTAs have one unit more
-            const int c_last = last < big ? (int)(last / (quota + 1)) : extra + (int)((last - big) / quota);
-            const int parts = c_last - (int)blockIdx.x + 1;
-            for (int i = lane; i < w.s.n_q; i += 32)
-              p.row_desc[(size_t)(w.s.q0 + i) * kKvHeads + g] = (int)blockIdx.x | parts << 8 | i << 20;
+          const int pb = kSlot * set + (e & 1);
+          if (j >= 0) {
+            if (!twait(bar(kBPFull + pb), phases >> pb & 1, wc)) {
+              ok = false;
+              break;
+            }
+            phases ^= 1u << pb;
+          }
+          tc_fence_after();
+          // MN-major without swizzle: 8 tokens x 8 channels are 128 contiguous bytes, the next 8 tokens
+          // follow, the next 8 channels are 2,048 further
+          const uint64_t vdesc = umma_desc_noswz_lbo_sbo(sbase + kOffV16 + (e & 1) * 32768, 128, 2048);
+          if (elect_one()) {
+            if (j >= 0) {
+#pragma unroll 4
+              for (int kk = 0; kk < 8; ++kk)  // 16 tokens each: 8 columns of P inside S's 32-column chunks
+                umma_f16_ts(tmem + kTmemO + 128 * set, tmem + kTmemS + 128 * set + 32 * (kk >> 1) + 8 * (kk & 1),
+                            vdesc + kk * (256 >> 4), idesc_pv, (j >= 2 || kk > 0) ? 1u : 0u);
+              if (!(two && set == 0)) umma_commit(bar(kBVEmpty + (e & 1)));
+            }
+            if (next) issue_qk(set, en, !(two && set == 0), j + 3 == n_jobs);
+            else umma_commit(bar(kBPvDone + set));  // the set's accumulator is final (or it has no job)
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kBRecFull + k % kRecs));
-          ++k;
-          const uint8_t* head = p.kv_pool + (size_t)g * kHeadBytes;
-          for (int i0 = a; ok && i0 < z; i0 += 32) {
-            const int i = i0 + lane, cnt = min(32, z - i0);
-            int blk = i;
-            if (p.sel) {
-              const int from = __shfl_sync(0xffffffffu, my_blk, i & 31);
-              blk = i < w.chosen ? from : w.first + i - w.chosen;
-            }
-            int phys = -1;
-            if (lane < cnt) {
-              phys = p.block_table[(size_t)b * p.max_pages + blk];
-              if (phys < 0 || phys >= p.n_pages) {
-                set_status(p.status, MSA_STATUS_BAD_PAGE);
-                phys = -1;
-              }
-            }
-            for (int j = 0; j < cnt; ++j, ++e) {
-              const int ph = __shfl_sync(0xffffffffu, phys, j), bl = __shfl_sync(0xffffffffu, blk, j);
-              const int st = e % kRaw;
-              if (!twait(bar(kBRawEmpty + st), ((e / kRaw) & 1) ^ 1, wc)) {
-                ok = false;
-                break;
-              }
-              if (lane == 0) {
-                const int pos = bl * kPageTokens;
-                s_info[e % kInfo] = make_int2(pos, ph < 0 ? 0 : min(kPageTokens, w.s.seq_len - pos));
-                if (ph < 0) {
-                  mbar_arrive(bar(kBRawFull + st));  // nothing to copy: no token of the page is valid
-                } else {
-                  mbar_arrive_expect_tx(bar(kBRawFull + st), kHeadBytes);
-                  bulk_g2s(sbase + kOffRaw + st * kHeadBytes, head + (size_t)ph * kKvPageBytes, kHeadBytes,
-                           bar(kBRawFull + st));
-                }
-                *s_issued = e + 1;
-              }
-              __syncwarp();
-            }
-          }
         }
+        e0 += n_pg;
       }
-    }
-    // no more segments
-    if (ok && twait(bar(kBRecEmpty + k % kRecs), ((k / kRecs) & 1) ^ 1, wc) && lane == 0) {
-      rec(k)->n_pg = -1;
-      mbar_arrive(bar(kBRecFull + k % kRecs));
-    }
-  } else if (warp == 1) {
-    // ---------------- MMA issuer ---------------------------------------------------------------------
-    // Job j of a segment belongs to set j & 1: page j with one row tile, tile j & 1 of page j / 2
-    // with two.  In turn: PV(j), then QK(j + 2) into the same columns.  The two sets' jobs
-    // alternate on one issuer, so that one set's products run under the other's softmax (an
-    // issuer per set lets two tiles fall into step: 603 against 482 us on 8 x 128K x 64 drafts).
-    // The warp stays together and elects a lane for the MMAs only: in a loop that one lane runs
-    // alone nothing is warp-uniform, and an MMA then takes three times as long to issue.
-    const uint32_t idesc_qk = umma_idesc_e4m3(128, 128);
-    // D fp32, A and B f16, A K-major, B MN-major
-    const uint32_t idesc_pv = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
-    int e0 = 0;
-    uint32_t phases = 0;  // of the four P barriers
-    bool ok = true;
-    for (int k = 0; ok; ++k) {
-      if (!twait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc)) break;
-      const int n_pg = __shfl_sync(0xffffffffu, rec(k)->n_pg, 0);
-      if (n_pg < 0) break;
-      const bool two = __shfl_sync(0xffffffffu, rec(k)->n_q, 0) > 32;
-      if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
-      const int n_jobs = two ? 2 * n_pg : n_pg;
-      if (!twait(bar(kBQFull), k & 1, wc)) break;
-      auto k_ready = [&](int e) { return twait(bar(kBKFull + (e & 1)), (e >> 1) & 1, wc); };
-      // QK of page e for a set (inside an elected lane); free_k: the last reader of the K tile.
-      // (The loops stay short: straight-line MMAs are long, and a long way round the warp's
-      // code misses the instruction cache.)
-      auto issue_qk = [&](int set, int e, bool free_k, bool free_q) {
-        const uint64_t qdesc = umma_desc_sw128(sbase + kOffQ + (two ? set : 0) * 16384);
-        // K-major without swizzle: 8 tokens x 16 channels are 128 contiguous bytes, the next 16
-        // channels 2,048 further (so that a converting thread's stores are at fixed offsets)
-        const uint64_t kdesc = umma_desc_noswz_lbo_sbo(sbase + kOffK8 + (e & 1) * 16384, 2048, 128);
-#pragma unroll 2
-        for (int kk = 0; kk < 4; ++kk)  // 32 channels each
-          umma_e4m3(tmem + kTmemS + 128 * set, qdesc + 2 * kk, kdesc + kk * (4096 >> 4), idesc_qk, kk > 0);
-        umma_commit(bar(kBSFull + set));
-        if (free_k) umma_commit(bar(kBKEmpty + (e & 1)));
-        if (free_q) umma_commit(bar(kBQEmpty));
-      };
-      // first QKs of both sets, then job after job
-      for (int j = -2; ok && j < n_jobs; ++j) {
-        const int set = j & 1;
-        const int e = e0 + (two ? j >> 1 : j), en = e + (two ? 1 : 2);
-        const bool next = j + 2 < n_jobs;
-        if (next && !(two && set) && !k_ready(en)) {
-          ok = false;
-          break;
-        }
-        if (j == 0 && k > 0 && !twait(bar(kBOFree), (k - 1) & 1, wc)) {  // both accumulators are read
-          ok = false;
-          break;
-        }
-        const int pb = kSlot * set + (e & 1);
-        if (j >= 0) {
-          if (!twait(bar(kBPFull + pb), phases >> pb & 1, wc)) {
-            ok = false;
-            break;
-          }
-          phases ^= 1u << pb;
-        }
-        tc_fence_after();
-        // MN-major without swizzle: 8 tokens x 8 channels are 128 contiguous bytes, the next 8 tokens
-        // follow, the next 8 channels are 2,048 further
-        const uint64_t vdesc = umma_desc_noswz_lbo_sbo(sbase + kOffV16 + (e & 1) * 32768, 128, 2048);
-        if (elect_one()) {
-          if (j >= 0) {
-#pragma unroll 4
-            for (int kk = 0; kk < 8; ++kk)  // 16 tokens each: 8 columns of P inside S's 32-column chunks
-              umma_f16_ts(tmem + kTmemO + 128 * set, tmem + kTmemS + 128 * set + 32 * (kk >> 1) + 8 * (kk & 1),
-                          vdesc + kk * (256 >> 4), idesc_pv, (j >= 2 || kk > 0) ? 1u : 0u);
-            if (!(two && set == 0)) umma_commit(bar(kBVEmpty + (e & 1)));
-          }
-          if (next) issue_qk(set, en, !(two && set == 0), j + 3 == n_jobs);
-          else umma_commit(bar(kBPvDone + set));  // the set's accumulator is final (or it has no job)
-        }
+      __syncwarp();
+      if (elect_one()) umma_commit(bar(kBDone));
+      __syncwarp();
+    } else if (warp == 2) {
+      // ---------------- query rows of a segment: row 4 i + h of draft i, head 4 g + h -----------------
+      for (int k = 0;; ++k) {
+        if (!twait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc)) break;
+        const SegRec r = *rec(k);
         __syncwarp();
+        if (r.n_pg < 0) break;
+        if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
+        if (k > 0 && !twait(bar(kBQEmpty), (k - 1) & 1, wc)) break;
+        // the second tile is also the exchange buffer of a segment with row copies (all segments or
+        // none wait: a parity does not tell phase k - 1 from k - 3, so every phase is seen in turn)
+        if (wide && k > 0 && !twait(bar(kBOFree), (k - 1) & 1, wc)) break;
+        const int copies = tree_copies(r.n_q), gap = 128 / copies;
+        for (int x = lane; x < r.n_q * 32; x += 32) {
+          const int row = x >> 3, c = x & 7;
+          const uint8_t* src = p.q + ((size_t)(r.q0 + (row >> 2)) * kQHeads + kGqa * r.g + (row & 3)) * kHeadDim + 16 * c;
+          for (int i = 0; i < copies; ++i)
+            cp_async16(sbase + kOffQ + (row + i * gap) * 128 + ((c ^ (row & 7)) << 4), src);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBQFull));
       }
-      e0 += n_pg;
     }
-    __syncwarp();
-    if (elect_one()) umma_commit(bar(kBDone));
-    __syncwarp();
-  } else if (warp == 2) {
-    // ---------------- query rows of a segment: row 4 i + h of draft i, head 4 g + h -----------------
-    for (int k = 0;; ++k) {
-      if (!twait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc)) break;
-      const SegRec r = *rec(k);
-      __syncwarp();
-      if (r.n_pg < 0) break;
-      if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
-      if (k > 0 && !twait(bar(kBQEmpty), (k - 1) & 1, wc)) break;
-      // the second tile is also the exchange buffer of a segment with row copies (all segments or
-      // none wait: a parity does not tell phase k - 1 from k - 3, so every phase is seen in turn)
-      if (wide && k > 0 && !twait(bar(kBOFree), (k - 1) & 1, wc)) break;
-      const int copies = tree_copies(r.n_q), gap = 128 / copies;
-      for (int x = lane; x < r.n_q * 32; x += 32) {
-        const int row = x >> 3, c = x & 7;
-        const uint8_t* src = p.q + ((size_t)(r.q0 + (row >> 2)) * kQHeads + kGqa * r.g + (row & 3)) * kHeadDim + 16 * c;
-        for (int i = 0; i < copies; ++i)
-          cp_async16(sbase + kOffQ + (row + i * gap) * 128 + ((c ^ (row & 7)) << 4), src);
-      }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBQFull));
-    }
-  }
   } else if (warp < 12) {
     regs_inc<120>();
     // ---------------- softmax: set = (warp - 4) / 4, row = TMEM lane ------------------------------------
@@ -825,7 +841,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
               }
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<float4*>(xb + 16 * (un * parts + me) + 4 * (i ^ (me >> 1 & 3))) =
+                *reinterpret_cast<float4*>(xb + 16 * (un * parts + me) + 4 * (i ^ (row >> 1 & 3))) =
                     make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
             }
           __syncwarp();
@@ -833,8 +849,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
           for (int i = lrow; i < 4 * units * n_rows; i += 128) {  // (row, unit, chunk)
             const int c = i & (4 * units - 1), ri = i >> (2 + ush), un = c >> 2;
             float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int ln = ri; ln < parts; ln += n_rows) {
-              const float4 z = *reinterpret_cast<const float4*>(xb + 16 * (un * parts + ln) + 4 * ((c & 3) ^ (ln >> 1 & 3)));
+            const float* part = xb + 16 * (un * parts + ri) + 4 * ((c & 3) ^ (ri >> 1 & 3));
+#pragma unroll 2
+            for (int cp = 0; cp < copies; ++cp, part += 16 * n_rows) {
+              const float4 z = *reinterpret_cast<const float4*>(part);
               y.x += z.x;
               y.y += z.y;
               y.z += z.z;
@@ -856,7 +874,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              v[i] = __float_as_uint((w0 > 0.f ? __uint_as_float(v[i]) * w0 : 0.f) + (w1 > 0.f ? __uint_as_float(u[i]) * w1 : 0.f));
+              v[i] = __float_as_uint((w0 > 0.f ? __uint_as_float(v[i]) * w0 : 0.f) +
+                                     (w1 > 0.f ? __uint_as_float(u[i]) * w1 : 0.f));
           } else {
             tmem_wait_ld();
           }
@@ -869,7 +888,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       }
       if (mine && copy == 0 && (two || set == 0)) {
         if (r.slot >= 0) p.part_ml[(size_t)r.slot * p.part_rows + row] = make_float2(m, L);
-        else if (p.lse) p.lse[at0 + (size_t)(row >> 2) * kQHeads + (row & 3)] = L != 0.f ? (m - kTreeBias + log2f(L)) * kTreeLn2 : -INFINITY;
+        else if (p.lse)
+          p.lse[at0 + (size_t)(row >> 2) * kQHeads + (row & 3)] = L != 0.f ? (m - kTreeBias + log2f(L)) * kTreeLn2 : -INFINITY;
       }
       tc_fence_before();
       __syncwarp();
@@ -884,108 +904,109 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
     const int sched = warp & 3, turn = (warp - 12) >> 2;
     const bool is_v = sched < 2 || (sched == 2 && turn < 2);
     const int part = is_v ? 3 * sched + turn : sched == 3 ? turn : 3;
-  if (is_v) {
-    // ---------------- V conversion: token tok, channels 64 half .. 64 half + 63 ----------------------
-    const int half = part >> 2, tok = 32 * (part & 3) + lane;
-    const uint32_t tab = sbase + kOffVTab + 16 * (lane & (kVTabCopies - 1));
-    const uint32_t raw0 = sbase + kOffRaw + kOffVc, out0 = sbase + kOffV16 + half * 16384 + tok * 16;
-    const uint32_t code0 = tok * 64 + 16 * code_chunk_pos(2 * half, tok), code1 = tok * 64 + 16 * code_chunk_pos(2 * half + 1, tok);
-    const uint32_t scale0 = (kOffKs - kOffKc) + 4 * half * kPageTokens + tok;
-    int e = 0;
-    bool ok = true;
-    for (int k = 0; ok; ++k) {
-      if (!twait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc)) break;
-      const int n_pg = rec(k)->n_pg;
-      const bool two = rec(k)->n_q > 32;
-      __syncwarp();
-      if (n_pg < 0) break;
-      if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
-      for (int i = 0; i < n_pg; ++i, ++e) {
-        const int st = e % kRaw, sl = e % kSlot;
-        if (!twait(bar(kBRawFull + st), (e / kRaw) & 1, wc) || !twait(bar(kBVEmpty + sl), ((e / kSlot) & 1) ^ 1, wc)) {
-          ok = false;
-          break;
-        }
-        const uint32_t raw = raw0 + st * kHeadBytes, dst = out0 + sl * 32768;
-        const int valid = s_info[e % kInfo].y;
-        uint4 w[2] = {lds128(raw + code0), lds128(raw + code1)}, t[4];
-        uint32_t sb[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) sb[u] = lds_u8(raw + scale0 + u * kPageTokens) & 127;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) t[u] = lds128(tab + sb[u] * (16 * kVTabCopies));
-        if (valid < kPageTokens && tok >= valid) {  // rows behind the sequence become zeros: a scale of zero
-#pragma unroll
-          for (int u = 0; u < 4; ++u) t[u] = make_uint4(0, 0, 0, 0);
-          w[0] = w[1] = make_uint4(0, 0, 0, 0);
-        }
-        // 8 channels of 128 tokens are 2,048 contiguous bytes
-#pragma unroll
-        for (int cc = 0; cc < 2; ++cc) {
-          sts128(dst + (4 * cc) * 2048, dequant8_f16(w[cc].x, t[2 * cc]));
-          sts128(dst + (4 * cc + 1) * 2048, dequant8_f16(w[cc].y, t[2 * cc]));
-          sts128(dst + (4 * cc + 2) * 2048, dequant8_f16(w[cc].z, t[2 * cc + 1]));
-          sts128(dst + (4 * cc + 3) * 2048, dequant8_f16(w[cc].w, t[2 * cc + 1]));
-        }
-        fence_proxy_async_smem();
+    if (is_v) {
+      // ---------------- V conversion: token tok, channels 64 half .. 64 half + 63 ----------------------
+      const int half = part >> 2, tok = 32 * (part & 3) + lane;
+      const uint32_t tab = sbase + kOffVTab + 16 * (lane & (kVTabCopies - 1));
+      const uint32_t raw0 = sbase + kOffRaw + kOffVc, out0 = sbase + kOffV16 + half * 16384 + tok * 16;
+      const uint32_t code0 = tok * 64 + 16 * code_chunk_pos(2 * half, tok);
+      const uint32_t code1 = tok * 64 + 16 * code_chunk_pos(2 * half + 1, tok);
+      const uint32_t scale0 = (kOffKs - kOffKc) + 4 * half * kPageTokens + tok;
+      int e = 0;
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        if (!twait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc)) break;
+        const int n_pg = rec(k)->n_pg;
+        const bool two = rec(k)->n_q > 32;
         __syncwarp();
-        if (lane == 0) {
-          if (two || (i & 1) == 0) mbar_arrive(bar(kBPFull + sl));
-          if (two || (i & 1) == 1) mbar_arrive(bar(kBPFull + 2 + sl));
-          mbar_arrive(bar(kBRawEmpty + st));
-        }
-      }
-    }
-  } else {
-    // ---------------- K conversion: token tok ----------------------------------------------------------
-    const int tok = 32 * part + lane;
-    const uint32_t tab = sbase + kOffKTab + 8 * (lane & (kKTabCopies - 1));
-    const uint32_t raw0 = sbase + kOffRaw + kOffKc, out0 = sbase + kOffK8 + tok * 16;
-    const uint32_t code0 = tok * 64 + 16 * code_chunk_pos(0, tok), scale0 = (kOffKs - kOffKc) + tok;
-    int e = 0;
-    bool ok = true;
-    for (int k = 0; ok; ++k) {
-      if (!twait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc)) break;
-      const int n_pg = rec(k)->n_pg;
-      __syncwarp();
-      if (n_pg < 0) break;
-      if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
-      for (int i = 0; i < n_pg; ++i, ++e) {
-        const int st = e % kRaw, sl = e % kSlot;
-        if (!twait(bar(kBRawFull + st), (e / kRaw) & 1, wc) || !twait(bar(kBKEmpty + sl), ((e / kSlot) & 1) ^ 1, wc)) {
-          ok = false;
-          break;
-        }
-        const uint32_t raw = raw0 + st * kHeadBytes, dst = out0 + sl * 16384;
-        // half of the channels at a time; 16 channels of 128 tokens are 2,048 contiguous bytes
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          // (code chunk c is at chunk c ^ x of the row: (code0 ^ 16 c) for the offset of chunk 0)
-          const uint32_t ch = raw + (code0 ^ (32 * h)), ch1 = raw + (code0 ^ (32 * h + 16));
-          const uint4 w[2] = {lds128(ch), lds128(ch1)};
+        if (n_pg < 0) break;
+        if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
+        for (int i = 0; i < n_pg; ++i, ++e) {
+          const int st = e % kRaw, sl = e % kSlot;
+          if (!twait(bar(kBRawFull + st), (e / kRaw) & 1, wc) || !twait(bar(kBVEmpty + sl), ((e / kSlot) & 1) ^ 1, wc)) {
+            ok = false;
+            break;
+          }
+          const uint32_t raw = raw0 + st * kHeadBytes, dst = out0 + sl * 32768;
+          const int valid = s_info[e % kInfo].y;
+          uint4 w[2] = {lds128(raw + code0), lds128(raw + code1)}, t[4];
           uint32_t sb[4];
-          uint2 t[4];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) sb[u] = lds_u8(raw + scale0 + (4 * h + u) * kPageTokens) & 127;
+          for (int u = 0; u < 4; ++u) sb[u] = lds_u8(raw + scale0 + u * kPageTokens) & 127;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) t[u] = lds64(tab + sb[u] * (8 * kKTabCopies));
+          for (int u = 0; u < 4; ++u) t[u] = lds128(tab + sb[u] * (16 * kVTabCopies));
+          if (valid < kPageTokens && tok >= valid) {  // rows behind the sequence become zeros: a scale of zero
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const uint2 a = dequant8(w[c].x, t[2 * c]), b = dequant8(w[c].y, t[2 * c]);
-            const uint2 d = dequant8(w[c].z, t[2 * c + 1]), f = dequant8(w[c].w, t[2 * c + 1]);
-            sts128(dst + (4 * h + 2 * c) * 2048, make_uint4(a.x, a.y, b.x, b.y));
-            sts128(dst + (4 * h + 2 * c + 1) * 2048, make_uint4(d.x, d.y, f.x, f.y));
+            for (int u = 0; u < 4; ++u) t[u] = make_uint4(0, 0, 0, 0);
+            w[0] = w[1] = make_uint4(0, 0, 0, 0);
+          }
+          // 8 channels of 128 tokens are 2,048 contiguous bytes
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            sts128(dst + (4 * cc) * 2048, dequant8_f16(w[cc].x, t[2 * cc]));
+            sts128(dst + (4 * cc + 1) * 2048, dequant8_f16(w[cc].y, t[2 * cc]));
+            sts128(dst + (4 * cc + 2) * 2048, dequant8_f16(w[cc].z, t[2 * cc + 1]));
+            sts128(dst + (4 * cc + 3) * 2048, dequant8_f16(w[cc].w, t[2 * cc + 1]));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (two || (i & 1) == 0) mbar_arrive(bar(kBPFull + sl));
+            if (two || (i & 1) == 1) mbar_arrive(bar(kBPFull + 2 + sl));
+            mbar_arrive(bar(kBRawEmpty + st));
           }
         }
-        fence_proxy_async_smem();
+      }
+    } else {
+      // ---------------- K conversion: token tok ----------------------------------------------------------
+      const int tok = 32 * part + lane;
+      const uint32_t tab = sbase + kOffKTab + 8 * (lane & (kKTabCopies - 1));
+      const uint32_t raw0 = sbase + kOffRaw + kOffKc, out0 = sbase + kOffK8 + tok * 16;
+      const uint32_t code0 = tok * 64 + 16 * code_chunk_pos(0, tok), scale0 = (kOffKs - kOffKc) + tok;
+      int e = 0;
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        if (!twait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc)) break;
+        const int n_pg = rec(k)->n_pg;
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(kBKFull + sl));
-          mbar_arrive(bar(kBRawEmpty + st));
+        if (n_pg < 0) break;
+        if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
+        for (int i = 0; i < n_pg; ++i, ++e) {
+          const int st = e % kRaw, sl = e % kSlot;
+          if (!twait(bar(kBRawFull + st), (e / kRaw) & 1, wc) || !twait(bar(kBKEmpty + sl), ((e / kSlot) & 1) ^ 1, wc)) {
+            ok = false;
+            break;
+          }
+          const uint32_t raw = raw0 + st * kHeadBytes, dst = out0 + sl * 16384;
+          // half of the channels at a time; 16 channels of 128 tokens are 2,048 contiguous bytes
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            // (code chunk c is at chunk c ^ x of the row: (code0 ^ 16 c) for the offset of chunk 0)
+            const uint32_t ch = raw + (code0 ^ (32 * h)), ch1 = raw + (code0 ^ (32 * h + 16));
+            const uint4 w[2] = {lds128(ch), lds128(ch1)};
+            uint32_t sb[4];
+            uint2 t[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) sb[u] = lds_u8(raw + scale0 + (4 * h + u) * kPageTokens) & 127;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) t[u] = lds64(tab + sb[u] * (8 * kKTabCopies));
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const uint2 a = dequant8(w[c].x, t[2 * c]), b = dequant8(w[c].y, t[2 * c]);
+              const uint2 d = dequant8(w[c].z, t[2 * c + 1]), f = dequant8(w[c].w, t[2 * c + 1]);
+              sts128(dst + (4 * h + 2 * c) * 2048, make_uint4(a.x, a.y, b.x, b.y));
+              sts128(dst + (4 * h + 2 * c + 1) * 2048, make_uint4(d.x, d.y, f.x, f.y));
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(kBKFull + sl));
+            mbar_arrive(bar(kBRawEmpty + st));
+          }
         }
       }
     }
-  }
   }
 
   // ---- teardown -------------------------------------------------------------------------
