@@ -32,16 +32,18 @@
 //   warps 12-23   K conversion (four warps, thread = token) and V conversion (eight,
 //                 thread = token and half of the channels).
 //
-// What bounds it.  A page of 18,432 bytes takes a CTA 0.81 us with up to 8 drafts, 1.01 us
-// up to 16, 1.27 us up to 32 and 2.24 us with two tiles; its products take the tensor pipe
-// 0.39 us per tile.  The rest is instruction issue and hand-offs: 1,958 warp instructions
-// of conversion a page (K 763, V 1,195), 911 (one draft) to 2,550 (32) of softmax, about
-// 1,450 of waits.  32 sequences of 32,768 tokens, one draft each: 188 us, 3.2 TB/s;
-// 8 of 131,072 with 64 drafts: 462 us, 1.13 PFLOP/s; one of 4,096: 15.4 us, a
-// chain of latencies (lengths and ranges 2.6, first page 2.4, its scores 1.4, joining
-// the row copies 1.7, the merge kernel 4).
+// What bounds it.  A page of 18,432 bytes takes a CTA 0.80 us with up to 8 drafts, 0.95 us up
+// to 16, 1.1 us up to 32 and 2.0 us with two tiles; its products take the tensor pipe 0.39 us
+// per tile.  The rest is instruction issue and hand-offs: 1,958 warp instructions of
+// conversion a page (K 763, V 1,195), 911 (one draft) to 2,550 (32) of softmax, about 1,450
+// of waits.  32 sequences of 32,768 tokens, one draft each: 185 us, 3.3 TB/s; 8 of 131,072
+// with 64 drafts: 414 us, 1.26 PFLOP/s; one of 4,096: 14.9 us, a chain of latencies
+// (lengths and ranges 2.6, first page 2.4, its scores 1.4, joining the row copies 1.7, the
+// merge kernel 4).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -85,15 +87,16 @@ constexpr float kTreeUnset = 3e38f;    // shift of a row without a reference: a 
 constexpr float kTreeLog2e = 1.4426950408889634f, kTreeLn2 = 0.6931471805599453f;
 
 // Weights of the partition, in units of 0.2 us: a page of a sequence with up to 8, 16,
-// 32 and 64 drafts (0.81, 1.01, 1.27 and 2.24 us per page of a CTA on 32K contexts), and
+// 32 and 64 drafts (0.80, 0.95, 1.1 and 2.0 us per page of a CTA on 32K contexts), and
 // the fixed part of a (sequence, KV head).  The least share of a CTA is a page's
 // weight, so that every CTA between a sequence's first and last has pages of it.
-__host__ __device__ __forceinline__ int tree_page_weight(int n_q) { return n_q <= 8 ? 4 : n_q <= 16 ? 5 : n_q <= 32 ? 6 : 11; }
-constexpr int kFixedWeight = 10, kLeastShare1 = 6, kLeastShare2 = 11;
+__host__ __device__ __forceinline__ int tree_page_weight(int n_q) { return n_q <= 8 ? 4 : n_q <= 16 ? 5 : n_q <= 32 ? 6 : 10; }
+constexpr int kFixedWeight = 10, kLeastShare1 = 6, kLeastShare2 = 10;
 
 // Copies of the query rows in a one-tile segment's 128 rows: with few rows every
 // warp quad (32 lanes of tensor memory) gets the same rows and its own share of a
-// page's tokens, so that no softmax warp is idle.
+// page's tokens, so that no softmax warp is idle (32 sequences of 32,768 tokens, one draft
+// each: 185 us, with two copies 211, with one 224).
 __host__ __device__ __forceinline__ int tree_copies(int n_q) { return n_q <= 8 ? 4 : n_q <= 16 ? 2 : 1; }
 
 struct SegRec {
@@ -408,9 +411,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
   const int G = (int)min((long long)gridDim.x, max(1ll, total / (wide ? kLeastShare2 : kLeastShare1)));
   const bool idle = (int)blockIdx.x >= G || total == 0;
 
-  // registers: 128 threads x 64 + 256 x 120 + 384 x 56 of the launch's 768 x 80
+  // registers: 128 threads x 80 (as launched) + 256 x 112 + 384 x 56 of the launch's 768 x 80
+  // (64, 120 and 56 cost the issuer and the page walk spills: 2 % on every case)
   if (warp < 4) {
-    regs_dec<64>();
     if (warp == 0) {
       // ---------------- segment records and page copies -------------------------------------
       int e = 0, k = 0;
@@ -636,28 +639,22 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       }
     }
   } else if (warp < 12) {
-    regs_inc<120>();
+    regs_inc<112>();
     // ---------------- softmax: set = (warp - 4) / 4, row = TMEM lane ------------------------------------
     const int set = (warp - 4) >> 2, quad = warp & 3, lrow = 32 * quad + lane;
     const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16);
     const uint32_t t_s = tl + kTmemS + 128 * set;
     const uint64_t scale2 = pair64(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
-    uint32_t zero[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) asm volatile("mov.u32 %0, 0;" : "=r"(zero[i]));
     int e0 = 0, jobs = 0;  // pages so far, jobs of this set so far
     bool ok = true;
-    for (int k = 0;; ++k) {
-      // (the set's warps leave together: they meet at named barriers below)
-      if (barrier_or(1 + set, 128, !twait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc))) break;
-      const SegRec r = *rec(k);
-      __syncwarp();
-      if (r.n_pg < 0) break;
-      if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
-      const int two = r.n_q > 32 ? 1 : 0;
+    // One segment; false: the set leaves.  A copy of the code per mode (0: one row tile with row
+    // copies, 1: one tile, 2: two tiles): with the counts known the page loop is shorter and needs
+    // fewer registers (8 sequences of 131,072 with 64 drafts: 414 us, 444 with one code for all).
+    auto segment = [&](const SegRec& r, int k, auto mode) -> bool {
+      constexpr int kMode = decltype(mode)::value, two = kMode == 2;
       const int n_jobs = r.n_pg << two;
       const int n_rows = kGqa * r.n_q;
-      const int copies = tree_copies(r.n_q), gap = 128 / copies;  // (one copy with two tiles)
+      const int copies = kMode == 0 ? tree_copies(r.n_q) : 1, gap = 128 / copies;
       const int row = two ? 128 * set + lrow : lrow & (gap - 1);
       const int copy = lrow / gap;
       const bool busy = row - lane < n_rows;  // some lane of the warp has a row
@@ -762,6 +759,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
             tmem_st_x16(t_s + 32 * c, o);
           }
           if (copies > 1) {  // the other copies' tokens
+            const uint32_t zero[16] = {};
 #pragma unroll 1
             for (int c = 0; c < 4; ++c)
               if (c < c0 || c >= c1) tmem_st_x16(t_s + 32 * c, zero);
@@ -784,7 +782,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBMl));
       ok = ok && twait(bar(kBMl), k & 1, wc);
-      if (barrier_or(1 + set, 128, !ok)) break;
+      if (barrier_or(1 + set, 128, !ok)) return false;
       // the row's parts (one per set and copy): the joint reference and sum, the weights of this lane's
       float w0 = 1.f, w1 = 0.f, m = m_ref, L = l;
       if (!two) {
@@ -894,6 +892,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBOFree));
+      return true;
+    };
+    for (int k = 0;; ++k) {
+      // (the set's warps leave together: they meet at named barriers below)
+      if (barrier_or(1 + set, 128, !twait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc))) break;
+      const SegRec r = *rec(k);
+      __syncwarp();
+      if (r.n_pg < 0) break;
+      if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
+      const bool go = tree_copies(r.n_q) > 1 ? segment(r, k, std::integral_constant<int, 0>{})
+                      : r.n_q <= 32          ? segment(r, k, std::integral_constant<int, 1>{})
+                                             : segment(r, k, std::integral_constant<int, 2>{});
+      if (!go) break;
       e0 += r.n_pg;
     }
   } else {
