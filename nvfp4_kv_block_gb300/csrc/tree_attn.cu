@@ -604,7 +604,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
               if (!(two && set == 0)) umma_commit(bar(kBVEmpty + (e & 1)));
             }
             if (next) issue_qk(set, en, !(two && set == 0), j + 3 == n_jobs);
-            else umma_commit(bar(kBPvDone + set));  // the set's accumulator is final (or it has no job)
+            else if (j >= 0) umma_commit(bar(kBPvDone + set));  // the set's accumulator is final
+            // (a set without a job: behind the wait for the last segment's readers, who would miss a phase)
+            if (n_jobs == 1 && j == 0) umma_commit(bar(kBPvDone + 1));
           }
           __syncwarp();
         }
