@@ -936,7 +936,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
         if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
         for (int i = 0; i < n_pg; ++i, ++e) {
           const int st = e % kRaw, sl = e % kSlot;
-          if (!twait(bar(kBRawFull + st), (e / kRaw) & 1, wc) || !twait(bar(kBVEmpty + sl), ((e / kSlot) & 1) ^ 1, wc)) {
+          if (!twait(bar(kBRawFull + st), (e / kRaw) & 1, wc)) {
             ok = false;
             break;
           }
@@ -952,6 +952,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
 #pragma unroll
             for (int u = 0; u < 4; ++u) t[u] = make_uint4(0, 0, 0, 0);
             w[0] = w[1] = make_uint4(0, 0, 0, 0);
+          }
+          // (the loads are under way while the slot's last PV ends)
+          if (!twait(bar(kBVEmpty + sl), ((e / kSlot) & 1) ^ 1, wc)) {
+            ok = false;
+            break;
           }
           // 8 channels of 128 tokens are 2,048 contiguous bytes
 #pragma unroll
