@@ -87,7 +87,7 @@ class Batch:
             e = 130 * 2.0**-24 * size
             fin = np.isfinite(l)
             np.testing.assert_array_equal(np.isneginf(lse[rows]), ~fin)
-            assert np.all(np.abs(lse[rows] - l)[fin] <= (e + keys * 2.0**-24 + 2.0**-21 + 2.0**-23 * np.abs(np.where(fin, l, 0)))[fin])
+            assert np.all(np.abs(np.where(fin, lse[rows], 0) - np.where(fin, l, 0))[fin] <= (e + keys * 2.0**-24 + 2.0**-21 + 2.0**-23 * np.abs(np.where(fin, l, 0)))[fin])
             rel = (2.0**-11 + 2 * e + 2 * keys * 2.0**-24)[..., None]
             tol = rel * mean + (keys * 2.0**-33)[..., None] * 448 / S_ENC_V
             tol = tol + eps * (np.abs(o) + tol) + 2.0**-25
@@ -253,6 +253,47 @@ def test_many_sequences():
     b = Batch(seqs, 11)
     out, lse, cache = b.run(BF16)
     b.check(out, lse, only=set(rng.choice(4096, 300).tolist()) | {0, 1, 4094, 4095})
+    assert cache.read_status() == 0
+
+
+def test_one_page_sequences_over_and_over():
+    """Segments of one page, in which one of the softmax sets has nothing to do, among wide ones."""
+    rng = np.random.default_rng(30)
+    seqs = [(int(rng.integers(0, 90)), int(rng.integers(1, 64)) if i % 9 == 4 else int(rng.integers(1, 3))) for i in range(900)]
+    b = Batch(seqs, 31)
+    dev = b.device()
+    bufs = ops.TreeBuffers(b.T, len(seqs), F16)
+    out, lse, cache = b.run(F16, cache_dev=dev, bufs=bufs)
+    b.check(out, lse, only=set(range(0, 900, 7)) | set(range(4, 900, 45)))
+    first = out.clone(), lse.clone()
+    for _ in range(30):
+        out, lse, _ = b.run(F16, cache_dev=dev, bufs=bufs)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    assert cache.read_status() == 0
+
+
+def test_captured_graph_follows_lengths_and_selections():
+    """A captured call replayed on longer sequences and other blocks than it was captured with."""
+    b = Batch([(3000, 4), (2000, 4)], 32)
+    cache, q, bt, lens, qsl = b.device()
+    sel = torch.full((2, 17), -1, dtype=torch.int32, device=DEV)
+    n_sel = torch.zeros(2, dtype=torch.int32, device=DEV)
+    short = torch.tensor([4, 4], dtype=torch.int32, device=DEV)
+    bufs = ops.TreeBuffers(b.T, 2, F16)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ops.tree_attn(cache, q, bt, short, qsl, bufs, sel=sel, n_sel=n_sel)
+    graph.replay()
+    short.copy_(lens)
+    sels = [[0, 3, 9, 22], [1, 2, 14]]
+    for i, s in enumerate(sels):
+        sel[i, : len(s)] = torch.tensor(s, dtype=torch.int32)
+        n_sel[i] = len(s)
+    graph.replay()
+    torch.cuda.synchronize()
+    b.dtype = F16
+    b.check(bufs.out, bufs.lse, sels=sels)
     assert cache.read_status() == 0
 
 
