@@ -11,6 +11,7 @@ import ctypes
 import math
 import os
 import re
+import struct
 
 import torch
 
@@ -69,6 +70,12 @@ class _Rows(ctypes.Structure):
         ("q_idx_stride", ctypes.c_int64),
         ("dtype", ctypes.c_int32),
     ]
+
+
+# The same layouts packed to bytes in one step: a third of the time for calls that are short.
+_CACHE = struct.Struct("@PPqiiiiffP")
+_ROWS = struct.Struct("@5P5qi0P")
+assert _CACHE.size == ctypes.sizeof(_Cache) and _ROWS.size == ctypes.sizeof(_Rows)
 
 
 _lib = None
@@ -193,6 +200,11 @@ class KVCache:
         return _Cache(self.kv_pool.data_ptr(), self.idx_pool.data_ptr(), self.n_pages, PAGE_TOKENS,
                       KV_HEADS, HEAD_DIM, IDX_DIM, self.s_enc_k, self.s_enc_v,
                       self.status.data_ptr())
+
+    def packed(self):
+        """``struct()`` as bytes."""
+        return _CACHE.pack(self.kv_pool.data_ptr(), self.idx_pool.data_ptr(), self.n_pages, PAGE_TOKENS, KV_HEADS,
+                           HEAD_DIM, IDX_DIM, self.s_enc_k, self.s_enc_v, self.status.data_ptr())
 
     def read_status(self):
         out = ctypes.c_int32(0)
@@ -421,12 +433,13 @@ def _raw_stream(dev):
 
 if hasattr(torch._C, "_cuda_getCurrentRawStream"):  # the same without a Stream object
     _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _device_of(cache):
     """Index of the cache's CUDA device, which has to be the current one."""
     dev = cache.kv_pool.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != _current_device():
         raise ValueError(f"the cache is on {cache.kv_pool.device}, not on the current CUDA device")
     return dev
 
@@ -504,21 +517,22 @@ def rope_table_scaled(max_pos, rot_dim=HEAD_DIM, base=10000.0, scaling=None, fac
 
 def _rows(t, name, shape, dtype, dev):
     """(pointer, token stride) of projected rows [n, heads, 128] or [n, 128]."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+            st = t.stride()
+            if st[-1] == 1 and (len(st) == 2 or st[1] == HEAD_DIM):
+                ptr, stride = t.data_ptr(), st[0] if shape[0] > 1 else 0
+                if not (ptr | stride * (4 if dtype is torch.float32 else 2)) & 15:
+                    return ptr, stride
+                raise ValueError(f"{name} and its token stride must be aligned to 16 bytes")
+            raise ValueError(f"{name} must have contiguous channels and heads")
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch tensor") from None
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype} like q, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on the cache's device cuda:{dev}, got {t.device}")
-    st = t.stride()
-    if st[-1] != 1 or (len(st) == 3 and st[1] != HEAD_DIM):
-        raise ValueError(f"{name} must have contiguous channels and heads")
-    ptr, stride = t.data_ptr(), st[0] if shape[0] > 1 else 0
-    if ptr & 15 or stride * (4 if dtype is torch.float32 else 2) & 15:
-        raise ValueError(f"{name} and its token stride must be aligned to 16 bytes")
-    return ptr, stride
+    raise ValueError(f"{name} must be on the cache's device cuda:{dev}, got {t.device}")
 
 
 def rotary_insert(cache, q, k, v, idx_k, cos_sin, positions, slot_mapping, q_idx=None, interleaved=False, q8=None,
@@ -544,19 +558,17 @@ def rotary_insert(cache, q, k, v, idx_k, cos_sin, positions, slot_mapping, q_idx
     if q8 is None:
         q8 = torch.empty((n, Q_HEADS, HEAD_DIM), dtype=torch.uint8, device=q.device)
     if q_idx is None:
-        qi8 = qip = qi8p = None
-        qis = 0
+        qi8 = qi8p = None
+        qip = qis = 0
     else:
         qip, qis = _rows(q_idx, "q_idx", (n, IDX_HEADS, IDX_DIM), dtype, dev)
         if qi8 is None:
             qi8 = torch.empty((n, IDX_HEADS, IDX_DIM), dtype=torch.uint8, device=q.device)
         qi8p = _arg(qi8, torch.uint8, (n, IDX_HEADS, IDX_DIM), dev, "qi8")
-    rows = _Rows(qp, kp, vp, ip, qip, qs, ks, vs, i_s, qis, code)
     max_pos, rot_dim = cos_sin.shape
-    c = cache.struct()
     _check(lib().msa_rotary_insert(
-        ctypes.byref(c), ctypes.byref(rows), n, _arg(cos_sin, torch.float32, (max_pos, rot_dim), dev, "cos_sin"), max_pos,
-        rot_dim, 1 if interleaved else 0, _arg(positions, torch.int32, (n,), dev, "positions"),
+        cache.packed(), _ROWS.pack(qp, kp, vp, ip, qip, qs, ks, vs, i_s, qis, code), n,
+        _arg(cos_sin, torch.float32, (max_pos, rot_dim), dev, "cos_sin"), max_pos, rot_dim, 1 if interleaved else 0, _arg(positions, torch.int32, (n,), dev, "positions"),
         _arg(slot_mapping, torch.int64, (n,), dev, "slot_mapping"),
         _arg(q8, torch.uint8, (n, Q_HEADS, HEAD_DIM), dev, "q8"), qi8p, _raw_stream(dev)))
     return q8, qi8
@@ -579,9 +591,8 @@ def read_kv(cache, slot_mapping, dtype=torch.bfloat16, k=None, v=None, idx_k=Non
     if first is None:
         k, v = (torch.zeros((n, KV_HEADS, HEAD_DIM), dtype=dtype, device=cache.kv_pool.device) for _ in range(2))
         idx_k = torch.zeros((n, IDX_DIM), dtype=dtype, device=cache.kv_pool.device)
-    c = cache.struct()
     _check(lib().msa_read_kv(
-        ctypes.byref(c), _arg(slot_mapping, torch.int64, (n,), dev, "slot_mapping"), n, code,
+        cache.packed(), _arg(slot_mapping, torch.int64, (n,), dev, "slot_mapping"), n, code,
         None if k is None else _arg(k, dtype, (n, KV_HEADS, HEAD_DIM), dev, "k"),
         None if v is None else _arg(v, dtype, (n, KV_HEADS, HEAD_DIM), dev, "v"),
         None if idx_k is None else _arg(idx_k, dtype, (n, IDX_DIM), dev, "idx_k"), _raw_stream(dev)))
@@ -622,9 +633,8 @@ def tree_attn(cache, q, block_table, seq_lens, q_start_loc, bufs, tree_mask=None
     if (sel is None) != (n_sel is None):
         raise ValueError("sel and n_sel come together")
     dev = _device_of(cache)
-    c = cache.struct()
     _check(lib().msa_tree_attn(
-        ctypes.byref(c), _arg(q, torch.uint8, (T, Q_HEADS, HEAD_DIM), dev, "q"), Q_HEADS,
+        cache.packed(), _arg(q, torch.uint8, (T, Q_HEADS, HEAD_DIM), dev, "q"), Q_HEADS,
         HEAD_DIM ** -0.5 if softmax_scale is None else float(softmax_scale),
         _arg(block_table, torch.int32, (n_seqs, max_pages), dev, "block_table"), max_pages,
         _arg(seq_lens, torch.int32, (n_seqs,), dev, "seq_lens"),
