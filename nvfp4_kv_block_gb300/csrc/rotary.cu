@@ -21,9 +21,11 @@
 // loaded once for the part's heads.  The scale bytes of the four tokens wait in
 // shared memory: a group's scales of consecutive tokens are consecutive bytes of the
 // page, and leave together.  8,192 bf16 tokens: 25 us, 4.1 TB/s of the bytes above; 16,384
-// fp32 tokens at scattered slots: 66 us, 5.1 TB/s.
+// fp32 tokens at scattered slots: 62 us, 5.5 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <algorithm>
 
 #include "common.cuh"
 
@@ -194,133 +196,137 @@ __global__ void __launch_bounds__(kRopeThreads, 6) rotary_insert_kernel(const __
     fence_barrier_init();
   }
   __syncthreads();
-  const int t0 = ((int)blockIdx.x * kWarps + warp) * kTile, cnt = min(kTile, p.n_tokens - t0);
-  if (cnt <= 0) return;
   const int head0 = kind == 0 ? 4 * (part - 2) : kind == 4 ? 4 * (part - 7) : 0, heads = kind == 3 ? 1 : kPartHeads;
   const uint32_t bytes = heads * kHeadDim * sizeof(T);
-  if (lane == 0) mbar_arrive_expect_tx(bar, cnt * bytes);
-  __syncwarp();
-  if (lane < cnt)
-    bulk_g2s(smem_u32(s_rows[warp]) + lane * kPart,
-             static_cast<const T*>(p.rows[kind]) + (size_t)(t0 + lane) * p.stride[kind] + head0 * kHeadDim, bytes, bar);
-  // lane = (token sub, part l of its rows)
-  const bool live = sub < cnt;
-  const int t = t0 + sub;
-  const int pos = live && p.rot > 0 ? p.positions[t] : 0;
-  int64_t slot = live && cached ? p.slot_mapping[t] : -1;
-  if (slot >= 0 && (slot >> 7) >= p.n_pages) {
-    set_status(p.status, MSA_STATUS_BAD_SLOT);
-    slot = -1;
-  }
-  const bool known = pos >= 0 && pos < p.max_pos;
-  if (part == 2 && p.rot > 0 && live && !known) set_status(p.status, MSA_STATUS_BAD_SEQ);
-  // half pairs: lanes below h have partner chunks h apart (values are not turned)
-  const int h = p.interleaved || kind == 2 ? 0 : p.rot >> 4;
-  const int ca = l < h ? l : 2 * l, cb = l < h ? l + h : 2 * l + 1;
-  const bool turned = live && known && kind != 2 && (p.interleaved ? 16 * l < p.rot : l < h);
-  float c[8], s[8];
-  if (turned) {
-    const float* cs = p.cos_sin + (size_t)pos * p.rot + 8 * l;
-    load8(cs, c);
-    load8(cs + (p.rot >> 1), s);
-  }
-  if (!__all_sync(0xffffffffu, mbar_wait(bar, 0, WaitCtl{&s_abort, p.wait_ns}))) {
-    // nothing of the tile is written, and the copies in flight are waited for
-    if (lane == 0) set_status(p.status, MSA_STATUS_TIMEOUT);
-    mbar_wait_drain(bar, 0, p.wait_ns);
-    return;
-  }
-  const uint8_t* ra = s_rows[warp] + sub * kPart + 8 * ca * sizeof(T);
-  const uint8_t* rb = s_rows[warp] + sub * kPart + 8 * cb * sizeof(T);
-  auto rows = [&](int hd, float (&a)[8], float (&b)[8]) {
-    to_floats(Chunk<T>(ra + hd * kHeadDim * sizeof(T)), a);
-    to_floats(Chunk<T>(rb + hd * kHeadDim * sizeof(T)), b);
-    if (!turned) return;
-    if (h) {
-#pragma unroll
-      for (int u = 0; u < 8; ++u) turn(a[u], b[u], c[u], s[u]);
-    } else {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        turn(a[2 * u], a[2 * u + 1], c[u], s[u]);
-        turn(b[2 * u], b[2 * u + 1], c[4 + u], s[4 + u]);
-      }
+  int phase = 0;
+  for (int t0 = ((int)blockIdx.x * kWarps + warp) * kTile, more = 1; t0 < p.n_tokens && more;
+       t0 += (int)gridDim.x * kWarps * kTile, phase ^= 1, more = sizeof(T) == 4) {
+    const int cnt = min(kTile, p.n_tokens - t0);
+    __syncwarp();  // the last tile is read
+    if (lane == 0) mbar_arrive_expect_tx(bar, cnt * bytes);
+    __syncwarp();
+    if (lane < cnt)
+      bulk_g2s(smem_u32(s_rows[warp]) + lane * kPart,
+               static_cast<const T*>(p.rows[kind]) + (size_t)(t0 + lane) * p.stride[kind] + head0 * kHeadDim, bytes, bar);
+    // lane = (token sub, part l of its rows)
+    const bool live = sub < cnt;
+    const int t = t0 + sub;
+    const int pos = live && p.rot > 0 ? p.positions[t] : 0;
+    int64_t slot = live && cached ? p.slot_mapping[t] : -1;
+    if (slot >= 0 && (slot >> 7) >= p.n_pages) {
+      set_status(p.status, MSA_STATUS_BAD_SLOT);
+      slot = -1;
     }
-  };
-  if (!cached) {
-    uint8_t* dst = (kind == 0 ? p.q8 + (size_t)t * kQHeads * kHeadDim : p.qi8 + (size_t)t * kIdxHeads * kIdxDim) + head0 * kHeadDim;
+    const bool known = pos >= 0 && pos < p.max_pos;
+    if (part == 2 && p.rot > 0 && live && !known) set_status(p.status, MSA_STATUS_BAD_SEQ);
+    // half pairs: lanes below h have partner chunks h apart (values are not turned)
+    const int h = p.interleaved || kind == 2 ? 0 : p.rot >> 4;
+    const int ca = l < h ? l : 2 * l, cb = l < h ? l + h : 2 * l + 1;
+    const bool turned = live && known && kind != 2 && (p.interleaved ? 16 * l < p.rot : l < h);
+    float c[8], s[8];
+    if (turned) {
+      const float* cs = p.cos_sin + (size_t)pos * p.rot + 8 * l;
+      load8(cs, c);
+      load8(cs + (p.rot >> 1), s);
+    }
+    if (!__all_sync(0xffffffffu, mbar_wait(bar, phase, WaitCtl{&s_abort, p.wait_ns}))) {
+      // nothing of the tile is written, and the copies in flight are waited for
+      if (lane == 0) set_status(p.status, MSA_STATUS_TIMEOUT);
+      mbar_wait_drain(bar, phase, p.wait_ns);
+      return;
+    }
+    const uint8_t* ra = s_rows[warp] + sub * kPart + 8 * ca * sizeof(T);
+    const uint8_t* rb = s_rows[warp] + sub * kPart + 8 * cb * sizeof(T);
+    auto rows = [&](int hd, float (&a)[8], float (&b)[8]) {
+      to_floats(Chunk<T>(ra + hd * kHeadDim * sizeof(T)), a);
+      to_floats(Chunk<T>(rb + hd * kHeadDim * sizeof(T)), b);
+      if (!turned) return;
+      if (h) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) turn(a[u], b[u], c[u], s[u]);
+      } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          turn(a[2 * u], a[2 * u + 1], c[u], s[u]);
+          turn(b[2 * u], b[2 * u + 1], c[4 + u], s[4 + u]);
+        }
+      }
+    };
+    if (!cached) {
+      uint8_t* dst = (kind == 0 ? p.q8 + (size_t)t * kQHeads * kHeadDim : p.qi8 + (size_t)t * kIdxHeads * kIdxDim) + head0 * kHeadDim;
 #pragma unroll 1
-    for (int hd = 0; hd < kPartHeads; ++hd, dst += kHeadDim) {
+      for (int hd = 0; hd < kPartHeads; ++hd, dst += kHeadDim) {
+        float a[8], b[8];
+        rows(hd, a, b);
+        if (live) {
+          *reinterpret_cast<uint2*>(dst + 8 * ca) = to_fp8x8(a);
+          *reinterpret_cast<uint2*>(dst + 8 * cb) = to_fp8x8(b);
+        }
+      }
+      continue;
+    }
+    const int off = (int)(slot & 127);
+    if (kind == 3) {
+      float a[8], b[8];
+      rows(0, a, b);
+      if (slot >= 0) {
+        uint8_t* dst = p.idx_pool + (size_t)(slot >> 7) * kIdxPageBytes + off * kIdxDim;
+        *reinterpret_cast<uint2*>(dst + (((ca >> 1) ^ (off & 7)) << 4) + 8 * (ca & 1)) = to_fp8x8(a);
+        *reinterpret_cast<uint2*>(dst + (((cb >> 1) ^ (off & 7)) << 4) + 8 * (cb & 1)) = to_fp8x8(b);
+      }
+      continue;
+    }
+    const float s_enc = kind == 1 ? p.s_enc_k : p.s_enc_v;
+    uint8_t* head = p.kv_pool + (size_t)(slot >= 0 ? slot >> 7 : 0) * kKvPageBytes + (kind == 1 ? kOffKc : kOffVc);
+    const int wa = off * 64 + (code_chunk_pos(ca >> 2, off) << 4) + 4 * (ca & 3);
+    const int wb = off * 64 + (code_chunk_pos(cb >> 2, off) << 4) + 4 * (cb & 3);
+    // the other chunk of a 16-channel group is c ^ 1; of lanes below h lane c or c - h has it
+    const int xa = ca ^ 1, xb = cb ^ 1;
+    const int la = (lane & 24) | (l >= h ? l : xa < h ? xa : xa - h), lb = (lane & 24) | (l >= h ? l : xb < h ? xb : xb - h);
+    uint8_t* scales = s_scales[warp] + sub;
+#pragma unroll 1
+    for (int hd = 0; hd < kPartHeads; ++hd, head += kHeadBytes) {
       float a[8], b[8];
       rows(hd, a, b);
-      if (live) {
-        *reinterpret_cast<uint2*>(dst + 8 * ca) = to_fp8x8(a);
-        *reinterpret_cast<uint2*>(dst + 8 * cb) = to_fp8x8(b);
+      bool fine_a, fine_b;
+      const float ma = max_abs(a, s_enc, fine_a), mb = max_abs(b, s_enc, fine_b);
+      float ga = fmaxf(ma, mb), gb = ga;
+      if (h) {
+        const float a1 = __shfl_sync(0xffffffffu, ma, la), a2 = __shfl_sync(0xffffffffu, mb, la);
+        const float b1 = __shfl_sync(0xffffffffu, ma, lb), b2 = __shfl_sync(0xffffffffu, mb, lb);
+        if (l < h) {
+          ga = fmaxf(ma, xa < h ? a1 : a2);
+          gb = fmaxf(mb, xb < h ? b1 : b2);
+        }
       }
-    }
-    return;
-  }
-  const int off = (int)(slot & 127);
-  if (kind == 3) {
-    float a[8], b[8];
-    rows(0, a, b);
-    if (slot >= 0) {
-      uint8_t* dst = p.idx_pool + (size_t)(slot >> 7) * kIdxPageBytes + off * kIdxDim;
-      *reinterpret_cast<uint2*>(dst + (((ca >> 1) ^ (off & 7)) << 4) + 8 * (ca & 1)) = to_fp8x8(a);
-      *reinterpret_cast<uint2*>(dst + (((cb >> 1) ^ (off & 7)) << 4) + 8 * (cb & 1)) = to_fp8x8(b);
-    }
-    return;
-  }
-  const float s_enc = kind == 1 ? p.s_enc_k : p.s_enc_v;
-  uint8_t* head = p.kv_pool + (size_t)(slot >= 0 ? slot >> 7 : 0) * kKvPageBytes + (kind == 1 ? kOffKc : kOffVc);
-  const int wa = off * 64 + (code_chunk_pos(ca >> 2, off) << 4) + 4 * (ca & 3);
-  const int wb = off * 64 + (code_chunk_pos(cb >> 2, off) << 4) + 4 * (cb & 3);
-  // the other chunk of a 16-channel group is c ^ 1; of lanes below h lane c or c - h has it
-  const int xa = ca ^ 1, xb = cb ^ 1;
-  const int la = (lane & 24) | (l >= h ? l : xa < h ? xa : xa - h), lb = (lane & 24) | (l >= h ? l : xb < h ? xb : xb - h);
-  uint8_t* scales = s_scales[warp] + sub;
-#pragma unroll 1
-  for (int hd = 0; hd < kPartHeads; ++hd, head += kHeadBytes) {
-    float a[8], b[8];
-    rows(hd, a, b);
-    bool fine_a, fine_b;
-    const float ma = max_abs(a, s_enc, fine_a), mb = max_abs(b, s_enc, fine_b);
-    float ga = fmaxf(ma, mb), gb = ga;
-    if (h) {
-      const float a1 = __shfl_sync(0xffffffffu, ma, la), a2 = __shfl_sync(0xffffffffu, mb, la);
-      const float b1 = __shfl_sync(0xffffffffu, ma, lb), b2 = __shfl_sync(0xffffffffu, mb, lb);
-      if (l < h) {
-        ga = fmaxf(ma, xa < h ? a1 : a2);
-        gb = fmaxf(mb, xb < h ? b1 : b2);
+      if (!(fine_a && fine_b)) {
+        const float most = fminf(1e30f / s_enc, 3e38f);
+        make_finite(a, most);
+        make_finite(b, most);
       }
+      const uint32_t sa = f32_to_e4m3(__fmul_rn(sixth(ga), s_enc)), sb = f32_to_e4m3(__fmul_rn(sixth(gb), s_enc));
+      const uint32_t va = code_word(a, s_enc, e4m3_to_f32(sa), s_inv[sa]), vb = code_word(b, s_enc, e4m3_to_f32(sb), s_inv[sb]);
+      if (slot >= 0) {
+        *reinterpret_cast<uint32_t*>(head + wa) = va;
+        *reinterpret_cast<uint32_t*>(head + wb) = vb;
+      }
+      if ((ca & 1) == 0) scales[(hd * 8 + (ca >> 1)) * kTile] = (uint8_t)sa;
+      if ((cb & 1) == 0) scales[(hd * 8 + (cb >> 1)) * kTile] = (uint8_t)sb;
     }
-    if (!(fine_a && fine_b)) {
-      const float most = fminf(1e30f / s_enc, 3e38f);
-      make_finite(a, most);
-      make_finite(b, most);
-    }
-    const uint32_t sa = f32_to_e4m3(__fmul_rn(sixth(ga), s_enc)), sb = f32_to_e4m3(__fmul_rn(sixth(gb), s_enc));
-    const uint32_t va = code_word(a, s_enc, e4m3_to_f32(sa), s_inv[sa]), vb = code_word(b, s_enc, e4m3_to_f32(sb), s_inv[sb]);
-    if (slot >= 0) {
-      *reinterpret_cast<uint32_t*>(head + wa) = va;
-      *reinterpret_cast<uint32_t*>(head + wb) = vb;
-    }
-    if ((ca & 1) == 0) scales[(hd * 8 + (ca >> 1)) * kTile] = (uint8_t)sa;
-    if ((cb & 1) == 0) scales[(hd * 8 + (cb >> 1)) * kTile] = (uint8_t)sb;
-  }
-  // the scale bytes: lane = (head, group) of the four tokens, as one word where they are consecutive
-  __syncwarp();
-  const uint32_t word = reinterpret_cast<const uint32_t*>(s_scales[warp])[lane];
-  const int64_t slot0 = __shfl_sync(0xffffffffu, slot, 0);
-  const bool run = __all_sync(0xffffffffu, slot == slot0 + sub && (slot0 & 3) == 0);
-  const size_t place = (size_t)(lane >> 3) * kHeadBytes + (kind == 1 ? kOffKs : kOffVs) + (lane & 7) * kPageTokens;
-  if (run) {
-    if (slot0 >= 0) *reinterpret_cast<uint32_t*>(p.kv_pool + (size_t)(slot0 >> 7) * kKvPageBytes + place + (slot0 & 127)) = word;
-  } else {
+    // the scale bytes: lane = (head, group) of the four tokens, as one word where they are consecutive
+    __syncwarp();
+    const uint32_t word = reinterpret_cast<const uint32_t*>(s_scales[warp])[lane];
+    const int64_t slot0 = __shfl_sync(0xffffffffu, slot, 0);
+    const bool run = __all_sync(0xffffffffu, slot == slot0 + sub && (slot0 & 3) == 0);
+    const size_t place = (size_t)(lane >> 3) * kHeadBytes + (kind == 1 ? kOffKs : kOffVs) + (lane & 7) * kPageTokens;
+    if (run) {
+      if (slot0 >= 0) *reinterpret_cast<uint32_t*>(p.kv_pool + (size_t)(slot0 >> 7) * kKvPageBytes + place + (slot0 & 127)) = word;
+    } else {
 #pragma unroll
-    for (int i = 0; i < kTile; ++i) {
-      const int64_t si = __shfl_sync(0xffffffffu, slot, 8 * i);
-      if (si >= 0) p.kv_pool[(size_t)(si >> 7) * kKvPageBytes + place + (si & 127)] = (uint8_t)(word >> (8 * i));
+      for (int i = 0; i < kTile; ++i) {
+        const int64_t si = __shfl_sync(0xffffffffu, slot, 8 * i);
+        if (si >= 0) p.kv_pool[(size_t)(si >> 7) * kKvPageBytes + place + (si & 127)] = (uint8_t)(word >> (8 * i));
+      }
     }
   }
 }
@@ -372,8 +378,13 @@ cudaError_t launch_rotary_insert(const msa_cache* c, const msa_rows* r, int n_to
   rp.qi8 = qi8;
   rp.status = c->status;
   rp.wait_ns = launch_settings().wait_ns;
-  const int per_block = kRopeThreads / 32 * kTile;
-  const dim3 grid((unsigned)((n_tokens + (long long)per_block - 1) / per_block), r->q_idx ? 9 : 7), block(kRopeThreads);
+  // tiles of a warp of fp32 rows: up to three while the grid still fills six CTAs per SM twice (16,384
+  // tokens at scattered slots: 62 us, 66 with one).  One of 16-bit rows (16,384 tokens: 41.6 us, 42.7
+  // with three).
+  const int per_block = kRopeThreads / 32 * kTile, parts = r->q_idx ? 9 : 7;
+  const long long blocks = ((long long)n_tokens + per_block - 1) / per_block;
+  const long long tiles = r->dtype == MSA_DTYPE_F32 ? std::min(3ll, std::max(1ll, blocks * parts / (12ll * n_sm))) : 1;
+  const dim3 grid((unsigned)((blocks + tiles - 1) / tiles), parts), block(kRopeThreads);
   if (r->dtype == MSA_DTYPE_F32) rotary_insert_kernel<float><<<grid, block, 0, stream>>>(rp);
   else if (r->dtype == MSA_DTYPE_BF16) rotary_insert_kernel<__nv_bfloat16><<<grid, block, 0, stream>>>(rp);
   else rotary_insert_kernel<__half><<<grid, block, 0, stream>>>(rp);

@@ -92,6 +92,24 @@ def test_large_call_in_page_order_and_without_index_queries():
     _check(parts, slots, pos, table, True, cache, q8, want[1], before)
 
 
+@pytest.mark.parametrize("n", [6500, 13001, 20011])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_large_call_equals_small_ones(n, dtype):
+    """Warps with several tiles each, the last ones partly empty, scattered and in runs."""
+    parts, slots, pos, pages, table = _inputs(n, DT[dtype], n, True, 64)
+    slots[1000:3000] = torch.arange(pages * 128, pages * 128 + 2000, device=DEV)
+    pages += 17
+    slots[77::501] = -1
+    a, b = _cache(pages)[0], _cache(pages)[0]
+    q8, qi8 = ops.rotary_insert(a, *parts[:4], table, pos, slots, q_idx=parts[4])
+    for lo in range(0, n, 1000):
+        c = slice(lo, lo + 1000)
+        w8, wi8 = ops.rotary_insert(b, *(p[c] for p in parts[:4]), table, pos[c], slots[c], q_idx=parts[4][c])
+        assert torch.equal(q8[c], w8) and torch.equal(qi8[c], wi8)
+    assert torch.equal(a.kv_pool, b.kv_pool) and torch.equal(a.idx_pool, b.idx_pool)
+    assert a.read_status() == 0
+
+
 def test_skipped_and_bad_slots_and_positions():
     n = 40
     parts, slots, pos, pages, table = _inputs(n, torch.float32, 11, False, 128)
