@@ -297,6 +297,38 @@ def test_captured_graph_follows_lengths_and_selections():
     assert cache.read_status() == 0
 
 
+def test_pages_whose_offsets_pass_32_bits():
+    """The last pages of pools of 19.9 and 4.4 GB, written, attended and read as in a small pool."""
+    b = Batch([(900, 5), (260, 1)], 33)
+    small, q, bt, lens, qsl = b.device()
+    n, far = small.n_pages, 270_000
+    kv = torch.empty((far, ops.KV_PAGE_BYTES), dtype=torch.uint8, device=DEV)
+    ix = torch.empty((far, ops.IDX_PAGE_BYTES), dtype=torch.uint8, device=DEV)
+    kv[far - n:] = small.kv_pool
+    ix[far - n:] = small.idx_pool
+    big = ops.KVCache.from_pools(kv, ix, S_ENC_K, S_ENC_V)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(34)
+    rows = torch.randn((6, 33, 128), generator=g, device=DEV).to(F16)
+    pos = torch.tensor([900, 901, 902, 903, 904, 260], dtype=torch.int32, device=DEV)
+    seq = torch.tensor([0, 0, 0, 0, 0, 1], device=DEV)
+    slots = bt[seq, pos.long() // 128].long() * 128 + pos % 128
+    table = ops.rope_table_scaled(1024, 128)
+    got = []
+    for cache, up in ((small, 0), (big, far - n)):
+        q8, _ = ops.rotary_insert(cache, rows[:, :16], rows[:, 16:20], rows[:, 20:24], rows[:, 24], table, pos,
+                                  slots + 128 * up)
+        bufs = ops.TreeBuffers(6, 2, F16)
+        pages = torch.where(bt >= 0, bt + up, bt)
+        got.append([q8, ops.tree_attn(cache, q8, pages, lens, qsl, bufs), bufs.lse, *ops.read_kv(cache, slots + 128 * up)])
+        assert cache.read_status() == 0
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+    assert torch.equal(big.kv_pool[far - n:], small.kv_pool) and torch.equal(big.idx_pool[far - n:], small.idx_pool)
+    b.q8, b.pool, b.dtype = got[1][0].cpu().numpy(), small.kv_pool.cpu().numpy(), F16
+    b.check(got[1][1], got[1][2])
+
+
 def test_repeats_are_bit_equal_and_workspaces_come_to_rest():
     b = Batch([(4000, 40), (6000, 3)], 12)
     dev = b.device()
