@@ -530,8 +530,8 @@ int msa_debug_fp8_page(const msa_cache* cache, int64_t page, uint8_t* k8, uint8_
  *                               runs out after wait_limit_ns: the call sets
  *                               MSA_STATUS_TIMEOUT, leaves sel/n_sel unwritten
  *                               and its workspace barrier word at rest;
- *   MSA_INJECT_ATTENTION_TIMEOUT  every CTA of the attention kernel leaves out
- *                               the copy of its first page, so the waits for it
+ *   MSA_INJECT_ATTENTION_TIMEOUT  every CTA of an attention kernel (sparse
+ *                               decode or tree) leaves out the copy of its first page, so the waits for it
  *                               run out after wait_limit_ns: the call sets
  *                               MSA_STATUS_TIMEOUT, its CTAs release tensor
  *                               memory only after their copies and tensor-core

@@ -279,6 +279,12 @@ __device__ __forceinline__ bool mbar_wait_drain(uint32_t bar, uint32_t parity, u
   return false;
 }
 
+// The limit of such a wait where copies are known to be on their way: a second at least, however
+// short the launch's own limit is.
+__device__ __forceinline__ unsigned long long drain_ns(unsigned long long limit_ns) {
+  return limit_ns > 1000000000ull ? limit_ns : 1000000000ull;
+}
+
 // Grid-wide barrier of a launch whose CTAs are all co-resident (cooperative
 // launch), on one 64-bit word of global memory: generation in the high half,
 // arrival count in the low half.  Called by one thread per CTA; every CTA must

@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kRopeThreads, 6) rotary_insert_kernel(const __
     if (!__all_sync(0xffffffffu, mbar_wait(bar, phase, WaitCtl{&s_abort, p.wait_ns}))) {
       // nothing of the tile is written, and the copies in flight are waited for
       if (lane == 0) set_status(p.status, MSA_STATUS_TIMEOUT);
-      mbar_wait_drain(bar, phase, p.wait_ns);
+      mbar_wait_drain(bar, phase, drain_ns(p.wait_ns));
       return;
     }
     const uint8_t* ra = s_rows[warp] + sub * kPart + 8 * ca * sizeof(T);

@@ -131,6 +131,7 @@ struct TreeParams {
   int part_rows;
   int* status;
   unsigned long long wait_ns;
+  int inject;  // test only: a CTA's first page is not copied, so that the waits for it run out
 };
 
 __device__ __forceinline__ bool elect_one() {
@@ -512,7 +513,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
                 if (lane == 0) {
                   const int pos = bl * kPageTokens;
                   s_info[e % kInfo] = make_int2(pos, ph < 0 ? 0 : min(kPageTokens, w.s.seq_len - pos));
-                  if (ph < 0) {
+                  if (p.inject && e == 0) {
+                  } else if (ph < 0) {
                     mbar_arrive(bar(kBRawFull + st));  // nothing to copy: no token of the page is valid
                   } else {
                     mbar_arrive_expect_tx(bar(kBRawFull + st), kHeadBytes);
@@ -1031,11 +1033,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
   tc_fence_before();
   __syncthreads();
   if (tid == 0) {
-    mbar_wait_drain(bar(kBDone), 0, p.wait_ns);  // every tcgen05.mma is done
+    mbar_wait_drain(bar(kBDone), 0, drain_ns(p.wait_ns));  // every tcgen05.mma is done
     if (*s_abort) {
       set_status(p.status, MSA_STATUS_TIMEOUT);
-      for (int e = max(0, *s_issued - kRaw); e < *s_issued; ++e)  // copies that may still be landing
-        mbar_wait_drain(bar(kBRawFull + e % kRaw), (e / kRaw) & 1, p.wait_ns);
+      for (int e = max(p.inject ? 1 : 0, *s_issued - kRaw); e < *s_issued; ++e)  // copies that may still be landing
+        mbar_wait_drain(bar(kBRawFull + e % kRaw), (e / kRaw) & 1, drain_ns(p.wait_ns));
     }
   }
   __syncthreads();
@@ -1158,6 +1160,7 @@ cudaError_t launch_tree_attn(const msa_cache* c, const uint8_t* q, float softmax
   tp.part_o = reinterpret_cast<float*>(w);
   tp.status = c->status;
   tp.wait_ns = launch_settings().wait_ns;
+  tp.inject = (launch_settings().inject & MSA_INJECT_ATTENTION_TIMEOUT) != 0;
   const int most = n_sm < kTreeCtas ? n_sm : kTreeCtas;
   e = launch_pdl(tree_attn_kernel, dim3(most), dim3(kTreeThreads), kTreeSmem, stream, tp);
   if (e != cudaSuccess) return e;

@@ -511,6 +511,26 @@ def test_two_calls_at_once_with_a_workspace_each():
         assert d[0].read_status() == 0
 
 
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_recovers():
+    """Every CTA leaves out the copy of its first page: its waits end after their limit, the CTA
+    waits for what it has in flight and returns; the workspace is at rest again."""
+    b = Batch([(4000, 3), (900, 40), (20, 1)], 35)
+    dev = b.device()
+    bufs = ops.TreeBuffers(b.T, 3, F16)
+    want = [x.clone() for x in b.run(F16, cache_dev=dev, bufs=bufs)[:2]]
+    try:
+        ops.set_fault_injection(ops.INJECT_ATTENTION_TIMEOUT, 5_000_000)
+        b.run(F16, cache_dev=dev, bufs=bufs)
+        assert dev[0].read_status() == ops.STATUS_TIMEOUT
+    finally:
+        ops.set_fault_injection(0, 0)
+    dev[0].status.zero_()
+    assert torch.count_nonzero(bufs.ws[: b.T * 16]) == 0
+    for _ in range(2):
+        out, lse, cache = b.run(F16, cache_dev=dev, bufs=bufs)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1]) and cache.read_status() == 0
+
+
 def test_refusals():
     b = Batch([(300, 2)], 17)
     cache, q, bt, lens, qsl = b.device()
