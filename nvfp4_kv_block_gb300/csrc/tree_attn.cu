@@ -32,12 +32,12 @@
 //   warps 12-23   K conversion (four warps, thread = token) and V conversion (eight,
 //                 thread = token and half of the channels).
 //
-// What bounds it.  A page of 18,432 bytes takes a CTA 0.80 us with up to 8 drafts, 0.95 us up
-// to 16, 1.1 us up to 32 and 2.0 us with two tiles; its products take the tensor pipe 0.39 us
+// What bounds it.  A page of 18,432 bytes takes a CTA 0.79 us with up to 8 drafts, 0.95 us up
+// to 16, 1.0 us up to 32 and 1.8 us with two tiles; its products take the tensor pipe 0.39 us
 // per tile.  The rest is instruction issue and hand-offs: 1,958 warp instructions of
-// conversion a page (K 763, V 1,195), 911 (one draft) to 2,550 (32) of softmax, about 1,450
-// of waits.  32 sequences of 32,768 tokens, one draft each: 185 us, 3.3 TB/s; 8 of 131,072
-// with 64 drafts: 414 us, 1.26 PFLOP/s; one of 4,096: 14.9 us, a chain of latencies
+// conversion a page (K 763, V 1,195), 911 (one draft) to 2,550 (32) of softmax, about 1,100
+// of waits.  32 sequences of 32,768 tokens, one draft each: 184 us, 3.3 TB/s; 8 of 131,072
+// with 64 drafts: 380 us, 1.37 PFLOP/s; one of 4,096: 14.8 us, a chain of latencies
 // (lengths and ranges 2.6, first page 2.4, its scores 1.4, joining the row copies 1.7, the
 // merge kernel 4).
 #include <cuda_bf16.h>
@@ -87,10 +87,15 @@ constexpr float kTreeUnset = 3e38f;    // shift of a row without a reference: a 
 constexpr float kTreeLog2e = 1.4426950408889634f, kTreeLn2 = 0.6931471805599453f;
 
 // Weights of the partition, in units of 0.2 us: a page of a sequence with up to 8, 16,
-// 32 and 64 drafts (0.80, 0.95, 1.1 and 2.0 us per page of a CTA on 32K contexts), and
-// the fixed part of a (sequence, KV head).  The least share of a CTA is a page's
-// weight, so that every CTA between a sequence's first and last has pages of it.
-__host__ __device__ __forceinline__ int tree_page_weight(int n_q) { return n_q <= 8 ? 4 : n_q <= 16 ? 5 : n_q <= 32 ? 6 : 10; }
+// 32 and 64 drafts (0.80, 0.95, 1.1 and 2.0 us per page of a CTA on 32K contexts; without
+// row copies 1.0 and 1.8 us up to 32 and 64), and the fixed part of a (sequence, KV head).
+// The least share of a CTA is a page's weight, so that every CTA between a sequence's
+// first and last has pages of it.
+template <bool kCopies>
+__device__ __forceinline__ int tree_page_weight(int n_q) {
+  if (!kCopies) return n_q <= 32 ? 5 : 9;
+  return n_q <= 8 ? 4 : n_q <= 16 ? 5 : n_q <= 32 ? 6 : 10;
+}
 constexpr int kFixedWeight = 10, kLeastShare1 = 6, kLeastShare2 = 10;
 
 // Copies of the query rows in a one-tile segment's 128 rows: with few rows every
@@ -233,6 +238,7 @@ struct SeqWork {
   SeqInfo s;
   int ctx, first, chosen, n_vis, pw;
 };
+template <bool kCopies>
 __device__ __forceinline__ SeqWork seq_work(const TreeParams& p, int b) {
   SeqWork w;
   // (all loads at once: a sequence's start is a chain of them)
@@ -248,7 +254,7 @@ __device__ __forceinline__ SeqWork seq_work(const TreeParams& p, int b) {
   w.first = w.ctx / kPageTokens;
   w.chosen = w.first;
   w.n_vis = 0;
-  w.pw = tree_page_weight(w.s.n_q);
+  w.pw = tree_page_weight<kCopies>(w.s.n_q);
   if (!w.s.ok || w.s.n_q == 0) return w;
   if (p.sel) {
     int top = -1;
@@ -294,6 +300,8 @@ __device__ __forceinline__ uint32_t pack16(float a, float b, bool f16) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// kCopies false: one copy of the rows whatever their number.
+template <bool kCopies>
 __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid_constant__ TreeParams p) {
   extern __shared__ uint8_t smem_raw[];
   // (pointer arithmetic, no integer cast: the accesses stay shared-memory instructions)
@@ -378,7 +386,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
     SeqWork last{};
     const int b0 = min(tid * per, p.n_seqs), b1 = min(b0 + per, p.n_seqs);
     for (int b = b0; b < b1; ++b) {
-      const SeqWork w = seq_work(p, b);
+      const SeqWork w = seq_work<kCopies>(p, b);
       last = w;
       if (!w.s.ok && blockIdx.x == 0) set_status(p.status, MSA_STATUS_BAD_SEQ);
       if (w.n_vis > 0) mine += (long long)kKvHeads * (w.pw * w.n_vis + kFixedWeight);
@@ -425,7 +433,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
         const long long lo = range_start(quota, extra, blockIdx.x), hi = range_start(quota, extra, blockIdx.x + 1);
         long long off = s_scan[26];
         for (int b = (int)s_scan[25]; ok && b < p.n_seqs && off < hi; ++b) {
-          const SeqWork w = per == 1 && b == (int)s_scan[25] ? *s_first : seq_work(p, b);
+          const SeqWork w = per == 1 && b == (int)s_scan[25] ? *s_first : seq_work<kCopies>(p, b);
           if (w.n_vis == 0) continue;
           const long long wg = (long long)w.pw * w.n_vis + kFixedWeight;
           // the selection, one entry per lane: its place among the chosen ones
@@ -629,7 +637,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
         // the second tile is also the exchange buffer of a segment with row copies (all segments or
         // none wait: a parity does not tell phase k - 1 from k - 3, so every phase is seen in turn)
         if (wide && k > 0 && !twait(bar(kBOFree), (k - 1) & 1, wc)) break;
-        const int copies = tree_copies(r.n_q), gap = 128 / copies;
+        const int copies = kCopies ? tree_copies(r.n_q) : 1, gap = 128 / copies;
         for (int x = lane; x < r.n_q * 32; x += 32) {
           const int row = x >> 3, c = x & 7;
           const uint8_t* src = p.q + ((size_t)(r.q0 + (row >> 2)) * kQHeads + kGqa * r.g + (row & 3)) * kHeadDim + 16 * c;
@@ -905,9 +913,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       __syncwarp();
       if (r.n_pg < 0) break;
       if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
-      const bool go = tree_copies(r.n_q) > 1 ? segment(r, k, std::integral_constant<int, 0>{})
-                      : r.n_q <= 32          ? segment(r, k, std::integral_constant<int, 1>{})
-                                             : segment(r, k, std::integral_constant<int, 2>{});
+      bool go;
+      if constexpr (kCopies) {
+        go = tree_copies(r.n_q) > 1 ? segment(r, k, std::integral_constant<int, 0>{})
+             : r.n_q <= 32          ? segment(r, k, std::integral_constant<int, 1>{})
+                                    : segment(r, k, std::integral_constant<int, 2>{});
+      } else {
+        go = r.n_q <= 32 ? segment(r, k, std::integral_constant<int, 1>{}) : segment(r, k, std::integral_constant<int, 2>{});
+      }
       if (!go) break;
       e0 += r.n_pg;
     }
@@ -1130,7 +1143,9 @@ cudaError_t launch_tree_attn(const msa_cache* c, const uint8_t* q, float softmax
   static DeviceSetup setup;
   int dev = 0, n_sm = 0;
   cudaError_t e = setup.get(&dev, &n_sm, [](int) {
-    return cudaFuncSetAttribute(tree_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTreeSmem);
+    constexpr auto kMax = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    const cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<true>, kMax, kTreeSmem);
+    return e != cudaSuccess ? e : cudaFuncSetAttribute(tree_attn_kernel<false>, kMax, kTreeSmem);
   });
   if (e != cudaSuccess) return e;
   TreeParams tp{};
@@ -1162,7 +1177,12 @@ cudaError_t launch_tree_attn(const msa_cache* c, const uint8_t* q, float softmax
   tp.wait_ns = launch_settings().wait_ns;
   tp.inject = (launch_settings().inject & MSA_INJECT_ATTENTION_TIMEOUT) != 0;
   const int most = n_sm < kTreeCtas ? n_sm : kTreeCtas;
-  e = launch_pdl(tree_attn_kernel, dim3(most), dim3(kTreeThreads), kTreeSmem, stream, tp);
+  // Without the row copies' code two tiles run faster (8 sequences of 131,072 with 64 drafts: 380 us,
+  // 415 with it; 24 of 30,720 with 17 to 32 drafts 172 to 179 us, 178 to 190), few drafts slower
+  // (8 to 16 drafts: 170 us, 161 with it): by the mean, mixtures of 1 to 64 drafts included
+  // (mean 14: 171 us both, 20: 176 and 184, 38: 261 and 278).
+  e = launch_pdl(n_q_total > 16ll * n_seqs ? tree_attn_kernel<false> : tree_attn_kernel<true>, dim3(most),
+                 dim3(kTreeThreads), kTreeSmem, stream, tp);
   if (e != cudaSuccess) return e;
   return launch_pdl(tree_merge_kernel, dim3((unsigned)(n_q_total * kKvHeads)), dim3(256), 0, stream, tp);
 }

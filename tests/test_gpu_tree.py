@@ -132,6 +132,8 @@ CASES = {
     "straddle_64": [(1000, 64)],
     "long_one": [(9000, 1)],
     "long_20": [(7000, 20)],
+    "mostly_wide": [(700, 33), (0, 5), (64, 64), (129, 1), (2000, 60), (1, 12)],
+    "mostly_small": [(500, 20), (300, 1), (200, 2), (1300, 4), (90, 40), (260, 1), (5, 1)],
     "mixed": [(700, 33), (0, 5), (300, 0), (64, 64), (129, 1), (2500, 8), (1, 1), (383, 2)],
 }
 
@@ -144,7 +146,7 @@ def test_chain(name):
     assert cache.read_status() == 0
 
 
-@pytest.mark.parametrize("name", ["no_context_64", "tile_32", "tiles_33", "straddle_64", "mixed", "edge_126_3"])
+@pytest.mark.parametrize("name", ["no_context_64", "tile_32", "tiles_33", "straddle_64", "mostly_wide", "mostly_small", "mixed", "edge_126_3"])
 @pytest.mark.parametrize("dtype", [BF16, F16])
 def test_tree(name, dtype):
     b = Batch(CASES[name], 2)
