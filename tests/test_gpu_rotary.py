@@ -245,6 +245,29 @@ def test_read_into_given_rows_leaves_the_others():
     assert torch.equal(idx, ops.read_kv(cache, slots.clamp(0, 383), dtype=torch.float32)[2])
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_rows_and_outputs_that_begin_at_16_bytes(dtype):
+    """Inputs and outputs 16 bytes into their storage (no wider alignment) as from the front."""
+    n, t = 300, DT[dtype]
+    e = 16 // torch.empty((), dtype=t).element_size()
+    parts, slots, pos, pages, table = _inputs(n, t, 41, False, 64)
+
+    def shifted(x):
+        y = torch.empty(x.numel() + e, dtype=x.dtype, device=DEV)[e:].view(x.shape)
+        assert y.data_ptr() % 32 == 16
+        return y.copy_(x)
+
+    a, b = _cache(pages)[0], _cache(pages)[0]
+    want = ops.rotary_insert(a, *parts[:4], table, pos, slots, q_idx=parts[4])
+    got = ops.rotary_insert(b, *(shifted(x) for x in parts[:4]), table, pos, slots, q_idx=shifted(parts[4]))
+    assert torch.equal(a.kv_pool, b.kv_pool) and torch.equal(a.idx_pool, b.idx_pool)
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
+    outs = [shifted(torch.zeros(shape, dtype=t, device=DEV)) for shape in ((n, 4, 128), (n, 4, 128), (n, 128))]
+    ops.read_kv(a, slots, k=outs[0], v=outs[1], idx_k=outs[2])
+    for x, y in zip(outs, ops.read_kv(a, slots, dtype=t)):
+        assert torch.equal(x, y)
+
+
 def test_written_rows_come_back():
     """Insert with this call, read back, and the same bytes through quantize_kv_insert."""
     n = 200

@@ -482,6 +482,26 @@ def test_calls_of_different_sizes_share_a_workspace():
         x.check(out, lse)
 
 
+def test_two_captured_graphs_share_a_workspace():
+    small, large = Batch([(5000, 2), (30, 1)], 36), Batch([(4000, 40), (3000, 30)], 37)
+    bufs = [ops.TreeBuffers(x.T, len(x.seqs), F16) for x in (small, large)]
+    bufs[0].ws = bufs[1].ws
+    devs, graphs = [x.device() for x in (small, large)], []
+    torch.cuda.synchronize()
+    for d, u in zip(devs, bufs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            ops.tree_attn(*d, u)
+    for _ in range(3):
+        for graph in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    for x, d, u in zip((small, large), devs, bufs):
+        x.dtype = F16
+        x.check(u.out, u.lse)
+        assert d[0].read_status() == 0
+
+
 def test_another_stream_than_the_tensors_own():
     b = Batch([(2000, 4), (100, 60)], 23)
     dev = b.device()
