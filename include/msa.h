@@ -92,10 +92,12 @@ typedef struct CUstream_st* msa_stream_t; /* same type as cudaStream_t */
  * copies and tensor-core operations in flight, releases tensor memory and
  * returns.  The context stays usable. */
 
-/* The KV cache and its metadata.  Caller-owned; the library only reads it. */
+/* The KV cache and its metadata.  Caller-owned; the library only reads it.  Both
+ * pools begin on 16-byte boundaries: a call whose kernels would meet a misaligned
+ * address returns MSA_ERR_INVALID_ARG. */
 typedef struct msa_cache {
-  void* kv_pool;        /* device, n_pages * 73,728 bytes (format above) */
-  void* idx_pool;       /* device, n_pages * 16,384 bytes (format above) */
+  void* kv_pool;        /* device, n_pages * 73,728 bytes (format above), 16-byte aligned */
+  void* idx_pool;       /* device, n_pages * 16,384 bytes (format above), 16-byte aligned */
   int64_t n_pages;      /* physical pages in both pools */
   int32_t page_tokens;  /* must be 128 */
   int32_t n_kv_heads;   /* must be 4 */

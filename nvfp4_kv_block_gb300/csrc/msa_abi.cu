@@ -65,6 +65,13 @@ int check_cache(const msa_cache* c) {
   return MSA_OK;
 }
 
+// The bytes that a call's kernels move at once decide what its pools have to be aligned to (1:
+// not touched).  Checked behind everything else, so that no other code hides.
+int check_pools(const msa_cache* c, uintptr_t kv, uintptr_t idx) {
+  const bool ok = reinterpret_cast<uintptr_t>(c->kv_pool) % kv == 0 && reinterpret_cast<uintptr_t>(c->idx_pool) % idx == 0;
+  return ok ? MSA_OK : MSA_ERR_INVALID_ARG;
+}
+
 int launched(cudaError_t e) { return e == cudaSuccess ? MSA_OK : MSA_ERR_LAUNCH_FAILED; }
 
 }  // namespace
@@ -80,6 +87,7 @@ int msa_quantize_kv_insert(const msa_cache* cache, const float* k, const float* 
   if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
        reinterpret_cast<uintptr_t>(idx_k)) & 15)
     return MSA_ERR_INVALID_ARG;  // float4 loads
+  if (int rc = check_pools(cache, 4, 4)) return rc;
   return launched(msa::launch_quantize_insert(cache, k, v, idx_k, slot_mapping, n_tokens,
                                               reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -108,6 +116,7 @@ int msa_indexer_topk(const msa_cache* cache, const uint8_t* q_idx, const float* 
     return MSA_ERR_INVALID_ARG;
   if (ws_bytes < msa_indexer_workspace_bytes(n_q_total, max_pages))
     return MSA_ERR_WORKSPACE_TOO_SMALL;
+  if (int rc = check_pools(cache, 1, 16)) return rc;
   return launched(msa::launch_indexer_topk(cache, q_idx, w, block_table, max_pages, seq_lens,
                                            q_start_loc, n_seqs, n_q_total, sel, n_sel, ws, 0,
                                            0x7FFFFFFF, nullptr,
@@ -132,6 +141,7 @@ int msa_indexer_topk_range(const msa_cache* cache, const uint8_t* q_idx, const f
     return MSA_ERR_INVALID_ARG;
   if (ws_bytes < msa_indexer_workspace_bytes(n_q_total, max_pages))
     return MSA_ERR_WORKSPACE_TOO_SMALL;
+  if (int rc = check_pools(cache, 1, 16)) return rc;
   // sel / n_sel are not written in range mode; the candidates are
   return launched(msa::launch_indexer_topk(cache, q_idx, w, block_table, max_pages, seq_lens,
                                            q_start_loc, n_seqs, n_q_total, nullptr, nullptr, ws,
@@ -174,6 +184,7 @@ int msa_indexer_topk_noalloc(const msa_cache* cache, const uint8_t* q_idx, const
     return MSA_ERR_INVALID_ARG;
   if (msa_indexer_workspace_bytes(n_q_total, max_pages) > MSA_INDEXER_NOALLOC_SCRATCH_BYTES)
     return MSA_ERR_SCRATCH_CAPACITY;
+  if (int rc = check_pools(cache, 1, 16)) return rc;
   return launched(msa::launch_indexer_topk_noalloc(cache, q_idx, w, block_table, max_pages,
                                                    seq_lens, q_start_loc, n_seqs, n_q_total, sel,
                                                    n_sel, reinterpret_cast<cudaStream_t>(stream)));
@@ -195,6 +206,7 @@ int msa_sparse_attn_decode(const msa_cache* cache, const uint8_t* q, int32_t n_q
                         !o_part || !lse_part || n_seqs == 0))
     return MSA_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(q) & 15) return MSA_ERR_INVALID_ARG;
+  if (int rc = check_pools(cache, 16, 1)) return rc;
   return launched(msa::launch_sparse_attn_tc(cache, q, softmax_scale, sel, n_sel, block_table,
                                           max_pages, seq_lens, q_start_loc, n_seqs, n_q_total,
                                           n_splits, o_part, lse_part,
@@ -229,6 +241,7 @@ int msa_debug_fp8_page(const msa_cache* cache, int64_t page, uint8_t* k8, uint8_
   if (page < 0 || page >= cache->n_pages || !k8 || !v8) return MSA_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(k8) | reinterpret_cast<uintptr_t>(v8)) & 15)
     return MSA_ERR_INVALID_ARG;
+  if (int rc = check_pools(cache, 8, 1)) return rc;
   return launched(
       msa::launch_debug_fp8_page(cache, page, k8, v8, reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -272,6 +285,7 @@ int msa_decode_fused(const msa_cache* cache, const uint8_t* q, const uint8_t* q_
       (reinterpret_cast<uintptr_t>(ws) & 15))
     return MSA_ERR_INVALID_ARG;
   if (ws_bytes < msa_decode_fused_workspace_bytes(n_q_total, max_pages)) return MSA_ERR_WORKSPACE_TOO_SMALL;
+  if (int rc = check_pools(cache, 16, 16)) return rc;
   return launched(msa::launch_decode_fused(cache, q, q_idx, w, softmax_scale, block_table, max_pages,
                                            seq_lens, q_start_loc, n_seqs, n_q_total, sel, n_sel, out,
                                            ws, reinterpret_cast<cudaStream_t>(stream)));
@@ -296,6 +310,7 @@ int msa_qkv_project_insert(const msa_cache* cache, const void* x, const void* w,
   if (((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w) | reinterpret_cast<uintptr_t>(cos_sin) |
         reinterpret_cast<uintptr_t>(q8) | reinterpret_cast<uintptr_t>(y_out)) & 15))
     return MSA_ERR_INVALID_ARG;
+  if (int rc = check_pools(cache, 4, 16)) return rc;
   return launched(msa::launch_qkv_fused(cache, x, w, n_tokens, d_model, gamma_q, gamma_k, gamma_idx, cos_sin,
                                         max_pos, positions, slot_mapping, eps, q8, y_out,
                                         reinterpret_cast<cudaStream_t>(stream)));
@@ -324,6 +339,7 @@ int msa_rotary_insert(const msa_cache* cache, const msa_rows* rows, int32_t n_to
     bits |= (uintptr_t)(s * size);
   }
   if (bits & 15) return MSA_ERR_INVALID_ARG;
+  if (int rc = check_pools(cache, 16, 16)) return rc;
   return launched(msa::launch_rotary_insert(cache, rows, n_tokens, cos_sin, max_pos, rot_dim, interleaved, positions,
                                             slot_mapping, q8, q_idx8, reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -346,6 +362,7 @@ int msa_read_kv(const msa_cache* cache, const int64_t* slot_mapping, int32_t n_t
   if (dtype != MSA_DTYPE_F32 && dtype != MSA_DTYPE_BF16 && dtype != MSA_DTYPE_F16) return MSA_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) | reinterpret_cast<uintptr_t>(idx_k)) & 15)
     return MSA_ERR_INVALID_ARG;
+  if (int rc = check_pools(cache, 16, 16)) return rc;
   return launched(msa::launch_read_kv(cache, slot_mapping, n_tokens, dtype, k, v, idx_k,
                                       reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -367,12 +384,12 @@ int msa_tree_attn(const msa_cache* cache, const uint8_t* q, int32_t n_q_heads, f
   if (n_q_total > 65535 || n_seqs > msa::kMaxSeqs || max_pages > kMaxPagesPerSeq) return MSA_ERR_UNSUPPORTED_SHAPE;
   if (n_q_total > 0 && (!q || !block_table || !seq_lens || !q_start_loc || !out || !ws || n_seqs == 0))
     return MSA_ERR_INVALID_ARG;
-  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(ws) |
-       reinterpret_cast<uintptr_t>(cache->kv_pool)) & 15)
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(ws)) & 15)
     return MSA_ERR_INVALID_ARG;
   // (the largest score, 128 products of 448 x 448, has to be a finite number)
   if (!isfinite(softmax_scale / cache->s_enc_k * 128.f * 448.f * 448.f * 2.f)) return MSA_ERR_INVALID_ARG;
   if (ws_bytes < msa_tree_attn_workspace_bytes(n_q_total)) return MSA_ERR_WORKSPACE_TOO_SMALL;
+  if (int rc = check_pools(cache, 16, 1)) return rc;
   return launched(msa::launch_tree_attn(cache, q, softmax_scale, block_table, max_pages, seq_lens, q_start_loc, n_seqs,
                                         n_q_total, tree_mask, sel, n_sel, dtype, out, lse, ws,
                                         reinterpret_cast<cudaStream_t>(stream)));
@@ -388,8 +405,7 @@ static int block_rows(const msa_cache* layers, int32_t n_layers, const int32_t* 
   if (n_layers > msa::kMaxLayers) return MSA_ERR_UNSUPPORTED_SHAPE;
   for (int l = 0; l < n_layers; ++l) {
     if (int rc = check_cache(&layers[l])) return rc;
-    if ((reinterpret_cast<uintptr_t>(layers[l].kv_pool) | reinterpret_cast<uintptr_t>(layers[l].idx_pool)) & 15)
-      return MSA_ERR_INVALID_ARG;
+    if (int rc = check_pools(&layers[l], 16, 16)) return rc;
   }
   if (n_blocks > 0 && (!pages || !rows)) return MSA_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(rows) & 15) return MSA_ERR_INVALID_ARG;

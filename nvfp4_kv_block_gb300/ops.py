@@ -179,8 +179,11 @@ class KVCache:
     @classmethod
     def from_pools(cls, kv_pool, idx_pool, s_enc_k, s_enc_v, status=None):
         """A cache over pools that the caller holds already: uint8 [n_pages, 73,728]
-        and [n_pages, 16,384] in the page format, and an int32 [1] status word (a
-        new one if None)."""
+        and [n_pages, 16,384] in the page format, each on a 16-byte boundary, and an int32
+        [1] status word (a new one if None)."""
+        for t, name in ((kv_pool, "kv_pool"), (idx_pool, "idx_pool")):
+            if isinstance(t, torch.Tensor) and t.data_ptr() % 16:
+                raise ValueError(f"{name} must begin on a 16-byte boundary")
         _ptr(kv_pool, torch.uint8, "kv_pool", 2)
         _ptr(idx_pool, torch.uint8, "idx_pool", 2)
         n = kv_pool.shape[0]
