@@ -766,6 +766,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
                 for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) - top);
                 sh = kTreeBias;
               }
+              __syncwarp();  // (tensor memory is read, written and waited for by whole warps)
               rescale(c, j >= 2, f);
             }
             tmem_st_x16(t_s + 32 * c, o);
@@ -834,6 +835,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
         if (copy == 0 && mine) rows[row] = make_float2(m, L);
 #pragma unroll 1
         for (int q = 0; q < 4; q += units) {
+          __syncwarp();
           if (q > 0) named_barrier_sync(1 + set, 128);
           if (busy)
 #pragma unroll 1
@@ -842,17 +844,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
               tmem_ld32x32b_x16(tl + kTmemO + 64 * set + 16 * (q + un), u);
               if (any1) tmem_ld32x32b_x16(tl + kTmemO + 128 + 64 * set + 16 * (q + un), v);
               tmem_wait_ld();
-              if (!mine) continue;
-              float x[16];
+              if (mine) {
+                float x[16];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                x[i] = w0 > 0.f ? __uint_as_float(u[i]) * w0 : 0.f;
-                if (any1 && w1 > 0.f) x[i] = fmaf(__uint_as_float(v[i]), w1, x[i]);
+                for (int i = 0; i < 16; ++i) {
+                  x[i] = w0 > 0.f ? __uint_as_float(u[i]) * w0 : 0.f;
+                  if (any1 && w1 > 0.f) x[i] = fmaf(__uint_as_float(v[i]), w1, x[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  *reinterpret_cast<float4*>(xb + 16 * (un * parts + me) + 4 * (i ^ (row >> 1 & 3))) =
+                      make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
               }
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<float4*>(xb + 16 * (un * parts + me) + 4 * (i ^ (row >> 1 & 3))) =
-                    make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+              __syncwarp();
             }
           __syncwarp();
           named_barrier_sync(1 + set, 128);
@@ -876,6 +880,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
         const int ca = two ? 0 : 2 * set, cz = two ? 4 : 2 * set + 2;
 #pragma unroll 1
         for (int c = ca; c < cz; ++c) {
+          __syncwarp();
           uint32_t v[32];
           tmem_ld32x32b_x32(tl + kTmemO + (two ? 128 * set : 0) + 32 * c, v);
           if (!two && any1) {
