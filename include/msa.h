@@ -466,7 +466,9 @@ int msa_read_kv(const msa_cache* cache, const int64_t* slot_mapping, int32_t n_t
  * of 0x7F or 0xFF (no number, never written by the library) counts as zero.
  * A query byte of 0x7F or 0xFF makes its row's out and lse NaN.  Rows that two
  * sequences claim (q_start_loc not ascending) hold numbers of no meaning.
- * softmax_scale > 0, and softmax_scale / s_enc_k times 2^26 finite.
+ * softmax_scale > 0, and softmax_scale / s_enc_k times 2^26 finite (where the quotient
+ * is below 2^-126, or underflows, every score is zero to fp32 and a row's out is the mean of
+ * the values that it sees).
  * Limits: n_seqs <= 4096, n_q_total <= 65535.  Two launches, both programmatic
  * dependents of the kernel before them.
  */

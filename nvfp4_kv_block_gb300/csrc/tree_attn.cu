@@ -43,6 +43,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
+#include <cfloat>
 #include <type_traits>
 
 #include "common.cuh"
@@ -1166,7 +1168,9 @@ cudaError_t launch_tree_attn(const msa_cache* c, const uint8_t* q, float softmax
   tp.tree_mask = reinterpret_cast<const unsigned long long*>(tree_mask);
   tp.sel = sel;
   tp.n_sel = n_sel;
-  tp.scale_log2 = softmax_scale / c->s_enc_k * kTreeLog2e;
+  // (a quotient below fp32's normal numbers is as good as the smallest: the scores, below 2^25 times
+  // it, leave every weight alike; zero would make a hidden token's -inf a NaN)
+  tp.scale_log2 = std::max(softmax_scale / c->s_enc_k * kTreeLog2e, FLT_MIN);
   tp.out_scale = 256.0f / c->s_enc_v;
   tp.out_f16 = dtype == MSA_DTYPE_F16;
   tp.out = static_cast<uint16_t*>(out);

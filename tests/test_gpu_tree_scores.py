@@ -164,3 +164,26 @@ def test_the_drafts_of_a_tree_are_turned_by_their_depth(inter, scaling):
         np.testing.assert_array_equal(got.cpu().numpy(), value.reshape(b.T, 4, 128))
     np.testing.assert_array_equal(ik.cpu().numpy(), formats.decode_e4m3(formats.encode_e4m3(want["idx"][:, 0].astype(np.float64))).astype(np.float32))
     assert cache.read_status() == 0
+
+
+@pytest.mark.parametrize("drafts", [1, 12, 40])
+def test_a_scale_whose_quotient_leaves_fp32_is_a_mean(drafts):
+    """softmax_scale / s_enc_k below fp32's smallest number: every visible key has the same weight, on
+    pages that end inside (whose other tokens are not seen) too."""
+    b = Batch([(1000, drafts), (128, drafts), (3, drafts)], 57)
+    cache, q, bt, lens, qsl = b.device()
+    cache.s_enc_k = 1e8
+    bufs = ops.TreeBuffers(b.T, 3, F16)
+    ops.tree_attn(cache, q, bt, lens, qsl, bufs, softmax_scale=1e-38)
+    torch.cuda.synchronize()
+    got, lse = bufs.out.double().cpu().numpy(), bufs.lse.double().cpu().numpy()
+    for s, (ctx, n) in enumerate(b.seqs):
+        _, v8 = zip(*(tree.page_operands(b.pool[b.bt[s, i]]) for i in range(-(-(ctx + n) // 128))))
+        v = formats.decode_e4m3(np.concatenate(v8)) / float(np.float32(S_ENC_V))
+        for j in range(n):
+            keys = ctx + j + 1
+            m, size = v[:keys].mean(0), np.abs(v[:keys]).mean(0)
+            tol = (2.0**-11 + 2 * keys * 2.0**-24) * size + 2.0**-11 * np.abs(m) + 2.0**-24
+            assert np.all(np.abs(got[b.qsl[s] + j] - m.repeat(4, 0)) <= tol.repeat(4, 0)), (s, j)
+            assert np.all(np.abs(lse[b.qsl[s] + j] - np.log(keys)) <= keys * 2.0**-24 + 2.0**-20), (s, j)
+    assert cache.read_status() == 0
