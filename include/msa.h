@@ -469,6 +469,7 @@ int msa_read_kv(const msa_cache* cache, const int64_t* slot_mapping, int32_t n_t
  * softmax_scale > 0, and softmax_scale / s_enc_k times 2^26 finite (where the quotient
  * is below 2^-126, or underflows, every score is zero to fp32 and a row's out is the mean of
  * the values that it sees).
+ * s_enc_v above 2^-120 and at most 2^100.
  * Limits: n_seqs <= 4096, n_q_total <= 65535.  Two launches, both programmatic
  * dependents of the kernel before them.
  */

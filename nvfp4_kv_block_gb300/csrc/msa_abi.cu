@@ -388,6 +388,9 @@ int msa_tree_attn(const msa_cache* cache, const uint8_t* q, int32_t n_q_heads, f
     return MSA_ERR_INVALID_ARG;
   // (the largest score, 128 products of 448 x 448, has to be a finite number)
   if (!isfinite(softmax_scale / cache->s_enc_k * 128.f * 448.f * 448.f * 2.f)) return MSA_ERR_INVALID_ARG;
+  // (2^8 / s_enc_v has to be finite, and a normal number behind the division by a row's sum of
+  // weights, below 2^34: 49,152 for each 32 tokens of 65,536 pages)
+  if (!isfinite(256.f / cache->s_enc_v) || cache->s_enc_v > 0x1p100f) return MSA_ERR_INVALID_ARG;
   if (ws_bytes < msa_tree_attn_workspace_bytes(n_q_total)) return MSA_ERR_WORKSPACE_TOO_SMALL;
   if (int rc = check_pools(cache, 16, 1)) return rc;
   return launched(msa::launch_tree_attn(cache, q, softmax_scale, block_table, max_pages, seq_lens, q_start_loc, n_seqs,
