@@ -4,10 +4,10 @@
 // An NVFP4 element is x = e2m1(code) * d with d = fl(sb * r), sb the E4M3 scale
 // of its 16 channels and r = fl(1 / s_enc) the tensor's decode factor; the
 // product is rounded to fp32 and then to the output type.  Index keys are E4M3
-// values.  Memory-bound: 704 bytes in and 1,152 values out per token.  Whole pages of
-// 131,072 tokens in bf16: 77 us, 5.1 TB/s of those bytes.  At scattered slots a scale is a
-// 32-byte sector of its own, 8 of them a row beside 64 bytes of codes: 20,011
-// scattered tokens in fp32: 25 us, 4.2 TB/s.
+// values.  704 bytes in and 1,152 values out per token.  Whole pages are bound by memory
+// (131,072 tokens in bf16: 76 us, 5.2 TB/s of those bytes), scattered slots by latency, a
+// chain of slot, scales, codes and store with no rate near its end (20,011 tokens in fp32:
+// 25 us, 4.2 TB/s, DRAM at 29 % and issue slots at 31 %; 16,384 in bf16: 18 us, 2.7 TB/s).
 //
 // A warp takes one KV head's K or V (or the index key) of a tile of tokens, four
 // tokens at a time: eight lanes a row, lane l its channels 16l .. 16l + 15: two
@@ -165,8 +165,8 @@ cudaError_t launch_read_kv(const msa_cache* c, const int64_t* slot_mapping, int 
   cudaError_t e = setup.get(&dev, &n_sm, [](int) { return cudaSuccess; });
   if (e != cudaSuccess) return e;
   // the largest tile that still makes 48 warps per SM: longer tiles share the loads of their
-  // scales, short ones fill the SMs (131,072 tokens: 78 us with 32, 88 with 8, 102 with 4;
-  // 300 tokens: 8 us with 4, 12 with 32)
+  // scales, short ones fill the SMs (single calls on a cold L2: 131,072 tokens in pages 78 us with
+  // 32, 82 with 16, 86 with 8, 100 with 4; 300 tokens 8 us with 4, 12 with 32)
   int tile = 32;
   while (tile > 4 && (long long)n_tokens / tile * 9 < 48ll * n_sm) tile >>= 1;
   const int wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) | reinterpret_cast<uintptr_t>(idx)) & 31) == 0;

@@ -11,7 +11,9 @@
 // in f16.  m moves only when 32 weights sum to more than 49,152, so that they stay
 // below f16's end and the accumulator is rescaled a few times per row;
 // they keep full f16 precision down to 2^-22 of the reference's (an E4M3 weight, with
-// its 17 binades, would lose the bulk of a long context behind one large key).
+// its 17 binades, would lose the bulk of a long context behind one large key).  A move
+// multiplies by less than 1/6 (its largest weight was above 1,536 = 6 2^8): l and the
+// accumulator in fp32, the weights of the page's earlier chunks with a second rounding to f16.
 // V8 is an f16 value by moving its seven magnitude bits: E4M3 bits << 7 is
 // v8 2^-8 exactly, subnormals included.
 //
@@ -32,12 +34,12 @@
 //   warps 12-23   K conversion (four warps, thread = token) and V conversion (eight,
 //                 thread = token and half of the channels).
 //
-// What bounds it.  A page of 18,432 bytes takes a CTA 0.79 us with up to 8 drafts, 0.95 us up
-// to 16, 1.0 us up to 32 and 1.8 us with two tiles; its products take the tensor pipe 0.39 us
+// What bounds it.  A page of 18,432 bytes takes a CTA 0.76 us with up to 8 drafts, 0.91 us up
+// to 16, 0.98 us up to 32 and 1.74 us with two tiles; its products take the tensor pipe 0.39 us
 // per tile.  The rest is instruction issue and hand-offs: 1,958 warp instructions of
 // conversion a page (K 763, V 1,195), 911 (one draft) to 2,550 (32) of softmax, about 1,100
-// of waits.  32 sequences of 32,768 tokens, one draft each: 184 us, 3.3 TB/s; 8 of 131,072
-// with 64 drafts: 380 us, 1.37 PFLOP/s; one of 4,096: 14.8 us, a chain of latencies
+// of waits.  32 sequences of 32,768 tokens, one draft each: 183 us, 3.3 TB/s; 8 of 131,072
+// with 64 drafts: 385 us, 1.35 PFLOP/s; one of 4,096: 14.8 us, a chain of latencies
 // (lengths and ranges 2.6, first page 2.4, its scores 1.4, joining the row copies 1.7, the
 // merge kernel 4).
 #include <cuda_bf16.h>
@@ -88,9 +90,10 @@ constexpr float kTreeMost = 49152.0f;  // largest sum of a chunk's weights, and 
 constexpr float kTreeUnset = 3e38f;    // shift of a row without a reference: a visible token's weight is infinite
 constexpr float kTreeLog2e = 1.4426950408889634f, kTreeLn2 = 0.6931471805599453f;
 
-// Weights of the partition, in units of 0.2 us: a page of a sequence with up to 8, 16,
-// 32 and 64 drafts (0.80, 0.95, 1.1 and 2.0 us per page of a CTA on 32K contexts; without
-// row copies 1.0 and 1.8 us up to 32 and 64), and the fixed part of a (sequence, KV head).
+// Weights of the partition, in units of about 0.19 us: a page of a sequence with up to 8, 16,
+// 32 and 64 drafts (0.76, 0.91, 1.02 and 1.82 us per page of a CTA, from 24 sequences of 16,384
+// and of 49,152 tokens; in the kernel without row copies 0.98 and 1.74 us up to 32 and 64),
+// and the fixed part of a (sequence, KV head).
 // The least share of a CTA is a page's weight, so that every CTA between a sequence's
 // first and last has pages of it.
 template <bool kCopies>
@@ -103,7 +106,7 @@ constexpr int kFixedWeight = 10, kLeastShare1 = 6, kLeastShare2 = 10;
 // Copies of the query rows in a one-tile segment's 128 rows: with few rows every
 // warp quad (32 lanes of tensor memory) gets the same rows and its own share of a
 // page's tokens, so that no softmax warp is idle (32 sequences of 32,768 tokens, one draft
-// each: 185 us, with two copies 211, with one 224).
+// each: 184 us, with two copies 211, with one 224).
 __host__ __device__ __forceinline__ int tree_copies(int n_q) { return n_q <= 8 ? 4 : n_q <= 16 ? 2 : 1; }
 
 struct SegRec {
@@ -1186,10 +1189,11 @@ cudaError_t launch_tree_attn(const msa_cache* c, const uint8_t* q, float softmax
   tp.wait_ns = launch_settings().wait_ns;
   tp.inject = (launch_settings().inject & MSA_INJECT_ATTENTION_TIMEOUT) != 0;
   const int most = n_sm < kTreeCtas ? n_sm : kTreeCtas;
-  // Without the row copies' code two tiles run faster (8 sequences of 131,072 with 64 drafts: 380 us,
-  // 415 with it; 24 of 30,720 with 17 to 32 drafts 172 to 179 us, 178 to 190), few drafts slower
-  // (8 to 16 drafts: 170 us, 161 with it): by the mean, mixtures of 1 to 64 drafts included
-  // (mean 14: 171 us both, 20: 176 and 184, 38: 261 and 278).
+  // Without the row copies' code two tiles run faster (8 sequences of 131,072 with 64 drafts: 386 us,
+  // 417 with it; 24 of 30,720 with 17 to 32 drafts 177 us, 187), few drafts slower (8 to 16 drafts:
+  // 170 us, 161 with it): by the mean, mixtures included (4 to 24 drafts, mean 14: 171 us both; 2 to
+  // 40, mean 21: 196 and 202; 1 to 64, mean 38: 263 and 278).  The lengths are on the device, so
+  // the mean is of the rows that the call passes: padding rows and empty sequences count.
   e = launch_pdl(n_q_total > 16ll * n_seqs ? tree_attn_kernel<false> : tree_attn_kernel<true>, dim3(most),
                  dim3(kTreeThreads), kTreeSmem, stream, tp);
   if (e != cudaSuccess) return e;

@@ -463,17 +463,23 @@ def _arg(t, dtype, shape, dev, name):
 
 def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_max_pos=None, beta_fast=32.0,
                      beta_slow=1.0):
-    """(frequencies of the rot_dim / 2 pairs, amplitude) of a rotary embedding.
+    """(frequencies of the rot_dim / 2 pairs, amplitude) of a rotary embedding
+    (J. Su et al., 2021).
 
     Unscaled: base^(-2i / rot_dim).  ``scaling`` stretches a model trained on
     ``original_max_pos`` positions to ``factor`` times as many:
-      "linear"  every position divided by the factor;
+      "linear"  every position divided by the factor (S. Chen et al., "Extending
+                Context Window of Large Language Models via Positional
+                Interpolation", 2023);
       "ntk"     base * factor^(rot_dim / (rot_dim - 2)): the slowest pair is
                 stretched by the factor, the fastest not at all;
       "yarn"    pairs that turn more than ``beta_fast`` times over the original
                 length keep their frequency, pairs below ``beta_slow`` turns are
                 divided by the factor, a linear ramp over the pair index between;
-                amplitude 0.1 ln(factor) + 1.
+                amplitude 0.1 ln(factor) + 1 (B. Peng, J. Quesnelle, H. Fan,
+                E. Shippole, "YaRN: Efficient Context Window Extension of Large
+                Language Models", 2023).  The ramp's ends are rounded outward to
+                whole pairs and held to 0 and rot_dim - 1.
     """
     if rot_dim % 16 or not 0 <= rot_dim <= HEAD_DIM:
         raise ValueError("rot_dim must be a multiple of 16 from 0 to 128")
@@ -496,6 +502,9 @@ def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_m
     def pair(turns):  # the (fractional) pair that turns so often over the original length
         return rot_dim * math.log(original_max_pos / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
 
+    # The ends of the ramp as models are trained with: whole pairs, and an upper end of at most
+    # rot_dim - 1, a channel's index (an end behind the last pair, rot_dim / 2 - 1, leaves that pair
+    # between its frequency and the divided one).  Ends that meet are kept apart by 1e-3 of a pair: a step.
     lo = max(math.floor(pair(beta_fast)), 0)
     hi = min(math.ceil(pair(beta_slow)), rot_dim - 1)
     out = []
@@ -571,7 +580,8 @@ def rotary_insert(cache, q, k, v, idx_k, cos_sin, positions, slot_mapping, q_idx
     max_pos, rot_dim = cos_sin.shape
     _check(lib().msa_rotary_insert(
         cache.packed(), _ROWS.pack(qp, kp, vp, ip, qip, qs, ks, vs, i_s, qis, code), n,
-        _arg(cos_sin, torch.float32, (max_pos, rot_dim), dev, "cos_sin"), max_pos, rot_dim, 1 if interleaved else 0, _arg(positions, torch.int32, (n,), dev, "positions"),
+        _arg(cos_sin, torch.float32, (max_pos, rot_dim), dev, "cos_sin"), max_pos, rot_dim, 1 if interleaved else 0,
+        _arg(positions, torch.int32, (n,), dev, "positions"),
         _arg(slot_mapping, torch.int64, (n,), dev, "slot_mapping"),
         _arg(q8, torch.uint8, (n, Q_HEADS, HEAD_DIM), dev, "q8"), qi8p, _raw_stream(dev)))
     return q8, qi8
@@ -606,9 +616,11 @@ TREE_MAX_DRAFTS = 64  # MSA_TREE_MAX_DRAFTS: query tokens of one sequence in tre
 
 
 class TreeBuffers:
-    """Outputs and scratch of tree_attn for up to n_q_total query tokens of up to
-    n_seqs sequences (reused across steps): out [n_q_total, 16, 128] in ``dtype``
-    (bf16 or fp16), lse [n_q_total, 16]."""
+    """Outputs and scratch of tree_attn calls with n_q_total query rows (exactly: rows
+    behind the last sequence are padding, and stay as they were) and up to n_seqs
+    sequences, reused across steps: out [n_q_total, 16, 128] in ``dtype`` (bf16 or
+    fp16), lse [n_q_total, 16].  Padding rows count where the kernel is chosen: buffers
+    of at most 16 rows a sequence keep the one that is faster for few drafts."""
 
     def __init__(self, n_q_total, n_seqs, dtype=torch.bfloat16, device="cuda"):
         if dtype not in (torch.bfloat16, torch.float16):
