@@ -7,7 +7,7 @@
 // values.  704 bytes in and 1,152 values out per token.  Whole pages are bound by memory
 // (131,072 tokens in bf16: 76 us, 5.2 TB/s of those bytes), scattered slots by latency, a
 // chain of slot, scales, codes and store with no rate near its end (20,011 tokens in fp32:
-// 25 us, 4.2 TB/s, DRAM at 29 % and issue slots at 31 %; 16,384 in bf16: 18 us, 2.7 TB/s).
+// 25 us, 4.2 TB/s, DRAM at 25 % and issue slots at 29 %; 16,384 in bf16: 18 us, 2.7 TB/s).
 //
 // A warp takes one KV head's K or V (or the index key) of a tile of tokens, four
 // tokens at a time: eight lanes a row, lane l its channels 16l .. 16l + 15: two
