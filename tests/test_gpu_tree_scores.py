@@ -187,3 +187,27 @@ def test_a_scale_whose_quotient_leaves_fp32_is_a_mean(drafts):
             assert np.all(np.abs(got[b.qsl[s] + j] - m.repeat(4, 0)) <= tol.repeat(4, 0)), (s, j)
             assert np.all(np.abs(lse[b.qsl[s] + j] - np.log(keys)) <= keys * 2.0**-24 + 2.0**-20), (s, j)
     assert cache.read_status() == 0
+
+
+@pytest.mark.parametrize("drafts,pad_rows,empty", [(1, 126, 0), (64, 0, 14), (20, 0, 8)])
+def test_padded_batches(drafts, pad_rows, empty):
+    """Padding rows and empty sequences choose the other kernel than the drafts alone would."""
+    b = Batch([(900, drafts), (2500, drafts)] + [(0, 0)] * empty, 58, pad_rows=pad_rows)
+    assert (2 * drafts > 16 * 2) != (b.T > 16 * len(b.seqs))
+    bufs = ops.TreeBuffers(b.T, len(b.seqs), F16)
+    bufs.out.fill_(3.0)
+    out, lse, cache = b.run(F16, bufs=bufs)
+    b.check(out, lse)
+    assert torch.all(out[2 * drafts:] == 3.0) and cache.read_status() == 0
+
+
+def test_a_query_that_is_no_number_and_sees_nothing_is_zeros():
+    b = Batch([(0, 3), (0, 20)], 59)
+    b.q8[0, 5, 17] = b.q8[1, 5, 17] = b.q8[4, 0, 0] = 0x7F
+    words = [0, 1, 0, 1, 0] + [3] * 18
+    out, lse, cache = b.run(F16, words)
+    for row in (0, 2, 4):
+        assert not out[row].any() and torch.isneginf(lse[row]).all()
+    bad = torch.zeros((b.T, 16), dtype=torch.bool, device=DEV)
+    bad[1, 5] = True
+    assert torch.equal(out.isnan().all(-1), bad) and torch.equal(lse.isnan(), bad) and cache.read_status() == 0
