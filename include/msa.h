@@ -87,6 +87,7 @@ typedef struct CUstream_st* msa_stream_t; /* same type as cudaStream_t */
 #define MSA_STATUS_BAD_SEQ 0x4        /* n_q < 0, n_q > seq_len or seq_len > max_pages*128 */
 #define MSA_STATUS_BAD_SELECTION 0x8  /* a selected block id outside 0..r_j */
 #define MSA_STATUS_TIMEOUT 0x10       /* a bounded on-chip wait gave up (results invalid) */
+#define MSA_STATUS_NO_PAGES 0x20      /* a page pool ran out of free pages */
 /* Every on-chip wait is bounded (2 s by default): a wait that runs out sets
  * MSA_STATUS_TIMEOUT, the kernel abandons its work, waits (bounded) for its own
  * copies and tensor-core operations in flight, releases tensor memory and
@@ -404,6 +405,21 @@ typedef struct msa_rows {
 int msa_rotary_insert(const msa_cache* cache, const msa_rows* rows, int32_t n_tokens, const float* cos_sin,
                       int32_t max_pos, int32_t rot_dim, int32_t interleaved, const int32_t* positions,
                       const int64_t* slot_mapping, uint8_t* q8, uint8_t* q_idx8, msa_stream_t stream);
+/*
+ * The same with positions on several axes (time, height and width of images and
+ * video, text alike on all of them): pair i turns by its axis's position,
+ *   positions     int32 [n_axes][n_tokens], n_axes 1 .. MSA_MAX_AXES;
+ *   axis_of_pair  HOST array of rot_dim / 2 bytes: axis of pair i, below n_axes
+ *                 (not read for one axis, where every pair is of axis 0);
+ * and uses the cos and sin of table row positions[axis_of_pair[i]][t].  A token with
+ * a position outside [0, max_pos) on any axis is left unturned and sets
+ * MSA_STATUS_BAD_SEQ.
+ */
+#define MSA_MAX_AXES 4
+int msa_rotary_insert_axes(const msa_cache* cache, const msa_rows* rows, int32_t n_tokens, const float* cos_sin,
+                           int32_t max_pos, int32_t rot_dim, int32_t interleaved, const int32_t* positions,
+                           int32_t n_axes, const uint8_t* axis_of_pair, const int64_t* slot_mapping, uint8_t* q8,
+                           uint8_t* q_idx8, msa_stream_t stream);
 /* RoPE table of given frequencies: cos_sin[pos][i] = amplitude * cos(pos * freq[i])
  * and cos_sin[pos][rot_dim / 2 + i] = amplitude * sin(pos * freq[i]), computed in
  * double precision and rounded to fp32.  freq is a HOST array of rot_dim / 2
@@ -513,6 +529,95 @@ int msa_unpack_blocks(const msa_cache* layers, int32_t n_layers, const uint8_t* 
                       const int32_t* pages, int32_t n_blocks, msa_stream_t stream);
 /* Bytes of one block-outer row: n_layers * 90,112 (0 for n_layers <= 0). */
 size_t msa_block_row_bytes(int32_t n_layers);
+
+/*
+ * Pages that sequences share.  A pool counts, for each page id below n_pages, the
+ * block-table entries that hold it, and keeps a mask of those that none holds (bit
+ * p % 32 of word p / 32).  A sequence is a row of block_table and its entry of
+ * seq_lens; it holds the row's entries that are not negative, also those behind its
+ * length.  Page p is the same page in every layer's pools, as in the block-outer rows.
+ * Every call below changes tables, lengths, counts and mask on the device, in stream
+ * order; calls on one pool must not overlap on the GPU.  Pages are dealt lowest number
+ * first in the order of the call's sequences; from the first sequence that finds too few
+ * of them on, none that needs a page gets one (MSA_STATUS_NO_PAGES).  Status bits go to
+ * pool->status.  n_seqs <= 4096, max_pages <= 65,536.
+ */
+typedef struct msa_page_pool {
+  int32_t* refs;        /* device, [n_pages] */
+  uint32_t* free_mask;  /* device, [(n_pages + 31) / 32] */
+  int32_t n_pages;
+  int32_t* status;      /* device int32, sticky MSA_STATUS_* bits; may be NULL */
+} msa_page_pool;
+
+/*
+ * Pages and slots for new tokens: sequence b gets room for n = q_start_loc[b + 1] -
+ * q_start_loc[b] tokens behind its length (entries of its row that hold a page already
+ * are used as they are) and grows by n.
+ *   slots  int64 [n_tokens] out: slot (page * 128 + offset) of every new token, in the
+ *          sequences' order, for msa_rotary_insert and its like; -1 for the tokens of a
+ *          sequence that could not grow and for rows behind the last sequence.
+ * A sequence that could not grow keeps its length and row: one without enough free
+ * pages, one with n < 0, tokens outside [0, n_tokens) or more than max_pages * 128 of
+ * them (MSA_STATUS_BAD_SEQ), one whose last tokens have no page (MSA_STATUS_BAD_PAGE).
+ * n_tokens <= 262,144.
+ */
+int msa_extend_sequences(const msa_page_pool* pool, int32_t* block_table, int32_t max_pages, int32_t* seq_lens,
+                         const int32_t* q_start_loc, int32_t n_seqs, int32_t n_tokens, int64_t* slots,
+                         msa_stream_t stream);
+
+/*
+ * Forks: for each of n pairs, row dst[i], which has to be empty, becomes a second copy
+ * of row src[i]: its full pages are shared, the tokens of its last page (if that is not
+ * full) are copied to a page of dst's own, in every layer.  Pages that src holds behind
+ * its length are not shared.
+ *   layers    HOST array of n_layers caches (1 .. 128), each with pool->n_pages pages
+ *             or more.
+ *   ws        device scratch of msa_fork_workspace_bytes(n) bytes, 16-byte aligned.
+ * A pair outside the table, with a target that has tokens or pages or that an earlier
+ * pair of the call names, is left out (MSA_STATUS_BAD_SEQ), so a row that is another
+ * pair's target counts as empty; so is one whose last page is outside the pool, and an
+ * entry outside it is taken over and flagged (MSA_STATUS_BAD_PAGE).  n <= 4096.
+ */
+int msa_fork_sequences(const msa_cache* layers, int32_t n_layers, const msa_page_pool* pool, int32_t* block_table,
+                       int32_t max_pages, int32_t* seq_lens, int32_t n_seqs, const int32_t* src, const int32_t* dst,
+                       int32_t n, void* ws, size_t ws_bytes, msa_stream_t stream);
+size_t msa_fork_workspace_bytes(int32_t n);
+
+/*
+ * Release of the rows listed in rows (int32 [n]; the same row twice counts once): every
+ * page they hold loses one count and is free when that was the last, the rows' entries
+ * become -1 and their lengths 0.  A page that nobody was counted for or outside the
+ * pool sets MSA_STATUS_BAD_PAGE, a row outside the table MSA_STATUS_BAD_SEQ.
+ */
+int msa_release_sequences(const msa_page_pool* pool, int32_t* block_table, int32_t max_pages, int32_t* seq_lens,
+                          int32_t n_seqs, const int32_t* rows, int32_t n, msa_stream_t stream);
+
+/*
+ * Page copies in every layer: page src[i] to page dst[i] (negative, or src[i] = dst[i]:
+ * none), the first tokens[i] tokens (NULL: all 128; the bytes of the others stay).  The
+ * targets must be distinct, and no target may be another pair's source.  A page outside
+ * a pool leaves the pair out and sets MSA_STATUS_BAD_PAGE in layers[0].status.
+ */
+int msa_copy_pages(const msa_cache* layers, int32_t n_layers, const int32_t* src, const int32_t* dst,
+                   const int32_t* tokens, int32_t n, msa_stream_t stream);
+
+/*
+ * Accepted drafts: of each sequence's n = q_start_loc[b + 1] - q_start_loc[b] last tokens
+ * (drafts that msa_tree_attn verified, at most MSA_TREE_MAX_DRAFTS) those stay whose bits
+ * accepted[b] has; the k-th of them moves to position ctx + k, ctx = seq_lens[b] - n, in
+ * every layer's K/V and index pages.  Keys keep the rotary position they were written
+ * with: a draft's is its depth's, which is k for a path from the root.
+ *   accepted  uint64 [n_seqs]; bits of drafts that do not exist are ignored.
+ *   new_lens  int32 [n_seqs] out, apart from seq_lens: ctx + the number of accepted drafts.
+ * Pages behind the new length stay in the row, for later tokens.  An inconsistent
+ * sequence keeps its length (MSA_STATUS_BAD_SEQ); a token whose page or whose new
+ * place's page is outside the pool is not moved (MSA_STATUS_BAD_PAGE).  Status bits go to
+ * layers[0].status.  The pages of drafts must not be shared with other sequences of the
+ * call (forks share full pages only).
+ */
+int msa_commit_drafts(const msa_cache* layers, int32_t n_layers, const int32_t* block_table, int32_t max_pages,
+                      const int32_t* seq_lens, const int32_t* q_start_loc, int32_t n_seqs, const uint64_t* accepted,
+                      int32_t* new_lens, msa_stream_t stream);
 
 /*
  * Helpers for the per-tensor scale.  msa_absmax folds max|x[i]| over n fp32

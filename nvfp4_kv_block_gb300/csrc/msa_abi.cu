@@ -33,12 +33,21 @@ cudaError_t launch_qkv_fused(const msa_cache*, const void*, const void*, int, in
                              const float*, const float*, int, const int*, const int64_t*, float, uint8_t*,
                              float*, cudaStream_t);
 cudaError_t launch_block_rows(const msa_cache*, int, const int*, int, uint8_t*, bool, cudaStream_t);
-cudaError_t launch_rotary_insert(const msa_cache*, const msa_rows*, int, const float*, int, int, int, const int*,
-                                 const int64_t*, uint8_t*, uint8_t*, cudaStream_t);
+cudaError_t launch_rotary_insert(const msa_cache*, const msa_rows*, int, const float*, int, int, int, const int*, int,
+                                 const uint8_t*, const int64_t*, uint8_t*, uint8_t*, cudaStream_t);
 cudaError_t launch_rope_table_freqs(float*, int, const double*, int, double, cudaStream_t);
 size_t tree_attn_workspace_bytes(int);
 cudaError_t launch_tree_attn(const msa_cache*, const uint8_t*, float, const int*, int, const int*, const int*, int, int,
                              const uint64_t*, const int*, const int*, int, void*, float*, void*, cudaStream_t);
+int max_extend_tokens();
+size_t fork_workspace_bytes(int);
+cudaError_t launch_extend(const msa_page_pool*, int*, int, int*, const int*, int, int, int64_t*, cudaStream_t);
+cudaError_t launch_fork(const msa_cache*, int, const msa_page_pool*, int*, int, int*, int, const int*, const int*, int,
+                        void*, cudaStream_t);
+cudaError_t launch_release(const msa_page_pool*, int*, int, int*, int, const int*, int, cudaStream_t);
+cudaError_t launch_copy_pages(const msa_cache*, int, const int*, const int*, const int*, int, cudaStream_t);
+cudaError_t launch_commit(const msa_cache*, int, const int*, int, const int*, const int*, int, const uint64_t*, int*,
+                          cudaStream_t);
 cudaError_t launch_read_kv(const msa_cache*, const int64_t*, int, int, void*, void*, void*, cudaStream_t);
 
 namespace {
@@ -70,6 +79,27 @@ int check_cache(const msa_cache* c) {
 int check_pools(const msa_cache* c, uintptr_t kv, uintptr_t idx) {
   const bool ok = reinterpret_cast<uintptr_t>(c->kv_pool) % kv == 0 && reinterpret_cast<uintptr_t>(c->idx_pool) % idx == 0;
   return ok ? MSA_OK : MSA_ERR_INVALID_ARG;
+}
+
+// Caches of n_layers layers whose pages are moved 16 bytes at a time.
+int check_layers(const msa_cache* layers, int32_t n_layers) {
+  if (!layers || n_layers <= 0) return MSA_ERR_INVALID_ARG;
+  if (n_layers > msa::kMaxLayers) return MSA_ERR_UNSUPPORTED_SHAPE;
+  for (int l = 0; l < n_layers; ++l) {
+    if (int rc = check_cache(&layers[l])) return rc;
+    if (int rc = check_pools(&layers[l], 16, 16)) return rc;
+  }
+  return MSA_OK;
+}
+
+int check_page_pool(const msa_page_pool* p) {
+  return p && p->refs && p->free_mask && p->n_pages > 0 ? MSA_OK : MSA_ERR_INVALID_ARG;
+}
+
+// A block table whose rows a call changes.
+int check_table(const int32_t* block_table, int32_t max_pages, const int32_t* seq_lens, int32_t n_seqs) {
+  if (!block_table || !seq_lens || max_pages <= 0 || n_seqs < 0) return MSA_ERR_INVALID_ARG;
+  return n_seqs > msa::kMaxSeqs || max_pages > kMaxPagesPerSeq ? MSA_ERR_UNSUPPORTED_SHAPE : MSA_OK;
 }
 
 int launched(cudaError_t e) { return e == cudaSuccess ? MSA_OK : MSA_ERR_LAUNCH_FAILED; }
@@ -316,14 +346,18 @@ int msa_qkv_project_insert(const msa_cache* cache, const void* x, const void* w,
                                         reinterpret_cast<cudaStream_t>(stream)));
 }
 
-int msa_rotary_insert(const msa_cache* cache, const msa_rows* rows, int32_t n_tokens, const float* cos_sin,
-                      int32_t max_pos, int32_t rot_dim, int32_t interleaved, const int32_t* positions,
-                      const int64_t* slot_mapping, uint8_t* q8, uint8_t* q_idx8, msa_stream_t stream) {
+static int rotary_insert(const msa_cache* cache, const msa_rows* rows, int32_t n_tokens, const float* cos_sin,
+                         int32_t max_pos, int32_t rot_dim, int32_t interleaved, const int32_t* positions,
+                         int32_t n_axes, const uint8_t* axis_of_pair, const int64_t* slot_mapping, uint8_t* q8,
+                         uint8_t* q_idx8, msa_stream_t stream) {
   if (int rc = check_cache(cache)) return rc;
   if (!rows || n_tokens < 0 || max_pos < 0 || (interleaved != 0 && interleaved != 1)) return MSA_ERR_INVALID_ARG;
   if (rows->dtype != MSA_DTYPE_F32 && rows->dtype != MSA_DTYPE_BF16 && rows->dtype != MSA_DTYPE_F16)
     return MSA_ERR_INVALID_ARG;
   if (rot_dim < 0 || rot_dim > msa::kHeadDim || rot_dim % 16 != 0) return MSA_ERR_UNSUPPORTED_SHAPE;
+  if (n_axes < 1 || n_axes > MSA_MAX_AXES) return MSA_ERR_UNSUPPORTED_SHAPE;
+  for (int i = 0; n_axes > 1 && i < rot_dim / 2; ++i)
+    if (!axis_of_pair || axis_of_pair[i] >= n_axes) return MSA_ERR_INVALID_ARG;
   if (n_tokens > 0 && (!rows->q || !rows->k || !rows->v || !rows->idx_k || !positions || !slot_mapping || !q8 ||
                        (rows->q_idx && !q_idx8) || (rot_dim > 0 && (!cos_sin || max_pos == 0))))
     return MSA_ERR_INVALID_ARG;
@@ -341,7 +375,23 @@ int msa_rotary_insert(const msa_cache* cache, const msa_rows* rows, int32_t n_to
   if (bits & 15) return MSA_ERR_INVALID_ARG;
   if (int rc = check_pools(cache, 16, 16)) return rc;
   return launched(msa::launch_rotary_insert(cache, rows, n_tokens, cos_sin, max_pos, rot_dim, interleaved, positions,
-                                            slot_mapping, q8, q_idx8, reinterpret_cast<cudaStream_t>(stream)));
+                                            n_axes, n_axes > 1 ? axis_of_pair : nullptr, slot_mapping, q8, q_idx8,
+                                            reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int msa_rotary_insert(const msa_cache* cache, const msa_rows* rows, int32_t n_tokens, const float* cos_sin,
+                      int32_t max_pos, int32_t rot_dim, int32_t interleaved, const int32_t* positions,
+                      const int64_t* slot_mapping, uint8_t* q8, uint8_t* q_idx8, msa_stream_t stream) {
+  return rotary_insert(cache, rows, n_tokens, cos_sin, max_pos, rot_dim, interleaved, positions, 1, nullptr,
+                       slot_mapping, q8, q_idx8, stream);
+}
+
+int msa_rotary_insert_axes(const msa_cache* cache, const msa_rows* rows, int32_t n_tokens, const float* cos_sin,
+                           int32_t max_pos, int32_t rot_dim, int32_t interleaved, const int32_t* positions,
+                           int32_t n_axes, const uint8_t* axis_of_pair, const int64_t* slot_mapping, uint8_t* q8,
+                           uint8_t* q_idx8, msa_stream_t stream) {
+  return rotary_insert(cache, rows, n_tokens, cos_sin, max_pos, rot_dim, interleaved, positions, n_axes, axis_of_pair,
+                       slot_mapping, q8, q_idx8, stream);
 }
 
 int msa_rope_table_freqs(float* cos_sin, int32_t max_pos, const double* freq, int32_t rot_dim, double amplitude,
@@ -402,14 +452,68 @@ size_t msa_block_row_bytes(int32_t n_layers) {
   return n_layers > 0 ? (size_t)n_layers * (msa::kKvPageBytes + msa::kIdxPageBytes) : 0;
 }
 
+int msa_extend_sequences(const msa_page_pool* pool, int32_t* block_table, int32_t max_pages, int32_t* seq_lens,
+                         const int32_t* q_start_loc, int32_t n_seqs, int32_t n_tokens, int64_t* slots,
+                         msa_stream_t stream) {
+  if (int rc = check_page_pool(pool)) return rc;
+  if (int rc = check_table(block_table, max_pages, seq_lens, n_seqs)) return rc;
+  if (n_tokens < 0 || !q_start_loc || (n_tokens > 0 && (!slots || n_seqs == 0))) return MSA_ERR_INVALID_ARG;
+  if (n_tokens > msa::max_extend_tokens()) return MSA_ERR_UNSUPPORTED_SHAPE;
+  return launched(msa::launch_extend(pool, block_table, max_pages, seq_lens, q_start_loc, n_seqs, n_tokens, slots,
+                                     reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t msa_fork_workspace_bytes(int32_t n) { return n > 0 ? msa::fork_workspace_bytes(n) : 16; }
+
+int msa_fork_sequences(const msa_cache* layers, int32_t n_layers, const msa_page_pool* pool, int32_t* block_table,
+                       int32_t max_pages, int32_t* seq_lens, int32_t n_seqs, const int32_t* src, const int32_t* dst,
+                       int32_t n, void* ws, size_t ws_bytes, msa_stream_t stream) {
+  if (int rc = check_layers(layers, n_layers)) return rc;
+  if (int rc = check_page_pool(pool)) return rc;
+  for (int l = 0; l < n_layers; ++l)
+    if (layers[l].n_pages < pool->n_pages) return MSA_ERR_INVALID_ARG;
+  if (int rc = check_table(block_table, max_pages, seq_lens, n_seqs)) return rc;
+  if (n < 0 || (n > 0 && (!src || !dst || !ws)) || (reinterpret_cast<uintptr_t>(ws) & 15)) return MSA_ERR_INVALID_ARG;
+  if (n > msa::kMaxSeqs) return MSA_ERR_UNSUPPORTED_SHAPE;
+  if (ws_bytes < msa_fork_workspace_bytes(n)) return MSA_ERR_WORKSPACE_TOO_SMALL;
+  return launched(msa::launch_fork(layers, n_layers, pool, block_table, max_pages, seq_lens, n_seqs, src, dst, n, ws,
+                                   reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int msa_release_sequences(const msa_page_pool* pool, int32_t* block_table, int32_t max_pages, int32_t* seq_lens,
+                          int32_t n_seqs, const int32_t* rows, int32_t n, msa_stream_t stream) {
+  if (int rc = check_page_pool(pool)) return rc;
+  if (int rc = check_table(block_table, max_pages, seq_lens, n_seqs)) return rc;
+  if (n < 0 || (n > 0 && !rows)) return MSA_ERR_INVALID_ARG;
+  if (n > msa::kMaxSeqs) return MSA_ERR_UNSUPPORTED_SHAPE;
+  return launched(msa::launch_release(pool, block_table, max_pages, seq_lens, n_seqs, rows, n,
+                                      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int msa_copy_pages(const msa_cache* layers, int32_t n_layers, const int32_t* src, const int32_t* dst,
+                   const int32_t* tokens, int32_t n, msa_stream_t stream) {
+  if (int rc = check_layers(layers, n_layers)) return rc;
+  if (n < 0 || (n > 0 && (!src || !dst))) return MSA_ERR_INVALID_ARG;
+  return launched(msa::launch_copy_pages(layers, n_layers, src, dst, tokens, n, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int msa_commit_drafts(const msa_cache* layers, int32_t n_layers, const int32_t* block_table, int32_t max_pages,
+                      const int32_t* seq_lens, const int32_t* q_start_loc, int32_t n_seqs, const uint64_t* accepted,
+                      int32_t* new_lens, msa_stream_t stream) {
+  if (int rc = check_layers(layers, n_layers)) return rc;
+  if (int rc = check_table(block_table, max_pages, seq_lens, n_seqs)) return rc;
+  if (!q_start_loc || (n_seqs > 0 && (!accepted || !new_lens))) return MSA_ERR_INVALID_ARG;
+  // (every CTA of a sequence reads its length: the new one cannot take its place)
+  const uintptr_t a = reinterpret_cast<uintptr_t>(seq_lens), b = reinterpret_cast<uintptr_t>(new_lens);
+  if (n_seqs > 0 && (a < b ? b - a : a - b) < (uintptr_t)n_seqs * sizeof(int32_t)) return MSA_ERR_INVALID_ARG;
+  return launched(msa::launch_commit(layers, n_layers, block_table, max_pages, seq_lens, q_start_loc, n_seqs, accepted,
+                                     new_lens, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 static int block_rows(const msa_cache* layers, int32_t n_layers, const int32_t* pages,
                       int32_t n_blocks, uint8_t* rows, bool pack, msa_stream_t stream) {
-  if (!layers || n_layers <= 0 || n_blocks < 0) return MSA_ERR_INVALID_ARG;
-  if (n_layers > msa::kMaxLayers) return MSA_ERR_UNSUPPORTED_SHAPE;
-  for (int l = 0; l < n_layers; ++l) {
-    if (int rc = check_cache(&layers[l])) return rc;
-    if (int rc = check_pools(&layers[l], 16, 16)) return rc;
-  }
+  if (n_blocks < 0) return MSA_ERR_INVALID_ARG;
+  if (int rc = check_layers(layers, n_layers)) return rc;
   if (n_blocks > 0 && (!pages || !rows)) return MSA_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(rows) & 15) return MSA_ERR_INVALID_ARG;
   return launched(msa::launch_block_rows(layers, n_layers, pages, n_blocks, rows, pack,
@@ -446,6 +550,7 @@ const char* msa_status_string(int code) {
     case MSA_STATUS_BAD_PAGE: return "device: block table entry outside the pool";
     case MSA_STATUS_BAD_SEQ: return "device: inconsistent sequence lengths / query counts";
     case MSA_STATUS_BAD_SELECTION: return "device: selected block outside 0..r_j";
+    case MSA_STATUS_NO_PAGES: return "device: no free page was left in the page pool";
     case MSA_STATUS_TIMEOUT: return "device: a bounded wait timed out; results invalid";
     default: return code > 0 ? "device: several status bits" : "unknown error";
   }

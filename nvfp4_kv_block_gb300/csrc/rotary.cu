@@ -46,7 +46,9 @@ struct RopeParams {
   int max_pos;
   int rot;
   int interleaved;
-  const int* positions;
+  const int* positions;  // [n_axes][n_tokens]
+  int n_axes;
+  uint32_t axes[4];      // axis of pair i: bits 2 (i % 16) and up of word i / 16
   const int64_t* slot_mapping;
   uint8_t* kv_pool;
   uint8_t* idx_pool;
@@ -175,7 +177,10 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
   b = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
 }
 
-template <typename T>
+// kAxes: a pair turns by the table row of its own axis's position (axis 0 for every pair otherwise).
+// A lane's eight pairs mostly share an axis (sections of 8 pairs and more): one row's loads; where
+// they do not, it takes the pairs from each axis's row.
+template <typename T, bool kAxes>
 __global__ void __launch_bounds__(kRopeThreads, 6) rotary_insert_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kPart = kPartHeads * kHeadDim * sizeof(T);  // bytes of a token's part
   constexpr int kWarps = kRopeThreads / 32;
@@ -211,13 +216,18 @@ __global__ void __launch_bounds__(kRopeThreads, 6) rotary_insert_kernel(const __
     // lane = (token sub, part l of its rows)
     const bool live = sub < cnt;
     const int t = t0 + sub;
-    const int pos = live && p.rot > 0 ? p.positions[t] : 0;
+    int pos[kAxes ? 4 : 1];
+    bool known = true;
+#pragma unroll
+    for (int a = 0; a < (kAxes ? 4 : 1); ++a) {
+      pos[a] = live && p.rot > 0 && (!kAxes || a < p.n_axes) ? p.positions[(size_t)a * p.n_tokens + t] : 0;
+      known &= pos[a] >= 0 && pos[a] < p.max_pos;
+    }
     int64_t slot = live && cached ? p.slot_mapping[t] : -1;
     if (slot >= 0 && (slot >> 7) >= p.n_pages) {
       set_status(p.status, MSA_STATUS_BAD_SLOT);
       slot = -1;
     }
-    const bool known = pos >= 0 && pos < p.max_pos;
     if (part == 2 && p.rot > 0 && live && !known) set_status(p.status, MSA_STATUS_BAD_SEQ);
     // half pairs: lanes below h have partner chunks h apart (values are not turned)
     const int h = p.interleaved || kind == 2 ? 0 : p.rot >> 4;
@@ -225,9 +235,33 @@ __global__ void __launch_bounds__(kRopeThreads, 6) rotary_insert_kernel(const __
     const bool turned = live && known && kind != 2 && (p.interleaved ? 16 * l < p.rot : l < h);
     float c[8], s[8];
     if (turned) {
-      const float* cs = p.cos_sin + (size_t)pos * p.rot + 8 * l;
-      load8(cs, c);
-      load8(cs + (p.rot >> 1), s);
+      if constexpr (kAxes) {
+        const uint32_t mine = p.axes[l >> 1] >> (16 * (l & 1)) & 0xFFFFu, first = mine & 3;
+        const float* cs = p.cos_sin + (size_t)(first < 2 ? (first ? pos[1] : pos[0]) : first == 2 ? pos[2] : pos[3]) * p.rot + 8 * l;
+        load8(cs, c);
+        load8(cs + (p.rot >> 1), s);
+        if (mine != first * 0x5555u) {
+#pragma unroll
+          for (int a = 0; a < 4; ++a) {
+            const uint32_t no = mine ^ (a * 0x5555u), is = ~(no | no >> 1) & 0x5555u;  // bit 2 u: pair u is of axis a
+            if (is == 0 || a == (int)first) continue;
+            float c1[8], s1[8];
+            cs = p.cos_sin + (size_t)pos[a] * p.rot + 8 * l;
+            load8(cs, c1);
+            load8(cs + (p.rot >> 1), s1);
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              if (is >> (2 * u) & 1) {
+                c[u] = c1[u];
+                s[u] = s1[u];
+              }
+          }
+        }
+      } else {
+        const float* cs = p.cos_sin + (size_t)pos[0] * p.rot + 8 * l;
+        load8(cs, c);
+        load8(cs + (p.rot >> 1), s);
+      }
     }
     if (!__all_sync(0xffffffffu, mbar_wait(bar, phase, WaitCtl{&s_abort, p.wait_ns}))) {
       // nothing of the tile is written, and the copies in flight are waited for
@@ -348,8 +382,8 @@ __global__ void rope_table_freqs_kernel(float* table, int max_pos, int half, Fre
 }  // namespace
 
 cudaError_t launch_rotary_insert(const msa_cache* c, const msa_rows* r, int n_tokens, const float* cos_sin,
-                                 int max_pos, int rot, int interleaved, const int* positions,
-                                 const int64_t* slot_mapping, uint8_t* q8, uint8_t* qi8, cudaStream_t stream) {
+                                 int max_pos, int rot, int interleaved, const int* positions, int n_axes,
+                                 const uint8_t* axis_of_pair, const int64_t* slot_mapping, uint8_t* q8, uint8_t* qi8, cudaStream_t stream) {
   if (n_tokens == 0) return cudaSuccess;
   static DeviceSetup setup;
   int dev = 0, n_sm = 0;
@@ -368,6 +402,8 @@ cudaError_t launch_rotary_insert(const msa_cache* c, const msa_rows* r, int n_to
   rp.rot = rot;
   rp.interleaved = interleaved;
   rp.positions = positions;
+  rp.n_axes = n_axes;
+  for (int i = 0; axis_of_pair && i < rot / 2; ++i) rp.axes[i / 16] |= (uint32_t)axis_of_pair[i] << (2 * (i % 16));
   rp.slot_mapping = slot_mapping;
   rp.kv_pool = static_cast<uint8_t*>(c->kv_pool);
   rp.idx_pool = static_cast<uint8_t*>(c->idx_pool);
@@ -385,9 +421,15 @@ cudaError_t launch_rotary_insert(const msa_cache* c, const msa_rows* r, int n_to
   const long long blocks = ((long long)n_tokens + per_block - 1) / per_block;
   const long long tiles = r->dtype == MSA_DTYPE_F32 ? std::min(3ll, std::max(1ll, blocks * parts / (12ll * n_sm))) : 1;
   const dim3 grid((unsigned)((blocks + tiles - 1) / tiles), parts), block(kRopeThreads);
-  if (r->dtype == MSA_DTYPE_F32) rotary_insert_kernel<float><<<grid, block, 0, stream>>>(rp);
-  else if (r->dtype == MSA_DTYPE_BF16) rotary_insert_kernel<__nv_bfloat16><<<grid, block, 0, stream>>>(rp);
-  else rotary_insert_kernel<__half><<<grid, block, 0, stream>>>(rp);
+  const bool axes = n_axes > 1;
+  auto launch = [&](auto zero) {
+    using T = decltype(zero);
+    if (axes) rotary_insert_kernel<T, true><<<grid, block, 0, stream>>>(rp);
+    else rotary_insert_kernel<T, false><<<grid, block, 0, stream>>>(rp);
+  };
+  if (r->dtype == MSA_DTYPE_F32) launch(0.f);
+  else if (r->dtype == MSA_DTYPE_BF16) launch(__nv_bfloat16{});
+  else launch(__half{});
   return cudaGetLastError();
 }
 

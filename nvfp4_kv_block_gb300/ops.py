@@ -31,6 +31,7 @@ NOALLOC_SCRATCH_BYTES = 8 << 20  # MSA_INDEXER_NOALLOC_SCRATCH_BYTES
 INJECT_BARRIER_TIMEOUT = 0x1     # MSA_INJECT_BARRIER_TIMEOUT
 INJECT_ATTENTION_TIMEOUT = 0x2   # MSA_INJECT_ATTENTION_TIMEOUT
 STATUS_BAD_SLOT, STATUS_BAD_PAGE, STATUS_BAD_SEQ, STATUS_BAD_SELECTION, STATUS_TIMEOUT = 0x1, 0x2, 0x4, 0x8, 0x10
+STATUS_NO_PAGES = 0x20
 IDX_PAGE_BYTES = 16_384
 
 ERRORS = {-1: "invalid argument", -2: "unsupported shape", -3: "workspace too small",
@@ -107,11 +108,19 @@ _SIGS = {
                                               ctypes.c_float, _P, _P, _P]),
     "msa_rope_table": (ctypes.c_int, [_P, _I32, ctypes.c_double, _P]),
     "msa_rotary_insert": (ctypes.c_int, [_P, _P, _I32, _P, _I32, _I32, _I32, _P, _P, _P, _P, _P]),
+    "msa_rotary_insert_axes": (ctypes.c_int, [_P, _P, _I32, _P, _I32, _I32, _I32, _P, _I32, ctypes.c_char_p, _P, _P, _P,
+                                              _P]),
     "msa_rope_table_freqs": (ctypes.c_int, [_P, _I32, _P, _I32, ctypes.c_double, _P]),
     "msa_read_kv": (ctypes.c_int, [_P, _P, _I32, _I32, _P, _P, _P, _P]),
     "msa_tree_attn": (ctypes.c_int, [_P, _P, _I32, ctypes.c_float, _P, _I32, _P, _P, _I32, _I32, _P, _P, _P, _I32, _P,
                                      _P, _P, ctypes.c_size_t, _P]),
     "msa_tree_attn_workspace_bytes": (ctypes.c_size_t, [_I32]),
+    "msa_extend_sequences": (ctypes.c_int, [_P, _P, _I32, _P, _P, _I32, _I32, _P, _P]),
+    "msa_fork_sequences": (ctypes.c_int, [_P, _I32, _P, _P, _I32, _P, _I32, _P, _P, _I32, _P, ctypes.c_size_t, _P]),
+    "msa_fork_workspace_bytes": (ctypes.c_size_t, [_I32]),
+    "msa_release_sequences": (ctypes.c_int, [_P, _P, _I32, _P, _I32, _P, _I32, _P]),
+    "msa_copy_pages": (ctypes.c_int, [_P, _I32, _P, _P, _P, _I32, _P]),
+    "msa_commit_drafts": (ctypes.c_int, [_P, _I32, _P, _I32, _P, _P, _I32, _P, _P, _P]),
     "msa_absmax": (ctypes.c_int, [_P, _I64, _P, _P]),
     "msa_encode_scale": (ctypes.c_float, [ctypes.c_float]),
     "msa_debug_fp8_page": (ctypes.c_int, [_P, _I64, _P, _P, _P]),
@@ -547,8 +556,39 @@ def _rows(t, name, shape, dtype, dev):
     raise ValueError(f"{name} must be on the cache's device cuda:{dev}, got {t.device}")
 
 
+MAX_AXES = 4  # MSA_MAX_AXES
+
+
+class RopeAxes:
+    """The axis of each rotary pair: ``n_axes`` and ``pairs`` (bytes, one per pair)."""
+
+    def __init__(self, n_axes, pairs):
+        self.n_axes, self.pairs = int(n_axes), bytes(pairs)
+        if not 1 <= self.n_axes <= MAX_AXES:
+            raise ValueError(f"1 to {MAX_AXES} axes, not {n_axes}")
+        if any(a >= self.n_axes for a in self.pairs):
+            raise ValueError(f"a pair's axis must be below {n_axes}")
+
+
+def rope_axes(sections, dealt=False):
+    """RopeAxes of ``sections``: how many pairs turn by each axis (time, height, width, ...;
+    their sum is rot_dim / 2).  The sections follow one another (pairs 0 .. sections[0] - 1
+    are the first axis's), or, when ``dealt``, the axes take the pairs in turn, axis
+    i % n_axes pair i, as long as i < n_axes * sections[i % n_axes]; the pairs that no axis
+    takes so are the first axis's."""
+    sections = [int(n) for n in sections]
+    if not sections or min(sections) < 0:
+        raise ValueError("sections must be counts of pairs")
+    m = len(sections)
+    if dealt:
+        pairs = [i % m if i < m * sections[i % m] else 0 for i in range(sum(sections))]
+    else:
+        pairs = [a for a, n in enumerate(sections) for _ in range(n)]
+    return RopeAxes(m, pairs)
+
+
 def rotary_insert(cache, q, k, v, idx_k, cos_sin, positions, slot_mapping, q_idx=None, interleaved=False, q8=None,
-                  qi8=None):
+                  qi8=None, axes=None):
     """Rotary positions on projected rows, FP8 queries and index queries (returned:
     uint8 [n, 16, 128] and [n, 8, 128], or None without ``q_idx``), and NVFP4 / FP8
     cache insertion at ``slot_mapping`` (negative: not inserted).
@@ -556,7 +596,9 @@ def rotary_insert(cache, q, k, v, idx_k, cos_sin, positions, slot_mapping, q_idx
     Rows are fp32, bf16 or fp16, [n, heads, 128] ([n, 128] index keys), contiguous
     within a token; slices of one projection's output will do.  ``cos_sin`` is fp32
     [max_pos, rot_dim]: the first rot_dim channels of each head are turned, in pairs
-    (i, i + rot_dim / 2), or (2i, 2i + 1) when ``interleaved``.
+    (i, i + rot_dim / 2), or (2i, 2i + 1) when ``interleaved``, by the table's row at
+    ``positions`` (int32 [n]), or, with ``axes`` (rope_axes, one entry per pair), at each
+    pair's own axis of ``positions`` (int32 [n_axes, n]).
     """
     n, dtype = q.shape[0], q.dtype
     code = _DTYPES.get(dtype)
@@ -578,6 +620,16 @@ def rotary_insert(cache, q, k, v, idx_k, cos_sin, positions, slot_mapping, q_idx
             qi8 = torch.empty((n, IDX_HEADS, IDX_DIM), dtype=torch.uint8, device=q.device)
         qi8p = _arg(qi8, torch.uint8, (n, IDX_HEADS, IDX_DIM), dev, "qi8")
     max_pos, rot_dim = cos_sin.shape
+    if axes is not None:
+        if len(axes.pairs) != rot_dim // 2:
+            raise ValueError(f"axes are of {len(axes.pairs)} pairs, the table of {rot_dim // 2}")
+        _check(lib().msa_rotary_insert_axes(
+            cache.packed(), _ROWS.pack(qp, kp, vp, ip, qip, qs, ks, vs, i_s, qis, code), n,
+            _arg(cos_sin, torch.float32, (max_pos, rot_dim), dev, "cos_sin"), max_pos, rot_dim, 1 if interleaved else 0,
+            _arg(positions, torch.int32, (axes.n_axes, n), dev, "positions"), axes.n_axes, axes.pairs,
+            _arg(slot_mapping, torch.int64, (n,), dev, "slot_mapping"),
+            _arg(q8, torch.uint8, (n, Q_HEADS, HEAD_DIM), dev, "q8"), qi8p, _raw_stream(dev)))
+        return q8, qi8
     _check(lib().msa_rotary_insert(
         cache.packed(), _ROWS.pack(qp, kp, vp, ip, qip, qs, ks, vs, i_s, qis, code), n,
         _arg(cos_sin, torch.float32, (max_pos, rot_dim), dev, "cos_sin"), max_pos, rot_dim, 1 if interleaved else 0,
@@ -661,6 +713,147 @@ def tree_attn(cache, q, block_table, seq_lens, q_start_loc, bufs, tree_mask=None
         _arg(bufs.lse, torch.float32, (T, Q_HEADS), dev, "bufs.lse"), bufs.ws.data_ptr(), bufs.ws.numel(),
         _raw_stream(dev)))
     return bufs.out
+
+
+class CacheLayers:
+    """The caches of a model's layers, in which page p is the same block: the array that
+    the calls on all layers take, made once.  The caches' pools stay theirs."""
+
+    def __init__(self, caches):
+        self.caches = list(caches)
+        if not self.caches:
+            raise ValueError("at least one cache")
+        if any(c.kv_pool.device != self.caches[0].kv_pool.device for c in self.caches):
+            raise ValueError("the caches must be on one device")
+        self.n = len(self.caches)
+        self.array = _layer_array(self.caches)
+
+    @staticmethod
+    def of(x):
+        """``x`` if it is one, else the CacheLayers of a cache or of a list of caches."""
+        return x if isinstance(x, CacheLayers) else CacheLayers([x] if isinstance(x, KVCache) else x)
+
+
+_POOL = struct.Struct("@PPiP")
+
+
+class PagePool:
+    """Counts of the block-table entries that hold each of n_pages pages: ``refs`` int32
+    [n_pages], and the free ones' mask, which the calls below keep in step (refs is read,
+    not written, by anyone else).  ``status``: int32 [1] word of sticky STATUS_* bits."""
+
+    def __init__(self, n_pages, status=None, device="cuda"):
+        self._set(torch.zeros(int(n_pages), dtype=torch.int32, device=device), status)
+
+    @classmethod
+    def from_refs(cls, refs, status=None):
+        """A pool over counts that the caller holds already (int32 [n_pages], no smaller than 0)."""
+        _ptr(refs, torch.int32, "refs", 1)
+        self = cls.__new__(cls)
+        self._set(refs, status)
+        return self
+
+    def _set(self, refs, status):
+        self.n_pages, self.refs = refs.shape[0], refs
+        if self.n_pages == 0:
+            raise ValueError("a pool has at least one page")
+        if status is None:
+            status = torch.zeros(1, dtype=torch.int32, device=refs.device)
+        _ptr(status, torch.int32, "status", 1)
+        if status.device != refs.device:
+            raise ValueError("refs and the status word must be on one device")
+        self.status = status
+        bits = torch.zeros(-(-self.n_pages // 32) * 32, dtype=torch.int64, device=refs.device)
+        bits[: self.n_pages] = refs == 0
+        words = (bits.view(-1, 32) << torch.arange(32, device=refs.device)).sum(1)
+        self.free_mask = torch.where(words >= 1 << 31, words - (1 << 32), words).to(torch.int32)
+        self._ws = torch.zeros(lib().msa_fork_workspace_bytes(4096), dtype=torch.uint8, device=refs.device)
+
+    def packed(self):
+        return _POOL.pack(self.refs.data_ptr(), self.free_mask.data_ptr(), self.n_pages, self.status.data_ptr())
+
+
+def _table(pool, block_table, seq_lens):
+    """(device, rows, columns, pointers) of a block table and its lengths."""
+    dev = pool.refs.get_device()
+    if dev != _current_device():
+        raise ValueError(f"the pool is on {pool.refs.device}, not on the current CUDA device")
+    n_seqs, max_pages = block_table.shape
+    return (dev, n_seqs, max_pages, _arg(block_table, torch.int32, (n_seqs, max_pages), dev, "block_table"),
+            _arg(seq_lens, torch.int32, (n_seqs,), dev, "seq_lens"))
+
+
+def extend_sequences(pool, block_table, seq_lens, q_start_loc, slots):
+    """Room for q_start_loc[b + 1] - q_start_loc[b] new tokens of each sequence: pages of
+    the pool for the entries of its row that have none (lowest pages first), its length
+    grown in place.  ``slots`` (int64 [n_tokens], returned) gets the slot of every new token,
+    or -1 where a sequence could not grow and for rows behind the last sequence."""
+    dev, n_seqs, max_pages, table, lens = _table(pool, block_table, seq_lens)
+    n = slots.shape[0]
+    _check(lib().msa_extend_sequences(pool.packed(), table, max_pages, lens,
+                                      _arg(q_start_loc, torch.int32, (n_seqs + 1,), dev, "q_start_loc"), n_seqs, n,
+                                      _arg(slots, torch.int64, (n,), dev, "slots"), _raw_stream(dev)))
+    return slots
+
+
+def fork_sequences(layers, pool, block_table, seq_lens, src, dst):
+    """Row dst[i] of the table, which has to be empty, becomes a second copy of row src[i]
+    (int32 [n] each): full pages are shared, the tokens of the last one are copied to a page
+    of its own in every layer (``layers``: CacheLayers, a list of caches or one cache)."""
+    layers = CacheLayers.of(layers)
+    dev, n_seqs, max_pages, table, lens = _table(pool, block_table, seq_lens)
+    _same_device(layers, dev)
+    n = src.shape[0]
+    _check(lib().msa_fork_sequences(layers.array, layers.n, pool.packed(), table, max_pages, lens, n_seqs,
+                                    _arg(src, torch.int32, (n,), dev, "src"), _arg(dst, torch.int32, (n,), dev, "dst"), n,
+                                    pool._ws.data_ptr(), pool._ws.numel(), _raw_stream(dev)))
+
+
+def release_sequences(pool, block_table, seq_lens, rows):
+    """Gives the pages of the table's rows ``rows`` (int32 [n]) back and empties the rows."""
+    dev, n_seqs, max_pages, table, lens = _table(pool, block_table, seq_lens)
+    n = rows.shape[0]
+    _check(lib().msa_release_sequences(pool.packed(), table, max_pages, lens, n_seqs,
+                                       _arg(rows, torch.int32, (n,), dev, "rows"), n, _raw_stream(dev)))
+
+
+def _same_device(layers, dev):
+    at = layers.caches[0].kv_pool.get_device()
+    if at != dev or at != _current_device():
+        raise ValueError(f"the caches are on {layers.caches[0].kv_pool.device}, not on the current CUDA device")
+
+
+def copy_pages(layers, src, dst, tokens=None):
+    """Page src[i] to page dst[i] (int32 [n] each; negative: none) in every layer, or its
+    first tokens[i] tokens (int32 [n]).  Targets are distinct and no pair's source."""
+    layers = CacheLayers.of(layers)
+    dev = src.get_device()
+    _same_device(layers, dev)
+    n = src.shape[0]
+    _check(lib().msa_copy_pages(layers.array, layers.n, _arg(src, torch.int32, (n,), dev, "src"),
+                                _arg(dst, torch.int32, (n,), dev, "dst"),
+                                None if tokens is None else _arg(tokens, torch.int32, (n,), dev, "tokens"), n,
+                                _raw_stream(dev)))
+
+
+def commit_drafts(layers, block_table, seq_lens, q_start_loc, accepted, new_lens=None):
+    """Of each sequence's last q_start_loc[b + 1] - q_start_loc[b] tokens (drafts that
+    tree_attn verified) those whose bits ``accepted`` (int64 [B]) has move together behind
+    its context, in every layer.  Returns the new lengths (``new_lens`` or a new tensor,
+    never seq_lens itself); the row keeps its pages."""
+    layers = CacheLayers.of(layers)
+    dev = seq_lens.get_device()
+    _same_device(layers, dev)
+    n_seqs, max_pages = block_table.shape
+    if new_lens is None:
+        new_lens = torch.empty_like(seq_lens)
+    _check(lib().msa_commit_drafts(
+        layers.array, layers.n, _arg(block_table, torch.int32, (n_seqs, max_pages), dev, "block_table"), max_pages,
+        _arg(seq_lens, torch.int32, (n_seqs,), dev, "seq_lens"),
+        _arg(q_start_loc, torch.int32, (n_seqs + 1,), dev, "q_start_loc"), n_seqs,
+        _arg(accepted, torch.int64, (n_seqs,), dev, "accepted"), _arg(new_lens, torch.int32, (n_seqs,), dev, "new_lens"),
+        _raw_stream(dev)))
+    return new_lens
 
 
 def set_fault_injection(flags=0, wait_limit_ns=0):
