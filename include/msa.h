@@ -505,6 +505,43 @@ int msa_tree_attn(const msa_cache* cache, const uint8_t* q, int32_t n_q_heads, f
 size_t msa_tree_attn_workspace_bytes(int32_t n_q_total);
 
 /*
+ * Attention of a prompt's tokens over the cached context: any number of query tokens a
+ * sequence (a whole prompt, a chunk of one, chunks of several prompts in one call), whose
+ * keys and values are in the cache already.
+ *
+ *   q, block_table, max_pages, seq_lens, q_start_loc, n_seqs, n_q_total as msa_tree_attn,
+ *               with any number of tokens a sequence.  Token i of a sequence is at position
+ *               pos = seq_lens[b] - n_q + i.
+ *   window      0, or the number of positions that a token sees, its own the last of them:
+ *               start = max(0, pos + 1 - window) (0: start = 0).
+ *   ends        int32 [n_q_total] or NULL: the tokens of its sequence that a token sees
+ *               end before position ends[j] (clamped to 0 .. seq_lens[b]), so that, for
+ *               instance, the tokens of an image see all of it.  NULL: ends[j] = pos + 1.
+ *               A token sees the positions start <= t < end; none where end <= start.
+ *   n_visited   pages that ws has room for: the sequences' pages from the first that
+ *               their first token sees to their last, summed over the call, at most (the
+ *               sum of ceil(seq_lens[b] / 128) always will do).  A sequence behind that
+ *               many sets MSA_STATUS_BAD_SEQ and keeps its rows.
+ *   dtype, out, lse as msa_tree_attn.
+ *   ws, ws_bytes scratch of at least msa_prefill_workspace_bytes(n_q_total, n_seqs,
+ *               n_visited) bytes, 16-byte aligned, nothing of which is kept between calls.
+ *               Calls sharing a workspace must not overlap on the GPU.
+ * Rows behind the last sequence, and those of an inconsistent one (MSA_STATUS_BAD_SEQ),
+ * are left as they were.  Operands, sums and special values as msa_tree_attn; the weights
+ * are rounded to f16 once (2^-11 relative, or 2^-33 of the weight at the row's reference).
+ * Rows are summed in an order that depends on the call's sizes only.
+ * softmax_scale > 0 and at most 2^26 s_enc_k / (448 * 448 * 128 log2(e)); s_enc_v above
+ * 2^-120 and at most 2^100.  Limits: n_seqs <= 4096, n_q_total <= 262,144, n_visited <=
+ * 1,048,576.  Three launches, programmatic dependents of the kernel before them.
+ */
+int msa_prefill_attn(const msa_cache* cache, const uint8_t* q, int32_t n_q_heads, float softmax_scale,
+                     const int32_t* block_table, int32_t max_pages, const int32_t* seq_lens,
+                     const int32_t* q_start_loc, int32_t n_seqs, int32_t n_q_total, int32_t window,
+                     const int32_t* ends, int32_t n_visited, int32_t dtype, void* out, float* lse, void* ws,
+                     size_t ws_bytes, msa_stream_t stream);
+size_t msa_prefill_workspace_bytes(int32_t n_q_total, int32_t n_seqs, int32_t n_visited);
+
+/*
  * Block-outer transfer rows (blog, "AMD uses different conversion and
  * communication mechanisms": a KV block kept as one contiguous row is moved in
  * one read instead of one read per page).  The row of a block holds, for every
@@ -648,7 +685,7 @@ int msa_debug_fp8_page(const msa_cache* cache, int64_t page, uint8_t* k8, uint8_
  *                               MSA_STATUS_TIMEOUT, leaves sel/n_sel unwritten
  *                               and its workspace barrier word at rest;
  *   MSA_INJECT_ATTENTION_TIMEOUT  every CTA of an attention kernel (sparse
- *                               decode or tree) leaves out the copy of its first page, so the waits for it
+ *                               decode, tree or prefill) leaves out the copy of its first page, so the waits for it
  *                               run out after wait_limit_ns: the call sets
  *                               MSA_STATUS_TIMEOUT, its CTAs release tensor
  *                               memory only after their copies and tensor-core

@@ -39,6 +39,9 @@ cudaError_t launch_rope_table_freqs(float*, int, const double*, int, double, cud
 size_t tree_attn_workspace_bytes(int);
 cudaError_t launch_tree_attn(const msa_cache*, const uint8_t*, float, const int*, int, const int*, const int*, int, int,
                              const uint64_t*, const int*, const int*, int, void*, float*, void*, cudaStream_t);
+size_t prefill_workspace_bytes(int, int, int);
+cudaError_t launch_prefill_attn(const msa_cache*, const uint8_t*, float, const int*, int, const int*, const int*, int,
+                                int, int, const int*, int, int, void*, float*, void*, cudaStream_t);
 int max_extend_tokens();
 size_t fork_workspace_bytes(int);
 cudaError_t launch_extend(const msa_page_pool*, int*, int, int*, const int*, int, int, int64_t*, cudaStream_t);
@@ -446,6 +449,36 @@ int msa_tree_attn(const msa_cache* cache, const uint8_t* q, int32_t n_q_heads, f
   return launched(msa::launch_tree_attn(cache, q, softmax_scale, block_table, max_pages, seq_lens, q_start_loc, n_seqs,
                                         n_q_total, tree_mask, sel, n_sel, dtype, out, lse, ws,
                                         reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t msa_prefill_workspace_bytes(int32_t n_q_total, int32_t n_seqs, int32_t n_visited) {
+  return n_q_total > 0 && n_seqs > 0 && n_visited >= 0 ? msa::prefill_workspace_bytes(n_q_total, n_seqs, n_visited) : 256;
+}
+
+int msa_prefill_attn(const msa_cache* cache, const uint8_t* q, int32_t n_q_heads, float softmax_scale,
+                     const int32_t* block_table, int32_t max_pages, const int32_t* seq_lens,
+                     const int32_t* q_start_loc, int32_t n_seqs, int32_t n_q_total, int32_t window,
+                     const int32_t* ends, int32_t n_visited, int32_t dtype, void* out, float* lse, void* ws,
+                     size_t ws_bytes, msa_stream_t stream) {
+  if (int rc = check_cache(cache)) return rc;
+  if (n_q_heads != msa::kQHeads) return MSA_ERR_UNSUPPORTED_SHAPE;
+  if (n_q_total < 0 || n_seqs < 0 || max_pages <= 0 || window < 0 || n_visited < 0 || !(softmax_scale > 0.f) ||
+      !isfinite(softmax_scale) || (dtype != MSA_DTYPE_BF16 && dtype != MSA_DTYPE_F16))
+    return MSA_ERR_INVALID_ARG;
+  if (n_q_total > 262144 || n_seqs > msa::kMaxSeqs || max_pages > kMaxPagesPerSeq || n_visited > (1 << 20))
+    return MSA_ERR_UNSUPPORTED_SHAPE;
+  if (n_q_total > 0 && (!q || !block_table || !seq_lens || !q_start_loc || !out || !ws || n_seqs == 0))
+    return MSA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(ws)) & 15) return MSA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(out) & 31) return MSA_ERR_INVALID_ARG;  // 32-byte stores
+  // (scores of 2^26 and less: the rounding of the reference's product is below the room above a weight of 2^8)
+  if (!(softmax_scale / cache->s_enc_k * (128.f * 448.f * 448.f * 1.4426950408889634f) <= 0x1p26f)) return MSA_ERR_INVALID_ARG;
+  if (!isfinite(256.f / cache->s_enc_v) || cache->s_enc_v > 0x1p100f) return MSA_ERR_INVALID_ARG;
+  if (ws_bytes < msa_prefill_workspace_bytes(n_q_total, n_seqs, n_visited)) return MSA_ERR_WORKSPACE_TOO_SMALL;
+  if (int rc = check_pools(cache, 16, 1)) return rc;
+  return launched(msa::launch_prefill_attn(cache, q, softmax_scale, block_table, max_pages, seq_lens, q_start_loc, n_seqs,
+                                           n_q_total, window, ends, n_visited, dtype, out, lse, ws,
+                                           reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t msa_block_row_bytes(int32_t n_layers) {

@@ -1,0 +1,897 @@
+// Attention of a prompt's tokens, any number a sequence, over the sequence's pages of the
+// NVFP4 cache: causal, within a window, or up to an end that each token brings along.
+//
+// Mathematics.  For a row (token, query head) with FP8 query q, the keys k8_t and values v8_t
+// dequantised to FP8 as in the other attention kernels, over start <= t < end,
+//   x_t = (q . k8_t) scale / s_enc_k log2(e),  out = sum_t 2^x_t v8_t / sum_t 2^x_t / s_enc_v,
+// in one pass over the pages with a reference m per row: weights 2^(x_t - m + 8), summed in
+// fp32, multiply V in f16 (a relative 2^-11; an E4M3 weight would lose the bulk of a long
+// context behind one large key).  m moves, to the page's maximum, only when a weight would
+// pass 49,152 (f16 ends at 65,504), so the accumulator is rescaled a few times per row.
+//
+// Three kernels.  (1) Every page that the call visits is converted once per KV head into the
+// operand tiles of the products, 16 KB of E4M3 keys and 32 KB of f16 values, by a kernel bound
+// by memory; it also writes down the tiles of 64 tokens and their pages.  (2) The attention: a job
+// is a tile (256 rows, 4 i + h for token i and head h of the group) and a KV head; the jobs'
+// pages in a row are cut into equal weighted ranges, one per persistent CTA.  (3) Jobs that
+// were cut leave fp32 rows that a third kernel joins in a fixed order.
+//
+// Roles of the attention's warps, all hand-offs mbarriers with bounded waits:
+//   warp 0      segment records, a bulk copy of 16 KB and one of 32 KB per page;
+//   warp 1      MMA issuer: S = Q K8^T (kind::f8f6f4, 128 x 128 x 128), then O += P V
+//               (kind::f16, P from tensor memory over S's own columns);
+//   warp 2      query rows of the next segment;
+//   warps 4-11  softmax, thread = row: a set of four warps for each 128 rows.
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <cfloat>
+
+#include "attn_ops.cuh"
+
+namespace msa {
+namespace {
+
+constexpr int kPrefillThreads = 384;
+constexpr int kTileTokens = 64;       // two row tiles of 32 tokens x 4 heads
+constexpr int kPrefillCtas = 152;     // most CTAs of a launch (the workspace is sized for them)
+constexpr int kStages = 3;            // pages in flight
+constexpr int kRecs = 4;
+constexpr int kInfo = 16;
+constexpr int kImageK = 16384, kImage = kImageK + 32768;  // bytes of a converted (page, KV head)
+
+constexpr int kOffQ = 0;                                  // 2 segments x 2 tiles [128 rows][128 B]
+constexpr int kOffK = kOffQ + 4 * 16384;                  // kStages x [8 groups of 16 channels][128 tokens][16 B]
+constexpr int kOffV = kOffK + kStages * kImageK;          // kStages x [16 groups of 8 channels][128 tokens][16 B]
+constexpr int kOffRecs = kOffV + kStages * 32768;         // kRecs x 64 B
+constexpr int kOffInfo = kOffRecs + kRecs * 64;           // int [kInfo]: page inside the pool
+constexpr int kOffScan = kOffInfo + kInfo * 4;            // long long [16]
+constexpr int kOffBars = kOffScan + 16 * 8;
+constexpr int kBKFull = 0, kBKEmpty = kBKFull + kStages, kBVFull = kBKEmpty + kStages, kBVEmpty = kBVFull + kStages,
+              kBQFull = kBVEmpty + kStages, kBQEmpty = kBQFull + 2, kBSFull = kBQEmpty + 2, kBPFull = kBSFull + 2,
+              kBPvDone = kBPFull + 4, kBOFree = kBPvDone + 2, kBRecFull = kBOFree + 2, kBRecEmpty = kBRecFull + kRecs,
+              kBDone = kBRecEmpty + kRecs, kBars = kBDone + 1;
+constexpr int kOffMisc = kOffBars + 8 * ((kBars + 1) & ~1);  // tmem, abort, K and V copies issued
+constexpr int kPrefillSmem = 1024 + kOffMisc + 16;
+static_assert(kPrefillSmem <= 232448, "shared memory of one CTA");
+constexpr uint32_t kTmemS = 0, kTmemO = 256;  // S of set s at 128 s, O of set s at 256 + 128 s
+constexpr float kBias = 8.0f;
+constexpr float kMostLog2 = 15.5849625f;  // log2(49,152)
+constexpr float kUnset = 3e38f;           // shift of a row without a reference
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// Weights of the partition: a page of a tile of up to 32 tokens and of one of up to 64, the fixed
+// part of a job, and the least share of a CTA (a page's weight at least, so that every CTA
+// between a job's first and last has pages of it).
+constexpr int kPage1 = 5, kPage2 = 9, kFixed = 10, kLeast = 10;
+
+struct TileRec {
+  int q0, n_tok;  // rows of the call
+  int pos;        // position of the first token
+  int len;        // tokens of the sequence
+  int page0;      // first page (block of the sequence), and how many (0: nothing to do)
+  int n_pg;
+  int ws_page;    // its place among the converted pages
+  int pad;
+};
+static_assert(sizeof(TileRec) == 32, "loaded by eight lanes");
+
+struct SegRec {
+  int n_pg;  // pages of the segment; -1: no more segments
+  int g, q0, n_tok, pos, len;
+  int page0;
+  int slot;  // partial slot, or -1: the segment is the whole job
+};
+static_assert(sizeof(SegRec) <= 64, "record slot");
+
+struct PrefillParams {
+  const uint8_t* kv_pool;
+  int64_t n_pages;
+  const uint8_t* q;  // [T][16][128]
+  const int* block_table;
+  int max_pages;
+  const int* seq_lens;
+  const int* q_start_loc;
+  int n_seqs;
+  int n_q_total;
+  int window;       // 0: none
+  const int* ends;  // [T] or null
+  float scale_log2;
+  float out_scale;  // 2^8 / s_enc_v
+  int out_f16;
+  uint16_t* out;  // [T][16][128]
+  float* lse;     // [T][16] or null
+  int* n_tiles;   // workspace from here on
+  TileRec* tiles;
+  int max_tiles;
+  int* desc;         // [max_tiles][4]: first CTA | parts << 8, 0 = nothing to join
+  int* page_ok;      // [cap]
+  int cap;           // converted pages that fit
+  float* part_o;     // [2 kPrefillCtas][part_rows][128]
+  float2* part_ml;   // [2 kPrefillCtas][part_rows]
+  int part_rows;
+  uint8_t* images;   // [cap][4][kImage]
+  int* status;
+  unsigned long long wait_ns;
+  int inject;  // test only: a CTA's first page is not copied, so that the waits for it run out
+};
+
+// ---- (1) conversion and tiles -------------------------------------------------------
+constexpr int kConvThreads = 256;
+constexpr int kConvKCopies = 4, kConvVCopies = 8;
+constexpr int kConvTables = 128 * (8 * kConvKCopies + 16 * kConvVCopies);
+
+// First page that a sequence's rows can see, and pages from there to its end.
+__device__ __forceinline__ int first_page(const PrefillParams& p, int pos) {
+  return p.window ? max(0, pos + 1 - p.window) / kPageTokens : 0;
+}
+
+__global__ void __launch_bounds__(kConvThreads) prefill_convert_kernel(const __grid_constant__ PrefillParams p) {
+  extern __shared__ __align__(16) uint8_t conv_smem[];
+  __shared__ int2 s_warp[kConvThreads / 32];
+  uint2* kt = reinterpret_cast<uint2*>(conv_smem);
+  uint4* vt = reinterpret_cast<uint4*>(conv_smem + 128 * 8 * kConvKCopies);
+  int* s_page = reinterpret_cast<int*>(conv_smem + kConvTables);  // [n_seqs + 1] pages before sequence b
+  int* s_tile = s_page + p.n_seqs + 1;                            // tiles before it
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid < 128) convert_tables<kConvKCopies, kConvVCopies>(tid, kt, vt);
+  pdl_wait();
+  pdl_trigger();
+  const int per = (p.n_seqs + kConvThreads - 1) / kConvThreads;
+  int2 mine = make_int2(0, 0);
+  auto work = [&](int b) {  // pages and tiles of a sequence
+    const SeqInfo s = load_seq(b, p.seq_lens, p.q_start_loc, p.max_pages, p.n_q_total);
+    if (!s.ok) {
+      if (blockIdx.x == 0) set_status(p.status, MSA_STATUS_BAD_SEQ);
+      return make_int2(0, 0);
+    }
+    if (s.n_q == 0) return make_int2(0, 0);
+    return make_int2((s.seq_len + kPageTokens - 1) / kPageTokens - first_page(p, s.seq_len - s.n_q),
+                     (s.n_q + kTileTokens - 1) / kTileTokens);
+  };
+  const int b0 = min(tid * per, p.n_seqs), b1 = min(b0 + per, p.n_seqs);
+  for (int b = b0; b < b1; ++b) {
+    const int2 w = work(b);
+    s_page[b + 1] = w.x;
+    s_tile[b + 1] = w.y;
+    mine.x += w.x;
+    mine.y += w.y;
+  }
+  int2 incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, incl.x, o), y = __shfl_up_sync(0xffffffffu, incl.y, o);
+    if (lane >= o) {
+      incl.x += x;
+      incl.y += y;
+    }
+  }
+  if (lane == 31) s_warp[warp] = incl;
+  __syncthreads();
+  int2 at = make_int2(incl.x - mine.x, incl.y - mine.y);
+  for (int i = 0; i < warp; ++i) {
+    at.x += s_warp[i].x;
+    at.y += s_warp[i].y;
+  }
+  if (tid == 0) s_page[0] = s_tile[0] = 0;
+  for (int b = b0; b < b1; ++b) {
+    at.x += s_page[b + 1];
+    at.y += s_tile[b + 1];
+    s_page[b + 1] = at.x;
+    s_tile[b + 1] = at.y;
+  }
+  __syncthreads();
+  // (what does not fit the workspace is left out: more pages than it is for, or rows that several
+  // sequences claim)
+  auto fits = [&](int b) { return s_page[b + 1] <= p.cap && s_tile[b + 1] <= p.max_tiles; };
+  auto find = [&](const int* prefix, int x) {  // the last b with prefix[b] <= x
+    int lo = 0, hi = p.n_seqs - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (prefix[mid] <= x) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+  };
+  const int n_tiles = min(s_tile[p.n_seqs], p.max_tiles);
+  if (blockIdx.x == 0) {
+    if (tid == 0) *p.n_tiles = n_tiles;
+    for (int b = tid; b < p.n_seqs; b += kConvThreads)
+      if (s_page[b + 1] > s_page[b] && !fits(b)) set_status(p.status, MSA_STATUS_BAD_SEQ);
+  }
+  // a warp per tile
+  for (int t = (int)blockIdx.x * (kConvThreads / 32) + warp; t < n_tiles; t += (int)gridDim.x * (kConvThreads / 32)) {
+    const int b = find(s_tile, t);
+    const SeqInfo s = load_seq(b, p.seq_lens, p.q_start_loc, p.max_pages, p.n_q_total);
+    TileRec r{};
+    const int i0 = kTileTokens * (t - s_tile[b]);
+    r.q0 = s.q0 + i0;
+    r.n_tok = min(kTileTokens, s.n_q - i0);
+    r.pos = s.seq_len - s.n_q + i0;
+    r.len = s.seq_len;
+    int top = r.pos + r.n_tok;  // behind the last key that some row sees
+    if (p.ends) {
+      top = max(lane < r.n_tok ? p.ends[r.q0 + lane] : 0, lane + 32 < r.n_tok ? p.ends[r.q0 + lane + 32] : 0);
+      top = min(__reduce_max_sync(0xffffffffu, top), r.len);
+    }
+    const int seq0 = first_page(p, s.seq_len - s.n_q);
+    r.page0 = first_page(p, r.pos);
+    r.n_pg = fits(b) ? max(1, (top + kPageTokens - 1) / kPageTokens - r.page0) : 0;
+    r.ws_page = s_page[b] + r.page0 - seq0;
+    if (lane == 0) p.tiles[t] = r;
+    if (lane < kKvHeads) p.desc[t * kKvHeads + lane] = 0;
+  }
+  // (page, head) units: thread = token and half of the channels
+  const int tok = tid & 127, half = tid >> 7;
+  const uint2* my_kt = kt + (lane & (kConvKCopies - 1));
+  const uint4* my_vt = vt + (lane & (kConvVCopies - 1));
+  const int units = min(s_page[p.n_seqs], p.cap) * kKvHeads;
+  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    const int page = u / kKvHeads, g = u % kKvHeads;
+    const int b = find(s_page, page);
+    if (!fits(b)) continue;
+    const int n_q = p.q_start_loc[b + 1] - p.q_start_loc[b];
+    const int blk = first_page(p, p.seq_lens[b] - n_q) + page - s_page[b];
+    const int phys = p.block_table[(size_t)b * p.max_pages + blk];
+    const bool ok = phys >= 0 && phys < p.n_pages;
+    if (tid == 0 && g == 0) {
+      if (!ok) set_status(p.status, MSA_STATUS_BAD_PAGE);
+      p.page_ok[page] = ok;
+    }
+    uint8_t* out = p.images + ((size_t)page * kKvHeads + g) * kImage;
+    uint4* ko = reinterpret_cast<uint4*>(out) + 4 * half * kPageTokens + tok;            // group 4 half + i: + 128 i
+    uint4* vo = reinterpret_cast<uint4*>(out + kImageK) + 8 * half * kPageTokens + tok;  // group 8 half + i
+    if (!ok) {  // zeros: the values meet weights of zero
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ko[i * kPageTokens] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) vo[i * kPageTokens] = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    const uint8_t* head = p.kv_pool + (size_t)phys * kKvPageBytes + (size_t)g * kHeadBytes;
+    uint4 kc[2], vc[2];
+    uint32_t ks[4], vs[4];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int off = tok * 64 + 16 * code_chunk_pos(2 * half + c, tok);
+      kc[c] = ld_stream_v4(head + kOffKc + off);
+      vc[c] = ld_stream_v4(head + kOffVc + off);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ks[i] = __ldg(head + kOffKs + (4 * half + i) * kPageTokens + tok) & 127;
+      vs[i] = __ldg(head + kOffVs + (4 * half + i) * kPageTokens + tok) & 127;
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const uint2 t0 = my_kt[ks[2 * c] * kConvKCopies], t1 = my_kt[ks[2 * c + 1] * kConvKCopies];
+      const uint2 a = dequant8(kc[c].x, t0), d = dequant8(kc[c].y, t0), e = dequant8(kc[c].z, t1), f = dequant8(kc[c].w, t1);
+      ko[(2 * c) * kPageTokens] = make_uint4(a.x, a.y, d.x, d.y);
+      ko[(2 * c + 1) * kPageTokens] = make_uint4(e.x, e.y, f.x, f.y);
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const uint4 t0 = my_vt[vs[2 * c] * kConvVCopies], t1 = my_vt[vs[2 * c + 1] * kConvVCopies];
+      vo[(4 * c) * kPageTokens] = dequant8_f16(vc[c].x, t0);
+      vo[(4 * c + 1) * kPageTokens] = dequant8_f16(vc[c].y, t0);
+      vo[(4 * c + 2) * kPageTokens] = dequant8_f16(vc[c].z, t1);
+      vo[(4 * c + 3) * kPageTokens] = dequant8_f16(vc[c].w, t1);
+    }
+  }
+}
+
+// ---- (2) attention --------------------------------------------------------------------
+// Start of CTA c's range of total = G quota + extra units.
+__device__ __forceinline__ long long range_start(long long quota, int extra, int c) { return c * quota + min(c, extra); }
+
+__device__ __forceinline__ int page_weight(int n_tok) { return n_tok <= 32 ? kPage1 : kPage2; }
+__device__ __forceinline__ int job_weight(int n_tok, int n_pg) { return n_pg > 0 ? kFixed + n_pg * page_weight(n_tok) : 0; }
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Bits 0 .. n - 1 (n clamped to 0 .. 32).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1; }
+
+// 32 bytes at once (aligned).
+__device__ __forceinline__ void st32(void* p, const uint32_t (&x)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
+               "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
+
+__global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const __grid_constant__ PrefillParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const uint32_t sbase = smem_u32(smem);
+  auto bar = [&](int i) { return sbase + kOffBars + 8 * i; };
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffMisc);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
+  int* s_issued = reinterpret_cast<int*>(smem + kOffMisc + 8);  // [2] K and V copies
+  const WaitCtl wc{s_abort, p.wait_ns};
+  auto rec = [&](int k) { return reinterpret_cast<SegRec*>(smem + kOffRecs + 64 * (k % kRecs)); };
+  int* s_info = reinterpret_cast<int*>(smem + kOffInfo);
+  long long* s_scan = reinterpret_cast<long long*>(smem + kOffScan);  // [12] warp sums, total, first job, its offset
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  // ---- prologue ------------------------------------------------------------------
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(bar(kBKFull + i), 1);
+      mbar_init(bar(kBKEmpty + i), 1);
+      mbar_init(bar(kBVFull + i), 1);
+      mbar_init(bar(kBVEmpty + i), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(kBQFull + s), 1);
+      mbar_init(bar(kBQEmpty + s), 1);
+      mbar_init(bar(kBSFull + s), 1);
+      mbar_init(bar(kBPFull + 2 * s), 4);
+      mbar_init(bar(kBPFull + 2 * s + 1), 4);
+      mbar_init(bar(kBPvDone + s), 1);
+      mbar_init(bar(kBOFree + s), 4);
+    }
+    for (int i = 0; i < kRecs; ++i) {
+      mbar_init(bar(kBRecFull + i), 1);
+      mbar_init(bar(kBRecEmpty + i), 1 + 1 + 8);  // MMA, queries, softmax
+    }
+    mbar_init(bar(kBDone), 1);
+    *s_abort = 0;
+    s_issued[0] = s_issued[1] = 0;
+    fence_barrier_init();
+  }
+  if (warp == 3) tmem_alloc(smem_u32(s_tmem), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  pdl_wait();
+  pdl_trigger();
+
+  // ---- this CTA's range of the weighted jobs: (KV head, tile), tile fastest ------------------
+  const int n_tiles = *p.n_tiles;
+  {
+    const int per = (n_tiles + kPrefillThreads - 1) / kPrefillThreads;
+    const int t0 = min(tid * per, n_tiles), t1 = min(t0 + per, n_tiles);
+    long long mine = 0;
+    for (int t = t0; t < t1; ++t) mine += job_weight(p.tiles[t].n_tok, p.tiles[t].n_pg);
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    long long before = 0, one = 0;
+    for (int i = 0; i < kPrefillThreads / 32; ++i) {
+      if (i < warp) before += s_scan[i];
+      one += s_scan[i];
+    }
+    const long long total = kKvHeads * one;
+    const int G = (int)min((long long)gridDim.x, max(1ll, total / kLeast));
+    if (total > 0 && (int)blockIdx.x < G) {
+      const long long lo = range_start(total / G, (int)(total % G), blockIdx.x);
+      const long long in = lo % one;
+      long long x = before + incl - mine;
+      if (mine > 0 && in >= x && in < x + mine) {  // the first job is one of this thread's
+        int t = t0;
+        for (;; ++t) {
+          const int w = job_weight(p.tiles[t].n_tok, p.tiles[t].n_pg);
+          if (in < x + w) break;
+          x += w;
+        }
+        s_scan[13] = (lo / one) * n_tiles + t;
+        s_scan[14] = lo - in + x;
+      }
+    }
+    if (tid == 0) s_scan[12] = total;
+    __syncthreads();
+  }
+  const long long total = s_scan[12];
+  const int G = (int)min((long long)gridDim.x, max(1ll, total / kLeast));
+  const bool idle = (int)blockIdx.x >= G || total == 0;
+
+  // registers: 128 threads x 80 + 256 x 208 of the launch's 384 x 168
+  if (warp < 4) {
+    regs_dec<80>();
+    if (warp == 0) {
+      // ---------------- segment records and page copies -------------------------------------
+      int e = 0, k = 0;
+      bool ok = true;
+      if (!idle) {
+        const long long quota = total / G;
+        const int extra = (int)(total - quota * G);
+        const long long lo = range_start(quota, extra, blockIdx.x), hi = range_start(quota, extra, blockIdx.x + 1);
+        long long off = s_scan[14];
+        int g = (int)(s_scan[13] / n_tiles), t = (int)(s_scan[13] % n_tiles);
+        while (ok && off < hi && g < kKvHeads) {
+          const int word = lane < 8 ? reinterpret_cast<const int*>(p.tiles + t)[lane] : 0;
+          TileRec r;
+          r.q0 = __shfl_sync(0xffffffffu, word, 0);
+          r.n_tok = __shfl_sync(0xffffffffu, word, 1);
+          r.pos = __shfl_sync(0xffffffffu, word, 2);
+          r.len = __shfl_sync(0xffffffffu, word, 3);
+          r.page0 = __shfl_sync(0xffffffffu, word, 4);
+          r.n_pg = __shfl_sync(0xffffffffu, word, 5);
+          r.ws_page = __shfl_sync(0xffffffffu, word, 6);
+          const int pw = page_weight(r.n_tok);
+          // page i starts at weight base + i pw; it belongs to the range that holds its start
+          const long long base = off + kFixed;
+          auto page_at = [&](long long x) {  // the first page that starts at weight x or behind it
+            if (x <= base) return 0;
+            return x - base > (long long)r.n_pg * pw ? r.n_pg : ((int)(x - base) + pw - 1) / pw;
+          };
+          const int a = r.n_pg > 0 ? page_at(lo) : 0, z = r.n_pg > 0 ? page_at(hi) : 0;
+          off += job_weight(r.n_tok, r.n_pg);
+          const int job = t * kKvHeads + g, gg = g;
+          if (++t == n_tiles) {
+            t = 0;
+            ++g;
+          }
+          if (a >= z) continue;
+          if (!twait(bar(kBRecEmpty + k % kRecs), ((k / kRecs) & 1) ^ 1, wc)) {
+            ok = false;
+            break;
+          }
+          const bool whole = a == 0 && z == r.n_pg;
+          if (lane == 0) {
+            SegRec* s = rec(k);
+            s->n_pg = z - a;
+            s->g = gg;
+            s->q0 = r.q0;
+            s->n_tok = r.n_tok;
+            s->pos = r.pos;
+            s->len = r.len;
+            s->page0 = r.page0 + a;
+            s->slot = whole ? -1 : 2 * (int)blockIdx.x + (a > 0 ? 0 : 1);
+            if (!whole && a == 0) {
+              // the first part tells the merge who has the others
+              const long long last = base + (long long)(r.n_pg - 1) * pw;
+              const long long big = extra * (quota + 1);  // the first `extra` CTAs have one unit more
+              const int c_last = last < big ? (int)(last / (quota + 1)) : extra + (int)((last - big) / quota);
+              p.desc[job] = (int)blockIdx.x | (c_last - (int)blockIdx.x + 1) << 8;
+            }
+            mbar_arrive(bar(kBRecFull + k % kRecs));
+          }
+          __syncwarp();
+          ++k;
+          const uint8_t* image = p.images + ((size_t)(r.ws_page + a) * kKvHeads + gg) * kImage;
+          for (int i0 = a; ok && i0 < z; i0 += 32) {
+            const int cnt = min(32, z - i0);
+            const int there = lane < cnt ? p.page_ok[r.ws_page + i0 + lane] : 0;
+            for (int j = 0; j < cnt; ++j, ++e, image += kKvHeads * kImage) {
+              const int st = e % kStages, ph = ((e / kStages) & 1) ^ 1, good = __shfl_sync(0xffffffffu, there, j);
+              if (!twait(bar(kBKEmpty + st), ph, wc)) {
+                ok = false;
+                break;
+              }
+              if (lane == 0) {
+                s_info[e % kInfo] = good;
+                if (!(p.inject && e == 0)) {
+                  mbar_arrive_expect_tx(bar(kBKFull + st), kImageK);
+                  bulk_g2s(sbase + kOffK + st * kImageK, image, kImageK, bar(kBKFull + st));
+                }
+                s_issued[0] = e + 1;
+              }
+              __syncwarp();
+              if (!twait(bar(kBVEmpty + st), ph, wc)) {
+                ok = false;
+                break;
+              }
+              if (lane == 0) {
+                if (!(p.inject && e == 0)) {
+                  mbar_arrive_expect_tx(bar(kBVFull + st), 32768);
+                  bulk_g2s(sbase + kOffV + st * 32768, image + kImageK, 32768, bar(kBVFull + st));
+                }
+                s_issued[1] = e + 1;
+              }
+              __syncwarp();
+            }
+          }
+        }
+      }
+      // no more segments
+      if (ok && twait(bar(kBRecEmpty + k % kRecs), ((k / kRecs) & 1) ^ 1, wc) && lane == 0) {
+        rec(k)->n_pg = -1;
+        mbar_arrive(bar(kBRecFull + k % kRecs));
+      }
+    } else if (warp == 1) {
+      // ---------------- MMA issuer ---------------------------------------------------------------------
+      // Job j of a segment: page j / sets, row tile j % sets.  In turn PV(j), then QK(j + sets) into the
+      // same columns; so one tile's products run under the other's softmax.  The warp stays together
+      // and elects a lane for the MMAs only (in a loop that one lane runs alone nothing is
+      // warp-uniform, and an MMA takes three times as long to issue).
+      const uint32_t idesc_qk = umma_idesc_e4m3(128, 128);
+      // D fp32, A and B f16, A K-major, B MN-major
+      const uint32_t idesc_pv = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+      int e0 = 0;
+      uint32_t p_par = 0, o_par = 0, o_any = 0;  // bit per set: parity of its next P, of its segments, whether it had one
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        if (!twait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc)) break;
+        const int n_pg = __shfl_sync(0xffffffffu, rec(k)->n_pg, 0);
+        if (n_pg < 0) break;
+        const int sets = __shfl_sync(0xffffffffu, rec(k)->n_tok, 0) > 32 ? 2 : 1;
+        if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
+        const int n_jobs = sets * n_pg;
+        if (!twait(bar(kBQFull + (k & 1)), (k >> 1) & 1, wc)) break;
+        for (int j = -sets; ok && j < n_jobs; ++j) {
+          const int set = sets == 2 ? j & 1 : 0;
+          const int e = e0 + (sets == 2 ? j >> 1 : j), en = e + 1;
+          const bool next = j + sets < n_jobs, last_set = set == sets - 1;
+          if (j >= 0) {
+            if (j < sets && (o_any >> set & 1) && !twait(bar(kBOFree + set), (o_par >> set & 1) ^ 1, wc)) {  // the accumulator is read
+              ok = false;
+              break;
+            }
+            if (set == 0 && !twait(bar(kBVFull + e % kStages), (e / kStages) & 1, wc)) {
+              ok = false;
+              break;
+            }
+            // MN-major without swizzle: 8 tokens x 8 channels are 128 contiguous bytes, the next 8 tokens
+            // follow, the next 8 channels are 2,048 further
+            const uint64_t vdesc = umma_desc_noswz_lbo_sbo(sbase + kOffV + (e % kStages) * 32768, 128, 2048);
+            for (int h = 0; h < 2; ++h) {
+              if (!twait(bar(kBPFull + 2 * set + h), p_par >> set & 1, wc)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              if (elect_one()) {
+                for (int kk = 4 * h; kk < 4 * h + 4; ++kk)  // 16 tokens each: 8 columns of P inside S's 32-column chunks
+                  umma_f16_ts(tmem + kTmemO + 128 * set, tmem + kTmemS + 128 * set + 32 * (kk >> 1) + 8 * (kk & 1),
+                              vdesc + kk * (256 >> 4), idesc_pv, (j >= sets || kk > 0) ? 1u : 0u);
+                if (h && last_set) umma_commit(bar(kBVEmpty + e % kStages));
+                if (h && !next) umma_commit(bar(kBPvDone + set));
+              }
+              __syncwarp();
+            }
+            if (!ok) break;
+            p_par ^= 1u << set;
+          }
+          if (!next) continue;
+          if (set == 0 && !twait(bar(kBKFull + en % kStages), (en / kStages) & 1, wc)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t qdesc = umma_desc_sw128(sbase + kOffQ + (2 * (k & 1) + set) * 16384);
+            // K-major without swizzle: 8 tokens x 16 channels are 128 contiguous bytes, the next 16
+            // channels 2,048 further
+            const uint64_t kdesc = umma_desc_noswz_lbo_sbo(sbase + kOffK + (en % kStages) * kImageK, 2048, 128);
+            for (int kk = 0; kk < 4; ++kk)  // 32 channels each
+              umma_e4m3(tmem + kTmemS + 128 * set, qdesc + 2 * kk, kdesc + kk * (4096 >> 4), idesc_qk, kk > 0);
+            umma_commit(bar(kBSFull + set));
+            if (last_set) umma_commit(bar(kBKEmpty + en % kStages));
+            if (j + sets == n_jobs - 1) umma_commit(bar(kBQEmpty + (k & 1)));
+          }
+          __syncwarp();
+        }
+        o_par ^= sets == 2 ? 3u : 1u;
+        o_any |= sets == 2 ? 3u : 1u;
+        e0 += n_pg;
+      }
+      __syncwarp();
+      if (elect_one()) umma_commit(bar(kBDone));
+      __syncwarp();
+    } else if (warp == 2) {
+      // ---------------- query rows of a segment: row 4 i + h of token i, head 4 g + h -----------------
+      for (int k = 0;; ++k) {
+        if (!twait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc)) break;
+        const SegRec r = *rec(k);
+        __syncwarp();
+        if (r.n_pg < 0) break;
+        if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
+        if (k > 1 && !twait(bar(kBQEmpty + (k & 1)), ((k >> 1) - 1) & 1, wc)) break;
+        for (int x = lane; x < r.n_tok * 32; x += 32) {
+          const int row = x >> 3, c = x & 7;
+          const uint8_t* src = p.q + ((size_t)(r.q0 + (row >> 2)) * kQHeads + kGqa * r.g + (row & 3)) * kHeadDim + 16 * c;
+          cp_async16(sbase + kOffQ + (k & 1) * 32768 + row * 128 + ((c ^ (row & 7)) << 4), src);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBQFull + (k & 1)));
+      }
+    }
+  } else {
+    regs_inc<208>();
+    // ---------------- softmax: set = (warp - 4) / 4, row = TMEM lane ------------------------------------
+    const int set = (warp - 4) >> 2, quad = warp & 3, lrow = 32 * quad + lane;
+    const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16);
+    const uint32_t t_s = tl + kTmemS + 128 * set, t_o = tl + kTmemO + 128 * set;
+    const uint64_t scale2 = pair64(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
+    int e0 = 0, jobs = 0, segs = 0;  // pages so far; jobs and segments of this set so far
+    for (int k = 0;; ++k) {
+      if (!twait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc)) break;
+      const SegRec r = *rec(k);
+      __syncwarp();
+      if (r.n_pg < 0) break;
+      if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
+      if (set == 1 && r.n_tok <= 32) {
+        e0 += r.n_pg;
+        continue;
+      }
+      const int row = 128 * set + lrow, n_rows = kGqa * r.n_tok, token = row >> 2;
+      const bool busy = row - lane < n_rows, mine = row < n_rows;
+      int start = 0, end = 0x7FFFFFFF;  // keys that the row sees
+      if (mine) {
+        const int pos = r.pos + token;
+        start = p.window ? max(0, pos + 1 - p.window) : 0;
+        end = p.ends ? min(max(p.ends[r.q0 + token], 0), r.len) : pos + 1;
+      }
+      float shift = kUnset, l = 0.f;  // kBias less the reference, and the sum of weights
+      bool ok = true;
+      for (int i = 0; i < r.n_pg; ++i) {
+        if (!twait(bar(kBSFull + set), jobs & 1, wc)) {
+          ok = false;
+          break;
+        }
+        ++jobs;
+        if (busy) {
+          tc_fence_after();
+          const int pos0 = (r.page0 + i) * kPageTokens;
+          const int lo = start - pos0, hi = s_info[(e0 + i) % kInfo] ? end - pos0 : 0;
+          const bool edge = __any_sync(0xffffffffu, lo > 0 || hi < kPageTokens);
+          uint32_t v[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32x32b_x32(t_s + 32 * c, v + 32 * c);
+          tmem_wait_ld();
+          if (edge) {  // -inf where the row does not see the token
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t vis = low_bits(hi - 32 * c) & ~low_bits(lo - 32 * c);
+#pragma unroll
+              for (int x = 0; x < 32; ++x) v[32 * c + x] = vis >> x & 1 ? v[32 * c + x] : 0xFF800000u;
+            }
+          }
+          float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int x = 0; x < 64; ++x)
+            tops[x & 3] = max3(tops[x & 3], __uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1]));
+          const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
+          const bool over = mine && fmaf(top, p.scale_log2, shift) > kMostLog2;
+          if (__any_sync(0xffffffffu, over)) {
+            float f = 1.f;
+            if (over) {
+              const float next = kBias - top * p.scale_log2;
+              f = fast_exp2(next - shift);  // (0 for the first: shift is kUnset)
+              shift = next;
+              l *= f;
+            }
+            __syncwarp();
+            if (i > 0) {  // (the PVs before this S are done)
+#pragma unroll 1
+              for (int c = 0; c < 8; ++c) {
+                uint32_t u[16];
+                tmem_ld32x32b_x16(t_o + 16 * c, u);
+                tmem_wait_ld();
+#pragma unroll
+                for (int x = 0; x < 16; ++x) u[x] = __float_as_uint(__uint_as_float(u[x]) * f);
+                tmem_st_x16(t_o + 16 * c, u);
+              }
+            }
+          }
+          const uint64_t shift2 = pair64(__float_as_uint(shift), __float_as_uint(shift));
+          uint64_t sums[2] = {0, 0};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[16];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              const uint2 y = split64(fma_f32x2(pair64(v[32 * c + 2 * x], v[32 * c + 2 * x + 1]), scale2, shift2));
+              const float a = fast_exp2(__uint_as_float(y.x)), b = fast_exp2(__uint_as_float(y.y));
+              sums[x & 1] = add_f32x2(sums[x & 1], pair64(__float_as_uint(a), __float_as_uint(b)));
+              o[x] = cvt_f16x2_f32(b, a);
+            }
+            tmem_st_x16(t_s + 32 * c, o);
+            if (c & 1) {
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(kBPFull + 2 * set + (c >> 1)));
+            }
+          }
+          const uint2 sum2 = split64(add_f32x2(sums[0], sums[1]));
+          l += __uint_as_float(sum2.x) + __uint_as_float(sum2.y);
+        } else if (lane == 0) {
+          mbar_arrive(bar(kBPFull + 2 * set));
+          mbar_arrive(bar(kBPFull + 2 * set + 1));
+        }
+        __syncwarp();
+      }
+      // ---- end of the segment: the accumulator is final ---------------------------------------------
+      if (!ok || !twait(bar(kBPvDone + set), segs & 1, wc)) break;
+      ++segs;
+      tc_fence_after();
+      if (busy) {
+        const size_t at = (size_t)(r.q0 + token) * kQHeads + kGqa * r.g + (row & 3);
+        const float inv = l != 0.f ? p.out_scale / l : 0.f;  // (a NaN of the query stays one)
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          tmem_ld32x32b_x32(t_o + 32 * c, v);
+          tmem_wait_ld();
+          if (mine) {
+            if (r.slot < 0) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t y[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                  y[x] = pack16(__uint_as_float(v[16 * h + 2 * x]) * inv, __uint_as_float(v[16 * h + 2 * x + 1]) * inv, p.out_f16);
+                st32(p.out + at * kHeadDim + 32 * c + 16 * h, y);
+              }
+            } else {
+              float* to = p.part_o + ((size_t)r.slot * p.part_rows + row) * kHeadDim + 32 * c;
+#pragma unroll
+              for (int h = 0; h < 4; ++h) {
+                uint32_t y[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) y[x] = v[8 * h + x];
+                st32(to + 8 * h, y);
+              }
+            }
+          }
+          __syncwarp();
+        }
+        if (mine) {
+          const float m = kBias - shift;
+          if (r.slot >= 0) p.part_ml[(size_t)r.slot * p.part_rows + row] = make_float2(m, l);
+          else if (p.lse) p.lse[at] = l != 0.f ? (m - kBias + log2f(l)) * kLn2 : -INFINITY;
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBOFree + set));
+      e0 += r.n_pg;
+    }
+  }
+
+  // ---- teardown -------------------------------------------------------------------------
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0) {
+    mbar_wait_drain(bar(kBDone), 0, drain_ns(p.wait_ns));  // every tcgen05.mma is done
+    if (*s_abort) {
+      set_status(p.status, MSA_STATUS_TIMEOUT);
+      for (int x = 0; x < 2; ++x)  // copies that may still be landing
+        for (int e = max(p.inject ? 1 : 0, s_issued[x] - kStages); e < s_issued[x]; ++e)
+          mbar_wait_drain(bar((x ? kBVFull : kBKFull) + e % kStages), (e / kStages) & 1, drain_ns(p.wait_ns));
+    }
+  }
+  __syncthreads();
+  if (warp == 3) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---- (3) jobs that were cut ---------------------------------------------------------------
+// out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.  Grid: (job, 32 rows); a warp takes four rows one
+// after the other, lane = 4 channels, eight parts' loads at once.
+constexpr int kMergeParts = 8;
+__global__ void __launch_bounds__(256) prefill_merge_kernel(const __grid_constant__ PrefillParams p) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int job = blockIdx.x, t = job / kKvHeads, g = job % kKvHeads;
+  pdl_wait();
+  if (t >= *p.n_tiles) return;
+  const int desc = p.desc[job];
+  if (desc == 0) return;
+  const int c0 = desc & 255, parts = desc >> 8;
+  const int q0 = p.tiles[t].q0, n_rows = kGqa * p.tiles[t].n_tok;
+  for (int row = 32 * blockIdx.y + warp; row < min(n_rows, 32 * (int)blockIdx.y + 32); row += 8) {
+    float M = -INFINITY, L = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < parts; i0 += kMergeParts) {
+      float4 x[kMergeParts];
+      float2 ml = make_float2(-INFINITY, 0.f);  // lane u: part i0 + u
+      auto slot = [&](int u) { return (size_t)(2 * (c0 + i0 + u) + (i0 + u == 0)) * p.part_rows + row; };
+      if (lane < kMergeParts && i0 + lane < parts) ml = p.part_ml[slot(lane)];
+#pragma unroll
+      for (int u = 0; u < kMergeParts; ++u) {
+        x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i0 + u < parts) x[u] = reinterpret_cast<const float4*>(p.part_o + slot(u) * kHeadDim)[lane];
+      }
+      const float top = fmaxf(M, warp_max_f32(ml.y != 0.f ? ml.x : -INFINITY));
+      const float f = M > -INFINITY ? fast_exp2(M - top) : 0.f, w = ml.y != 0.f ? fast_exp2(ml.x - top) : 0.f;
+      M = top;
+      L *= f;
+      o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+      for (int u = 0; u < kMergeParts; ++u) {
+        const float wu = __shfl_sync(0xffffffffu, w, u);
+        L = fmaf(__shfl_sync(0xffffffffu, ml.y, u), wu, L);
+        o.x = fmaf(x[u].x, wu, o.x);
+        o.y = fmaf(x[u].y, wu, o.y);
+        o.z = fmaf(x[u].z, wu, o.z);
+        o.w = fmaf(x[u].w, wu, o.w);
+      }
+    }
+    const float inv = L != 0.f ? p.out_scale / L : 0.f;  // (a NaN of the query stays one)
+    const size_t at = (size_t)(q0 + (row >> 2)) * kQHeads + kGqa * g + (row & 3);
+    *reinterpret_cast<uint2*>(p.out + at * kHeadDim + 4 * lane) =
+        make_uint2(pack16(o.x * inv, o.y * inv, p.out_f16), pack16(o.z * inv, o.w * inv, p.out_f16));
+    if (p.lse && lane == 0) p.lse[at] = L != 0.f ? (M - kBias + log2f(L)) * kLn2 : -INFINITY;
+  }
+}
+
+int prefill_rows(int n_q_total) { return kGqa * std::min(n_q_total, kTileTokens); }
+int prefill_tiles(int n_q_total, int n_seqs) { return n_q_total / kTileTokens + std::min(n_q_total, n_seqs); }
+size_t padded(size_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
+
+size_t prefill_workspace_bytes(int n_q_total, int n_seqs, int n_pages) {
+  const size_t rows = prefill_rows(n_q_total), tiles = prefill_tiles(n_q_total, n_seqs);
+  return 256 + padded(tiles * sizeof(TileRec)) + padded(tiles * kKvHeads * sizeof(int)) + padded((size_t)n_pages * sizeof(int)) +
+         padded(2 * kPrefillCtas * rows * sizeof(float2)) + 2 * kPrefillCtas * rows * kHeadDim * sizeof(float) +
+         (size_t)n_pages * kKvHeads * kImage;
+}
+
+cudaError_t launch_prefill_attn(const msa_cache* c, const uint8_t* q, float softmax_scale, const int* block_table,
+                                int max_pages, const int* seq_lens, const int* q_start_loc, int n_seqs, int n_q_total,
+                                int window, const int* ends, int n_visited, int dtype, void* out, float* lse, void* ws,
+                                cudaStream_t stream) {
+  if (n_q_total == 0 || n_seqs == 0) return cudaSuccess;
+  static DeviceSetup setup;
+  int dev = 0, n_sm = 0;
+  const int conv_smem = kConvTables + 2 * (n_seqs + 1) * (int)sizeof(int);
+  cudaError_t e = setup.get(&dev, &n_sm, [](int) {
+    constexpr auto kMax = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    const cudaError_t e = cudaFuncSetAttribute(prefill_attn_kernel, kMax, kPrefillSmem);
+    return e != cudaSuccess ? e : cudaFuncSetAttribute(prefill_convert_kernel, kMax, kConvTables + 2 * (kMaxSeqs + 1) * (int)sizeof(int));
+  });
+  if (e != cudaSuccess) return e;
+  PrefillParams pp{};
+  pp.kv_pool = static_cast<const uint8_t*>(c->kv_pool);
+  pp.n_pages = c->n_pages;
+  pp.q = q;
+  pp.block_table = block_table;
+  pp.max_pages = max_pages;
+  pp.seq_lens = seq_lens;
+  pp.q_start_loc = q_start_loc;
+  pp.n_seqs = n_seqs;
+  pp.n_q_total = n_q_total;
+  pp.window = window;
+  pp.ends = ends;
+  // (a quotient below fp32's normal numbers is as good as the smallest: every score is zero then)
+  pp.scale_log2 = std::max(softmax_scale / c->s_enc_k * kLog2e, FLT_MIN);
+  pp.out_scale = 256.0f / c->s_enc_v;
+  pp.out_f16 = dtype == MSA_DTYPE_F16;
+  pp.out = static_cast<uint16_t*>(out);
+  pp.lse = lse;
+  pp.part_rows = prefill_rows(n_q_total);
+  pp.max_tiles = prefill_tiles(n_q_total, n_seqs);
+  pp.cap = n_visited;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  auto piece = [&](size_t bytes) {
+    uint8_t* at = w;
+    w += padded(bytes);
+    return at;
+  };
+  pp.n_tiles = reinterpret_cast<int*>(piece(256));
+  pp.tiles = reinterpret_cast<TileRec*>(piece(pp.max_tiles * sizeof(TileRec)));
+  pp.desc = reinterpret_cast<int*>(piece((size_t)pp.max_tiles * kKvHeads * sizeof(int)));
+  pp.page_ok = reinterpret_cast<int*>(piece((size_t)pp.cap * sizeof(int)));
+  pp.part_ml = reinterpret_cast<float2*>(piece(2 * kPrefillCtas * (size_t)pp.part_rows * sizeof(float2)));
+  pp.part_o = reinterpret_cast<float*>(piece(2 * kPrefillCtas * (size_t)pp.part_rows * kHeadDim * sizeof(float)));
+  pp.images = w;
+  pp.status = c->status;
+  pp.wait_ns = launch_settings().wait_ns;
+  pp.inject = (launch_settings().inject & MSA_INJECT_ATTENTION_TIMEOUT) != 0;
+  const long long units = (long long)n_visited * kKvHeads;
+  const int conv_grid = (int)std::max(1ll, std::min(units, 5ll * n_sm));
+  e = launch_pdl(prefill_convert_kernel, dim3(conv_grid), dim3(kConvThreads), conv_smem, stream, pp);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(prefill_attn_kernel, dim3(std::min(n_sm, kPrefillCtas)), dim3(kPrefillThreads), kPrefillSmem, stream, pp);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(prefill_merge_kernel, dim3((unsigned)(pp.max_tiles * kKvHeads), (pp.part_rows + 31) / 32), dim3(256), 0,
+                    stream, pp);
+}
+
+}  // namespace msa

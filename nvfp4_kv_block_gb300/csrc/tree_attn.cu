@@ -42,14 +42,13 @@
 // with 64 drafts: 385 us, 1.35 PFLOP/s; one of 4,096: 14.8 us, a chain of latencies
 // (lengths and ranges 2.6, first page 2.4, its scores 1.4, joining the row copies 1.7, the
 // merge kernel 4).
-#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <algorithm>
 #include <cfloat>
 #include <type_traits>
 
-#include "common.cuh"
+#include "attn_ops.cuh"
 
 namespace msa {
 namespace {
@@ -144,84 +143,6 @@ struct TreeParams {
   int inject;  // test only: a CTA's first page is not copied, so that the waits for it run out
 };
 
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
-  return r != 0;
-}
-// Waits (the whole warp) for the phase with the given parity: as mbar_wait, bounded in
-// time and given up when another role has, but short in code (there are thirty of them).
-__device__ __forceinline__ bool twait(uint32_t bar, uint32_t parity, const WaitCtl& w) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  const unsigned long long t0 = globaltimer_ns();
-  for (;;) {
-#pragma unroll 1
-    for (int i = 0; i < 16; ++i)
-      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    if (__any_sync(0xffffffffu, *w.abort || globaltimer_ns() - t0 > w.limit_ns)) {
-      *w.abort = 1;
-      return false;
-    }
-  }
-}
-__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-// kind::f16 with A in tensor memory (row m in lane m, two f16 per column), B in shared memory.
-__device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-// Shared memory by 32-bit address (every access in program order).
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-__device__ __forceinline__ uint64_t pair64(uint32_t a, uint32_t b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint2 split64(uint64_t x) {
-  uint2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(r.x), "=r"(r.y) : "l"(x));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 // OR of a predicate over the threads of a named barrier (all of them wait).
 __device__ __forceinline__ bool barrier_or(int id, int nthreads, bool pred) {
   uint32_t r;
@@ -233,10 +154,6 @@ __device__ __forceinline__ bool barrier_or(int id, int nthreads, bool pred) {
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-
 // Blocks a sequence's drafts visit: `chosen` of the selection, then those that can
 // hold drafts; and the units' weight.
 struct SeqWork {
@@ -279,16 +196,6 @@ static_assert(sizeof(SeqWork) <= 64, "beside the scan");
 // Start of CTA c's range of total = G quota + extra units.
 __device__ __forceinline__ long long range_start(long long quota, int extra, int c) { return c * quota + min(c, extra); }
 
-// One code word (8 channels) -> 8 f16 values v8 2^-8, through the scale's table:
-// hi = E4M3 magnitude bits >> 1, lo = their last bit << 7, per E2M1 magnitude.
-__device__ __forceinline__ uint4 dequant8_f16(uint32_t w, uint4 t) {
-  const uint32_t m = w & 0x77777777u, m2 = m >> 16;
-  const uint32_t h0 = prmt(t.x, t.y, m) | (w & 0x80808080u);
-  const uint32_t h1 = prmt(t.x, t.y, m2) | ((w << 4) & 0x80808080u);
-  const uint32_t l0 = prmt(t.z, t.w, m), l1 = prmt(t.z, t.w, m2);
-  return make_uint4(prmt(l0, h0, 0x5140u), prmt(l0, h0, 0x7362u), prmt(l1, h1, 0x5140u), prmt(l1, h1, 0x7362u));
-}
-
 // The 32 drafts' bits of the positions pos .. pos + 31 for a row with mask word tm
 // (bits of drafts that exist only): context tokens are visible.
 __device__ __forceinline__ uint32_t visible_bits(unsigned long long tm, int pos, int ctx) {
@@ -297,12 +204,6 @@ __device__ __forceinline__ uint32_t visible_bits(unsigned long long tm, int pos,
   if (sh >= 0) return (uint32_t)(tm >> sh);
   if (sh <= -32) return 0xFFFFFFFFu;
   return ((uint32_t)tm << -sh) | ((1u << -sh) - 1u);
-}
-
-__device__ __forceinline__ uint32_t pack16(float a, float b, bool f16) {
-  if (f16) return cvt_f16x2_f32(b, a);
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // kCopies false: one copy of the rows whatever their number.
@@ -327,23 +228,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
   {
     uint2* kt = reinterpret_cast<uint2*>(smem + kOffKTab);
     uint4* vt = reinterpret_cast<uint4*>(smem + kOffVTab);
-    if (tid < 128) {
-      const float mags[8] = {0.f, 0.5f, 1.f, 1.5f, 2.f, 3.f, 4.f, 6.f};
-      // (0x7F is no number and never written: it counts as zero)
-      const float s = tid == 127 ? 0.f : e4m3_to_f32((uint32_t)tid);
-      uint32_t k[2] = {0, 0}, hi[2] = {0, 0}, lo[2] = {0, 0};
-#pragma unroll
-      for (int m = 0; m < 8; ++m) {
-        const uint32_t e = f32_to_e4m3(mags[m] * s);
-        k[m >> 2] |= e << (8 * (m & 3));
-        hi[m >> 2] |= (e >> 1) << (8 * (m & 3));
-        lo[m >> 2] |= ((e & 1) << 7) << (8 * (m & 3));
-      }
-#pragma unroll
-      for (int c = 0; c < kKTabCopies; ++c) kt[tid * kKTabCopies + c] = make_uint2(k[0], k[1]);
-#pragma unroll
-      for (int c = 0; c < kVTabCopies; ++c) vt[tid * kVTabCopies + c] = make_uint4(hi[0], hi[1], lo[0], lo[1]);
-    }
+    if (tid < 128) convert_tables<kKTabCopies, kVTabCopies>(tid, kt, vt);
   }
   if (tid == 0) {
     for (int i = 0; i < kRaw; ++i) {

@@ -115,6 +115,9 @@ _SIGS = {
     "msa_tree_attn": (ctypes.c_int, [_P, _P, _I32, ctypes.c_float, _P, _I32, _P, _P, _I32, _I32, _P, _P, _P, _I32, _P,
                                      _P, _P, ctypes.c_size_t, _P]),
     "msa_tree_attn_workspace_bytes": (ctypes.c_size_t, [_I32]),
+    "msa_prefill_attn": (ctypes.c_int, [_P, _P, _I32, ctypes.c_float, _P, _I32, _P, _P, _I32, _I32, _I32, _P, _I32, _I32,
+                                        _P, _P, _P, ctypes.c_size_t, _P]),
+    "msa_prefill_workspace_bytes": (ctypes.c_size_t, [_I32, _I32, _I32]),
     "msa_extend_sequences": (ctypes.c_int, [_P, _P, _I32, _P, _P, _I32, _I32, _P, _P]),
     "msa_fork_sequences": (ctypes.c_int, [_P, _I32, _P, _P, _I32, _P, _I32, _P, _P, _I32, _P, ctypes.c_size_t, _P]),
     "msa_fork_workspace_bytes": (ctypes.c_size_t, [_I32]),
@@ -712,6 +715,48 @@ def tree_attn(cache, q, block_table, seq_lens, q_start_loc, bufs, tree_mask=None
         _arg(bufs.out, bufs.out.dtype, (T, Q_HEADS, HEAD_DIM), dev, "bufs.out"),
         _arg(bufs.lse, torch.float32, (T, Q_HEADS), dev, "bufs.lse"), bufs.ws.data_ptr(), bufs.ws.numel(),
         _raw_stream(dev)))
+    return bufs.out
+
+
+class PrefillBuffers:
+    """Outputs and scratch of prefill_attn calls with n_q_total query rows (exactly: rows behind
+    the last sequence stay as they were), up to n_seqs sequences and n_pages pages of their
+    contexts (the sum of ceil(seq_len / 128), or of those within the window): out [n_q_total,
+    16, 128] in ``dtype`` (bf16 or fp16), lse [n_q_total, 16], and 196,608 bytes of scratch a
+    page.  ``ws``: scratch of other buffers, to share it between layers or steps."""
+
+    def __init__(self, n_q_total, n_seqs, n_pages, dtype=torch.bfloat16, device="cuda", ws=None):
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError(f"prefill_attn's output is bfloat16 or float16, not {dtype}")
+        self.T, self.n_seqs, self.n_pages = int(n_q_total), int(n_seqs), int(n_pages)
+        nbytes = lib().msa_prefill_workspace_bytes(self.T, self.n_seqs, self.n_pages)
+        self.ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if ws is None else ws
+        self.out = torch.zeros((self.T, Q_HEADS, HEAD_DIM), dtype=dtype, device=device)
+        self.lse = torch.zeros((self.T, Q_HEADS), dtype=torch.float32, device=device)
+
+
+def prefill_attn(cache, q, block_table, seq_lens, q_start_loc, bufs, window=0, ends=None, softmax_scale=None):
+    """Attention of each sequence's query tokens (its last ones, any number of them, already in
+    the cache) over its cached context: token i at position pos sees the positions t with
+    start <= t < end, start = max(0, pos + 1 - window) (0 without a window), end = pos + 1
+    or, with ``ends`` (int32 [T]), its entry there (at most the sequence's length: the tokens of
+    an image that see all of it).  Returns bufs.out [T, 16, 128] (zeros where a token sees
+    nothing); bufs.lse [T, 16] has the log-sum-exp of the logits."""
+    T = bufs.T
+    n_seqs, max_pages = block_table.shape
+    if n_seqs > bufs.n_seqs:
+        raise ValueError(f"bufs are for up to {bufs.n_seqs} sequences")
+    dev = _device_of(cache)
+    _check(lib().msa_prefill_attn(
+        cache.packed(), _arg(q, torch.uint8, (T, Q_HEADS, HEAD_DIM), dev, "q"), Q_HEADS,
+        HEAD_DIM ** -0.5 if softmax_scale is None else float(softmax_scale),
+        _arg(block_table, torch.int32, (n_seqs, max_pages), dev, "block_table"), max_pages,
+        _arg(seq_lens, torch.int32, (n_seqs,), dev, "seq_lens"),
+        _arg(q_start_loc, torch.int32, (n_seqs + 1,), dev, "q_start_loc"), n_seqs, T, int(window),
+        None if ends is None else _arg(ends, torch.int32, (T,), dev, "ends"), bufs.n_pages, _DTYPES[bufs.out.dtype],
+        _arg(bufs.out, bufs.out.dtype, (T, Q_HEADS, HEAD_DIM), dev, "bufs.out"),
+        _arg(bufs.lse, torch.float32, (T, Q_HEADS), dev, "bufs.lse"),
+        _arg(bufs.ws, torch.uint8, bufs.ws.shape, dev, "bufs.ws"), bufs.ws.numel(), _raw_stream(dev)))
     return bufs.out
 
 
