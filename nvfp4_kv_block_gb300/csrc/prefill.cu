@@ -41,22 +41,22 @@ constexpr int kInfo = 16;
 constexpr int kImageK = 16384, kImage = kImageK + 32768;  // bytes of a converted (page, KV head)
 
 constexpr int kOffQ = 0;                                  // 2 segments x 2 tiles [128 rows][128 B]
-constexpr int kOffK = kOffQ + 4 * 16384;                  // kStages x [8 groups of 16 channels][128 tokens][16 B]
-constexpr int kOffV = kOffK + kStages * kImageK;          // kStages x [16 groups of 8 channels][128 tokens][16 B]
-constexpr int kOffRecs = kOffV + kStages * 32768;         // kRecs x 64 B
+// kStages x (K [8 groups of 16 channels][128 tokens][16 B], V [16 groups of 8 channels][128 tokens][16 B])
+constexpr int kOffK = kOffQ + 4 * 16384;
+constexpr int kOffRecs = kOffK + kStages * kImage;        // kRecs x 64 B
 constexpr int kOffInfo = kOffRecs + kRecs * 64;           // int [kInfo]: page inside the pool
-constexpr int kOffScan = kOffInfo + kInfo * 4;            // long long [16]
-constexpr int kOffBars = kOffScan + 16 * 8;
-constexpr int kBKFull = 0, kBKEmpty = kBKFull + kStages, kBVFull = kBKEmpty + kStages, kBVEmpty = kBVFull + kStages,
-              kBQFull = kBVEmpty + kStages, kBQEmpty = kBQFull + 2, kBSFull = kBQEmpty + 2, kBPFull = kBSFull + 2,
-              kBPvDone = kBPFull + 4, kBOFree = kBPvDone + 2, kBRecFull = kBOFree + 2, kBRecEmpty = kBRecFull + kRecs,
+constexpr int kOffScan = kOffInfo + kInfo * 4;            // long long [32]
+constexpr int kOffBars = kOffScan + 32 * 8;
+constexpr int kBFull = 0, kBEmpty = kBFull + kStages, kBQFull = kBEmpty + kStages, kBQEmpty = kBQFull + 2,
+              kBSFull = kBQEmpty + 2, kBPFull = kBSFull + 2, kBPvDone = kBPFull + 2, kBOFree = kBPvDone + 2, kBRecFull = kBOFree + 2, kBRecEmpty = kBRecFull + kRecs,
               kBDone = kBRecEmpty + kRecs, kBars = kBDone + 1;
-constexpr int kOffMisc = kOffBars + 8 * ((kBars + 1) & ~1);  // tmem, abort, K and V copies issued
+constexpr int kOffMisc = kOffBars + 8 * ((kBars + 1) & ~1);  // tmem, abort, pages issued
 constexpr int kPrefillSmem = 1024 + kOffMisc + 16;
 static_assert(kPrefillSmem <= 232448, "shared memory of one CTA");
+static_assert(kOffBars % 8 == 0, "barriers");
 constexpr uint32_t kTmemS = 0, kTmemO = 256;  // S of set s at 128 s, O of set s at 256 + 128 s
 constexpr float kBias = 8.0f;
-constexpr float kMostLog2 = 15.5849625f;  // log2(49,152)
+constexpr float kMost = 49152.0f;  // largest sum of 64 weights, and so largest weight
 constexpr float kUnset = 3e38f;           // shift of a row without a reference
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -286,11 +286,6 @@ __device__ __forceinline__ long long range_start(long long quota, int extra, int
 __device__ __forceinline__ int page_weight(int n_tok) { return n_tok <= 32 ? kPage1 : kPage2; }
 __device__ __forceinline__ int job_weight(int n_tok, int n_pg) { return n_pg > 0 ? kFixed + n_pg * page_weight(n_tok) : 0; }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
 // Bits 0 .. n - 1 (n clamped to 0 .. 32).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1; }
 
@@ -301,6 +296,80 @@ __device__ __forceinline__ void st32(void* p, const uint32_t (&x)[8]) {
                : "memory");
 }
 
+// Waits as twait does, with a shorter way through when the phase completes: a hand-over between two
+// warps takes about 110 cycles without the time hint and the vote, 170 with them.
+__device__ __forceinline__ bool swait(uint32_t bar, uint32_t parity, const WaitCtl& w) {
+  auto poll = [&] {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+  };
+  bool ok = poll();
+  if (!ok) {
+    const unsigned long long t0 = globaltimer_ns();
+    for (;;) {
+#pragma unroll 1
+      for (int i = 0; i < 64 && !ok; ++i) ok = poll();
+      if (ok || *w.abort || globaltimer_ns() - t0 > w.limit_ns) break;
+    }
+  }
+  if (__all_sync(0xffffffffu, ok)) return true;
+  *w.abort = 1;
+  return false;
+}
+
+// Waits for tensor memory loads; the 32 values (one of them) are not touched before.
+__device__ __forceinline__ void wait_ld32(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
+                 "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                 "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+               :
+               : "memory");
+}
+// Weights of 32 scores as f16 pairs, and their sums.
+__device__ __forceinline__ void weigh32(const uint32_t (&v)[32], uint64_t scale2, uint64_t shift2, uint64_t (&sums)[2], uint32_t* o) {
+#pragma unroll
+  for (int x = 0; x < 16; ++x) {
+    const uint2 y = split64(fma_f32x2(pair64(v[2 * x], v[2 * x + 1]), scale2, shift2));
+    const float a = fast_exp2(__uint_as_float(y.x)), b = fast_exp2(__uint_as_float(y.y));
+    sums[x & 1] = add_f32x2(sums[x & 1], pair64(__float_as_uint(a), __float_as_uint(b)));
+    o[x] = cvt_f16x2_f32(b, a);
+  }
+}
+// A row's accumulator, and its weights of a page's first half, times f.
+__device__ __forceinline__ void scale_acc(uint32_t t_o, float f) {
+#pragma unroll 1
+  for (int c = 0; c < kHeadDim; c += 16) {
+    uint32_t u[16];
+    tmem_ld32x32b_x16(t_o + c, u);
+    tmem_wait_ld();
+#pragma unroll
+    for (int x = 0; x < 16; ++x) u[x] = __float_as_uint(__uint_as_float(u[x]) * f);
+    tmem_st_x16(t_o + c, u);
+  }
+}
+__device__ __forceinline__ void scale_p(uint32_t t_p, float f) {
+  tmem_wait_st();
+#pragma unroll 1
+  for (int c = 0; c < 64; c += 32) {
+    uint32_t u[16];
+    tmem_ld32x32b_x16(t_p + c, u);
+    tmem_wait_ld();
+#pragma unroll
+    for (int x = 0; x < 16; ++x) {
+      const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&u[x]));
+      u[x] = cvt_f16x2_f32(w.y * f, w.x * f);
+    }
+    tmem_st_x16(t_p + c, u);
+  }
+}
+
 __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const __grid_constant__ PrefillParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -308,27 +377,24 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
   auto bar = [&](int i) { return sbase + kOffBars + 8 * i; };
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
-  int* s_issued = reinterpret_cast<int*>(smem + kOffMisc + 8);  // [2] K and V copies
+  int* s_issued = reinterpret_cast<int*>(smem + kOffMisc + 8);  // pages
   const WaitCtl wc{s_abort, p.wait_ns};
   auto rec = [&](int k) { return reinterpret_cast<SegRec*>(smem + kOffRecs + 64 * (k % kRecs)); };
   int* s_info = reinterpret_cast<int*>(smem + kOffInfo);
-  long long* s_scan = reinterpret_cast<long long*>(smem + kOffScan);  // [12] warp sums, total, first job, its offset
+  long long* s_scan = reinterpret_cast<long long*>(smem + kOffScan);  // [20] warp sums; 24: total, first job, its offset
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   // ---- prologue ------------------------------------------------------------------
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(bar(kBKFull + i), 1);
-      mbar_init(bar(kBKEmpty + i), 1);
-      mbar_init(bar(kBVFull + i), 1);
-      mbar_init(bar(kBVEmpty + i), 1);
+      mbar_init(bar(kBFull + i), 1);
+      mbar_init(bar(kBEmpty + i), 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(kBQFull + s), 1);
       mbar_init(bar(kBQEmpty + s), 1);
       mbar_init(bar(kBSFull + s), 1);
-      mbar_init(bar(kBPFull + 2 * s), 4);
-      mbar_init(bar(kBPFull + 2 * s + 1), 4);
+      mbar_init(bar(kBPFull + s), 4);
       mbar_init(bar(kBPvDone + s), 1);
       mbar_init(bar(kBOFree + s), 4);
     }
@@ -338,7 +404,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
     }
     mbar_init(bar(kBDone), 1);
     *s_abort = 0;
-    s_issued[0] = s_issued[1] = 0;
+    *s_issued = 0;
     fence_barrier_init();
   }
   if (warp == 3) tmem_alloc(smem_u32(s_tmem), 512);
@@ -382,14 +448,14 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
           if (in < x + w) break;
           x += w;
         }
-        s_scan[13] = (lo / one) * n_tiles + t;
-        s_scan[14] = lo - in + x;
+        s_scan[25] = (lo / one) * n_tiles + t;
+        s_scan[26] = lo - in + x;
       }
     }
-    if (tid == 0) s_scan[12] = total;
+    if (tid == 0) s_scan[24] = total;
     __syncthreads();
   }
-  const long long total = s_scan[12];
+  const long long total = s_scan[24];
   const int G = (int)min((long long)gridDim.x, max(1ll, total / kLeast));
   const bool idle = (int)blockIdx.x >= G || total == 0;
 
@@ -404,8 +470,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
         const long long quota = total / G;
         const int extra = (int)(total - quota * G);
         const long long lo = range_start(quota, extra, blockIdx.x), hi = range_start(quota, extra, blockIdx.x + 1);
-        long long off = s_scan[14];
-        int g = (int)(s_scan[13] / n_tiles), t = (int)(s_scan[13] % n_tiles);
+        long long off = s_scan[26];
+        int g = (int)(s_scan[25] / n_tiles), t = (int)(s_scan[25] % n_tiles);
         while (ok && off < hi && g < kKvHeads) {
           const int word = lane < 8 ? reinterpret_cast<const int*>(p.tiles + t)[lane] : 0;
           TileRec r;
@@ -463,29 +529,17 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
             const int there = lane < cnt ? p.page_ok[r.ws_page + i0 + lane] : 0;
             for (int j = 0; j < cnt; ++j, ++e, image += kKvHeads * kImage) {
               const int st = e % kStages, ph = ((e / kStages) & 1) ^ 1, good = __shfl_sync(0xffffffffu, there, j);
-              if (!twait(bar(kBKEmpty + st), ph, wc)) {
+              if (!twait(bar(kBEmpty + st), ph, wc)) {
                 ok = false;
                 break;
               }
               if (lane == 0) {
                 s_info[e % kInfo] = good;
                 if (!(p.inject && e == 0)) {
-                  mbar_arrive_expect_tx(bar(kBKFull + st), kImageK);
-                  bulk_g2s(sbase + kOffK + st * kImageK, image, kImageK, bar(kBKFull + st));
+                  mbar_arrive_expect_tx(bar(kBFull + st), kImage);
+                  bulk_g2s(sbase + kOffK + st * kImage, image, kImage, bar(kBFull + st));
                 }
-                s_issued[0] = e + 1;
-              }
-              __syncwarp();
-              if (!twait(bar(kBVEmpty + st), ph, wc)) {
-                ok = false;
-                break;
-              }
-              if (lane == 0) {
-                if (!(p.inject && e == 0)) {
-                  mbar_arrive_expect_tx(bar(kBVFull + st), 32768);
-                  bulk_g2s(sbase + kOffV + st * 32768, image + kImageK, 32768, bar(kBVFull + st));
-                }
-                s_issued[1] = e + 1;
+                *s_issued = e + 1;
               }
               __syncwarp();
             }
@@ -506,73 +560,70 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
       const uint32_t idesc_qk = umma_idesc_e4m3(128, 128);
       // D fp32, A and B f16, A K-major, B MN-major
       const uint32_t idesc_pv = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
-      int e0 = 0;
+      // K-major without swizzle: 8 tokens x 16 channels are 128 contiguous bytes, the next 16 channels
+      // 2,048 further.  MN-major without swizzle: 8 tokens x 8 channels are 128 contiguous bytes, the
+      // next 8 tokens follow, the next 8 channels are 2,048 further
+      const uint64_t kdesc0 = umma_desc_noswz_lbo_sbo(sbase + kOffK, 2048, 128);
+      const uint64_t vdesc0 = umma_desc_noswz_lbo_sbo(sbase + kOffK + kImageK, 128, 2048);
+      const uint64_t qdesc0 = umma_desc_sw128(sbase + kOffQ);
       uint32_t p_par = 0, o_par = 0, o_any = 0;  // bit per set: parity of its next P, of its segments, whether it had one
+      int st = kStages - 1, full = 0;            // stage of the page before the next one; parity of the next one's
       bool ok = true;
       for (int k = 0; ok; ++k) {
-        if (!twait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc)) break;
+        if (!swait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc)) break;
         const int n_pg = __shfl_sync(0xffffffffu, rec(k)->n_pg, 0);
         if (n_pg < 0) break;
         const int sets = __shfl_sync(0xffffffffu, rec(k)->n_tok, 0) > 32 ? 2 : 1;
         if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
-        const int n_jobs = sets * n_pg;
-        if (!twait(bar(kBQFull + (k & 1)), (k >> 1) & 1, wc)) break;
-        for (int j = -sets; ok && j < n_jobs; ++j) {
-          const int set = sets == 2 ? j & 1 : 0;
-          const int e = e0 + (sets == 2 ? j >> 1 : j), en = e + 1;
-          const bool next = j + sets < n_jobs, last_set = set == sets - 1;
-          if (j >= 0) {
-            if (j < sets && (o_any >> set & 1) && !twait(bar(kBOFree + set), (o_par >> set & 1) ^ 1, wc)) {  // the accumulator is read
-              ok = false;
-              break;
-            }
-            if (set == 0 && !twait(bar(kBVFull + e % kStages), (e / kStages) & 1, wc)) {
-              ok = false;
-              break;
-            }
-            // MN-major without swizzle: 8 tokens x 8 channels are 128 contiguous bytes, the next 8 tokens
-            // follow, the next 8 channels are 2,048 further
-            const uint64_t vdesc = umma_desc_noswz_lbo_sbo(sbase + kOffV + (e % kStages) * 32768, 128, 2048);
-            for (int h = 0; h < 2; ++h) {
-              if (!twait(bar(kBPFull + 2 * set + h), p_par >> set & 1, wc)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              if (elect_one()) {
-                for (int kk = 4 * h; kk < 4 * h + 4; ++kk)  // 16 tokens each: 8 columns of P inside S's 32-column chunks
-                  umma_f16_ts(tmem + kTmemO + 128 * set, tmem + kTmemS + 128 * set + 32 * (kk >> 1) + 8 * (kk & 1),
-                              vdesc + kk * (256 >> 4), idesc_pv, (j >= sets || kk > 0) ? 1u : 0u);
-                if (h && last_set) umma_commit(bar(kBVEmpty + e % kStages));
-                if (h && !next) umma_commit(bar(kBPvDone + set));
-              }
-              __syncwarp();
-            }
-            if (!ok) break;
-            p_par ^= 1u << set;
-          }
-          if (!next) continue;
-          if (set == 0 && !twait(bar(kBKFull + en % kStages), (en / kStages) & 1, wc)) {
+        if (!swait(bar(kBQFull + (k & 1)), (k >> 1) & 1, wc)) break;
+        // i: the page whose P is awaited (-1: none yet); QK of page i + 1 goes behind its PV
+        for (int i = -1; ok && i < n_pg; ++i) {
+          const int next = st == kStages - 1 ? 0 : st + 1;
+          const bool more = i + 1 < n_pg;
+          if (more && !swait(bar(kBFull + next), full, wc)) {
             ok = false;
             break;
           }
-          tc_fence_after();
-          if (elect_one()) {
-            const uint64_t qdesc = umma_desc_sw128(sbase + kOffQ + (2 * (k & 1) + set) * 16384);
-            // K-major without swizzle: 8 tokens x 16 channels are 128 contiguous bytes, the next 16
-            // channels 2,048 further
-            const uint64_t kdesc = umma_desc_noswz_lbo_sbo(sbase + kOffK + (en % kStages) * kImageK, 2048, 128);
-            for (int kk = 0; kk < 4; ++kk)  // 32 channels each
-              umma_e4m3(tmem + kTmemS + 128 * set, qdesc + 2 * kk, kdesc + kk * (4096 >> 4), idesc_qk, kk > 0);
-            umma_commit(bar(kBSFull + set));
-            if (last_set) umma_commit(bar(kBKEmpty + en % kStages));
-            if (j + sets == n_jobs - 1) umma_commit(bar(kBQEmpty + (k & 1)));
+          for (int set = 0; set < sets; ++set) {
+            if (i >= 0) {
+              if (!swait(bar(kBPFull + set), p_par >> set & 1, wc) ||
+                  // (the first PV writes over an accumulator that has to be read)
+                  (i == 0 && (o_any >> set & 1) && !swait(bar(kBOFree + set), (o_par >> set & 1) ^ 1, wc))) {
+                ok = false;
+                break;
+              }
+              p_par ^= 1u << set;
+            }
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t s = tmem + kTmemS + 128 * set;
+              if (i >= 0) {
+                const uint64_t vdesc = vdesc0 + st * (kImage >> 4);
+#pragma unroll 4
+                for (int kk = 0; kk < 8; ++kk)  // 16 tokens each: 8 columns of P inside S's 32-column chunks
+                  umma_f16_ts(s + kTmemO - kTmemS, s + 32 * (kk >> 1) + 8 * (kk & 1), vdesc + kk * (256 >> 4), idesc_pv,
+                              (i > 0 || kk > 0) ? 1u : 0u);
+                if (set == sets - 1) umma_commit(bar(kBEmpty + st));
+                if (!more) umma_commit(bar(kBPvDone + set));
+              }
+              if (more) {
+                const uint64_t qdesc = qdesc0 + (2 * (k & 1) + set) * (16384 >> 4), kdesc = kdesc0 + next * (kImage >> 4);
+#pragma unroll 2
+                for (int kk = 0; kk < 4; ++kk)  // 32 channels each
+                  umma_e4m3(s, qdesc + 2 * kk, kdesc + kk * (4096 >> 4), idesc_qk, kk > 0);
+                umma_commit(bar(kBSFull + set));
+                if (i + 2 == n_pg && set == sets - 1) umma_commit(bar(kBQEmpty + (k & 1)));
+              }
+            }
+            __syncwarp();
           }
-          __syncwarp();
+          if (more) {
+            st = next;
+            full ^= next == kStages - 1;
+          }
         }
         o_par ^= sets == 2 ? 3u : 1u;
         o_any |= sets == 2 ? 3u : 1u;
-        e0 += n_pg;
       }
       __syncwarp();
       if (elect_one()) umma_commit(bar(kBDone));
@@ -601,113 +652,125 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
     regs_inc<208>();
     // ---------------- softmax: set = (warp - 4) / 4, row = TMEM lane ------------------------------------
     const int set = (warp - 4) >> 2, quad = warp & 3, lrow = 32 * quad + lane;
-    const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16);
-    const uint32_t t_s = tl + kTmemS + 128 * set, t_o = tl + kTmemO + 128 * set;
+    const uint32_t t_s = tmem + ((uint32_t)(32 * quad) << 16) + kTmemS + 128 * set, t_o = t_s + kTmemO - kTmemS;
     const uint64_t scale2 = pair64(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
-    int e0 = 0, jobs = 0, segs = 0;  // pages so far; jobs and segments of this set so far
+    uint32_t e = 0, par = 0;  // pages so far; bit 0: parity of this set's jobs, bit 1: of its segments
     for (int k = 0;; ++k) {
-      if (!twait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc)) break;
+      if (!swait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc)) break;
       const SegRec r = *rec(k);
       __syncwarp();
       if (r.n_pg < 0) break;
       if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
       if (set == 1 && r.n_tok <= 32) {
-        e0 += r.n_pg;
+        e += r.n_pg;
         continue;
       }
-      const int row = 128 * set + lrow, n_rows = kGqa * r.n_tok, token = row >> 2;
-      const bool busy = row - lane < n_rows, mine = row < n_rows;
-      int start = 0, end = 0x7FFFFFFF;  // keys that the row sees
+      const int token = 32 * set + (lrow >> 2);
+      const bool busy = 32 * set + 8 * quad < r.n_tok, mine = token < r.n_tok;
+      // keys that the row sees, counted from the first one of the page
+      int start = 0, end = 0x7FFFFFFF;
       if (mine) {
         const int pos = r.pos + token;
-        start = p.window ? max(0, pos + 1 - p.window) : 0;
-        end = p.ends ? min(max(p.ends[r.q0 + token], 0), r.len) : pos + 1;
+        start = (p.window ? max(0, pos + 1 - p.window) : 0) - r.page0 * kPageTokens;
+        end = (p.ends ? min(max(p.ends[r.q0 + token], 0), r.len) : pos + 1) - r.page0 * kPageTokens;
       }
       float shift = kUnset, l = 0.f;  // kBias less the reference, and the sum of weights
       bool ok = true;
-      for (int i = 0; i < r.n_pg; ++i) {
-        if (!twait(bar(kBSFull + set), jobs & 1, wc)) {
+      for (const uint32_t e0 = e; e - e0 < (uint32_t)r.n_pg; ++e) {
+        if (!swait(bar(kBSFull + set), par & 1, wc)) {
           ok = false;
           break;
         }
-        ++jobs;
+        par ^= 1;
         if (busy) {
           tc_fence_after();
-          const int pos0 = (r.page0 + i) * kPageTokens;
-          const int lo = start - pos0, hi = s_info[(e0 + i) % kInfo] ? end - pos0 : 0;
-          const bool edge = __any_sync(0xffffffffu, lo > 0 || hi < kPageTokens);
-          uint32_t v[128];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32x32b_x32(t_s + 32 * c, v + 32 * c);
-          tmem_wait_ld();
-          if (edge) {  // -inf where the row does not see the token
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const uint32_t vis = low_bits(hi - 32 * c) & ~low_bits(lo - 32 * c);
-#pragma unroll
-              for (int x = 0; x < 32; ++x) v[32 * c + x] = vis >> x & 1 ? v[32 * c + x] : 0xFF800000u;
-            }
-          }
-          float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int x = 0; x < 64; ++x)
-            tops[x & 3] = max3(tops[x & 3], __uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1]));
-          const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
-          const bool over = mine && fmaf(top, p.scale_log2, shift) > kMostLog2;
-          if (__any_sync(0xffffffffu, over)) {
-            float f = 1.f;
-            if (over) {
-              const float next = kBias - top * p.scale_log2;
-              f = fast_exp2(next - shift);  // (0 for the first: shift is kUnset)
-              shift = next;
-              l *= f;
-            }
-            __syncwarp();
-            if (i > 0) {  // (the PVs before this S are done)
+          const int hi = s_info[e % kInfo] ? end : 0;
+          if (__any_sync(0xffffffffu, start > 0 || hi < kPageTokens)) {  // -inf where the row does not see the token
 #pragma unroll 1
-              for (int c = 0; c < 8; ++c) {
+            for (int c = 0; c < kPageTokens; c += 32) {
+              uint32_t v[32];
+              tmem_ld32x32b_x32(t_s + c, v);
+              const uint32_t vis = low_bits(hi - c) & ~low_bits(start - c);
+              tmem_wait_ld();
+#pragma unroll
+              for (int x = 0; x < 32; ++x) v[x] = vis >> x & 1 ? v[x] : 0xFF800000u;
+              tmem_st32(t_s + c, v);
+            }
+            tmem_wait_st();
+          }
+          // Half a page at a time, the next 32 scores loaded under the exponentials of 32.  There is no pass
+          // for the maximum: 64 weights that sum to 49,152 or less have none above it, and others (a
+          // row's first ones: its shift is kUnset) move the reference and are weighed again.
+          uint32_t v[2][32];
+          tmem_ld32x32b_x32(t_s, v[0]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint64_t shift2 = pair64(__float_as_uint(shift), __float_as_uint(shift));
+            uint64_t sums[2] = {0, 0};
+            uint32_t o[32];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              wait_ld32(v[c]);
+              if (h + c < 2) tmem_ld32x32b_x32(t_s + 64 * h + 32 * c + 32, v[(c + 1) & 1]);
+              weigh32(v[c], scale2, shift2, sums, o + 16 * c);
+            }
+            const uint2 sum2 = split64(add_f32x2(sums[0], sums[1]));
+            float sum = __uint_as_float(sum2.x) + __uint_as_float(sum2.y);
+            const bool over = mine && sum > kMost;
+            if (__any_sync(0xffffffffu, over)) {
+              // (S of this half is as it was; the other half's load may be under way)
+              wait_ld32(v[0]);
+              float top = -INFINITY;
+#pragma unroll 1
+              for (int c = 0; c < 64; c += 16) {
                 uint32_t u[16];
-                tmem_ld32x32b_x16(t_o + 16 * c, u);
+                tmem_ld32x32b_x16(t_s + 64 * h + c, u);
                 tmem_wait_ld();
 #pragma unroll
-                for (int x = 0; x < 16; ++x) u[x] = __float_as_uint(__uint_as_float(u[x]) * f);
-                tmem_st_x16(t_o + 16 * c, u);
+                for (int x = 0; x < 16; ++x) top = fmaxf(top, __uint_as_float(u[x]));
               }
-            }
-          }
-          const uint64_t shift2 = pair64(__float_as_uint(shift), __float_as_uint(shift));
-          uint64_t sums[2] = {0, 0};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t o[16];
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              const uint2 y = split64(fma_f32x2(pair64(v[32 * c + 2 * x], v[32 * c + 2 * x + 1]), scale2, shift2));
-              const float a = fast_exp2(__uint_as_float(y.x)), b = fast_exp2(__uint_as_float(y.y));
-              sums[x & 1] = add_f32x2(sums[x & 1], pair64(__float_as_uint(a), __float_as_uint(b)));
-              o[x] = cvt_f16x2_f32(b, a);
-            }
-            tmem_st_x16(t_s + 32 * c, o);
-            if (c & 1) {
-              tmem_wait_st();
-              tc_fence_before();
+              float f = 1.f;
+              if (over) {
+                const float next = kBias - top * p.scale_log2;
+                f = fast_exp2(next - shift);  // (0 for the first: shift is kUnset)
+                shift = next;
+                l *= f;
+              }
               __syncwarp();
-              if (lane == 0) mbar_arrive(bar(kBPFull + 2 * set + (c >> 1)));
+              if (e != e0) scale_acc(t_o, f);  // (the PVs before this S are done)
+              if (h) scale_p(t_s, f);
+              const uint64_t again2 = pair64(__float_as_uint(shift), __float_as_uint(shift));
+              sums[0] = sums[1] = 0;
+#pragma unroll 1
+              for (int c = 0; c < 64; c += 32) {
+                uint32_t u[32], y[16];
+                tmem_ld32x32b_x32(t_s + 64 * h + c, u);
+                tmem_wait_ld();
+                weigh32(u, scale2, again2, sums, y);
+                tmem_st_x16(t_s + 64 * h + c, y);
+              }
+              const uint2 again = split64(add_f32x2(sums[0], sums[1]));
+              sum = __uint_as_float(again.x) + __uint_as_float(again.y);
+            } else {
+              tmem_st_x16(t_s + 64 * h, o);
+              tmem_st_x16(t_s + 64 * h + 32, o + 16);
             }
+            l += sum;
           }
-          const uint2 sum2 = split64(add_f32x2(sums[0], sums[1]));
-          l += __uint_as_float(sum2.x) + __uint_as_float(sum2.y);
-        } else if (lane == 0) {
-          mbar_arrive(bar(kBPFull + 2 * set));
-          mbar_arrive(bar(kBPFull + 2 * set + 1));
+          tmem_wait_st();
+          tc_fence_before();
         }
         __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBPFull + set));
+        start -= kPageTokens;
+        if (mine) end -= kPageTokens;
       }
       // ---- end of the segment: the accumulator is final ---------------------------------------------
-      if (!ok || !twait(bar(kBPvDone + set), segs & 1, wc)) break;
-      ++segs;
+      if (!ok || !swait(bar(kBPvDone + set), par >> 1, wc)) break;
+      par ^= 2;
       tc_fence_after();
       if (busy) {
+        const int row = 128 * set + lrow;
         const size_t at = (size_t)(r.q0 + token) * kQHeads + kGqa * r.g + (row & 3);
         const float inv = l != 0.f ? p.out_scale / l : 0.f;  // (a NaN of the query stays one)
 #pragma unroll 1
@@ -747,7 +810,6 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBOFree + set));
-      e0 += r.n_pg;
     }
   }
 
@@ -759,9 +821,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
     mbar_wait_drain(bar(kBDone), 0, drain_ns(p.wait_ns));  // every tcgen05.mma is done
     if (*s_abort) {
       set_status(p.status, MSA_STATUS_TIMEOUT);
-      for (int x = 0; x < 2; ++x)  // copies that may still be landing
-        for (int e = max(p.inject ? 1 : 0, s_issued[x] - kStages); e < s_issued[x]; ++e)
-          mbar_wait_drain(bar((x ? kBVFull : kBKFull) + e % kStages), (e / kStages) & 1, drain_ns(p.wait_ns));
+      for (int e = max(p.inject ? 1 : 0, *s_issued - kStages); e < *s_issued; ++e)  // copies that may still be landing
+        mbar_wait_drain(bar(kBFull + e % kStages), (e / kStages) & 1, drain_ns(p.wait_ns));
     }
   }
   __syncthreads();

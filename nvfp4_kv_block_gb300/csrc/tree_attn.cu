@@ -143,17 +143,6 @@ struct TreeParams {
   int inject;  // test only: a CTA's first page is not copied, so that the waits for it run out
 };
 
-// OR of a predicate over the threads of a named barrier (all of them wait).
-__device__ __forceinline__ bool barrier_or(int id, int nthreads, bool pred) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, %2, %3, p;\n"
-      " selp.u32 %0, 1, 0, q;\n}"
-      : "=r"(r)
-      : "r"((uint32_t)pred), "r"(id), "r"(nthreads)
-      : "memory");
-  return r != 0;
-}
 // Blocks a sequence's drafts visit: `chosen` of the selection, then those that can
 // hold drafts; and the units' weight.
 struct SeqWork {

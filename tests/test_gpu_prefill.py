@@ -4,8 +4,10 @@ Tolerances are those of test_gpu_tree.py, with an exponential that is off by 2^-
 row's reference moves (by a factor below 2^-7.5, so that what earlier moves left sums to less
 than twice the last one's), by the reference's own rounding, ten steps of 2^-24 of the scores'
 size: a logit is off by e = 140 * 2^-24 of the sum of its products' sizes and 2^-20; the weights
-are rounded to f16 once, 2^-11 relative or 2^-25 under the bias of 2^8; a sum of n terms in fp32
-adds n 2^-24, a move a rounding of the accumulator (there are fewer than 200).
+are rounded to f16, 2^-11 relative or 2^-25 under the bias of 2^8, and those of a page's first 64
+tokens once more when the reference moves for its others (together below 2.001 * 2^-11, or two
+steps of 2^-25); a sum of n terms in fp32 adds n 2^-24, a move a rounding of the accumulator
+(there are fewer than 200).
 """
 
 import numpy as np
@@ -82,7 +84,7 @@ class Prompts(Batch):
             np.testing.assert_array_equal(np.isneginf(lse[rows]), ~fin)
             l0, g0 = np.where(fin, l, 0), np.where(fin, lse[rows], 0)
             assert np.all(np.abs(g0 - l0) <= e + (keys + 200) * 2.0**-24 + 2.0**-23 * np.abs(l0)), (s, ctx, n)
-            tol = (2.0**-11 + 2 * e + 2 * (keys + 200) * 2.0**-24)[..., None] * mean + (keys * 2.0**-33)[..., None] * 448 / S_ENC_V
+            tol = (2.001 * 2.0**-11 + 2 * e + 2 * (keys + 200) * 2.0**-24)[..., None] * mean + (keys * 2.0**-32)[..., None] * 448 / S_ENC_V
             tol = tol + step * (np.abs(o) + tol) + 2.0**-25
             off = np.abs(out[rows] - o)
             assert np.all(off <= tol), (s, ctx, n, int((off > tol).sum()), float(off.max()), float(np.abs(o).max()))
