@@ -13,26 +13,29 @@
 // operand tiles of the products, 16 KB of E4M3 keys and 32 KB of f16 values, by a kernel bound
 // by memory; it also writes down the tiles of 64 tokens and their pages.  (2) The attention: a job
 // is a tile (256 rows, 4 i + h for token i and head h of the group) and a KV head; the jobs'
-// pages in a row are cut into equal weighted ranges, one per persistent CTA.  (3) Jobs that
-// were cut leave fp32 rows that a third kernel joins in a fixed order.
+// pages in a row are cut into equal weighted ranges, one per persistent CTA.  A job that was cut
+// leaves fp32 rows, which the last of its parts joins in the order of the parts (each warp for
+// its rows, behind a counter).  (3) Jobs in more than kInline parts are joined by a kernel of their own.
 //
 // Roles of the attention's warps, all hand-offs mbarriers with bounded waits:
 //   warp 0      segment records, a bulk copy of 16 KB and one of 32 KB per page;
 //   warp 1      MMA issuer: S = Q K8^T (kind::f8f6f4, 128 x 128 x 128), then O += P V
 //               (kind::f16, P from tensor memory over S's own columns);
 //   warp 2      query rows of the next segment;
-//   warps 4-11  softmax, thread = row: a set of four warps for each 128 rows.
+//   warps 4-11  softmax, thread = row: a set of four warps for each 128 rows;
+//   warps 12-15 rows of finished segments on their way out.
 #include <cuda_fp16.h>
 
 #include <algorithm>
 #include <cfloat>
 
 #include "attn_ops.cuh"
+#include "tensor_map.cuh"
 
 namespace msa {
 namespace {
 
-constexpr int kPrefillThreads = 384;
+constexpr int kPrefillThreads = 512;
 constexpr int kTileTokens = 64;       // two row tiles of 32 tokens x 4 heads
 constexpr int kPrefillCtas = 152;     // most CTAs of a launch (the workspace is sized for them)
 constexpr int kStages = 3;            // pages in flight
@@ -46,9 +49,11 @@ constexpr int kOffK = kOffQ + 4 * 16384;
 constexpr int kOffRecs = kOffK + kStages * kImage;        // kRecs x 64 B
 constexpr int kOffInfo = kOffRecs + kRecs * 64;           // int [kInfo]: page inside the pool
 constexpr int kOffScan = kOffInfo + kInfo * 4;            // long long [32]
-constexpr int kOffBars = kOffScan + 32 * 8;
+constexpr int kOffMl = kOffScan + 32 * 8;                 // float2 [2 sets][2 parities][128]: a row's reference and sum
+constexpr int kOffBars = kOffMl + 2 * 2 * 128 * 8;
 constexpr int kBFull = 0, kBEmpty = kBFull + kStages, kBQFull = kBEmpty + kStages, kBQEmpty = kBQFull + 2,
-              kBSFull = kBQEmpty + 2, kBPFull = kBSFull + 2, kBPvDone = kBPFull + 2, kBOFree = kBPvDone + 2, kBRecFull = kBOFree + 2, kBRecEmpty = kBRecFull + kRecs,
+              kBSFull = kBQEmpty + 2, kBPFull = kBSFull + 2, kBPvDone = kBPFull + 2, kBOFree = kBPvDone + 2, kBMl = kBOFree + 2, kBRecFull = kBMl + 4,  // kBMl: [set][parity]
+              kBRecEmpty = kBRecFull + kRecs,
               kBDone = kBRecEmpty + kRecs, kBars = kBDone + 1;
 constexpr int kOffMisc = kOffBars + 8 * ((kBars + 1) & ~1);  // tmem, abort, pages issued
 constexpr int kPrefillSmem = 1024 + kOffMisc + 16;
@@ -65,6 +70,8 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // between a job's first and last has pages of it).
 constexpr int kPage1 = 5, kPage2 = 9, kFixed = 10, kLeast = 10;
 
+constexpr int kInline = 6;  // parts of a job that its last one joins
+
 struct TileRec {
   int q0, n_tok;  // rows of the call
   int pos;        // position of the first token
@@ -80,11 +87,16 @@ struct SegRec {
   int n_pg;  // pages of the segment; -1: no more segments
   int g, q0, n_tok, pos, len;
   int page0;
-  int slot;  // partial slot, or -1: the segment is the whole job
+  int part, parts;  // which part of the job the segment is, and of how many
+  int c0;           // CTA of part 0
+  int job;
 };
+// Place of part i of a job whose first part is CTA c0's: a CTA's last segment, then first ones.
+__device__ __forceinline__ size_t part_slot(int c0, int i) { return 2 * (c0 + i) + (i == 0); }
 static_assert(sizeof(SegRec) <= 64, "record slot");
 
 struct PrefillParams {
+  CUtensorMap out_map;  // out as [T][16][128], boxes of 8 tokens x 4 heads x 64 channels
   const uint8_t* kv_pool;
   int64_t n_pages;
   const uint8_t* q;  // [T][16][128]
@@ -104,12 +116,15 @@ struct PrefillParams {
   int* n_tiles;   // workspace from here on
   TileRec* tiles;
   int max_tiles;
-  int* desc;         // [max_tiles][4]: first CTA | parts << 8, 0 = nothing to join
+  int* n_big;        // jobs of the third kernel, and which: job, first CTA | parts << 8
+  int2* big;         // [4 max_tiles]
+  int* tickets;      // [max_tiles][4][8]: parts that a warp's rows are there of
   int* page_ok;      // [cap]
   int cap;           // converted pages that fit
-  float* part_o;     // [2 kPrefillCtas][part_rows][128]
-  float2* part_ml;   // [2 kPrefillCtas][part_rows]
-  int part_rows;
+  // a part's rows, 32 (a softmax warp's) at a time: [2 kPrefillCtas][part_quads]
+  float4* part_o;    // ... [32 of 4 channels][32 rows]
+  float2* part_ml;   // ... [32 rows]: reference and sum
+  int part_quads;
   uint8_t* images;   // [cap][4][kImage]
   int* status;
   unsigned long long wait_ns;
@@ -194,7 +209,10 @@ __global__ void __launch_bounds__(kConvThreads) prefill_convert_kernel(const __g
   };
   const int n_tiles = min(s_tile[p.n_seqs], p.max_tiles);
   if (blockIdx.x == 0) {
-    if (tid == 0) *p.n_tiles = n_tiles;
+    if (tid == 0) {
+      *p.n_tiles = n_tiles;
+      *p.n_big = 0;
+    }
     for (int b = tid; b < p.n_seqs; b += kConvThreads)
       if (s_page[b + 1] > s_page[b] && !fits(b)) set_status(p.status, MSA_STATUS_BAD_SEQ);
   }
@@ -218,7 +236,7 @@ __global__ void __launch_bounds__(kConvThreads) prefill_convert_kernel(const __g
     r.n_pg = fits(b) ? max(1, (top + kPageTokens - 1) / kPageTokens - r.page0) : 0;
     r.ws_page = s_page[b] + r.page0 - seq0;
     if (lane == 0) p.tiles[t] = r;
-    if (lane < kKvHeads) p.desc[t * kKvHeads + lane] = 0;
+    p.tickets[t * 32 + lane] = 0;
   }
   // (page, head) units: thread = token and half of the channels
   const int tok = tid & 127, half = tid >> 7;
@@ -290,9 +308,8 @@ __device__ __forceinline__ int job_weight(int n_tok, int n_pg) { return n_pg > 0
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1; }
 
 // 32 bytes at once (aligned).
-__device__ __forceinline__ void st32(void* p, const uint32_t (&x)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
-               "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+__device__ __forceinline__ void st32(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f, uint32_t g, uint32_t h) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h)
                : "memory");
 }
 
@@ -370,6 +387,145 @@ __device__ __forceinline__ void scale_p(uint32_t t_p, float f) {
   }
 }
 
+// Bulk copies from shared memory, and waits for a thread's own: read, or done.
+__device__ __forceinline__ void bulk_s2g(void* to, uint32_t from, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(from), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void tensor_s2g(const CUtensorMap* map, int x, int y, int z, uint32_t from) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x), "r"(y), "r"(z),
+               "r"(from)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_read_wait() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// A warp's 32 rows of a finished segment (lane = row; own: its reference and sum) from the accumulator
+// to the output, or to the place of the segment's part of a job.  stage: 8 KB of shared memory.
+__device__ __forceinline__ void put_rows(const PrefillParams& p, const SegRec& r, int set, int quad, int lane, uint32_t t_o,
+                                         uint32_t stage, int token, float2 own) {
+  auto rows_of = [&](int i) { return (part_slot(r.c0, i) * p.part_quads + 4 * set + quad) * 32; };
+  float m = own.x, l = own.y;
+  bool join = false;
+  float w[kInline];  // the parts' weights
+  if (r.parts > 1) {
+    int* ticket = p.tickets + (r.job * 8 + 4 * set + quad);
+    // (the last part need not write what it has, if it is known to be)
+    if (r.parts <= kInline) {
+      int there;
+      asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(there) : "l"(ticket) : "memory");
+      join = __all_sync(0xffffffffu, there == r.parts - 1);
+    }
+    if (!join) {
+      p.part_ml[rows_of(r.part) + lane] = own;
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {  // 64 channels of 32 rows: [16 of 4 channels][32 rows]
+        uint32_t v[64];
+        tmem_ld32x32b_x64(t_o + 64 * c, v);
+        tmem_wait_ld();
+        if (lane == 0) bulk_read_wait();
+        __syncwarp();
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+          sts128(stage + (x * 32 + lane) * 16, make_uint4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          bulk_s2g(p.part_o + (rows_of(r.part) + 16 * c) * 32, stage, 8192);
+          bulk_commit();
+        }
+      }
+      if (r.parts > kInline) return;
+      __threadfence();
+      __syncwarp();
+      int before = 0;
+      if (lane == 0) {
+        bulk_wait();
+        __threadfence();
+        before = atomicAdd(ticket, 1);
+      }
+      join = __shfl_sync(0xffffffffu, before, 0) == r.parts - 1;
+      if (!join) return;
+    }
+    __threadfence();
+    float2 ml[kInline];
+    float top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kInline; ++i) {
+      ml[i] = make_float2(-INFINITY, 0.f);
+      if (i < r.parts) ml[i] = i == r.part ? own : __ldcg(p.part_ml + rows_of(i) + lane);
+    }
+#pragma unroll
+    for (int i = 0; i < kInline; ++i)
+      if (ml[i].y != 0.f) top = fmaxf(top, ml[i].x);
+#pragma unroll
+    for (int i = 0; i < kInline; ++i) {
+      w[i] = ml[i].y != 0.f ? fast_exp2(ml[i].x - top) : 0.f;
+      sum = fmaf(ml[i].y, w[i], sum);
+    }
+    m = top;
+    l = sum;
+  }
+  const float inv = l != 0.f ? p.out_scale / l : 0.f;  // (a NaN of the query stays one)
+  const bool full = 32 * set + 8 * quad + 8 <= r.n_tok, mine = token < r.n_tok;
+  const size_t at = (size_t)(r.q0 + token) * kQHeads + kGqa * r.g + (lane & 3);
+  if (mine && p.lse) p.lse[at] = l != 0.f ? (m - kBias + log2f(l)) * kLn2 : -INFINITY;
+  if (lane == 0) bulk_read_wait();
+  __syncwarp();
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {  // 32 channels
+    uint32_t v[32];
+    tmem_ld32x32b_x32(t_o + 32 * c, v);
+    wait_ld32(v);
+    if (join) {  // parts in their order, this one's from where it is
+      float s[32] = {};
+#pragma unroll 1
+      for (int i = 0; i < r.parts; ++i) {
+        if (i == r.part) {
+#pragma unroll
+          for (int x = 0; x < 32; ++x) s[x] = fmaf(__uint_as_float(v[x]), w[i], s[x]);
+        } else {
+          const float4* from = p.part_o + (rows_of(i) + 8 * c) * 32 + lane;
+          float4 z[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) z[x] = __ldcg(from + x * 32);
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            s[4 * x] = fmaf(z[x].x, w[i], s[4 * x]);
+            s[4 * x + 1] = fmaf(z[x].y, w[i], s[4 * x + 1]);
+            s[4 * x + 2] = fmaf(z[x].z, w[i], s[4 * x + 2]);
+            s[4 * x + 3] = fmaf(z[x].w, w[i], s[4 * x + 3]);
+          }
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(s[x]);
+    }
+    uint32_t y[16];
+#pragma unroll
+    for (int x = 0; x < 16; ++x) y[x] = pack16(__uint_as_float(v[2 * x]) * inv, __uint_as_float(v[2 * x + 1]) * inv, p.out_f16);
+    if (full) {
+      // boxes of 64 channels x 4 heads x 8 tokens: rows of 128 bytes, swizzled
+      const uint32_t box = stage + (c >> 1) * 4096;
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        sts128(box + lane * 128 + (((4 * (c & 1) + x) ^ (lane & 7)) << 4), make_uint4(y[4 * x], y[4 * x + 1], y[4 * x + 2], y[4 * x + 3]));
+      if (c & 1) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tensor_s2g(&p.out_map, 32 * (c - 1), kGqa * r.g, r.q0 + 32 * set + 8 * quad, box);
+          bulk_commit();
+        }
+      }
+    } else if (mine) {  // the last tokens of a sequence: a box would go on into the next one's rows
+      uint16_t* to = p.out + at * kHeadDim + 32 * c;
+      st32(to, y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7]);
+      st32(to + 16, y[8], y[9], y[10], y[11], y[12], y[13], y[14], y[15]);
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const __grid_constant__ PrefillParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -392,15 +548,17 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(kBQFull + s), 1);
-      mbar_init(bar(kBQEmpty + s), 1);
+      mbar_init(bar(kBQEmpty + s), 1 + 4);  // the products, and the outputs that leave through the tiles
       mbar_init(bar(kBSFull + s), 1);
       mbar_init(bar(kBPFull + s), 4);
       mbar_init(bar(kBPvDone + s), 1);
       mbar_init(bar(kBOFree + s), 4);
+      mbar_init(bar(kBMl + 2 * s), 4);
+      mbar_init(bar(kBMl + 2 * s + 1), 4);
     }
     for (int i = 0; i < kRecs; ++i) {
       mbar_init(bar(kBRecFull + i), 1);
-      mbar_init(bar(kBRecEmpty + i), 1 + 1 + 8);  // MMA, queries, softmax
+      mbar_init(bar(kBRecEmpty + i), 1 + 1 + 8 + 4);  // MMA, queries, softmax, outputs
     }
     mbar_init(bar(kBDone), 1);
     *s_abort = 0;
@@ -459,9 +617,9 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
   const int G = (int)min((long long)gridDim.x, max(1ll, total / kLeast));
   const bool idle = (int)blockIdx.x >= G || total == 0;
 
-  // registers: 128 threads x 80 + 256 x 208 of the launch's 384 x 168
+  // registers: 128 threads x 64 + 256 x 160 + 128 x 128 of the launch's 512 x 128
   if (warp < 4) {
-    regs_dec<80>();
+    regs_dec<64>();
     if (warp == 0) {
       // ---------------- segment records and page copies -------------------------------------
       int e = 0, k = 0;
@@ -501,8 +659,11 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
             ok = false;
             break;
           }
-          const bool whole = a == 0 && z == r.n_pg;
           if (lane == 0) {
+            // who has the page that starts at a weight (the first `extra` CTAs have one unit more)
+            const long long big = extra * (quota + 1);
+            auto owner = [&](long long x) { return x < big ? (int)(x / (quota + 1)) : extra + (int)((x - big) / quota); };
+            const int c0 = owner(base), parts = owner(base + (long long)(r.n_pg - 1) * pw) - c0 + 1;
             SegRec* s = rec(k);
             s->n_pg = z - a;
             s->g = gg;
@@ -511,14 +672,11 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
             s->pos = r.pos;
             s->len = r.len;
             s->page0 = r.page0 + a;
-            s->slot = whole ? -1 : 2 * (int)blockIdx.x + (a > 0 ? 0 : 1);
-            if (!whole && a == 0) {
-              // the first part tells the merge who has the others
-              const long long last = base + (long long)(r.n_pg - 1) * pw;
-              const long long big = extra * (quota + 1);  // the first `extra` CTAs have one unit more
-              const int c_last = last < big ? (int)(last / (quota + 1)) : extra + (int)((last - big) / quota);
-              p.desc[job] = (int)blockIdx.x | (c_last - (int)blockIdx.x + 1) << 8;
-            }
+            s->part = (int)blockIdx.x - c0;
+            s->parts = parts;
+            s->c0 = c0;
+            s->job = job;
+            if (parts > kInline && a == 0) p.big[atomicAdd(p.n_big, 1)] = make_int2(job, c0 | parts << 8);
             mbar_arrive(bar(kBRecFull + k % kRecs));
           }
           __syncwarp();
@@ -648,13 +806,13 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
         if (lane == 0) mbar_arrive(bar(kBQFull + (k & 1)));
       }
     }
-  } else {
-    regs_inc<208>();
+  } else if (warp < 12) {
+    regs_inc<160>();
     // ---------------- softmax: set = (warp - 4) / 4, row = TMEM lane ------------------------------------
     const int set = (warp - 4) >> 2, quad = warp & 3, lrow = 32 * quad + lane;
     const uint32_t t_s = tmem + ((uint32_t)(32 * quad) << 16) + kTmemS + 128 * set, t_o = t_s + kTmemO - kTmemS;
     const uint64_t scale2 = pair64(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
-    uint32_t e = 0, par = 0;  // pages so far; bit 0: parity of this set's jobs, bit 1: of its segments
+    uint32_t e = 0, par = 0, segs = 0;  // pages so far, parity of this set's jobs, its segments
     for (int k = 0;; ++k) {
       if (!swait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc)) break;
       const SegRec r = *rec(k);
@@ -677,7 +835,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
       float shift = kUnset, l = 0.f;  // kBias less the reference, and the sum of weights
       bool ok = true;
       for (const uint32_t e0 = e; e - e0 < (uint32_t)r.n_pg; ++e) {
-        if (!swait(bar(kBSFull + set), par & 1, wc)) {
+        if (!swait(bar(kBSFull + set), par, wc)) {
           ok = false;
           break;
         }
@@ -765,52 +923,53 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
         start -= kPageTokens;
         if (mine) end -= kPageTokens;
       }
-      // ---- end of the segment: the accumulator is final ---------------------------------------------
-      if (!ok || !swait(bar(kBPvDone + set), par >> 1, wc)) break;
-      par ^= 2;
-      tc_fence_after();
-      if (busy) {
-        const int row = 128 * set + lrow;
-        const size_t at = (size_t)(r.q0 + token) * kQHeads + kGqa * r.g + (row & 3);
-        const float inv = l != 0.f ? p.out_scale / l : 0.f;  // (a NaN of the query stays one)
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[32];
-          tmem_ld32x32b_x32(t_o + 32 * c, v);
-          tmem_wait_ld();
-          if (mine) {
-            if (r.slot < 0) {
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                uint32_t y[8];
-#pragma unroll
-                for (int x = 0; x < 8; ++x)
-                  y[x] = pack16(__uint_as_float(v[16 * h + 2 * x]) * inv, __uint_as_float(v[16 * h + 2 * x + 1]) * inv, p.out_f16);
-                st32(p.out + at * kHeadDim + 32 * c + 16 * h, y);
-              }
-            } else {
-              float* to = p.part_o + ((size_t)r.slot * p.part_rows + row) * kHeadDim + 32 * c;
-#pragma unroll
-              for (int h = 0; h < 4; ++h) {
-                uint32_t y[8];
-#pragma unroll
-                for (int x = 0; x < 8; ++x) y[x] = v[8 * h + x];
-                st32(to + 8 * h, y);
-              }
-            }
-          }
-          __syncwarp();
-        }
-        if (mine) {
-          const float m = kBias - shift;
-          if (r.slot >= 0) p.part_ml[(size_t)r.slot * p.part_rows + row] = make_float2(m, l);
-          else if (p.lse) p.lse[at] = l != 0.f ? (m - kBias + log2f(l)) * kLn2 : -INFINITY;
-        }
-      }
-      tc_fence_before();
+      if (!ok) break;
+      reinterpret_cast<float2*>(smem + kOffMl)[256 * set + 128 * (segs & 1) + lrow] = make_float2(kBias - shift, l);
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBOFree + set));
+      if (lane == 0) mbar_arrive(bar(kBMl + 2 * set + (segs & 1)));
+      ++segs;
     }
+  } else {
+    // ---------------- outputs: the rows of a finished segment, one set after the other, while the softmax
+    // warps are at the next.  They leave through shared memory (the segment's query tiles, which are of no
+    // use any more) by bulk copies: stores of the threads themselves take an SM 4,000 cycles for a tile,
+    // and hold up every other access to shared memory, barriers among them. -------------------------------
+    const int quad = warp & 3, lrow = 32 * quad + lane;
+    uint32_t seg[2] = {0, 0};  // segments of each set
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      if (!swait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc)) break;
+      const SegRec r = *rec(k);
+      __syncwarp();
+      if (r.n_pg < 0) break;
+      if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
+      const uint32_t stage = sbase + kOffQ + (k & 1) * 32768 + quad * 8192;
+#pragma unroll
+      for (int set = 0; set < 2; ++set) {
+        if (set == 1 && r.n_tok <= 32) continue;
+        const uint32_t n = seg[set]++;
+        if (!ok || !swait(bar(kBMl + 2 * set + (n & 1)), n >> 1 & 1, wc) || !swait(bar(kBPvDone + set), n & 1, wc)) {
+          ok = false;
+          continue;
+        }
+        const uint32_t t_o = tmem + ((uint32_t)(32 * quad) << 16) + kTmemO + 128 * set;
+        const int token = 32 * set + (lrow >> 2);
+        const float2 own = reinterpret_cast<const float2*>(smem + kOffMl)[256 * set + 128 * (n & 1) + lrow];
+        tc_fence_after();
+        if (32 * set + 8 * quad < r.n_tok) put_rows(p, r, set, quad, lane, t_o, stage, token, own);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBOFree + set));
+      }
+      // (the tiles may be written again)
+      if (lane == 0) {
+        bulk_read_wait();
+        mbar_arrive(bar(kBQEmpty + (k & 1)));
+      }
+      __syncwarp();
+    }
+    if (lane == 0) bulk_wait();
+    __syncwarp();
   }
 
   // ---- teardown -------------------------------------------------------------------------
@@ -833,64 +992,86 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
 }
 
 // ---- (3) jobs that were cut ---------------------------------------------------------------
-// out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.  Grid: (job, 32 rows); a warp takes four rows one
-// after the other, lane = 4 channels, eight parts' loads at once.
-constexpr int kMergeParts = 8;
+// out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.  A CTA takes 32 rows of a job after the other: lane =
+// row, warp = 16 channels, four parts' loads at once.
+constexpr int kMergeParts = 4, kQuads = kGqa * kTileTokens / 32;
 __global__ void __launch_bounds__(256) prefill_merge_kernel(const __grid_constant__ PrefillParams p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int job = blockIdx.x, t = job / kKvHeads, g = job % kKvHeads;
   pdl_wait();
-  if (t >= *p.n_tiles) return;
-  const int desc = p.desc[job];
-  if (desc == 0) return;
-  const int c0 = desc & 255, parts = desc >> 8;
-  const int q0 = p.tiles[t].q0, n_rows = kGqa * p.tiles[t].n_tok;
-  for (int row = 32 * blockIdx.y + warp; row < min(n_rows, 32 * (int)blockIdx.y + 32); row += 8) {
-    float M = -INFINITY, L = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int units = *p.n_big * kQuads;
+  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    const int2 big = p.big[u / kQuads];
+    const int t = big.x / kKvHeads, g = big.x % kKvHeads, quad = u % kQuads, c0 = big.y & 255, parts = big.y >> 8;
+    const int q0 = p.tiles[t].q0, n_rows = kGqa * p.tiles[t].n_tok, row = 32 * quad + lane;
+    if (32 * quad >= n_rows) continue;
+    float M = -INFINITY, L = 0.f, o[16] = {};
     for (int i0 = 0; i0 < parts; i0 += kMergeParts) {
-      float4 x[kMergeParts];
-      float2 ml = make_float2(-INFINITY, 0.f);  // lane u: part i0 + u
-      auto slot = [&](int u) { return (size_t)(2 * (c0 + i0 + u) + (i0 + u == 0)) * p.part_rows + row; };
-      if (lane < kMergeParts && i0 + lane < parts) ml = p.part_ml[slot(lane)];
+      float4 x[kMergeParts][4];
+      float2 ml[kMergeParts];
 #pragma unroll
-      for (int u = 0; u < kMergeParts; ++u) {
-        x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i0 + u < parts) x[u] = reinterpret_cast<const float4*>(p.part_o + slot(u) * kHeadDim)[lane];
+      for (int i = 0; i < kMergeParts; ++i) {
+        ml[i] = make_float2(-INFINITY, 0.f);
+        if (i0 + i < parts) {
+          const size_t at = (part_slot(c0, i0 + i) * p.part_quads + quad) * 32;
+          ml[i] = p.part_ml[at + lane];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) x[i][c] = p.part_o[(at + 4 * warp + c) * 32 + lane];
+        }
       }
-      const float top = fmaxf(M, warp_max_f32(ml.y != 0.f ? ml.x : -INFINITY));
-      const float f = M > -INFINITY ? fast_exp2(M - top) : 0.f, w = ml.y != 0.f ? fast_exp2(ml.x - top) : 0.f;
+      float top = M;
+#pragma unroll
+      for (int i = 0; i < kMergeParts; ++i)
+        if (ml[i].y != 0.f) top = fmaxf(top, ml[i].x);
+      const float f = M > -INFINITY ? fast_exp2(M - top) : 0.f;
       M = top;
       L *= f;
-      o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
 #pragma unroll
-      for (int u = 0; u < kMergeParts; ++u) {
-        const float wu = __shfl_sync(0xffffffffu, w, u);
-        L = fmaf(__shfl_sync(0xffffffffu, ml.y, u), wu, L);
-        o.x = fmaf(x[u].x, wu, o.x);
-        o.y = fmaf(x[u].y, wu, o.y);
-        o.z = fmaf(x[u].z, wu, o.z);
-        o.w = fmaf(x[u].w, wu, o.w);
+      for (int c = 0; c < 16; ++c) o[c] *= f;
+#pragma unroll
+      for (int i = 0; i < kMergeParts; ++i) {
+        if (i0 + i >= parts) break;
+        const float w = ml[i].y != 0.f ? fast_exp2(ml[i].x - top) : 0.f;
+        L = fmaf(ml[i].y, w, L);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          o[4 * c] = fmaf(x[i][c].x, w, o[4 * c]);
+          o[4 * c + 1] = fmaf(x[i][c].y, w, o[4 * c + 1]);
+          o[4 * c + 2] = fmaf(x[i][c].z, w, o[4 * c + 2]);
+          o[4 * c + 3] = fmaf(x[i][c].w, w, o[4 * c + 3]);
+        }
       }
     }
+    if (row >= n_rows) continue;
     const float inv = L != 0.f ? p.out_scale / L : 0.f;  // (a NaN of the query stays one)
     const size_t at = (size_t)(q0 + (row >> 2)) * kQHeads + kGqa * g + (row & 3);
-    *reinterpret_cast<uint2*>(p.out + at * kHeadDim + 4 * lane) =
-        make_uint2(pack16(o.x * inv, o.y * inv, p.out_f16), pack16(o.z * inv, o.w * inv, p.out_f16));
-    if (p.lse && lane == 0) p.lse[at] = L != 0.f ? (M - kBias + log2f(L)) * kLn2 : -INFINITY;
+    uint32_t y[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) y[c] = pack16(o[2 * c] * inv, o[2 * c + 1] * inv, p.out_f16);
+    st32(p.out + at * kHeadDim + 16 * warp, y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7]);
+    if (p.lse && warp == 0) p.lse[at] = L != 0.f ? (M - kBias + log2f(L)) * kLn2 : -INFINITY;
   }
 }
 
-int prefill_rows(int n_q_total) { return kGqa * std::min(n_q_total, kTileTokens); }
+int prefill_quads(int n_q_total) { return (kGqa * std::min(n_q_total, kTileTokens) + 31) / 32; }
 int prefill_tiles(int n_q_total, int n_seqs) { return n_q_total / kTileTokens + std::min(n_q_total, n_seqs); }
+bool make_out_map(CUtensorMap* m, void* out, int n_q_total) {
+  const auto fn = tensor_map_encoder();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {kHeadDim, kQHeads, (cuuint64_t)n_q_total};
+  const cuuint64_t strides[2] = {kHeadDim * 2, kQHeads * kHeadDim * 2};
+  const cuuint32_t box[3] = {64, kGqa, 8}, steps[3] = {1, 1, 1};
+  // (16-bit words whatever their type)
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, out, dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 size_t padded(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 
 size_t prefill_workspace_bytes(int n_q_total, int n_seqs, int n_pages) {
-  const size_t rows = prefill_rows(n_q_total), tiles = prefill_tiles(n_q_total, n_seqs);
-  return 256 + padded(tiles * sizeof(TileRec)) + padded(tiles * kKvHeads * sizeof(int)) + padded((size_t)n_pages * sizeof(int)) +
-         padded(2 * kPrefillCtas * rows * sizeof(float2)) + 2 * kPrefillCtas * rows * kHeadDim * sizeof(float) +
+  const size_t quads = prefill_quads(n_q_total), tiles = prefill_tiles(n_q_total, n_seqs);
+  return 256 + padded(tiles * sizeof(TileRec)) + padded(tiles * kKvHeads * sizeof(int2)) + padded(tiles * 32 * sizeof(int)) + padded((size_t)n_pages * sizeof(int)) +
+         padded(2 * kPrefillCtas * quads * 32 * sizeof(float2)) + 2 * kPrefillCtas * quads * 32 * kHeadDim * sizeof(float) +
          (size_t)n_pages * kKvHeads * kImage;
 }
 
@@ -925,8 +1106,9 @@ cudaError_t launch_prefill_attn(const msa_cache* c, const uint8_t* q, float soft
   pp.out_scale = 256.0f / c->s_enc_v;
   pp.out_f16 = dtype == MSA_DTYPE_F16;
   pp.out = static_cast<uint16_t*>(out);
+  if (!make_out_map(&pp.out_map, out, n_q_total)) return cudaErrorInvalidValue;
   pp.lse = lse;
-  pp.part_rows = prefill_rows(n_q_total);
+  pp.part_quads = prefill_quads(n_q_total);
   pp.max_tiles = prefill_tiles(n_q_total, n_seqs);
   pp.cap = n_visited;
   uint8_t* w = static_cast<uint8_t*>(ws);
@@ -936,11 +1118,13 @@ cudaError_t launch_prefill_attn(const msa_cache* c, const uint8_t* q, float soft
     return at;
   };
   pp.n_tiles = reinterpret_cast<int*>(piece(256));
+  pp.n_big = pp.n_tiles + 1;
   pp.tiles = reinterpret_cast<TileRec*>(piece(pp.max_tiles * sizeof(TileRec)));
-  pp.desc = reinterpret_cast<int*>(piece((size_t)pp.max_tiles * kKvHeads * sizeof(int)));
+  pp.big = reinterpret_cast<int2*>(piece((size_t)pp.max_tiles * kKvHeads * sizeof(int2)));
+  pp.tickets = reinterpret_cast<int*>(piece((size_t)pp.max_tiles * 32 * sizeof(int)));
   pp.page_ok = reinterpret_cast<int*>(piece((size_t)pp.cap * sizeof(int)));
-  pp.part_ml = reinterpret_cast<float2*>(piece(2 * kPrefillCtas * (size_t)pp.part_rows * sizeof(float2)));
-  pp.part_o = reinterpret_cast<float*>(piece(2 * kPrefillCtas * (size_t)pp.part_rows * kHeadDim * sizeof(float)));
+  pp.part_ml = reinterpret_cast<float2*>(piece(2 * kPrefillCtas * (size_t)pp.part_quads * 32 * sizeof(float2)));
+  pp.part_o = reinterpret_cast<float4*>(piece(2 * kPrefillCtas * (size_t)pp.part_quads * 32 * kHeadDim * sizeof(float)));
   pp.images = w;
   pp.status = c->status;
   pp.wait_ns = launch_settings().wait_ns;
@@ -951,8 +1135,9 @@ cudaError_t launch_prefill_attn(const msa_cache* c, const uint8_t* q, float soft
   if (e != cudaSuccess) return e;
   e = launch_pdl(prefill_attn_kernel, dim3(std::min(n_sm, kPrefillCtas)), dim3(kPrefillThreads), kPrefillSmem, stream, pp);
   if (e != cudaSuccess) return e;
-  return launch_pdl(prefill_merge_kernel, dim3((unsigned)(pp.max_tiles * kKvHeads), (pp.part_rows + 31) / 32), dim3(256), 0,
-                    stream, pp);
+  // no job has more than kInline parts if its pages weigh no more than the least shares of so many CTAs
+  if (kFixed + (long long)n_visited * kPage2 <= (kInline - 1) * kLeast) return cudaSuccess;
+  return launch_pdl(prefill_merge_kernel, dim3(4 * std::min(n_sm, kPrefillCtas)), dim3(256), 0, stream, pp);
 }
 
 }  // namespace msa

@@ -28,10 +28,8 @@
 //   warps 2-5   epilogue: thread = token row, one head's 128 columns at a time
 //               in registers: RMS norm and RoPE are thread-local, so is the
 //               NVFP4 quantiser (a 16-channel group lives in one thread).
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include "common.cuh"
+#include "tensor_map.cuh"
 
 namespace msa {
 namespace {
@@ -339,24 +337,10 @@ __global__ void __launch_bounds__(kQkvThreads, 2) qkv_fused_kernel(const __grid_
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  });
-  return fn;
-}
-
 // 2D tensor map of a row-major bf16 matrix [rows][cols], box 64 columns x 128 rows,
 // 128-byte swizzle; rows beyond the matrix read as zeros.
 bool make_map(CUtensorMap* m, const void* base, int rows, int cols) {
-  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  const auto fn = tensor_map_encoder();
   if (!fn) return false;
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
