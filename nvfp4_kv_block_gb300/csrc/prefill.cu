@@ -40,6 +40,11 @@ constexpr int kTileTokens = 64;       // two row tiles of 32 tokens x 4 heads
 constexpr int kPrefillCtas = 152;     // most CTAs of a launch (the workspace is sized for them)
 constexpr int kStages = 3;            // pages in flight
 constexpr int kRecs = 4;
+#ifndef PVU
+#define PVU 4
+#define QKU 2
+#endif
+constexpr int kPvUnroll = PVU, kQkUnroll = QKU;
 constexpr int kInfo = 16;
 constexpr int kImageK = 16384, kImage = kImageK + 32768;  // bytes of a converted (page, KV head)
 
@@ -400,129 +405,115 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 __device__ __forceinline__ void bulk_read_wait() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// A warp's 32 rows of a finished segment (lane = row; own: its reference and sum) from the accumulator
-// to the output, or to the place of the segment's part of a job.  stage: 8 KB of shared memory.
-__device__ __forceinline__ void put_rows(const PrefillParams& p, const SegRec& r, int set, int quad, int lane, uint32_t t_o,
-                                         uint32_t stage, int token, float2 own) {
-  auto rows_of = [&](int i) { return (part_slot(r.c0, i) * p.part_quads + 4 * set + quad) * 32; };
-  float m = own.x, l = own.y;
-  bool join = false;
-  float w[kInline];  // the parts' weights
-  if (r.parts > 1) {
-    int* ticket = p.tickets + (r.job * 8 + 4 * set + quad);
-    // (the last part need not write what it has, if it is known to be)
-    if (r.parts <= kInline) {
-      int there;
-      asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(there) : "l"(ticket) : "memory");
-      join = __all_sync(0xffffffffu, there == r.parts - 1);
-    }
-    if (!join) {
-      p.part_ml[rows_of(r.part) + lane] = own;
-#pragma unroll 1
-      for (int c = 0; c < 2; ++c) {  // 64 channels of 32 rows: [16 of 4 channels][32 rows]
-        uint32_t v[64];
-        tmem_ld32x32b_x64(t_o + 64 * c, v);
-        tmem_wait_ld();
-        if (lane == 0) bulk_read_wait();
-        __syncwarp();
+// 32 channels (the c-th of four) of 32 rows, lane = row, on their way out: into a box of 64 channels x 4
+// heads x 8 tokens in shared memory (rows of 128 bytes, swizzled), which leaves with its second half.
+__device__ __forceinline__ void put32(const PrefillParams& p, const SegRec& r, const float (&o)[32], float inv, int c, int tok0,
+                                      int lane, uint32_t stage) {
+  uint32_t y[16];
 #pragma unroll
-        for (int x = 0; x < 16; ++x)
-          sts128(stage + (x * 32 + lane) * 16, make_uint4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]));
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          bulk_s2g(p.part_o + (rows_of(r.part) + 16 * c) * 32, stage, 8192);
-          bulk_commit();
-        }
-      }
-      if (r.parts > kInline) return;
-      __threadfence();
+  for (int x = 0; x < 16; ++x) y[x] = pack16(o[2 * x] * inv, o[2 * x + 1] * inv, p.out_f16);
+  if (tok0 + 8 <= r.n_tok) {
+    const uint32_t box = stage + (c >> 1) * 4096;
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      sts128(box + lane * 128 + (((4 * (c & 1) + x) ^ (lane & 7)) << 4), make_uint4(y[4 * x], y[4 * x + 1], y[4 * x + 2], y[4 * x + 3]));
+    if (c & 1) {
+      fence_proxy_async_smem();
       __syncwarp();
-      int before = 0;
       if (lane == 0) {
-        bulk_wait();
-        __threadfence();
-        before = atomicAdd(ticket, 1);
+        tensor_s2g(&p.out_map, 32 * (c - 1), kGqa * r.g, r.q0 + tok0, box);
+        bulk_commit();
       }
-      join = __shfl_sync(0xffffffffu, before, 0) == r.parts - 1;
-      if (!join) return;
     }
-    __threadfence();
-    float2 ml[kInline];
-    float top = -INFINITY, sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < kInline; ++i) {
-      ml[i] = make_float2(-INFINITY, 0.f);
-      if (i < r.parts) ml[i] = i == r.part ? own : __ldcg(p.part_ml + rows_of(i) + lane);
-    }
-#pragma unroll
-    for (int i = 0; i < kInline; ++i)
-      if (ml[i].y != 0.f) top = fmaxf(top, ml[i].x);
-#pragma unroll
-    for (int i = 0; i < kInline; ++i) {
-      w[i] = ml[i].y != 0.f ? fast_exp2(ml[i].x - top) : 0.f;
-      sum = fmaf(ml[i].y, w[i], sum);
-    }
-    m = top;
-    l = sum;
+  } else if (tok0 + (lane >> 2) < r.n_tok) {  // the last tokens of a sequence: a box would go on into the next one's rows
+    uint16_t* to = p.out + ((size_t)(r.q0 + tok0 + (lane >> 2)) * kQHeads + kGqa * r.g + (lane & 3)) * kHeadDim + 32 * c;
+    st32(to, y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7]);
+    st32(to + 16, y[8], y[9], y[10], y[11], y[12], y[13], y[14], y[15]);
   }
-  const float inv = l != 0.f ? p.out_scale / l : 0.f;  // (a NaN of the query stays one)
-  const bool full = 32 * set + 8 * quad + 8 <= r.n_tok, mine = token < r.n_tok;
-  const size_t at = (size_t)(r.q0 + token) * kQHeads + kGqa * r.g + (lane & 3);
-  if (mine && p.lse) p.lse[at] = l != 0.f ? (m - kBias + log2f(l)) * kLn2 : -INFINITY;
-  if (lane == 0) bulk_read_wait();
+}
+__device__ __forceinline__ void put_lse(const PrefillParams& p, const SegRec& r, float m, float l, int tok0, int lane) {
+  const int token = tok0 + (lane >> 2);
+  if (p.lse && token < r.n_tok)
+    p.lse[(size_t)(r.q0 + token) * kQHeads + kGqa * r.g + (lane & 3)] = l != 0.f ? (m - kBias + log2f(l)) * kLn2 : -INFINITY;
+}
+
+// A segment's part of a cut job (a warp's 32 rows from token tok0 on; own: a row's reference and sum): its
+// rows on their way to the part's place.  freed: called when the accumulator is read.
+template <typename F>
+__device__ __forceinline__ void put_part(const PrefillParams& p, const SegRec& r, float2 own, int tok0, int lane, uint32_t t_o,
+                                         uint32_t stage, F&& freed) {
+  auto rows_of = [&](int i) { return (part_slot(r.c0, i) * p.part_quads + (tok0 >> 3)) * 32; };
+  p.part_ml[rows_of(r.part) + lane] = own;
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {  // 64 channels of 32 rows: [16 of 4 channels][32 rows]
+    uint32_t v[64];
+    tmem_ld32x32b_x64(t_o + 64 * c, v);
+    tmem_wait_ld();
+    if (c) freed();
+    if (lane == 0) bulk_read_wait();
+    __syncwarp();
+#pragma unroll
+    for (int x = 0; x < 16; ++x)
+      sts128(stage + (x * 32 + lane) * 16, make_uint4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]));
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      bulk_s2g(p.part_o + (rows_of(r.part) + 16 * c) * 32, stage, 8192);
+      bulk_commit();
+    }
+  }
+}
+// Behind it, when the rows are there: if those of all parts are now, the parts' sum to the output.
+__device__ __forceinline__ void join_parts(const PrefillParams& p, const SegRec& r, int tok0, int lane, uint32_t stage) {
+  auto rows_of = [&](int i) { return (part_slot(r.c0, i) * p.part_quads + (tok0 >> 3)) * 32; };
+  __threadfence();
   __syncwarp();
+  int before = 0;
+  if (lane == 0) {
+    bulk_wait();
+    __threadfence();
+    before = atomicAdd(p.tickets + (r.job * 8 + (tok0 >> 3)), 1);
+  }
+  if (__shfl_sync(0xffffffffu, before, 0) != r.parts - 1) return;
+  __threadfence();
+  float2 ml[kInline];
+  float top = -INFINITY, sum = 0.f, w[kInline];
+#pragma unroll
+  for (int i = 0; i < kInline; ++i) ml[i] = i < r.parts ? __ldcg(p.part_ml + rows_of(i) + lane) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+  for (int i = 0; i < kInline; ++i)
+    if (ml[i].y != 0.f) top = fmaxf(top, ml[i].x);
+#pragma unroll
+  for (int i = 0; i < kInline; ++i) {
+    w[i] = ml[i].y != 0.f ? fast_exp2(ml[i].x - top) : 0.f;
+    sum = fmaf(ml[i].y, w[i], sum);
+  }
+  put_lse(p, r, top, sum, tok0, lane);
+  const float inv = sum != 0.f ? p.out_scale / sum : 0.f;  // (a NaN of the query stays one)
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {  // 32 channels
-    uint32_t v[32];
-    tmem_ld32x32b_x32(t_o + 32 * c, v);
-    wait_ld32(v);
-    if (join) {  // parts in their order, this one's from where it is
-      float s[32] = {};
+  for (int c = 0; c < 4; ++c) {
+    float s[32] = {};
 #pragma unroll 1
-      for (int i = 0; i < r.parts; ++i) {
-        if (i == r.part) {
+    for (int i = 0; i < r.parts; i += 2) {  // two parts' loads at once
+      float4 z[2][8];
 #pragma unroll
-          for (int x = 0; x < 32; ++x) s[x] = fmaf(__uint_as_float(v[x]), w[i], s[x]);
-        } else {
-          const float4* from = p.part_o + (rows_of(i) + 8 * c) * 32 + lane;
-          float4 z[8];
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int x = 0; x < 8; ++x) z[x] = __ldcg(from + x * 32);
+        for (int x = 0; x < 8; ++x)
+          z[h][x] = i + h < r.parts ? __ldcg(p.part_o + (rows_of(i + h) + 8 * c + x) * 32 + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            s[4 * x] = fmaf(z[x].x, w[i], s[4 * x]);
-            s[4 * x + 1] = fmaf(z[x].y, w[i], s[4 * x + 1]);
-            s[4 * x + 2] = fmaf(z[x].z, w[i], s[4 * x + 2]);
-            s[4 * x + 3] = fmaf(z[x].w, w[i], s[4 * x + 3]);
-          }
+      for (int h = 0; h < 2; ++h) {
+        const float f = i + h < r.parts ? w[i + h] : 0.f;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          s[4 * x] = fmaf(z[h][x].x, f, s[4 * x]);
+          s[4 * x + 1] = fmaf(z[h][x].y, f, s[4 * x + 1]);
+          s[4 * x + 2] = fmaf(z[h][x].z, f, s[4 * x + 2]);
+          s[4 * x + 3] = fmaf(z[h][x].w, f, s[4 * x + 3]);
         }
       }
-#pragma unroll
-      for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(s[x]);
     }
-    uint32_t y[16];
-#pragma unroll
-    for (int x = 0; x < 16; ++x) y[x] = pack16(__uint_as_float(v[2 * x]) * inv, __uint_as_float(v[2 * x + 1]) * inv, p.out_f16);
-    if (full) {
-      // boxes of 64 channels x 4 heads x 8 tokens: rows of 128 bytes, swizzled
-      const uint32_t box = stage + (c >> 1) * 4096;
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        sts128(box + lane * 128 + (((4 * (c & 1) + x) ^ (lane & 7)) << 4), make_uint4(y[4 * x], y[4 * x + 1], y[4 * x + 2], y[4 * x + 3]));
-      if (c & 1) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tensor_s2g(&p.out_map, 32 * (c - 1), kGqa * r.g, r.q0 + 32 * set + 8 * quad, box);
-          bulk_commit();
-        }
-      }
-    } else if (mine) {  // the last tokens of a sequence: a box would go on into the next one's rows
-      uint16_t* to = p.out + at * kHeadDim + 32 * c;
-      st32(to, y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7]);
-      st32(to + 16, y[8], y[9], y[10], y[11], y[12], y[13], y[14], y[15]);
-    }
+    put32(p, r, s, inv, c, tok0, lane, stage);
   }
 }
 
@@ -537,7 +528,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
   const WaitCtl wc{s_abort, p.wait_ns};
   auto rec = [&](int k) { return reinterpret_cast<SegRec*>(smem + kOffRecs + 64 * (k % kRecs)); };
   int* s_info = reinterpret_cast<int*>(smem + kOffInfo);
-  long long* s_scan = reinterpret_cast<long long*>(smem + kOffScan);  // [20] warp sums; 24: total, first job, its offset
+  long long* s_scan = reinterpret_cast<long long*>(smem + kOffScan);  // [20] warp sums; 24: total, first job, its offset, last job, its offset
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   // ---- prologue ------------------------------------------------------------------
@@ -596,18 +587,22 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
     const long long total = kKvHeads * one;
     const int G = (int)min((long long)gridDim.x, max(1ll, total / kLeast));
     if (total > 0 && (int)blockIdx.x < G) {
-      const long long lo = range_start(total / G, (int)(total % G), blockIdx.x);
-      const long long in = lo % one;
-      long long x = before + incl - mine;
-      if (mine > 0 && in >= x && in < x + mine) {  // the first job is one of this thread's
-        int t = t0;
-        for (;; ++t) {
-          const int w = job_weight(p.tiles[t].n_tok, p.tiles[t].n_pg);
-          if (in < x + w) break;
-          x += w;
+      // the jobs that hold the range's first and last weight, if they are among this thread's tiles
+#pragma unroll 1
+      for (int end = 0; end < 2; ++end) {
+        const long long at = range_start(total / G, (int)(total % G), (int)blockIdx.x + end) - end;
+        const long long in = at % one;
+        long long x = before + incl - mine;
+        if (mine > 0 && in >= x && in < x + mine) {
+          int t = t0;
+          for (;; ++t) {
+            const int w = job_weight(p.tiles[t].n_tok, p.tiles[t].n_pg);
+            if (in < x + w) break;
+            x += w;
+          }
+          s_scan[25 + 2 * end] = (at / one) * n_tiles + t;
+          s_scan[26 + 2 * end] = at - in + x;
         }
-        s_scan[25] = (lo / one) * n_tiles + t;
-        s_scan[26] = lo - in + x;
       }
     }
     if (tid == 0) s_scan[24] = total;
@@ -628,78 +623,86 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
         const long long quota = total / G;
         const int extra = (int)(total - quota * G);
         const long long lo = range_start(quota, extra, blockIdx.x), hi = range_start(quota, extra, blockIdx.x + 1);
-        long long off = s_scan[26];
-        int g = (int)(s_scan[25] / n_tiles), t = (int)(s_scan[25] % n_tiles);
-        while (ok && off < hi && g < kKvHeads) {
-          const int word = lane < 8 ? reinterpret_cast<const int*>(p.tiles + t)[lane] : 0;
-          TileRec r;
-          r.q0 = __shfl_sync(0xffffffffu, word, 0);
-          r.n_tok = __shfl_sync(0xffffffffu, word, 1);
-          r.pos = __shfl_sync(0xffffffffu, word, 2);
-          r.len = __shfl_sync(0xffffffffu, word, 3);
-          r.page0 = __shfl_sync(0xffffffffu, word, 4);
-          r.n_pg = __shfl_sync(0xffffffffu, word, 5);
-          r.ws_page = __shfl_sync(0xffffffffu, word, 6);
-          const int pw = page_weight(r.n_tok);
-          // page i starts at weight base + i pw; it belongs to the range that holds its start
-          const long long base = off + kFixed;
-          auto page_at = [&](long long x) {  // the first page that starts at weight x or behind it
-            if (x <= base) return 0;
-            return x - base > (long long)r.n_pg * pw ? r.n_pg : ((int)(x - base) + pw - 1) / pw;
-          };
-          const int a = r.n_pg > 0 ? page_at(lo) : 0, z = r.n_pg > 0 ? page_at(hi) : 0;
-          off += job_weight(r.n_tok, r.n_pg);
-          const int job = t * kKvHeads + g, gg = g;
-          if (++t == n_tiles) {
-            t = 0;
-            ++g;
-          }
-          if (a >= z) continue;
-          if (!twait(bar(kBRecEmpty + k % kRecs), ((k / kRecs) & 1) ^ 1, wc)) {
-            ok = false;
-            break;
-          }
-          if (lane == 0) {
-            // who has the page that starts at a weight (the first `extra` CTAs have one unit more)
-            const long long big = extra * (quota + 1);
-            auto owner = [&](long long x) { return x < big ? (int)(x / (quota + 1)) : extra + (int)((x - big) / quota); };
-            const int c0 = owner(base), parts = owner(base + (long long)(r.n_pg - 1) * pw) - c0 + 1;
-            SegRec* s = rec(k);
-            s->n_pg = z - a;
-            s->g = gg;
-            s->q0 = r.q0;
-            s->n_tok = r.n_tok;
-            s->pos = r.pos;
-            s->len = r.len;
-            s->page0 = r.page0 + a;
-            s->part = (int)blockIdx.x - c0;
-            s->parts = parts;
-            s->c0 = c0;
-            s->job = job;
-            if (parts > kInline && a == 0) p.big[atomicAdd(p.n_big, 1)] = make_int2(job, c0 | parts << 8);
-            mbar_arrive(bar(kBRecFull + k % kRecs));
-          }
-          __syncwarp();
-          ++k;
-          const uint8_t* image = p.images + ((size_t)(r.ws_page + a) * kKvHeads + gg) * kImage;
-          for (int i0 = a; ok && i0 < z; i0 += 32) {
-            const int cnt = min(32, z - i0);
-            const int there = lane < cnt ? p.page_ok[r.ws_page + i0 + lane] : 0;
-            for (int j = 0; j < cnt; ++j, ++e, image += kKvHeads * kImage) {
-              const int st = e % kStages, ph = ((e / kStages) & 1) ^ 1, good = __shfl_sync(0xffffffffu, there, j);
-              if (!twait(bar(kBEmpty + st), ph, wc)) {
-                ok = false;
-                break;
-              }
-              if (lane == 0) {
-                s_info[e % kInfo] = good;
-                if (!(p.inject && e == 0)) {
-                  mbar_arrive_expect_tx(bar(kBFull + st), kImage);
-                  bulk_g2s(sbase + kOffK + st * kImage, image, kImage, bar(kBFull + st));
+        // A job that goes on in the next CTA's range comes first: its rows are then there long before the
+        // other parts' are, and are joined under other segments.
+        long long early = -1;
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+          long long off = s_scan[pass ? 26 : 28];
+          int g = (int)(s_scan[pass ? 25 : 27] / n_tiles), t = (int)(s_scan[pass ? 25 : 27] % n_tiles);
+          while (ok && off < hi && g < kKvHeads) {
+            const int word = lane < 8 ? reinterpret_cast<const int*>(p.tiles + t)[lane] : 0;
+            TileRec r;
+            r.q0 = __shfl_sync(0xffffffffu, word, 0);
+            r.n_tok = __shfl_sync(0xffffffffu, word, 1);
+            r.pos = __shfl_sync(0xffffffffu, word, 2);
+            r.len = __shfl_sync(0xffffffffu, word, 3);
+            r.page0 = __shfl_sync(0xffffffffu, word, 4);
+            r.n_pg = __shfl_sync(0xffffffffu, word, 5);
+            r.ws_page = __shfl_sync(0xffffffffu, word, 6);
+            const int pw = page_weight(r.n_tok);
+            // page i starts at weight base + i pw; it belongs to the range that holds its start
+            const long long base = off + kFixed;
+            auto page_at = [&](long long x) {  // the first page that starts at weight x or behind it
+              if (x <= base) return 0;
+              return x - base > (long long)r.n_pg * pw ? r.n_pg : ((int)(x - base) + pw - 1) / pw;
+            };
+            const int a = r.n_pg > 0 ? page_at(lo) : 0, z = r.n_pg > 0 ? page_at(hi) : 0;
+            const bool take = a < z && (pass ? off != early : z < r.n_pg);
+            if (take && pass == 0) early = off;
+            off += job_weight(r.n_tok, r.n_pg);
+            const int job = t * kKvHeads + g, gg = g;
+            if (++t == n_tiles) {
+              t = 0;
+              ++g;
+            }
+            if (!take) continue;
+            if (!twait(bar(kBRecEmpty + k % kRecs), ((k / kRecs) & 1) ^ 1, wc)) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) {
+              // who has the page that starts at a weight (the first `extra` CTAs have one unit more)
+              const long long big = extra * (quota + 1);
+              auto owner = [&](long long x) { return x < big ? (int)(x / (quota + 1)) : extra + (int)((x - big) / quota); };
+              const int c0 = owner(base), parts = owner(base + (long long)(r.n_pg - 1) * pw) - c0 + 1;
+              SegRec* s = rec(k);
+              s->n_pg = z - a;
+              s->g = gg;
+              s->q0 = r.q0;
+              s->n_tok = r.n_tok;
+              s->pos = r.pos;
+              s->len = r.len;
+              s->page0 = r.page0 + a;
+              s->part = (int)blockIdx.x - c0;
+              s->parts = parts;
+              s->c0 = c0;
+              s->job = job;
+              if (parts > kInline && a == 0) p.big[atomicAdd(p.n_big, 1)] = make_int2(job, c0 | parts << 8);
+              mbar_arrive(bar(kBRecFull + k % kRecs));
+            }
+            __syncwarp();
+            ++k;
+            const uint8_t* image = p.images + ((size_t)(r.ws_page + a) * kKvHeads + gg) * kImage;
+            for (int i0 = a; ok && i0 < z; i0 += 32) {
+              const int cnt = min(32, z - i0);
+              const int there = lane < cnt ? p.page_ok[r.ws_page + i0 + lane] : 0;
+              for (int j = 0; j < cnt; ++j, ++e, image += kKvHeads * kImage) {
+                const int st = e % kStages, ph = ((e / kStages) & 1) ^ 1, good = __shfl_sync(0xffffffffu, there, j);
+                if (!twait(bar(kBEmpty + st), ph, wc)) {
+                  ok = false;
+                  break;
                 }
-                *s_issued = e + 1;
+                if (lane == 0) {
+                  s_info[e % kInfo] = good;
+                  if (!(p.inject && e == 0)) {
+                    mbar_arrive_expect_tx(bar(kBFull + st), kImage);
+                    bulk_g2s(sbase + kOffK + st * kImage, image, kImage, bar(kBFull + st));
+                  }
+                  *s_issued = e + 1;
+                }
+                __syncwarp();
               }
-              __syncwarp();
             }
           }
         }
@@ -711,9 +714,9 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
       }
     } else if (warp == 1) {
       // ---------------- MMA issuer ---------------------------------------------------------------------
-      // Job j of a segment: page j / sets, row tile j % sets.  In turn PV(j), then QK(j + sets) into the
-      // same columns; so one tile's products run under the other's softmax.  The warp stays together
-      // and elects a lane for the MMAs only (in a loop that one lane runs alone nothing is
+      // For each page and row tile PV, then the tile's next QK into the same columns (the next segment's
+      // first one behind the last); so one tile's products run under the other's softmax.  The warp stays
+      // together and elects a lane for the MMAs only (in a loop that one lane runs alone nothing is
       // warp-uniform, and an MMA takes three times as long to issue).
       const uint32_t idesc_qk = umma_idesc_e4m3(128, 128);
       // D fp32, A and B f16, A K-major, B MN-major
@@ -724,64 +727,97 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
       const uint64_t kdesc0 = umma_desc_noswz_lbo_sbo(sbase + kOffK, 2048, 128);
       const uint64_t vdesc0 = umma_desc_noswz_lbo_sbo(sbase + kOffK + kImageK, 128, 2048);
       const uint64_t qdesc0 = umma_desc_sw128(sbase + kOffQ);
+      // (inside an elected lane)
+      auto pv = [&](int set, int stage, uint32_t acc) {
+        const uint32_t s = tmem + kTmemS + 128 * set;
+        const uint64_t vdesc = vdesc0 + stage * (kImage >> 4);
+#pragma unroll kPvUnroll
+        for (int kk = 0; kk < 8; ++kk, acc = 1)  // 16 tokens each: 8 columns of P inside S's 32-column chunks
+          umma_f16_ts(s + kTmemO - kTmemS, s + 32 * (kk >> 1) + 8 * (kk & 1), vdesc + kk * (256 >> 4), idesc_pv, acc);
+      };
+      auto qk = [&](int set, int stage, int k) {
+        const uint32_t s = tmem + kTmemS + 128 * set;
+        const uint64_t qdesc = qdesc0 + (2 * (k & 1) + set) * (16384 >> 4), kdesc = kdesc0 + stage * (kImage >> 4);
+#pragma unroll kQkUnroll
+        for (int kk = 0; kk < 4; ++kk)  // 32 channels each
+          umma_e4m3(s, qdesc + 2 * kk, kdesc + kk * (4096 >> 4), idesc_qk, kk > 0);
+        umma_commit(bar(kBSFull + set));
+      };
       uint32_t p_par = 0, o_par = 0, o_any = 0;  // bit per set: parity of its next P, of its segments, whether it had one
-      int st = kStages - 1, full = 0;            // stage of the page before the next one; parity of the next one's
+      int st = kStages - 1, full = 0;            // stage of the page whose P is awaited; parity of the next one's stage
+      int n_pg = 0, sets = 0;                    // the segment
       bool ok = true;
-      for (int k = 0; ok; ++k) {
-        if (!swait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc)) break;
-        const int n_pg = __shfl_sync(0xffffffffu, rec(k)->n_pg, 0);
-        if (n_pg < 0) break;
-        const int sets = __shfl_sync(0xffffffffu, rec(k)->n_tok, 0) > 32 ? 2 : 1;
-        if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
-        if (!swait(bar(kBQFull + (k & 1)), (k >> 1) & 1, wc)) break;
-        // i: the page whose P is awaited (-1: none yet); QK of page i + 1 goes behind its PV
-        for (int i = -1; ok && i < n_pg; ++i) {
+      for (int k = -1; ok;) {
+        // all pages but the last (a short loop: a long way round the warp's code misses the instruction cache,
+        // which the softmax's code fills: 2,420 cycles a page, 2,800 with the segment's end in the loop)
+        uint32_t acc = 0;
+        for (int i = 1; i < n_pg; ++i, acc = 1) {
           const int next = st == kStages - 1 ? 0 : st + 1;
-          const bool more = i + 1 < n_pg;
-          if (more && !swait(bar(kBFull + next), full, wc)) {
+          if (!swait(bar(kBFull + next), full, wc)) {
             ok = false;
             break;
           }
           for (int set = 0; set < sets; ++set) {
-            if (i >= 0) {
-              if (!swait(bar(kBPFull + set), p_par >> set & 1, wc) ||
-                  // (the first PV writes over an accumulator that has to be read)
-                  (i == 0 && (o_any >> set & 1) && !swait(bar(kBOFree + set), (o_par >> set & 1) ^ 1, wc))) {
-                ok = false;
-                break;
-              }
-              p_par ^= 1u << set;
+            if (!swait(bar(kBPFull + set), p_par >> set & 1, wc)) {
+              ok = false;
+              break;
             }
             tc_fence_after();
             if (elect_one()) {
-              const uint32_t s = tmem + kTmemS + 128 * set;
-              if (i >= 0) {
-                const uint64_t vdesc = vdesc0 + st * (kImage >> 4);
-#pragma unroll 4
-                for (int kk = 0; kk < 8; ++kk)  // 16 tokens each: 8 columns of P inside S's 32-column chunks
-                  umma_f16_ts(s + kTmemO - kTmemS, s + 32 * (kk >> 1) + 8 * (kk & 1), vdesc + kk * (256 >> 4), idesc_pv,
-                              (i > 0 || kk > 0) ? 1u : 0u);
-                if (set == sets - 1) umma_commit(bar(kBEmpty + st));
-                if (!more) umma_commit(bar(kBPvDone + set));
-              }
-              if (more) {
-                const uint64_t qdesc = qdesc0 + (2 * (k & 1) + set) * (16384 >> 4), kdesc = kdesc0 + next * (kImage >> 4);
-#pragma unroll 2
-                for (int kk = 0; kk < 4; ++kk)  // 32 channels each
-                  umma_e4m3(s, qdesc + 2 * kk, kdesc + kk * (4096 >> 4), idesc_qk, kk > 0);
-                umma_commit(bar(kBSFull + set));
-                if (i + 2 == n_pg && set == sets - 1) umma_commit(bar(kBQEmpty + (k & 1)));
-              }
+              pv(set, st, acc);
+              if (set == sets - 1) umma_commit(bar(kBEmpty + st));
+              qk(set, next, k);
             }
             __syncwarp();
           }
-          if (more) {
-            st = next;
-            full ^= next == kStages - 1;
-          }
+          if (!ok) break;
+          p_par ^= sets == 2 ? 3u : 1u;
+          st = next;
+          full ^= next == kStages - 1;
         }
-        o_par ^= sets == 2 ? 3u : 1u;
-        o_any |= sets == 2 ? 3u : 1u;
+        if (!ok) break;
+        // the last one, and the next segment's first
+        if (!swait(bar(kBRecFull + (k + 1) % kRecs), ((k + 1) / kRecs) & 1, wc)) break;
+        const int next_pg = __shfl_sync(0xffffffffu, rec(k + 1)->n_pg, 0);
+        const int next_sets = next_pg < 0 ? 0 : __shfl_sync(0xffffffffu, rec(k + 1)->n_tok, 0) > 32 ? 2 : 1;
+        const int next = st == kStages - 1 ? 0 : st + 1;
+        if (next_sets) {
+          if (lane == 0) mbar_arrive(bar(kBRecEmpty + (k + 1) % kRecs));
+          if (!swait(bar(kBQFull + ((k + 1) & 1)), ((k + 1) >> 1) & 1, wc) || !swait(bar(kBFull + next), full, wc)) break;
+        }
+#pragma unroll 1
+        for (int set = 0; set < max(sets, next_sets); ++set) {
+          if (set < sets && !swait(bar(kBPFull + set), p_par >> set & 1, wc)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (elect_one()) {
+            if (set < sets) {
+              pv(set, st, acc);
+              umma_commit(bar(kBPvDone + set));
+              if (set == sets - 1) {
+                umma_commit(bar(kBEmpty + st));
+                umma_commit(bar(kBQEmpty + (k & 1)));
+              }
+            }
+            if (set < next_sets) qk(set, next, k + 1);
+          }
+          __syncwarp();
+        }
+        if (!ok || !next_sets) break;
+        const uint32_t had = sets == 2 ? 3u : (uint32_t)sets, has = next_sets == 2 ? 3u : 1u;
+        p_par ^= had;
+        o_par ^= had;
+        o_any |= had;
+        ++k;
+        n_pg = next_pg;
+        sets = next_sets;
+        st = next;
+        full ^= next == kStages - 1;
+        // (the first PVs write over accumulators that have to be read)
+        for (int set = 0; set < 2 && ok; ++set)
+          if ((has & o_any) >> set & 1) ok = swait(bar(kBOFree + set), (o_par >> set & 1) ^ 1, wc);
       }
       __syncwarp();
       if (elect_one()) umma_commit(bar(kBDone));
@@ -953,14 +989,40 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
           continue;
         }
         const uint32_t t_o = tmem + ((uint32_t)(32 * quad) << 16) + kTmemO + 128 * set;
-        const int token = 32 * set + (lrow >> 2);
+        const int tok0 = 32 * set + 8 * quad;  // the warp's first token
         const float2 own = reinterpret_cast<const float2*>(smem + kOffMl)[256 * set + 128 * (n & 1) + lrow];
+        auto freed = [&] {  // the accumulator is read
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBOFree + set));
+        };
         tc_fence_after();
-        if (32 * set + 8 * quad < r.n_tok) put_rows(p, r, set, quad, lane, t_o, stage, token, own);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBOFree + set));
+        if (tok0 >= r.n_tok) {
+          freed();
+        } else if (r.parts > 1) {
+          put_part(p, r, own, tok0, lane, t_o, stage, freed);
+        } else {
+          const float inv = own.y != 0.f ? p.out_scale / own.y : 0.f;  // (a NaN of the query stays one)
+          if (lane == 0) bulk_read_wait();
+          __syncwarp();
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[32];
+            tmem_ld32x32b_x32(t_o + 32 * c, v);
+            wait_ld32(v);
+            if (c == 3) freed();
+            float o[32];
+#pragma unroll
+            for (int x = 0; x < 32; ++x) o[x] = __uint_as_float(v[x]);
+            put32(p, r, o, inv, c, tok0, lane, stage);
+          }
+          put_lse(p, r, own.x, own.y, tok0, lane);
+        }
       }
+      if (ok && r.parts > 1 && r.parts <= kInline)
+#pragma unroll 1
+        for (int set = 0; set < 2; ++set)
+          if (32 * set + 8 * quad < r.n_tok) join_parts(p, r, 32 * set + 8 * quad, lane, stage);
       // (the tiles may be written again)
       if (lane == 0) {
         bulk_read_wait();
