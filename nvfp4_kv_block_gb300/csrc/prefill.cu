@@ -40,11 +40,6 @@ constexpr int kTileTokens = 64;       // two row tiles of 32 tokens x 4 heads
 constexpr int kPrefillCtas = 152;     // most CTAs of a launch (the workspace is sized for them)
 constexpr int kStages = 3;            // pages in flight
 constexpr int kRecs = 4;
-#ifndef PVU
-#define PVU 4
-#define QKU 2
-#endif
-constexpr int kPvUnroll = PVU, kQkUnroll = QKU;
 constexpr int kInfo = 16;
 constexpr int kImageK = 16384, kImage = kImageK + 32768;  // bytes of a converted (page, KV head)
 
@@ -54,7 +49,8 @@ constexpr int kOffK = kOffQ + 4 * 16384;
 constexpr int kOffRecs = kOffK + kStages * kImage;        // kRecs x 64 B
 constexpr int kOffInfo = kOffRecs + kRecs * 64;           // int [kInfo]: page inside the pool
 constexpr int kOffScan = kOffInfo + kInfo * 4;            // long long [32]
-constexpr int kOffMl = kOffScan + 32 * 8;                 // float2 [2 sets][2 parities][128]: a row's reference and sum
+constexpr int kOffRange = kOffScan + 32 * 8;              // long long [kPrefillCtas + 1]
+constexpr int kOffMl = kOffRange + 160 * 8;                 // float2 [2 sets][2 parities][128]: a row's reference and sum
 constexpr int kOffBars = kOffMl + 2 * 2 * 128 * 8;
 constexpr int kBFull = 0, kBEmpty = kBFull + kStages, kBQFull = kBEmpty + kStages, kBQEmpty = kBQFull + 2,
               kBSFull = kBQEmpty + 2, kBPFull = kBSFull + 2, kBPvDone = kBPFull + 2, kBOFree = kBPvDone + 2, kBMl = kBOFree + 2, kBRecFull = kBMl + 4,  // kBMl: [set][parity]
@@ -73,7 +69,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // Weights of the partition: a page of a tile of up to 32 tokens and of one of up to 64, the fixed
 // part of a job, and the least share of a CTA (a page's weight at least, so that every CTA
 // between a job's first and last has pages of it).
-constexpr int kPage1 = 5, kPage2 = 9, kFixed = 10, kLeast = 10;
+constexpr int kPage1 = 9, kPage2 = 9, kFixed = 16, kSmall = 45, kLeast = 10;
 
 constexpr int kInline = 6;  // parts of a job that its last one joins
 
@@ -303,11 +299,13 @@ __global__ void __launch_bounds__(kConvThreads) prefill_convert_kernel(const __g
 }
 
 // ---- (2) attention --------------------------------------------------------------------
-// Start of CTA c's range of total = G quota + extra units.
-__device__ __forceinline__ long long range_start(long long quota, int extra, int c) { return c * quota + min(c, extra); }
-
+// a / b of weights: in 32 bits where they fit (nearly always; a 64-bit division is a subroutine, and ten of
+// them took 1.3 us of a call's start).
+__device__ __forceinline__ long long quot(long long a, long long b) {
+  return (a | b) >> 31 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
 __device__ __forceinline__ int page_weight(int n_tok) { return n_tok <= 32 ? kPage1 : kPage2; }
-__device__ __forceinline__ int job_weight(int n_tok, int n_pg) { return n_pg > 0 ? kFixed + n_pg * page_weight(n_tok) : 0; }
+__device__ __forceinline__ int job_weight(int n_tok, int n_pg) { return n_pg > 0 ? max(kFixed + n_pg * page_weight(n_tok), kSmall) : 0; }
 
 // Bits 0 .. n - 1 (n clamped to 0 .. 32).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1; }
@@ -528,7 +526,9 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
   const WaitCtl wc{s_abort, p.wait_ns};
   auto rec = [&](int k) { return reinterpret_cast<SegRec*>(smem + kOffRecs + 64 * (k % kRecs)); };
   int* s_info = reinterpret_cast<int*>(smem + kOffInfo);
-  long long* s_scan = reinterpret_cast<long long*>(smem + kOffScan);  // [20] warp sums; 24: total, first job, its offset, last job, its offset
+  // [24] warp sums; 24: start of the cut jobs, CTAs, whole jobs of each, first cut job, its start, last one, its start
+  long long* s_scan = reinterpret_cast<long long*>(smem + kOffScan);
+  long long* s_range = reinterpret_cast<long long*>(smem + kOffRange);  // [CTAs + 1] starts of the CTAs' ranges of the cut jobs
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   // ---- prologue ------------------------------------------------------------------
@@ -585,13 +585,50 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
       one += s_scan[i];
     }
     const long long total = kKvHeads * one;
-    const int G = (int)min((long long)gridDim.x, max(1ll, total / kLeast));
+    const int n_jobs = kKvHeads * n_tiles, G = (int)min((long long)gridDim.x, max(1ll, quot(total, kLeast)));
+    const long long quota = quot(total, G);
+    // Whole jobs c, c + G, ... of CTA c: as many rounds as leave every CTA a share of the cut ones
+    auto weight = [&](int job) {
+      const TileRec* r = p.tiles + job % n_tiles;
+      return job_weight(r->n_tok, r->n_pg);
+    };
+    int whole = total > 0 ? n_jobs / G : 0;
+    long long w = 0;
+    if (tid < G)
+      for (int i = 0; i < whole; ++i) w += weight(tid + i * G);
+    while (__syncthreads_or(whole > 0 && tid < G && w + kLeast > quota)) {
+      --whole;
+      if (tid < G) w -= weight(tid + whole * G);
+    }
+    // and what is left to each, of the jobs behind them
+    long long left = total > 0 && tid < G ? quota + (tid < (int)(total - quota * G)) - w : 0, upto = left;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    if (lane == 31 && warp < 8) s_scan[16 + warp] = upto;
+    const int first_g = total > 0 ? whole * G / n_tiles : 0, first_t = total > 0 ? whole * G % n_tiles : 0;
+    if (t0 <= first_t && first_t < t1) {
+      long long x = first_g * one + before + incl - mine;
+      for (int t = t0; t < first_t; ++t) x += job_weight(p.tiles[t].n_tok, p.tiles[t].n_pg);
+      s_scan[24] = x;
+    }
+    __syncthreads();
+    for (int i = 0; i < warp && i < 8; ++i) upto += s_scan[16 + i];
+    if (tid <= G && tid <= kPrefillCtas) s_range[tid] = s_scan[24] + upto - left;
+    if (tid == 0) {
+      s_scan[25] = total > 0 ? G : 0;
+      s_scan[26] = whole;
+    }
+    __syncthreads();
     if (total > 0 && (int)blockIdx.x < G) {
-      // the jobs that hold the range's first and last weight, if they are among this thread's tiles
+      // the jobs that hold the first and the last weight of the CTA's range, if they are among this thread's tiles
 #pragma unroll 1
       for (int end = 0; end < 2; ++end) {
-        const long long at = range_start(total / G, (int)(total % G), (int)blockIdx.x + end) - end;
-        const long long in = at % one;
+        const long long at = s_range[blockIdx.x + end] - end;
+        const int g = (int)quot(at, one);
+        const long long in = at - g * one;
         long long x = before + incl - mine;
         if (mine > 0 && in >= x && in < x + mine) {
           int t = t0;
@@ -600,17 +637,15 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
             if (in < x + w) break;
             x += w;
           }
-          s_scan[25 + 2 * end] = (at / one) * n_tiles + t;
-          s_scan[26 + 2 * end] = at - in + x;
+          s_scan[27 + 2 * end] = (long long)g << 32 | t;
+          s_scan[28 + 2 * end] = at - in + x;
         }
       }
     }
-    if (tid == 0) s_scan[24] = total;
     __syncthreads();
   }
-  const long long total = s_scan[24];
-  const int G = (int)min((long long)gridDim.x, max(1ll, total / kLeast));
-  const bool idle = (int)blockIdx.x >= G || total == 0;
+  const int G = (int)s_scan[25], whole = (int)s_scan[26];
+  const bool idle = (int)blockIdx.x >= G;
 
   // registers: 128 threads x 64 + 256 x 160 + 128 x 128 of the launch's 512 x 128
   if (warp < 4) {
@@ -620,26 +655,81 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
       int e = 0, k = 0;
       bool ok = true;
       if (!idle) {
-        const long long quota = total / G;
-        const int extra = (int)(total - quota * G);
-        const long long lo = range_start(quota, extra, blockIdx.x), hi = range_start(quota, extra, blockIdx.x + 1);
-        // A job that goes on in the next CTA's range comes first: its rows are then there long before the
-        // other parts' are, and are joined under other segments.
+        const long long lo = s_range[blockIdx.x], hi = s_range[blockIdx.x + 1];
+        auto tile = [&](int t) {
+          const int word = lane < 8 ? reinterpret_cast<const int*>(p.tiles + t)[lane] : 0;
+          TileRec r;
+          r.q0 = __shfl_sync(0xffffffffu, word, 0);
+          r.n_tok = __shfl_sync(0xffffffffu, word, 1);
+          r.pos = __shfl_sync(0xffffffffu, word, 2);
+          r.len = __shfl_sync(0xffffffffu, word, 3);
+          r.page0 = __shfl_sync(0xffffffffu, word, 4);
+          r.n_pg = __shfl_sync(0xffffffffu, word, 5);
+          r.ws_page = __shfl_sync(0xffffffffu, word, 6);
+          return r;
+        };
+        // the pages a .. z - 1 of a tile and KV head
+        auto segment = [&](const TileRec& r, int t, int g, int a, int z, int c0, int parts) {
+          if (!twait(bar(kBRecEmpty + k % kRecs), ((k / kRecs) & 1) ^ 1, wc)) return false;
+          if (lane == 0) {
+            SegRec* s = rec(k);
+            s->n_pg = z - a;
+            s->g = g;
+            s->q0 = r.q0;
+            s->n_tok = r.n_tok;
+            s->pos = r.pos;
+            s->len = r.len;
+            s->page0 = r.page0 + a;
+            s->part = (int)blockIdx.x - c0;
+            s->parts = parts;
+            s->c0 = c0;
+            s->job = t * kKvHeads + g;
+            if (parts > kInline && a == 0) p.big[atomicAdd(p.n_big, 1)] = make_int2(s->job, c0 | parts << 8);
+            mbar_arrive(bar(kBRecFull + k % kRecs));
+          }
+          __syncwarp();
+          ++k;
+          const uint8_t* image = p.images + ((size_t)(r.ws_page + a) * kKvHeads + g) * kImage;
+          for (int i0 = a; i0 < z; i0 += 32) {
+            const int cnt = min(32, z - i0);
+            const int there = lane < cnt ? p.page_ok[r.ws_page + i0 + lane] : 0;
+            for (int j = 0; j < cnt; ++j, ++e, image += kKvHeads * kImage) {
+              const int st = e % kStages, ph = ((e / kStages) & 1) ^ 1, good = __shfl_sync(0xffffffffu, there, j);
+              if (!twait(bar(kBEmpty + st), ph, wc)) return false;
+              if (lane == 0) {
+                s_info[e % kInfo] = good;
+                if (!(p.inject && e == 0)) {
+                  mbar_arrive_expect_tx(bar(kBFull + st), kImage);
+                  bulk_g2s(sbase + kOffK + st * kImage, image, kImage, bar(kBFull + st));
+                }
+                *s_issued = e + 1;
+              }
+              __syncwarp();
+            }
+          }
+          return true;
+        };
+        auto owner = [&](long long x) {  // the CTA whose range holds a weight
+          int c = 0;
+          for (int step = 128; step; step >>= 1)
+            if (c + step < G && s_range[c + step] <= x) c += step;
+          return c;
+        };
+        // The range of jobs that are cut comes first, and of these the one that goes on in the next CTA's
+        // range: the parts' rows are then written and joined under whole jobs.
         long long early = -1;
 #pragma unroll 1
-        for (int pass = 0; pass < 2; ++pass) {
-          long long off = s_scan[pass ? 26 : 28];
-          int g = (int)(s_scan[pass ? 25 : 27] / n_tiles), t = (int)(s_scan[pass ? 25 : 27] % n_tiles);
-          while (ok && off < hi && g < kKvHeads) {
-            const int word = lane < 8 ? reinterpret_cast<const int*>(p.tiles + t)[lane] : 0;
-            TileRec r;
-            r.q0 = __shfl_sync(0xffffffffu, word, 0);
-            r.n_tok = __shfl_sync(0xffffffffu, word, 1);
-            r.pos = __shfl_sync(0xffffffffu, word, 2);
-            r.len = __shfl_sync(0xffffffffu, word, 3);
-            r.page0 = __shfl_sync(0xffffffffu, word, 4);
-            r.n_pg = __shfl_sync(0xffffffffu, word, 5);
-            r.ws_page = __shfl_sync(0xffffffffu, word, 6);
+        for (int pass = 0; pass < 3; ++pass) {
+          const bool cut = pass < 2;
+          long long off = cut ? s_scan[pass ? 28 : 30] : 0;
+          int g = (int)(s_scan[pass ? 27 : 29] >> 32), t = (int)s_scan[pass ? 27 : 29];
+          for (int i = 0; ok && (cut ? off < hi && g < kKvHeads : i < whole); ++i) {
+            if (!cut) {
+              const int job = (int)blockIdx.x + i * G;
+              g = job / n_tiles;
+              t = job % n_tiles;
+            }
+            const TileRec r = tile(t);
             const int pw = page_weight(r.n_tok);
             // page i starts at weight base + i pw; it belongs to the range that holds its start
             const long long base = off + kFixed;
@@ -647,62 +737,17 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
               if (x <= base) return 0;
               return x - base > (long long)r.n_pg * pw ? r.n_pg : ((int)(x - base) + pw - 1) / pw;
             };
-            const int a = r.n_pg > 0 ? page_at(lo) : 0, z = r.n_pg > 0 ? page_at(hi) : 0;
-            const bool take = a < z && (pass ? off != early : z < r.n_pg);
-            if (take && pass == 0) early = off;
+            const int a = cut && r.n_pg > 0 ? page_at(lo) : 0, z = cut && r.n_pg > 0 ? page_at(hi) : r.n_pg;
+            const bool take = a < z && (pass ? !cut || off != early : z < r.n_pg);
+            if (take) {
+              if (pass == 0) early = off;
+              const int c0 = cut ? owner(base) : (int)blockIdx.x;
+              ok = segment(r, t, g, a, z, c0, cut ? owner(base + (long long)(r.n_pg - 1) * pw) - c0 + 1 : 1);
+            }
             off += job_weight(r.n_tok, r.n_pg);
-            const int job = t * kKvHeads + g, gg = g;
             if (++t == n_tiles) {
               t = 0;
               ++g;
-            }
-            if (!take) continue;
-            if (!twait(bar(kBRecEmpty + k % kRecs), ((k / kRecs) & 1) ^ 1, wc)) {
-              ok = false;
-              break;
-            }
-            if (lane == 0) {
-              // who has the page that starts at a weight (the first `extra` CTAs have one unit more)
-              const long long big = extra * (quota + 1);
-              auto owner = [&](long long x) { return x < big ? (int)(x / (quota + 1)) : extra + (int)((x - big) / quota); };
-              const int c0 = owner(base), parts = owner(base + (long long)(r.n_pg - 1) * pw) - c0 + 1;
-              SegRec* s = rec(k);
-              s->n_pg = z - a;
-              s->g = gg;
-              s->q0 = r.q0;
-              s->n_tok = r.n_tok;
-              s->pos = r.pos;
-              s->len = r.len;
-              s->page0 = r.page0 + a;
-              s->part = (int)blockIdx.x - c0;
-              s->parts = parts;
-              s->c0 = c0;
-              s->job = job;
-              if (parts > kInline && a == 0) p.big[atomicAdd(p.n_big, 1)] = make_int2(job, c0 | parts << 8);
-              mbar_arrive(bar(kBRecFull + k % kRecs));
-            }
-            __syncwarp();
-            ++k;
-            const uint8_t* image = p.images + ((size_t)(r.ws_page + a) * kKvHeads + gg) * kImage;
-            for (int i0 = a; ok && i0 < z; i0 += 32) {
-              const int cnt = min(32, z - i0);
-              const int there = lane < cnt ? p.page_ok[r.ws_page + i0 + lane] : 0;
-              for (int j = 0; j < cnt; ++j, ++e, image += kKvHeads * kImage) {
-                const int st = e % kStages, ph = ((e / kStages) & 1) ^ 1, good = __shfl_sync(0xffffffffu, there, j);
-                if (!twait(bar(kBEmpty + st), ph, wc)) {
-                  ok = false;
-                  break;
-                }
-                if (lane == 0) {
-                  s_info[e % kInfo] = good;
-                  if (!(p.inject && e == 0)) {
-                    mbar_arrive_expect_tx(bar(kBFull + st), kImage);
-                    bulk_g2s(sbase + kOffK + st * kImage, image, kImage, bar(kBFull + st));
-                  }
-                  *s_issued = e + 1;
-                }
-                __syncwarp();
-              }
             }
           }
         }
@@ -731,14 +776,14 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
       auto pv = [&](int set, int stage, uint32_t acc) {
         const uint32_t s = tmem + kTmemS + 128 * set;
         const uint64_t vdesc = vdesc0 + stage * (kImage >> 4);
-#pragma unroll kPvUnroll
+#pragma unroll 4
         for (int kk = 0; kk < 8; ++kk, acc = 1)  // 16 tokens each: 8 columns of P inside S's 32-column chunks
           umma_f16_ts(s + kTmemO - kTmemS, s + 32 * (kk >> 1) + 8 * (kk & 1), vdesc + kk * (256 >> 4), idesc_pv, acc);
       };
       auto qk = [&](int set, int stage, int k) {
         const uint32_t s = tmem + kTmemS + 128 * set;
         const uint64_t qdesc = qdesc0 + (2 * (k & 1) + set) * (16384 >> 4), kdesc = kdesc0 + stage * (kImage >> 4);
-#pragma unroll kQkUnroll
+#pragma unroll 2
         for (int kk = 0; kk < 4; ++kk)  // 32 channels each
           umma_e4m3(s, qdesc + 2 * kk, kdesc + kk * (4096 >> 4), idesc_qk, kk > 0);
         umma_commit(bar(kBSFull + set));
