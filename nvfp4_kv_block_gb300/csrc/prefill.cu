@@ -51,7 +51,8 @@ constexpr int kOffInfo = kOffRecs + kRecs * 64;           // int [kInfo]: page i
 constexpr int kOffScan = kOffInfo + kInfo * 4;            // long long [32]
 constexpr int kOffRange = kOffScan + 32 * 8;              // long long [kPrefillCtas + 1]
 constexpr int kOffMl = kOffRange + 160 * 8;                 // float2 [2 sets][2 parities][128]: a row's reference and sum
-constexpr int kOffBars = kOffMl + 2 * 2 * 128 * 8;
+constexpr int kOffJoin = (kOffMl + 2 * 2 * 128 * 8 + 1023) / 1024 * 1024;  // 4 output warps x [32 rows][64 B]
+constexpr int kOffBars = kOffJoin + 4 * 2048;
 constexpr int kBFull = 0, kBEmpty = kBFull + kStages, kBQFull = kBEmpty + kStages, kBQEmpty = kBQFull + 2,
               kBSFull = kBQEmpty + 2, kBPFull = kBSFull + 2, kBPvDone = kBPFull + 2, kBOFree = kBPvDone + 2, kBMl = kBOFree + 2, kBRecFull = kBMl + 4,  // kBMl: [set][parity]
               kBRecEmpty = kBRecFull + kRecs,
@@ -97,7 +98,7 @@ __device__ __forceinline__ size_t part_slot(int c0, int i) { return 2 * (c0 + i)
 static_assert(sizeof(SegRec) <= 64, "record slot");
 
 struct PrefillParams {
-  CUtensorMap out_map;  // out as [T][16][128], boxes of 8 tokens x 4 heads x 64 channels
+  CUtensorMap out_map, out_map32;  // out as [T][16][128], boxes of 8 tokens x 4 heads x 64 and 32 channels
   const uint8_t* kv_pool;
   int64_t n_pages;
   const uint8_t* q;  // [T][16][128]
@@ -329,6 +330,10 @@ __device__ __forceinline__ bool swait(uint32_t bar, uint32_t parity, const WaitC
     return ok != 0;
   };
   bool ok = poll();
+  if (ok) {
+    __syncwarp();
+    return true;
+  }
   if (!ok) {
     const unsigned long long t0 = globaltimer_ns();
     for (;;) {
@@ -404,22 +409,29 @@ __device__ __forceinline__ void bulk_read_wait() { asm volatile("cp.async.bulk.w
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // 32 channels (the c-th of four) of 32 rows, lane = row, on their way out: into a box of 64 channels x 4
-// heads x 8 tokens in shared memory (rows of 128 bytes, swizzled), which leaves with its second half.
+// heads x 8 tokens in shared memory (rows of 128 bytes, swizzled), which leaves with its second half, or
+// (kNarrow) into one of 32 channels.
+template <bool kNarrow>
 __device__ __forceinline__ void put32(const PrefillParams& p, const SegRec& r, const float (&o)[32], float inv, int c, int tok0,
                                       int lane, uint32_t stage) {
   uint32_t y[16];
 #pragma unroll
   for (int x = 0; x < 16; ++x) y[x] = pack16(o[2 * x] * inv, o[2 * x + 1] * inv, p.out_f16);
   if (tok0 + 8 <= r.n_tok) {
-    const uint32_t box = stage + (c >> 1) * 4096;
+    const uint32_t box = kNarrow ? stage : stage + (c >> 1) * 4096;
+    if (kNarrow) {
+      if (lane == 0) bulk_read_wait();
+      __syncwarp();
+    }
 #pragma unroll
     for (int x = 0; x < 4; ++x)
-      sts128(box + lane * 128 + (((4 * (c & 1) + x) ^ (lane & 7)) << 4), make_uint4(y[4 * x], y[4 * x + 1], y[4 * x + 2], y[4 * x + 3]));
-    if (c & 1) {
+      sts128(kNarrow ? box + lane * 64 + ((x ^ (lane >> 1 & 3)) << 4) : box + lane * 128 + (((4 * (c & 1) + x) ^ (lane & 7)) << 4),
+             make_uint4(y[4 * x], y[4 * x + 1], y[4 * x + 2], y[4 * x + 3]));
+    if (kNarrow || (c & 1)) {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        tensor_s2g(&p.out_map, 32 * (c - 1), kGqa * r.g, r.q0 + tok0, box);
+        tensor_s2g(kNarrow ? &p.out_map32 : &p.out_map, kNarrow ? 32 * c : 32 * (c - 1), kGqa * r.g, r.q0 + tok0, box);
         bulk_commit();
       }
     }
@@ -436,7 +448,8 @@ __device__ __forceinline__ void put_lse(const PrefillParams& p, const SegRec& r,
 }
 
 // A segment's part of a cut job (a warp's 32 rows from token tok0 on; own: a row's reference and sum): its
-// rows on their way to the part's place.  freed: called when the accumulator is read.
+// rows on their way to the part's place (zeros where a row saw nothing).  freed: called when the accumulator
+// is read.
 template <typename F>
 __device__ __forceinline__ void put_part(const PrefillParams& p, const SegRec& r, float2 own, int tok0, int lane, uint32_t t_o,
                                          uint32_t stage, F&& freed) {
@@ -448,6 +461,9 @@ __device__ __forceinline__ void put_part(const PrefillParams& p, const SegRec& r
     tmem_ld32x32b_x64(t_o + 64 * c, v);
     tmem_wait_ld();
     if (c) freed();
+    if (own.y == 0.f)
+#pragma unroll
+      for (int x = 0; x < 64; ++x) v[x] = 0;
     if (lane == 0) bulk_read_wait();
     __syncwarp();
 #pragma unroll
@@ -511,7 +527,7 @@ __device__ __forceinline__ void join_parts(const PrefillParams& p, const SegRec&
         }
       }
     }
-    put32(p, r, s, inv, c, tok0, lane, stage);
+    put32<true>(p, r, s, inv, c, tok0, lane, stage);
   }
 }
 
@@ -913,6 +929,12 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
         start = (p.window ? max(0, pos + 1 - p.window) : 0) - r.page0 * kPageTokens;
         end = (p.ends ? min(max(p.ends[r.q0 + token], 0), r.len) : pos + 1) - r.page0 * kPageTokens;
       }
+      // (a row that sees nothing is weighed as if it saw all, so that its warp's pages need no masks; its sum is 0)
+      const bool none = end <= start;
+      if (none) {
+        start = 0;
+        end = 0x7FFFFFFF;
+      }
       float shift = kUnset, l = 0.f;  // kBias less the reference, and the sum of weights
       bool ok = true;
       for (const uint32_t e0 = e; e - e0 < (uint32_t)r.n_pg; ++e) {
@@ -928,8 +950,9 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
 #pragma unroll 1
             for (int c = 0; c < kPageTokens; c += 32) {
               uint32_t v[32];
-              tmem_ld32x32b_x32(t_s + c, v);
               const uint32_t vis = low_bits(hi - c) & ~low_bits(start - c);
+              if (__all_sync(0xffffffffu, vis == 0xFFFFFFFFu)) continue;
+              tmem_ld32x32b_x32(t_s + c, v);
               tmem_wait_ld();
 #pragma unroll
               for (int x = 0; x < 32; ++x) v[x] = vis >> x & 1 ? v[x] : 0xFF800000u;
@@ -1002,10 +1025,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBPFull + set));
         start -= kPageTokens;
-        if (mine) end -= kPageTokens;
+        if (mine && !none) end -= kPageTokens;
       }
       if (!ok) break;
-      reinterpret_cast<float2*>(smem + kOffMl)[256 * set + 128 * (segs & 1) + lrow] = make_float2(kBias - shift, l);
+      reinterpret_cast<float2*>(smem + kOffMl)[256 * set + 128 * (segs & 1) + lrow] = make_float2(kBias - shift, none ? 0.f : l);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBMl + 2 * set + (segs & 1)));
       ++segs;
@@ -1058,22 +1081,22 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
             if (c == 3) freed();
             float o[32];
 #pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] = __uint_as_float(v[x]);
-            put32(p, r, o, inv, c, tok0, lane, stage);
+            for (int x = 0; x < 32; ++x) o[x] = own.y != 0.f ? __uint_as_float(v[x]) : 0.f;
+            put32<false>(p, r, o, inv, c, tok0, lane, stage);
           }
           put_lse(p, r, own.x, own.y, tok0, lane);
         }
       }
-      if (ok && r.parts > 1 && r.parts <= kInline)
-#pragma unroll 1
-        for (int set = 0; set < 2; ++set)
-          if (32 * set + 8 * quad < r.n_tok) join_parts(p, r, 32 * set + 8 * quad, lane, stage);
       // (the tiles may be written again)
       if (lane == 0) {
         bulk_read_wait();
         mbar_arrive(bar(kBQEmpty + (k & 1)));
       }
       __syncwarp();
+      if (ok && r.parts > 1 && r.parts <= kInline)
+#pragma unroll 1
+        for (int set = 0; set < 2; ++set)
+          if (32 * set + 8 * quad < r.n_tok) join_parts(p, r, 32 * set + 8 * quad, lane, sbase + kOffJoin + quad * 2048);
     }
     if (lane == 0) bulk_wait();
     __syncwarp();
@@ -1161,15 +1184,15 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const __grid_constan
 
 int prefill_quads(int n_q_total) { return (kGqa * std::min(n_q_total, kTileTokens) + 31) / 32; }
 int prefill_tiles(int n_q_total, int n_seqs) { return n_q_total / kTileTokens + std::min(n_q_total, n_seqs); }
-bool make_out_map(CUtensorMap* m, void* out, int n_q_total) {
+bool make_out_map(CUtensorMap* m, void* out, int n_q_total, cuuint32_t channels) {
   const auto fn = tensor_map_encoder();
   if (!fn) return false;
   const cuuint64_t dims[3] = {kHeadDim, kQHeads, (cuuint64_t)n_q_total};
   const cuuint64_t strides[2] = {kHeadDim * 2, kQHeads * kHeadDim * 2};
-  const cuuint32_t box[3] = {64, kGqa, 8}, steps[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {channels, kGqa, 8}, steps[3] = {1, 1, 1};
   // (16-bit words whatever their type)
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, out, dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            channels == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 size_t padded(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -1213,7 +1236,7 @@ cudaError_t launch_prefill_attn(const msa_cache* c, const uint8_t* q, float soft
   pp.out_scale = 256.0f / c->s_enc_v;
   pp.out_f16 = dtype == MSA_DTYPE_F16;
   pp.out = static_cast<uint16_t*>(out);
-  if (!make_out_map(&pp.out_map, out, n_q_total)) return cudaErrorInvalidValue;
+  if (!make_out_map(&pp.out_map, out, n_q_total, 64) || !make_out_map(&pp.out_map32, out, n_q_total, 32)) return cudaErrorInvalidValue;
   pp.lse = lse;
   pp.part_quads = prefill_quads(n_q_total);
   pp.max_tiles = prefill_tiles(n_q_total, n_seqs);
