@@ -522,17 +522,20 @@ size_t msa_tree_attn_workspace_bytes(int32_t n_q_total);
  *               their first token sees to their last, summed over the call, at most (the
  *               sum of ceil(seq_lens[b] / 128) always will do).  A sequence behind that
  *               many sets MSA_STATUS_BAD_SEQ and keeps its rows.
- *   dtype, out, lse as msa_tree_attn.
+ *   dtype, out, lse as msa_tree_attn; out on a 32-byte boundary.
  *   ws, ws_bytes scratch of at least msa_prefill_workspace_bytes(n_q_total, n_seqs,
  *               n_visited) bytes, 16-byte aligned, nothing of which is kept between calls.
  *               Calls sharing a workspace must not overlap on the GPU.
  * Rows behind the last sequence, and those of an inconsistent one (MSA_STATUS_BAD_SEQ),
  * are left as they were.  Operands, sums and special values as msa_tree_attn; the weights
- * are rounded to f16 once (2^-11 relative, or 2^-33 of the weight at the row's reference).
- * Rows are summed in an order that depends on the call's sizes only.
+ * are rounded to f16 (2^-11 relative, or 2^-33 of the weight at the row's reference) once,
+ * those of the first 64 tokens of a page once more where the page's others move the row's
+ * reference.  Rows are summed in an order that depends on the call's sizes and the device's
+ * SMs only.
  * softmax_scale > 0 and at most 2^26 s_enc_k / (448 * 448 * 128 log2(e)); s_enc_v above
  * 2^-120 and at most 2^100.  Limits: n_seqs <= 4096, n_q_total <= 262,144, n_visited <=
- * 1,048,576.  Three launches, programmatic dependents of the kernel before them.
+ * 1,048,576.  Three launches (two, when n_visited is small), programmatic dependents of
+ * the kernel before them.
  */
 int msa_prefill_attn(const msa_cache* cache, const uint8_t* q, int32_t n_q_heads, float softmax_scale,
                      const int32_t* block_table, int32_t max_pages, const int32_t* seq_lens,
@@ -649,8 +652,8 @@ int msa_copy_pages(const msa_cache* layers, int32_t n_layers, const int32_t* src
  * Pages behind the new length stay in the row, for later tokens.  An inconsistent
  * sequence keeps its length (MSA_STATUS_BAD_SEQ); a token whose page or whose new
  * place's page is outside the pool is not moved (MSA_STATUS_BAD_PAGE).  Status bits go to
- * layers[0].status.  The pages of drafts must not be shared with other sequences of the
- * call (forks share full pages only).
+ * layers[0].status.  The pages of drafts must not be shared: a fork comes before the drafts
+ * or behind their commit (one made between shares the full pages among them).
  */
 int msa_commit_drafts(const msa_cache* layers, int32_t n_layers, const int32_t* block_table, int32_t max_pages,
                       const int32_t* seq_lens, const int32_t* q_start_loc, int32_t n_seqs, const uint64_t* accepted,

@@ -723,7 +723,8 @@ class PrefillBuffers:
     the last sequence stay as they were), up to n_seqs sequences and n_pages pages of their
     contexts (the sum of ceil(seq_len / 128), or of those within the window): out [n_q_total,
     16, 128] in ``dtype`` (bf16 or fp16), lse [n_q_total, 16], and 196,608 bytes of scratch a
-    page.  ``ws``: scratch of other buffers, to share it between layers or steps."""
+    page.  ``ws``: scratch of other buffers, to share it between layers or steps (calls that
+    share it must not overlap on the GPU)."""
 
     def __init__(self, n_q_total, n_seqs, n_pages, dtype=torch.bfloat16, device="cuda", ws=None):
         if dtype not in (torch.bfloat16, torch.float16):
@@ -746,6 +747,8 @@ def prefill_attn(cache, q, block_table, seq_lens, q_start_loc, bufs, window=0, e
     n_seqs, max_pages = block_table.shape
     if n_seqs > bufs.n_seqs:
         raise ValueError(f"bufs are for up to {bufs.n_seqs} sequences")
+    if not 0 <= window < 1 << 31:
+        raise ValueError(f"a window is 0 or a number of tokens, not {window}")
     dev = _device_of(cache)
     _check(lib().msa_prefill_attn(
         cache.packed(), _arg(q, torch.uint8, (T, Q_HEADS, HEAD_DIM), dev, "q"), Q_HEADS,
@@ -785,7 +788,9 @@ _POOL = struct.Struct("@PPiP")
 class PagePool:
     """Counts of the block-table entries that hold each of n_pages pages: ``refs`` int32
     [n_pages], and the free ones' mask, which the calls below keep in step (refs is read,
-    not written, by anyone else).  ``status``: int32 [1] word of sticky STATUS_* bits."""
+    not written, by anyone else).  Calls on one pool must not overlap on the GPU: one stream,
+    or streams that wait for one another.  ``status``: int32 [1] word of sticky STATUS_*
+    bits."""
 
     def __init__(self, n_pages, status=None, device="cuda"):
         self._set(torch.zeros(int(n_pages), dtype=torch.int32, device=device), status)
@@ -885,7 +890,8 @@ def commit_drafts(layers, block_table, seq_lens, q_start_loc, accepted, new_lens
     """Of each sequence's last q_start_loc[b + 1] - q_start_loc[b] tokens (drafts that
     tree_attn verified) those whose bits ``accepted`` (int64 [B]) has move together behind
     its context, in every layer.  Returns the new lengths (``new_lens`` or a new tensor,
-    never seq_lens itself); the row keeps its pages."""
+    never seq_lens itself); the row keeps its pages.  A fork of a sequence comes before its
+    drafts or behind their commit: its full pages are shared."""
     layers = CacheLayers.of(layers)
     dev = seq_lens.get_device()
     _same_device(layers, dev)

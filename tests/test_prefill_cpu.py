@@ -2,6 +2,10 @@
 
 import ctypes
 
+import pytest
+import torch
+
+from nvfp4_kv_block_gb300 import ops
 from test_abi_cpu import _cache, lib  # noqa: F401
 
 P = ctypes.c_void_p
@@ -31,3 +35,15 @@ def test_prefill_is_checked_on_the_host(lib):  # noqa: F811
     assert large - small in range(4 * 49152, 4 * 49152 + 257) and lib.msa_prefill_workspace_bytes(0, 1, 1) == 256
     off = _cache(kv_pool=168, idx_pool=160, n_pages=4)
     assert lib.msa_prefill_attn(ctypes.byref(off), FAKE, 16, 0.1, FAKE, 4, FAKE, FAKE, 1, 0, 0, None, 8, 1, FAKE, None, FAKE, 1 << 40, None) == -1
+
+
+@pytest.mark.parametrize("window", [-1, 1 << 31, (1 << 32) + 5])
+def test_a_window_is_a_number_of_tokens(lib, window):  # noqa: F811
+    bufs = ops.PrefillBuffers(3, 1, 2, device="cpu")
+    table = torch.zeros(1, 2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="window"):
+        ops.prefill_attn(None, None, table, None, None, bufs, window=window)
+    with pytest.raises(ValueError, match="sequences"):
+        ops.prefill_attn(None, None, table.expand(2, 2), None, None, bufs)
+    with pytest.raises(TypeError):
+        ops.PrefillBuffers(3, 1, 2, torch.float32, device="cpu")
