@@ -12,6 +12,13 @@
 // the mask (a bit a page: 61,440 pages are 7.5 KB, where their counts are 240 KB), finds the
 // first free pages by a scan over the words' bit counts and writes tables and slots.  Bytes
 // of tokens move in a second, wide launch, the bytes of the tokens that exist only.
+//
+// Every kernel is a programmatic dependent of the one before it and lets the next begin
+// launching at once; it touches memory behind pdl_wait only (release, fork and extension of
+// 256 rows, 43.8 us a round; 49.8 with plain launches).  On the GPU the round takes 3.4 for
+// the release, 8 for the plan, 28 for the copies (12 layers, 246 MB read and written, 8.8 TB/s: partly
+// from L2) and 7.5 for the extension: three chains of a few dependent loads and one launch bound
+// by memory.  A commit of 8 x 8 drafts takes 2.4 us, of 64 x 64 in 12 layers 6 to 7.5 (9.8 MB).
 #include "common.cuh"
 
 namespace msa {
@@ -114,6 +121,8 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const __grid_const
   int* s_len = s_start + kMaxSeqs + 1;      // [n_seqs] tokens before, or -1: no page was left or no sequence
   int* s_warp = s_len + kMaxSeqs + 1;
   const int tid = threadIdx.x;
+  pdl_wait();
+  pdl_trigger();
   // sequences per * tid ..: what each is short of
   const int per = (p.n_seqs + kPlanThreads - 1) / kPlanThreads;
   int need[kOwnSeqs], mine = 0;
@@ -199,6 +208,7 @@ struct ForkParams {
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const __grid_constant__ ForkParams p) {
   __shared__ int list[kMaxSeqs], claim[kMaxSeqs], s_warp[32];
   const int tid = threadIdx.x;
+  pdl_wait();
   pdl_trigger();
   for (int i = tid; i < p.n_seqs; i += kPlanThreads) claim[i] = 0x7FFFFFFF;
   __syncthreads();
@@ -312,8 +322,9 @@ __device__ __forceinline__ void copy_page_part(const LayerPools& l, int layer, i
 // Grid: (pair, 1 + layer and part); y = 0: the target's row of the table and the counts of the pages it shares.
 __global__ void __launch_bounds__(kCopyThreads) fork_copy_kernel(const __grid_constant__ ForkParams p) {
   const int x = blockIdx.x, y = (int)blockIdx.y - 1;
-  const int src = p.src[x], dst = p.dst[x];
   pdl_wait();
+  pdl_trigger();
+  const int src = p.src[x], dst = p.dst[x];
   const int4 plan = p.plan[x];
   if (plan.x < 0) return;
   if (y >= 0) {
@@ -347,6 +358,8 @@ struct ReleaseParams {
   const int* rows;
 };
 __global__ void __launch_bounds__(kCopyThreads) release_kernel(const __grid_constant__ ReleaseParams p) {
+  pdl_wait();
+  pdl_trigger();
   const int b = p.rows[blockIdx.x];
   if (b < 0 || b >= p.n_seqs) {
     if (threadIdx.x == 0) set_status(p.pool.status, MSA_STATUS_BAD_SEQ);
@@ -380,6 +393,8 @@ struct CopyParams {
   int* status;
 };
 __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_constant__ CopyParams p) {
+  pdl_wait();
+  pdl_trigger();
   const int from = p.src[blockIdx.x], to = p.dst[blockIdx.x];
   if (from < 0 || to < 0 || from == to) return;
   const int tokens = p.tokens ? p.tokens[blockIdx.x] : kPageTokens;
@@ -409,6 +424,8 @@ __global__ void __launch_bounds__(kCopyThreads) commit_kernel(const __grid_const
   __shared__ int s_from[64], s_to[64];  // slots of the tokens that move: page * 128 + offset
   __shared__ int64_t s_page[2][64];
   const int b = blockIdx.x, part = blockIdx.y % kParts, layer = blockIdx.y / kParts, tid = threadIdx.x;
+  pdl_wait();
+  pdl_trigger();
   const SeqInfo s = load_seq(b, p.seq_lens, p.q_start_loc, p.max_pages, 0x7FFFFFFF);
   const bool lead = blockIdx.y == 0;
   if (!s.ok || s.n_q > MSA_TREE_MAX_DRAFTS) {
@@ -514,8 +531,7 @@ cudaError_t launch_extend(const msa_page_pool* pool, int* block_table, int max_p
   });
   if (e != cudaSuccess) return e;
   const ExtendParams p{pool_of(pool), block_table, max_pages, seq_lens, q_start_loc, n_seqs, n_tokens, slots};
-  extend_kernel<<<1, kPlanThreads, kExtendSmem, stream>>>(p);
-  return cudaGetLastError();
+  return launch_pdl(extend_kernel, dim3(1), dim3(kPlanThreads), kExtendSmem, stream, p);
 }
 
 cudaError_t launch_fork(const msa_cache* layers, int n_layers, const msa_page_pool* pool, int* block_table,
@@ -524,8 +540,7 @@ cudaError_t launch_fork(const msa_cache* layers, int n_layers, const msa_page_po
   if (n == 0) return cudaSuccess;
   const ForkParams p{pool_of(pool), block_table, max_pages, seq_lens, n_seqs, src, dst, n, static_cast<int4*>(ws),
                      layer_pools(layers, n_layers)};
-  fork_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_pdl(fork_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
   if (e != cudaSuccess) return e;
   return launch_pdl(fork_copy_kernel, dim3(n, 1 + n_layers * kParts), dim3(kCopyThreads), 0, stream, p);
 }
@@ -534,16 +549,14 @@ cudaError_t launch_release(const msa_page_pool* pool, int* block_table, int max_
                            const int* rows, int n, cudaStream_t stream) {
   if (n == 0) return cudaSuccess;
   const ReleaseParams p{pool_of(pool), block_table, max_pages, seq_lens, n_seqs, rows};
-  release_kernel<<<n, kCopyThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_pdl(release_kernel, dim3(n), dim3(kCopyThreads), 0, stream, p);
 }
 
 cudaError_t launch_copy_pages(const msa_cache* layers, int n_layers, const int* src, const int* dst, const int* tokens,
                               int n, cudaStream_t stream) {
   if (n == 0) return cudaSuccess;
   const CopyParams p{layer_pools(layers, n_layers), src, dst, tokens, layers[0].status};
-  copy_pages_kernel<<<dim3(n, n_layers * kParts), kCopyThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_pdl(copy_pages_kernel, dim3(n, n_layers * kParts), dim3(kCopyThreads), 0, stream, p);
 }
 
 cudaError_t launch_commit(const msa_cache* layers, int n_layers, const int* block_table, int max_pages,
@@ -552,8 +565,7 @@ cudaError_t launch_commit(const msa_cache* layers, int n_layers, const int* bloc
   if (n_seqs == 0) return cudaSuccess;
   const CommitParams p{layer_pools(layers, n_layers), block_table, max_pages, seq_lens, q_start_loc,
                        reinterpret_cast<const unsigned long long*>(accepted), new_lens, layers[0].status};
-  commit_kernel<<<dim3(n_seqs, n_layers * kParts), kCopyThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_pdl(commit_kernel, dim3(n_seqs, n_layers * kParts), dim3(kCopyThreads), 0, stream, p);
 }
 
 }  // namespace msa

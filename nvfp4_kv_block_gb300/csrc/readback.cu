@@ -5,9 +5,10 @@
 // of its 16 channels and r = fl(1 / s_enc) the tensor's decode factor; the
 // product is rounded to fp32 and then to the output type.  Index keys are E4M3
 // values.  704 bytes in and 1,152 values out per token.  Whole pages are bound by memory
-// (131,072 tokens in bf16: 76 us, 5.2 TB/s of those bytes), scattered slots by latency, a
+// (131,072 tokens in bf16: 74 us, 5.3 TB/s of those bytes), scattered slots by latency, a
 // chain of slot, scales, codes and store with no rate near its end (20,011 tokens in fp32:
-// 25 us, 4.2 TB/s, DRAM at 25 % and issue slots at 29 %; 16,384 in bf16: 18 us, 2.7 TB/s).
+// 23 us, 4.6 TB/s, DRAM at 25 % and issue slots at 29 %; 16,384 in bf16: 18 us, 2.7 TB/s).
+// A programmatic dependent, as the rotary insert (2 us less a call, one after the other).
 //
 // A warp takes one KV head's K or V (or the index key) of a tile of tokens, four
 // tokens at a time: eight lanes a row, lane l its channels 16l .. 16l + 15: two
@@ -97,6 +98,8 @@ __device__ __forceinline__ void decode_word(uint32_t w, float d, float* x) {
 template <typename T>
 __global__ void __launch_bounds__(kReadThreads) read_kv_kernel(const __grid_constant__ ReadParams p) {
   const int lane = threadIdx.x & 31, l = lane & 7, sub = lane >> 3;
+  pdl_wait();
+  pdl_trigger();
   const long long n_jobs = (long long)((p.n_tokens + p.tile - 1) / p.tile) * 9;
   const long long job0 = ((long long)blockIdx.x * kReadThreads + threadIdx.x) >> 5;
   const long long step = ((long long)gridDim.x * kReadThreads) >> 5;
@@ -176,10 +179,8 @@ cudaError_t launch_read_kv(const msa_cache* c, const int64_t* slot_mapping, int 
   long long blocks = (warps + kReadThreads / 32 - 1) / (kReadThreads / 32);
   if (blocks > 64ll * n_sm) blocks = 64ll * n_sm;
   const dim3 grid((unsigned)blocks), block(kReadThreads);
-  if (dtype == MSA_DTYPE_F32) read_kv_kernel<float><<<grid, block, 0, stream>>>(rp);
-  else if (dtype == MSA_DTYPE_BF16) read_kv_kernel<__nv_bfloat16><<<grid, block, 0, stream>>>(rp);
-  else read_kv_kernel<__half><<<grid, block, 0, stream>>>(rp);
-  return cudaGetLastError();
+  return launch_pdl(dtype == MSA_DTYPE_F32 ? read_kv_kernel<float> : dtype == MSA_DTYPE_BF16 ? read_kv_kernel<__nv_bfloat16> : read_kv_kernel<__half>,
+                    grid, block, 0, stream, rp);
 }
 
 }  // namespace msa
