@@ -15,7 +15,8 @@
 // is a tile (256 rows, 4 i + h for token i and head h of the group) and a KV head; the jobs'
 // pages in a row are cut into equal weighted ranges, one per persistent CTA.  A job that was cut
 // leaves fp32 rows, which the last of its parts joins in the order of the parts (each warp for
-// its rows, behind a counter).  (3) Jobs in more than kInline parts are joined by a kernel of their own.
+// its rows, behind a counter).  (3) Jobs in more parts, and those of calls without whole jobs, are joined by a
+// kernel of their own.
 //
 // Roles of the attention's warps, all hand-offs mbarriers with bounded waits:
 //   warp 0      segment records, a bulk copy of 16 KB and one of 32 KB per page;
@@ -24,6 +25,16 @@
 //   warp 2      query rows of the next segment;
 //   warps 4-11  softmax, thread = row: a set of four warps for each 128 rows;
 //   warps 12-15 rows of finished segments on their way out.
+//
+// What bounds it.  A page of two row tiles is 1,536 cycles of the tensor pipe (PV 512 and QK 256 each) and
+// takes about 2,330: a set's chain is its softmax (850 cycles for 128 keys), the hand-over of the weights
+// (290), PV and the next QK into the same columns (820), the hand-over of the scores (400), and the two
+// sets run half a period apart.  Two tiles of scores and two accumulators are all of tensor memory, so there is no
+// third one to fill the gaps.  2,048 tokens over 131,072: 1,095 us, 2.02 PFLOP/s (1.90 is the measured bf16 rate; at
+// that rate for PV and twice it for QK the products alone take 877); 8,192 from the beginning: 162 us, the products 109;
+// 4,096 with a window of 4,096: 97, 55.  Tiles of 64 tokens x 4 heads: a page's 48 KB then feed two products
+// of 128 rows, 21 bytes a cycle and SM from L2.  100 tokens: 17 to 19 us, two launches and a chain of some
+// thirty latencies.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -67,12 +78,24 @@ constexpr float kMost = 49152.0f;  // largest sum of 64 weights, and so largest 
 constexpr float kUnset = 3e38f;           // shift of a row without a reference
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// Weights of the partition: a page of a tile of up to 32 tokens and of one of up to 64, the fixed
-// part of a job, and the least share of a CTA (a page's weight at least, so that every CTA
-// between a job's first and last has pages of it).
-constexpr int kPage1 = 9, kPage2 = 9, kFixed = 16, kSmall = 45, kLeast = 10;
+// Weights of the partition: a page of a tile of up to 32 tokens and of one of up to 64 (one set's chain
+// takes as long as two sets': 2,330 cycles); the fixed part of a job, records, queries and the rows' way out
+// (16: 8,192 tokens 170 us, 159 with 24, 165 with 40; 14 other calls, geometric mean, 62.3, 59.7, and 20 to 32 alike);
+// the least weight of a job (one of a page or two takes as long as five: the chain of its first scores and of its rows'
+// way out); and the least share of a CTA (a page's weight at least, so that every CTA between a job's first and
+// last has pages of it).
+constexpr int kPage1 = 9, kPage2 = 9, kFixed = 24, kSmall = 45, kLeast = 10;
 
-constexpr int kInline = 6;  // parts of a job that its last one joins
+// Jobs stay whole if the CTA with most then has no more than an equal share and kCut: parts cost their rows'
+// way to memory and back, some 16,000 cycles, with nothing under it at a call's end.  The same 14 calls: 59.0 us where
+// all is cut, 54.7 with 30, 51.8 with 100, 52.6 with 150 (sequences of 69 to 126 tokens: 36.8 and 24.4).
+constexpr int kCut = 100;
+
+// Parts of a job that its last one joins: under other jobs' pages where CTAs have whole jobs behind the cut ones
+// (up to 6; with a window of 4,096 97 us, 100 with 2 parts at most and the third kernel for the others), none where
+// they have not: the third kernel's many CTAs read the parts at once (45 us against 31 for sequences of 5 to
+// 110 tokens over 1,943).
+constexpr int kInline = 6, kAlone = 1;
 
 struct TileRec {
   int q0, n_tok;  // rows of the call
@@ -92,6 +115,7 @@ struct SegRec {
   int part, parts;  // which part of the job the segment is, and of how many
   int c0;           // CTA of part 0
   int job;
+  int join;  // the last part joins them
 };
 // Place of part i of a job whose first part is CTA c0's: a CTA's last segment, then first ones.
 __device__ __forceinline__ size_t part_slot(int c0, int i) { return 2 * (c0 + i) + (i == 0); }
@@ -134,6 +158,9 @@ struct PrefillParams {
 };
 
 // ---- (1) conversion and tiles -------------------------------------------------------
+// Once a call and not in every tile's CTA: a page of 8,192 tokens' prompt is seen by up to 128 tiles, and converting
+// it costs 2,000 warp instructions a head each time.  18 KB in, 48 KB out per page and head; a call more of it
+// takes 6 us for 64 pages, 47 for 1,040 (6.0 TB/s of those bytes, a part of which stays in L2 for the attention).
 constexpr int kConvThreads = 256;
 constexpr int kConvKCopies = 4, kConvVCopies = 8;
 constexpr int kConvTables = 128 * (8 * kConvKCopies + 16 * kConvVCopies);
@@ -542,7 +569,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
   const WaitCtl wc{s_abort, p.wait_ns};
   auto rec = [&](int k) { return reinterpret_cast<SegRec*>(smem + kOffRecs + 64 * (k % kRecs)); };
   int* s_info = reinterpret_cast<int*>(smem + kOffInfo);
-  // [24] warp sums; 24: start of the cut jobs, CTAs, whole jobs of each, first cut job, its start, last one, its start
+  // [24] warp sums; 24: start of the cut jobs, CTAs, whole jobs of each (-1: all), first cut job, its start, last one, its start
   long long* s_scan = reinterpret_cast<long long*>(smem + kOffScan);
   long long* s_range = reinterpret_cast<long long*>(smem + kOffRange);  // [CTAs + 1] starts of the CTAs' ranges of the cut jobs
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -603,15 +630,17 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
     const long long total = kKvHeads * one;
     const int n_jobs = kKvHeads * n_tiles, G = (int)min((long long)gridDim.x, max(1ll, quot(total, kLeast)));
     const long long quota = quot(total, G);
-    // Whole jobs c, c + G, ... of CTA c: as many rounds as leave every CTA a share of the cut ones
     auto weight = [&](int job) {
       const TileRec* r = p.tiles + job % n_tiles;
       return job_weight(r->n_tok, r->n_pg);
     };
+    // Whole jobs c, c + G, ... of CTA c: all, or as many rounds as leave every CTA a share of the cut ones
     int whole = total > 0 ? n_jobs / G : 0;
     long long w = 0;
     if (tid < G)
       for (int i = 0; i < whole; ++i) w += weight(tid + i * G);
+    const int rest = tid < G && tid + whole * G < n_jobs ? weight(tid + whole * G) : 0;
+    const bool cut = __syncthreads_or(w + rest > quota + kCut);
     while (__syncthreads_or(whole > 0 && tid < G && w + kLeast > quota)) {
       --whole;
       if (tid < G) w -= weight(tid + whole * G);
@@ -634,11 +663,11 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
     for (int i = 0; i < warp && i < 8; ++i) upto += s_scan[16 + i];
     if (tid <= G && tid <= kPrefillCtas) s_range[tid] = s_scan[24] + upto - left;
     if (tid == 0) {
-      s_scan[25] = total > 0 ? G : 0;
-      s_scan[26] = whole;
+      s_scan[25] = total == 0 ? 0 : cut ? G : min(G, n_jobs);
+      s_scan[26] = cut ? whole : -1;
     }
     __syncthreads();
-    if (total > 0 && (int)blockIdx.x < G) {
+    if (total > 0 && cut && (int)blockIdx.x < G) {
       // the jobs that hold the first and the last weight of the CTA's range, if they are among this thread's tiles
 #pragma unroll 1
       for (int end = 0; end < 2; ++end) {
@@ -700,7 +729,9 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
             s->parts = parts;
             s->c0 = c0;
             s->job = t * kKvHeads + g;
-            if (parts > kInline && a == 0) p.big[atomicAdd(p.n_big, 1)] = make_int2(s->job, c0 | parts << 8);
+            const int most = whole > 0 ? kInline : kAlone;
+            s->join = parts > 1 && parts <= most;
+            if (parts > most && a == 0) p.big[atomicAdd(p.n_big, 1)] = make_int2(s->job, c0 | parts << 8);
             mbar_arrive(bar(kBRecFull + k % kRecs));
           }
           __syncwarp();
@@ -735,11 +766,12 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
         // range: the parts' rows are then written and joined under whole jobs.
         long long early = -1;
 #pragma unroll 1
-        for (int pass = 0; pass < 3; ++pass) {
+        for (int pass = whole < 0 ? 2 : 0; pass < 3; ++pass) {
           const bool cut = pass < 2;
+          const int mine = whole >= 0 ? whole : (kKvHeads * n_tiles - (int)blockIdx.x + G - 1) / G;
           long long off = cut ? s_scan[pass ? 28 : 30] : 0;
           int g = (int)(s_scan[pass ? 27 : 29] >> 32), t = (int)s_scan[pass ? 27 : 29];
-          for (int i = 0; ok && (cut ? off < hi && g < kKvHeads : i < whole); ++i) {
+          for (int i = 0; ok && (cut ? off < hi && g < kKvHeads : i < mine); ++i) {
             if (!cut) {
               const int job = (int)blockIdx.x + i * G;
               g = job / n_tiles;
@@ -1093,7 +1125,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
         mbar_arrive(bar(kBQEmpty + (k & 1)));
       }
       __syncwarp();
-      if (ok && r.parts > 1 && r.parts <= kInline)
+      if (ok && r.join)
 #pragma unroll 1
         for (int set = 0; set < 2; ++set)
           if (32 * set + 8 * quad < r.n_tok) join_parts(p, r, 32 * set + 8 * quad, lane, sbase + kOffJoin + quad * 2048);
@@ -1265,8 +1297,8 @@ cudaError_t launch_prefill_attn(const msa_cache* c, const uint8_t* q, float soft
   if (e != cudaSuccess) return e;
   e = launch_pdl(prefill_attn_kernel, dim3(std::min(n_sm, kPrefillCtas)), dim3(kPrefillThreads), kPrefillSmem, stream, pp);
   if (e != cudaSuccess) return e;
-  // no job has more than kInline parts if its pages weigh no more than the least shares of so many CTAs
-  if (kFixed + (long long)n_visited * kPage2 <= (kInline - 1) * kLeast) return cudaSuccess;
+  // (a job has no more parts than pages)
+  if (n_visited <= kAlone) return cudaSuccess;
   return launch_pdl(prefill_merge_kernel, dim3(4 * std::min(n_sm, kPrefillCtas)), dim3(256), 0, stream, pp);
 }
 

@@ -193,6 +193,25 @@ def test_many_prompts():
     assert cache.read_status() == 0
 
 
+BATCHES = {  # jobs of 64 tokens x a KV head: fewer or more than SMs, alike or one far longer than the others
+    "short_alike": [(90, 64)] * 70,
+    "one_to_each": [(500, 60)] * 30,
+    "some_twice": [(1000, 64)] * 40,
+    "cut_behind_whole_ones": [(1500, 64)] * 45,
+    "one_far_longer": [(50, 64)] * 45 + [(9000, 64)],
+    "a_few_long": [(6000, 50), (3000, 64)],
+}
+
+
+@pytest.mark.parametrize("name", BATCHES)
+def test_batches_that_share_out_differently(name):
+    b = Prompts(BATCHES[name], 50)
+    out, lse, cache = b.go(BF16)
+    n = len(b.seqs)
+    b.same(out, lse, BF16, only={0, 1, n // 2, n - 1})
+    assert cache.read_status() == 0 and torch.isfinite(out).all()
+
+
 @pytest.mark.parametrize("ctx,n,window", [(0, 5000, 0), (20000, 1500, 0), (9000, 2000, 3000)])
 def test_large_prompts_by_samples_of_rows(ctx, n, window):
     b = Prompts([(ctx, n)], 12)
