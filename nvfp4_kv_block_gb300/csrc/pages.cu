@@ -108,11 +108,22 @@ struct ExtendParams {
   int n_seqs;
   int n_tokens;
   int64_t* slots;
+  int wide;  // the slots behind each sequence's first are left to slots_kernel
 };
 // Pages that one call can deal: a sequence touches at most n / 128 + 2 blocks.
 constexpr int kMaxExtendTokens = 262144;
 constexpr int kMaxDealt = kMaxExtendTokens / kPageTokens + 2 * kMaxSeqs;
 constexpr int kExtendSmem = (kMaxDealt + 2 * (kMaxSeqs + 1) + 32) * sizeof(int);
+// Entries of a sequence that one thread looks at and deals; a warp takes more of them (with the release behind
+// it, 16 rows of 2,048 tokens: 13 us, 18 where a warp takes 9 entries and more; one of 8,192: 9.5, 16 without warps).
+constexpr int kOwnEntries = 20;
+// Tokens whose slots the planning CTA writes, 1,024 at a time; a wide launch behind it those of more
+// (with the release, 4,096 tokens: 7.8 us, 8.5 by a wide launch; 262,144: 324 and 33).
+constexpr int kPlanTokens = 4096;
+
+__device__ __forceinline__ int64_t slot_at(const int* row, int pos) {
+  return (int64_t)row[pos / kPageTokens] * kPageTokens + pos % kPageTokens;
+}
 
 __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const __grid_constant__ ExtendParams p) {
   extern __shared__ int smem[];
@@ -120,37 +131,50 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const __grid_const
   int* s_start = list + kMaxDealt;          // [n_seqs + 1] first token
   int* s_len = s_start + kMaxSeqs + 1;      // [n_seqs] tokens before, or -1: no page was left or no sequence
   int* s_warp = s_len + kMaxSeqs + 1;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31;
   pdl_wait();
   pdl_trigger();
-  // sequences per * tid ..: what each is short of
+  // sequences per * tid ..: the entries from first to last get pages; what each is short of (-1: left out)
   const int per = (p.n_seqs + kPlanThreads - 1) / kPlanThreads;
-  int need[kOwnSeqs], mine = 0;
+  int need[kOwnSeqs], first[kOwnSeqs], last[kOwnSeqs], mine = 0;
 #pragma unroll
   for (int i = 0; i < kOwnSeqs; ++i) {
     const int b = per * tid + i;
     need[i] = -1;
-    if (i >= per || b >= p.n_seqs) continue;
-    const int start = p.q_start_loc[b], n = p.q_start_loc[b + 1] - start, len = p.seq_lens[b];
-    s_start[b] = start;
-    if (b == p.n_seqs - 1) s_start[b + 1] = start + n;
-    const bool ok = n >= 0 && start >= 0 && n <= p.n_tokens - start && len >= 0 && (long long)len + n <= (long long)p.max_pages * kPageTokens;
-    s_len[b] = ok ? len : -1;
-    if (!ok) {
-      set_status(p.pool.status, MSA_STATUS_BAD_SEQ);
-      continue;
+    first[i] = 0;
+    last[i] = -1;
+    if (i < per && b < p.n_seqs) {
+      const int start = p.q_start_loc[b], n = p.q_start_loc[b + 1] - start, len = p.seq_lens[b];
+      s_start[b] = start;
+      if (b == p.n_seqs - 1) s_start[b + 1] = start + n;
+      bool ok = n >= 0 && start >= 0 && n <= p.n_tokens - start && len >= 0 && (long long)len + n <= (long long)p.max_pages * kPageTokens;
+      const int* row = p.block_table + (size_t)b * p.max_pages;
+      if (!ok) {
+        set_status(p.pool.status, MSA_STATUS_BAD_SEQ);
+      } else if (n > 0 && len % kPageTokens && row[len / kPageTokens] < 0) {  // tokens without a page
+        set_status(p.pool.status, MSA_STATUS_BAD_PAGE);
+        ok = false;
+      }
+      s_len[b] = ok ? len : -1;
+      if (ok) {
+        need[i] = 0;
+        first[i] = (len + kPageTokens - 1) / kPageTokens;
+        last[i] = n > 0 ? (len + n - 1) / kPageTokens : -1;
+        if (last[i] - first[i] < kOwnEntries)
+#pragma unroll
+          for (int u = 0; u < kOwnEntries; ++u) need[i] += first[i] + u <= last[i] && row[first[i] + u] < 0;
+      }
     }
-    const int* row = p.block_table + (size_t)b * p.max_pages;
-    if (n > 0 && len % kPageTokens && row[len / kPageTokens] < 0) {  // tokens without a page
-      set_status(p.pool.status, MSA_STATUS_BAD_PAGE);
-      s_len[b] = -1;
-      continue;
-    }
-    need[i] = 0;
-    const int last = n > 0 ? (len + n - 1) / kPageTokens : -1;
+    for (uint32_t m = __ballot_sync(0xffffffffu, last[i] - first[i] >= kOwnEntries); m; m &= m - 1) {
+      const int who = __ffs(m) - 1, x1 = __shfl_sync(0xffffffffu, last[i], who);
+      const int* row = p.block_table + (size_t)(per * (tid - lane + who) + i) * p.max_pages;
+      int count = 0;
 #pragma unroll 4
-    for (int x = (len + kPageTokens - 1) / kPageTokens; x <= last; ++x) need[i] += row[x] < 0;
-    mine += need[i];
+      for (int x = __shfl_sync(0xffffffffu, first[i], who) + lane; x <= x1; x += 32) count += row[x] < 0;
+      count = __reduce_add_sync(0xffffffffu, count);
+      if (lane == who) need[i] = count;
+    }
+    mine += max(need[i], 0);
   }
   int want;
   int at = block_scan(mine, s_warp, want);
@@ -159,24 +183,53 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const __grid_const
 #pragma unroll
   for (int i = 0; i < kOwnSeqs; ++i) {
     const int b = per * tid + i;
-    if (need[i] < 0) continue;
-    const int n = p.q_start_loc[b + 1] - p.q_start_loc[b], len = s_len[b];
-    if (need[i] > 0 && at + need[i] > have) {
-      set_status(p.pool.status, MSA_STATUS_NO_PAGES);
-      s_len[b] = -1;
-    } else {
-      int* row = p.block_table + (size_t)b * p.max_pages;
-      for (int x = (len + kPageTokens - 1) / kPageTokens, k = at; k < at + need[i]; ++x)
-        if (row[x] < 0) {
-          const int page = list[k++];
+    bool dealt = false;
+    if (need[i] >= 0) {
+      const int n = p.q_start_loc[b + 1] - p.q_start_loc[b], len = s_len[b];
+      dealt = need[i] == 0 || at + need[i] <= have;
+      if (!dealt) {
+        set_status(p.pool.status, MSA_STATUS_NO_PAGES);
+        s_len[b] = -1;
+      } else if (n > 0) {
+        p.seq_lens[b] = len + n;
+      }
+      if (dealt && last[i] - first[i] < kOwnEntries) {
+        int* row = p.block_table + (size_t)b * p.max_pages;
+        for (int x = first[i], k = at; k < at + need[i]; ++x)
+          if (row[x] < 0) {
+            const int page = list[k++];
+            take(p.pool, page);
+            row[x] = page;
+          }
+      }
+    }
+    for (uint32_t m = __ballot_sync(0xffffffffu, dealt && need[i] > 0 && last[i] - first[i] >= kOwnEntries); m; m &= m - 1) {
+      const int who = __ffs(m) - 1, x1 = __shfl_sync(0xffffffffu, last[i], who);
+      int* row = p.block_table + (size_t)(per * (tid - lane + who) + i) * p.max_pages;
+      int k = __shfl_sync(0xffffffffu, at, who);
+      for (int x0 = __shfl_sync(0xffffffffu, first[i], who); x0 <= x1; x0 += 32) {
+        const int x = x0 + lane;
+        const bool empty = x <= x1 && row[x] < 0;
+        const uint32_t all = __ballot_sync(0xffffffffu, empty);
+        if (empty) {
+          const int page = list[k + __popc(all & ((1u << lane) - 1))];
           take(p.pool, page);
           row[x] = page;
         }
-      if (n > 0) p.seq_lens[b] = len + n;
+        k += __popc(all);
+      }
     }
-    at += need[i];
+    at += max(need[i], 0);
   }
   __syncthreads();
+  if (p.wide) {
+    for (int b = tid; b < p.n_seqs; b += kPlanThreads) {
+      const int t = s_start[b];
+      if (t >= 0 && t < p.n_tokens && s_start[b + 1] > t)
+        p.slots[t] = s_len[b] >= 0 ? slot_at(p.block_table + (size_t)b * p.max_pages, s_len[b]) : -1;
+    }
+    return;
+  }
   for (int t = tid; t < p.n_tokens; t += kPlanThreads) {
     int lo = 0, hi = p.n_seqs - 1;
     while (lo < hi) {
@@ -184,12 +237,31 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const __grid_const
       if (s_start[mid] <= t) lo = mid; else hi = mid - 1;
     }
     int64_t slot = -1;
-    if (t >= s_start[lo] && t < s_start[lo + 1] && s_len[lo] >= 0) {
-      const int pos = s_len[lo] + t - s_start[lo];
-      slot = (int64_t)p.block_table[(size_t)lo * p.max_pages + pos / kPageTokens] * kPageTokens + pos % kPageTokens;
-    }
+    if (t >= s_start[lo] && t < s_start[lo + 1] && s_len[lo] >= 0)
+      slot = slot_at(p.block_table + (size_t)lo * p.max_pages, s_len[lo] + t - s_start[lo]);
     p.slots[t] = slot;
   }
+}
+// The slots behind a sequence's first one, whose sign says whether the sequence grew.
+__global__ void __launch_bounds__(kCopyThreads) slots_kernel(const __grid_constant__ ExtendParams p) {
+  pdl_wait();
+  pdl_trigger();
+  const int t = blockIdx.x * kCopyThreads + threadIdx.x;
+  if (t >= p.n_tokens) return;
+  int lo = 0, hi = p.n_seqs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.q_start_loc[mid] <= t) lo = mid; else hi = mid - 1;
+  }
+  const int start = p.q_start_loc[lo], n = p.q_start_loc[lo + 1] - start;
+  int64_t slot = -1;
+  if (t >= start && t - start < n) {
+    if (t == start) return;
+    const long long pos = (long long)p.seq_lens[lo] - n + (t - start);
+    if (start >= 0 && p.slots[start] >= 0 && pos >= 0 && pos < (long long)p.max_pages * kPageTokens)
+      slot = slot_at(p.block_table + (size_t)lo * p.max_pages, (int)pos);
+  }
+  p.slots[t] = slot;
 }
 
 // ---- forks ------------------------------------------------------------------------
@@ -530,8 +602,9 @@ cudaError_t launch_extend(const msa_page_pool* pool, int* block_table, int max_p
     return cudaFuncSetAttribute(extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kExtendSmem);
   });
   if (e != cudaSuccess) return e;
-  const ExtendParams p{pool_of(pool), block_table, max_pages, seq_lens, q_start_loc, n_seqs, n_tokens, slots};
-  return launch_pdl(extend_kernel, dim3(1), dim3(kPlanThreads), kExtendSmem, stream, p);
+  const ExtendParams p{pool_of(pool), block_table, max_pages, seq_lens, q_start_loc, n_seqs, n_tokens, slots, n_tokens > kPlanTokens};
+  if (const cudaError_t r = launch_pdl(extend_kernel, dim3(1), dim3(kPlanThreads), kExtendSmem, stream, p); r != cudaSuccess || !p.wide) return r;
+  return launch_pdl(slots_kernel, dim3((n_tokens + kCopyThreads - 1) / kCopyThreads), dim3(kCopyThreads), 0, stream, p);
 }
 
 cudaError_t launch_fork(const msa_cache* layers, int n_layers, const msa_page_pool* pool, int* block_table,

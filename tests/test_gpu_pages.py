@@ -121,6 +121,23 @@ def test_extend_a_whole_prompt_and_reserved_pages():
     s.release([1])
 
 
+@pytest.mark.parametrize("total", [2048, 4096, 4097, 6000])
+def test_extend_by_thousands_of_tokens(total):
+    """Rows of many pages and of few, one too long, one of nothing, from the middle of a page; then the pool runs dry."""
+    s = State(72, 5, 60)
+    s.extend([5, 0, 130, 1, 0])
+    s.extend([total - 1039, 0, 1000, 0, 30], pad=9)
+    s.extend([7, 60 * 128 + 1, 5, 0, 0], pad=9)                   # the second is longer than its row
+    s.extend([1, 1, 1, 1, 1])
+    s.extend([1500, 0, 40, 7000, 2], pad=1)                       # from the fourth on none finds its pages
+    s.release([0, 4])
+    s.extend([0, 0, 0, 2500, 900])
+    s.release([3, 2])
+    rows = State(700, 257, 3)
+    rows.extend([20 + i % 9 for i in range(257)])
+    rows.extend([130 if i % 31 == 0 else 3 for i in range(257)], pad=2000)
+
+
 def test_extend_refusals():
     s = State(20, 4, 2)
     s.extend([1, 250, 257, 5])         # the third is longer than its row
