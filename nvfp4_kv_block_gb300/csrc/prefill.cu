@@ -1154,63 +1154,74 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
 }
 
 // ---- (3) jobs that were cut ---------------------------------------------------------------
-// out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.  A CTA takes 32 rows of a job after the other: lane =
-// row, warp = 16 channels, four parts' loads at once.
-constexpr int kMergeParts = 4, kQuads = kGqa * kTileTokens / 32;
-__global__ void __launch_bounds__(256) prefill_merge_kernel(const __grid_constant__ PrefillParams p) {
+// out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.  A unit is 32 rows of a job, lane = row; a warp takes
+// 4 kChunks of its channels, kParts parts' loads at once.  Eight warps a unit with four parts at once keep more units
+// going; where there are fewer units than CTAs (few tokens over a long context: many parts) sixteen warps
+// with eight halve the chain of loads (two sequences of up to 64 tokens over 6,034: 34.7 us, 31.7).
+constexpr int kMergeThreads = 512, kQuads = kGqa * kTileTokens / 32;
+template <int kParts, int kChunks>
+__device__ __forceinline__ void merge_unit(const PrefillParams& p, int u, int chunk0, int lane) {
+  const int2 big = p.big[u / kQuads];
+  const int t = big.x / kKvHeads, g = big.x % kKvHeads, quad = u % kQuads, c0 = big.y & 255, parts = big.y >> 8;
+  const int q0 = p.tiles[t].q0, n_rows = kGqa * p.tiles[t].n_tok, row = 32 * quad + lane;
+  if (32 * quad >= n_rows) return;
+  float M = -INFINITY, L = 0.f, o[4 * kChunks] = {};
+  for (int i0 = 0; i0 < parts; i0 += kParts) {
+    float4 x[kParts][kChunks];
+    float2 ml[kParts];
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+      ml[i] = make_float2(-INFINITY, 0.f);
+      if (i0 + i < parts) {
+        const size_t at = (part_slot(c0, i0 + i) * p.part_quads + quad) * 32;
+        ml[i] = p.part_ml[at + lane];
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) x[i][c] = p.part_o[(at + chunk0 + c) * 32 + lane];
+      }
+    }
+    float top = M;
+#pragma unroll
+    for (int i = 0; i < kParts; ++i)
+      if (ml[i].y != 0.f) top = fmaxf(top, ml[i].x);
+    const float f = M > -INFINITY ? fast_exp2(M - top) : 0.f;
+    M = top;
+    L *= f;
+#pragma unroll
+    for (int c = 0; c < 4 * kChunks; ++c) o[c] *= f;
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+      if (i0 + i >= parts) break;
+      const float w = ml[i].y != 0.f ? fast_exp2(ml[i].x - top) : 0.f;
+      L = fmaf(ml[i].y, w, L);
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        o[4 * c] = fmaf(x[i][c].x, w, o[4 * c]);
+        o[4 * c + 1] = fmaf(x[i][c].y, w, o[4 * c + 1]);
+        o[4 * c + 2] = fmaf(x[i][c].z, w, o[4 * c + 2]);
+        o[4 * c + 3] = fmaf(x[i][c].w, w, o[4 * c + 3]);
+      }
+    }
+  }
+  if (row >= n_rows) return;
+  const float inv = L != 0.f ? p.out_scale / L : 0.f;  // (a NaN of the query stays one)
+  const size_t at = (size_t)(q0 + (row >> 2)) * kQHeads + kGqa * g + (row & 3);
+#pragma unroll
+  for (int h = 0; h < kChunks / 2; ++h) {
+    uint32_t y[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) y[c] = pack16(o[8 * h + 2 * c] * inv, o[8 * h + 2 * c + 1] * inv, p.out_f16);
+    *reinterpret_cast<uint4*>(p.out + at * kHeadDim + 4 * chunk0 + 8 * h) = make_uint4(y[0], y[1], y[2], y[3]);
+  }
+  if (p.lse && chunk0 == 0) p.lse[at] = L != 0.f ? (M - kBias + log2f(L)) * kLn2 : -INFINITY;
+}
+__global__ void __launch_bounds__(kMergeThreads) prefill_merge_kernel(const __grid_constant__ PrefillParams p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
   const int units = *p.n_big * kQuads;
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
-    const int2 big = p.big[u / kQuads];
-    const int t = big.x / kKvHeads, g = big.x % kKvHeads, quad = u % kQuads, c0 = big.y & 255, parts = big.y >> 8;
-    const int q0 = p.tiles[t].q0, n_rows = kGqa * p.tiles[t].n_tok, row = 32 * quad + lane;
-    if (32 * quad >= n_rows) continue;
-    float M = -INFINITY, L = 0.f, o[16] = {};
-    for (int i0 = 0; i0 < parts; i0 += kMergeParts) {
-      float4 x[kMergeParts][4];
-      float2 ml[kMergeParts];
-#pragma unroll
-      for (int i = 0; i < kMergeParts; ++i) {
-        ml[i] = make_float2(-INFINITY, 0.f);
-        if (i0 + i < parts) {
-          const size_t at = (part_slot(c0, i0 + i) * p.part_quads + quad) * 32;
-          ml[i] = p.part_ml[at + lane];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) x[i][c] = p.part_o[(at + 4 * warp + c) * 32 + lane];
-        }
-      }
-      float top = M;
-#pragma unroll
-      for (int i = 0; i < kMergeParts; ++i)
-        if (ml[i].y != 0.f) top = fmaxf(top, ml[i].x);
-      const float f = M > -INFINITY ? fast_exp2(M - top) : 0.f;
-      M = top;
-      L *= f;
-#pragma unroll
-      for (int c = 0; c < 16; ++c) o[c] *= f;
-#pragma unroll
-      for (int i = 0; i < kMergeParts; ++i) {
-        if (i0 + i >= parts) break;
-        const float w = ml[i].y != 0.f ? fast_exp2(ml[i].x - top) : 0.f;
-        L = fmaf(ml[i].y, w, L);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          o[4 * c] = fmaf(x[i][c].x, w, o[4 * c]);
-          o[4 * c + 1] = fmaf(x[i][c].y, w, o[4 * c + 1]);
-          o[4 * c + 2] = fmaf(x[i][c].z, w, o[4 * c + 2]);
-          o[4 * c + 3] = fmaf(x[i][c].w, w, o[4 * c + 3]);
-        }
-      }
-    }
-    if (row >= n_rows) continue;
-    const float inv = L != 0.f ? p.out_scale / L : 0.f;  // (a NaN of the query stays one)
-    const size_t at = (size_t)(q0 + (row >> 2)) * kQHeads + kGqa * g + (row & 3);
-    uint32_t y[8];
-#pragma unroll
-    for (int c = 0; c < 8; ++c) y[c] = pack16(o[2 * c] * inv, o[2 * c + 1] * inv, p.out_f16);
-    st32(p.out + at * kHeadDim + 16 * warp, y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7]);
-    if (p.lse && warp == 0) p.lse[at] = L != 0.f ? (M - kBias + log2f(L)) * kLn2 : -INFINITY;
+  if (units <= (int)gridDim.x) {
+    if ((int)blockIdx.x < units) merge_unit<8, 2>(p, blockIdx.x, 2 * warp, lane);
+  } else {
+    for (int u = 2 * blockIdx.x + (warp >> 3); u < units; u += 2 * gridDim.x) merge_unit<4, 4>(p, u, 4 * (warp & 7), lane);
   }
 }
 
@@ -1299,7 +1310,7 @@ cudaError_t launch_prefill_attn(const msa_cache* c, const uint8_t* q, float soft
   if (e != cudaSuccess) return e;
   // (a job has no more parts than pages)
   if (n_visited <= kAlone) return cudaSuccess;
-  return launch_pdl(prefill_merge_kernel, dim3(4 * std::min(n_sm, kPrefillCtas)), dim3(256), 0, stream, pp);
+  return launch_pdl(prefill_merge_kernel, dim3(2 * std::min(n_sm, kPrefillCtas)), dim3(kMergeThreads), 0, stream, pp);
 }
 
 }  // namespace msa
