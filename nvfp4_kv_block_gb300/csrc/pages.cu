@@ -15,7 +15,7 @@
 //
 // Every kernel is a programmatic dependent of the one before it and lets the next begin
 // launching at once; it touches memory behind pdl_wait only (release, fork and extension of
-// 256 rows, 43.8 us a round; 49.8 with plain launches).  On the GPU the round takes 3.4 for
+// 256 rows, 43.8 us a pass; 49.8 with plain launches).  On the GPU the pass takes 3.4 for
 // the release, 8 for the plan, 28 for the copies (12 layers, 246 MB read and written, 8.8 TB/s: partly
 // from L2) and 7.5 for the extension: three chains of a few dependent loads and one launch bound
 // by memory.  A commit of 8 x 8 drafts takes 2.4 us, of 64 x 64 in 12 layers 6 to 7.5 (9.8 MB).

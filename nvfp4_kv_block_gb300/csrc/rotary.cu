@@ -23,7 +23,7 @@
 // page, and leave together.  8,192 bf16 tokens: 25 us, 4.1 TB/s of the bytes above; 16,384
 // fp32 tokens at scattered slots: 62 us, 5.5 TB/s.  As a programmatic dependent of the kernel before
 // it, which lets the next one begin launching (memory is touched behind pdl_wait only): with the
-// read-back behind it 29.8 us a round, 33.3 with plain launches.  Positions on several axes cost an
+// read-back behind it 29.8 us a pass, 33.3 with plain launches.  Positions on several axes cost an
 // int32 a token and axis more, and table rows of which a pair reads its own: 8,185 fp16 tokens (slices) on three
 // axes, dealt pair by pair, and the read-back 31.9 us.
 #include <cuda_bf16.h>
