@@ -13,7 +13,8 @@
 // operand tiles of the products, 16 KB of E4M3 keys and 32 KB of f16 values, by a kernel bound
 // by memory; it also writes down the tiles of 64 tokens and their pages.  (2) The attention: a job
 // is a tile (256 rows, 4 i + h for token i and head h of the group) and a KV head; the jobs'
-// pages in a row are cut into equal weighted ranges, one per persistent CTA.  A job that was cut
+// pages in a row are cut into equal weighted ranges, one per persistent CTA, or, where that is nearly as even, jobs are
+// taken whole from a queue.  A job that was cut
 // leaves fp32 rows, which the last of its parts joins in the order of the parts (each warp for
 // its rows, behind a counter).  (3) Jobs in more parts, and those of calls without whole jobs, are joined by a
 // kernel of their own.
@@ -31,7 +32,7 @@
 // (290), PV and the next QK into the same columns (820), the hand-over of the scores (400), and the two
 // sets run half a period apart.  Two tiles of scores and two accumulators are all of tensor memory, so there is no
 // third one to fill the gaps.  2,048 tokens over 131,072: 1,095 us, 2.02 PFLOP/s (1.90 is the measured bf16 rate; at
-// that rate for PV and twice it for QK the products alone take 877); 8,192 from the beginning: 162 us, the products 109;
+// that rate for PV and twice it for QK the products alone take 877); 8,192 from the beginning: 158 us, the products 109;
 // 4,096 with a window of 4,096: 97, 55.  Tiles of 64 tokens x 4 heads: a page's 48 KB then feed two products
 // of 128 rows, 21 bytes a cycle and SM from L2.  100 tokens: 17 to 19 us, two launches and a chain of some
 // thirty latencies.
@@ -88,7 +89,9 @@ constexpr int kPage1 = 9, kPage2 = 9, kFixed = 24, kSmall = 45, kLeast = 10;
 
 // Jobs stay whole if the CTA with most then has no more than an equal share and kCut: parts cost their rows'
 // way to memory and back, some 16,000 cycles, with nothing under it at a call's end.  The same 14 calls: 59.0 us where
-// all is cut, 54.7 with 30, 51.8 with 100, 52.6 with 150 (sequences of 69 to 126 tokens: 36.8 and 24.4).
+// all is cut, 54.7 with 30, 51.8 with 100, 52.6 with 150 (sequences of 69 to 126 tokens: 36.8 and 24.4).  They are
+// taken from a queue, the last tile of all, which sees most of its sequence, first (8,192 tokens: 163 us, of which a
+// fifth was cut, 158; 16 chunks of 300: 45.4 and 43.2).  Which CTA takes a job changes no row of it.
 constexpr int kCut = 100;
 
 // Parts of a job that its last one joins: under other jobs' pages where CTAs have whole jobs behind the cut ones
@@ -142,6 +145,7 @@ struct PrefillParams {
   int* n_tiles;   // workspace from here on
   TileRec* tiles;
   int max_tiles;
+  int* next;         // whole jobs that were taken from the queue
   int* n_big;        // jobs of the third kernel, and which: job, first CTA | parts << 8
   int2* big;         // [4 max_tiles]
   int* tickets;      // [max_tiles][4][8]: parts that a warp's rows are there of
@@ -241,6 +245,7 @@ __global__ void __launch_bounds__(kConvThreads) prefill_convert_kernel(const __g
     if (tid == 0) {
       *p.n_tiles = n_tiles;
       *p.n_big = 0;
+      *p.next = 0;
     }
     for (int b = tid; b < p.n_seqs; b += kConvThreads)
       if (s_page[b + 1] > s_page[b] && !fits(b)) set_status(p.status, MSA_STATUS_BAD_SEQ);
@@ -634,13 +639,22 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
       const TileRec* r = p.tiles + job % n_tiles;
       return job_weight(r->n_tok, r->n_pg);
     };
-    // Whole jobs c, c + G, ... of CTA c: all, or as many rounds as leave every CTA a share of the cut ones
+    // Whole jobs c, c + G, ... of CTA c: as many rounds as leave every CTA a share of the cut ones
     int whole = total > 0 ? n_jobs / G : 0;
     long long w = 0;
     if (tid < G)
       for (int i = 0; i < whole; ++i) w += weight(tid + i * G);
     const int rest = tid < G && tid + whole * G < n_jobs ? weight(tid + whole * G) : 0;
-    const bool cut = __syncthreads_or(w + rest > quota + kCut);
+    // None is cut if all of them, dealt like that, leave no CTA with more than an equal share and kCut, or if a
+    // queue of them, last tile first, does: a job begins when the ones before it, S in all, are out, at S / G or earlier
+    bool late = false;
+    long long upto_t = before + incl - mine;
+    for (int t = t0; t < t1; ++t) {
+      const int w = job_weight(p.tiles[t].n_tok, p.tiles[t].n_pg);
+      upto_t += w;
+      late |= kKvHeads * (one - upto_t) + (kKvHeads - 1 + G) * (long long)w > G * (quota + kCut);
+    }
+    const bool dealt = __syncthreads_or(w + rest > quota + kCut), cut = __syncthreads_or(late) && dealt;
     while (__syncthreads_or(whole > 0 && tid < G && w + kLeast > quota)) {
       --whole;
       if (tid < G) w -= weight(tid + whole * G);
@@ -768,14 +782,14 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
 #pragma unroll 1
         for (int pass = whole < 0 ? 2 : 0; pass < 3; ++pass) {
           const bool cut = pass < 2;
-          const int mine = whole >= 0 ? whole : (kKvHeads * n_tiles - (int)blockIdx.x + G - 1) / G;
+          int x = (int)blockIdx.x;  // place in the queue
           long long off = cut ? s_scan[pass ? 28 : 30] : 0;
           int g = (int)(s_scan[pass ? 27 : 29] >> 32), t = (int)s_scan[pass ? 27 : 29];
-          for (int i = 0; ok && (cut ? off < hi && g < kKvHeads : i < mine); ++i) {
+          for (int i = 0; ok && (cut ? off < hi && g < kKvHeads : whole < 0 ? x < kKvHeads * n_tiles : i < whole); ++i) {
             if (!cut) {
               const int job = (int)blockIdx.x + i * G;
-              g = job / n_tiles;
-              t = job % n_tiles;
+              g = whole < 0 ? x % kKvHeads : job / n_tiles;
+              t = whole < 0 ? n_tiles - 1 - x / kKvHeads : job % n_tiles;
             }
             const TileRec r = tile(t);
             const int pw = page_weight(r.n_tok);
@@ -792,6 +806,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
               const int c0 = cut ? owner(base) : (int)blockIdx.x;
               ok = segment(r, t, g, a, z, c0, cut ? owner(base + (long long)(r.n_pg - 1) * pw) - c0 + 1 : 1);
             }
+            if (whole < 0) x = G + __shfl_sync(0xffffffffu, lane == 0 ? atomicAdd(p.next, 1) : 0, 0);
             off += job_weight(r.n_tok, r.n_pg);
             if (++t == n_tiles) {
               t = 0;
@@ -1292,6 +1307,7 @@ cudaError_t launch_prefill_attn(const msa_cache* c, const uint8_t* q, float soft
   };
   pp.n_tiles = reinterpret_cast<int*>(piece(256));
   pp.n_big = pp.n_tiles + 1;
+  pp.next = pp.n_tiles + 2;
   pp.tiles = reinterpret_cast<TileRec*>(piece(pp.max_tiles * sizeof(TileRec)));
   pp.big = reinterpret_cast<int2*>(piece((size_t)pp.max_tiles * kKvHeads * sizeof(int2)));
   pp.tickets = reinterpret_cast<int*>(piece((size_t)pp.max_tiles * 32 * sizeof(int)));
