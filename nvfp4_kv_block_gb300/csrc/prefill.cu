@@ -20,7 +20,7 @@
 // kernel of their own.
 //
 // Roles of the attention's warps, all hand-offs mbarriers with bounded waits:
-//   warp 0      segment records, a bulk copy of 16 KB and one of 32 KB per page;
+//   warp 0      segment records, a bulk copy of 48 KB per page;
 //   warp 1      MMA issuer: S = Q K8^T (kind::f8f6f4, 128 x 128 x 128), then O += P V
 //               (kind::f16, P from tensor memory over S's own columns);
 //   warp 2      query rows of the next segment;
@@ -32,7 +32,7 @@
 // (290), PV and the next QK into the same columns (820), the hand-over of the scores (400), and the two
 // sets run half a period apart.  Two tiles of scores and two accumulators are all of tensor memory, so there is no
 // third one to fill the gaps.  2,048 tokens over 131,072: 1,095 us, 2.02 PFLOP/s (1.90 is the measured bf16 rate; at
-// that rate for PV and twice it for QK the products alone take 877); 8,192 from the beginning: 158 us, the products 109;
+// that rate for PV and twice it for QK the products alone take 877); 8,192 from the beginning: 160 us, the products 109;
 // 4,096 with a window of 4,096: 97, 55.  Tiles of 64 tokens x 4 heads: a page's 48 KB then feed two products
 // of 128 rows, 21 bytes a cycle and SM from L2.  100 tokens: 17 to 19 us, two launches and a chain of some
 // thirty latencies.
@@ -70,7 +70,9 @@ constexpr int kBFull = 0, kBEmpty = kBFull + kStages, kBQFull = kBEmpty + kStage
               kBRecEmpty = kBRecFull + kRecs,
               kBDone = kBRecEmpty + kRecs, kBars = kBDone + 1;
 constexpr int kOffMisc = kOffBars + 8 * ((kBars + 1) & ~1);  // tmem, abort, pages issued
-constexpr int kPrefillSmem = 1024 + kOffMisc + 16;
+constexpr int kSorted = 256;  // tiles that a queue has in order of their weights
+constexpr int kOffOrder = kOffMisc + 16;                     // uint16_t [kSorted]
+constexpr int kPrefillSmem = 1024 + kOffOrder + 2 * kSorted;
 static_assert(kPrefillSmem <= 232448, "shared memory of one CTA");
 static_assert(kOffBars % 8 == 0, "barriers");
 constexpr uint32_t kTmemS = 0, kTmemO = 256;  // S of set s at 128 s, O of set s at 256 + 128 s
@@ -90,8 +92,9 @@ constexpr int kPage1 = 9, kPage2 = 9, kFixed = 24, kSmall = 45, kLeast = 10;
 // Jobs stay whole if the CTA with most then has no more than an equal share and kCut: parts cost their rows'
 // way to memory and back, some 16,000 cycles, with nothing under it at a call's end.  The same 14 calls: 59.0 us where
 // all is cut, 54.7 with 30, 51.8 with 100, 52.6 with 150 (sequences of 69 to 126 tokens: 36.8 and 24.4).  They are
-// taken from a queue, the last tile of all, which sees most of its sequence, first (8,192 tokens: 163 us, of which a
-// fifth was cut, 158; 16 chunks of 300: 45.4 and 43.2).  Which CTA takes a job changes no row of it.
+// taken from a queue, the heaviest first (of up to 256 tiles, each ranked by one thread; the last tile of all, which
+// sees most of its sequence, where there are more): 8,192 tokens 163 us with cut jobs, 160; 15 chunks of up to 249
+// tokens at places up to 2,111, last tile first 56.5, heaviest first 48.0.  Which CTA takes a job changes no row of it.
 constexpr int kCut = 100;
 
 // Parts of a job that its last one joins: under other jobs' pages where CTAs have whole jobs behind the cut ones
@@ -576,6 +579,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
   int* s_info = reinterpret_cast<int*>(smem + kOffInfo);
   // [24] warp sums; 24: start of the cut jobs, CTAs, whole jobs of each (-1: all), first cut job, its start, last one, its start
   long long* s_scan = reinterpret_cast<long long*>(smem + kOffScan);
+  uint16_t* s_order = reinterpret_cast<uint16_t*>(smem + kOffOrder);
+  int* s_weight = reinterpret_cast<int*>(smem + kOffJoin);  // of the first kSorted tiles, here only
   long long* s_range = reinterpret_cast<long long*>(smem + kOffRange);  // [CTAs + 1] starts of the CTAs' ranges of the cut jobs
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
@@ -626,6 +631,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
       if (lane >= o) incl += v;
     }
     if (lane == 31) s_scan[warp] = incl;
+    if (tid < kSorted) s_weight[tid] = (int)mine;
     __syncthreads();
     long long before = 0, one = 0;
     for (int i = 0; i < kPrefillThreads / 32; ++i) {
@@ -646,13 +652,33 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
       for (int i = 0; i < whole; ++i) w += weight(tid + i * G);
     const int rest = tid < G && tid + whole * G < n_jobs ? weight(tid + whole * G) : 0;
     // None is cut if all of them, dealt like that, leave no CTA with more than an equal share and kCut, or if a
-    // queue of them, last tile first, does: a job begins when the ones before it, S in all, are out, at S / G or earlier
+    // queue of them, heaviest first (or last tile first), does: a job begins when the ones before it, S in all, are out, at S / G or earlier
     bool late = false;
-    long long upto_t = before + incl - mine;
-    for (int t = t0; t < t1; ++t) {
-      const int w = job_weight(p.tiles[t].n_tok, p.tiles[t].n_pg);
-      upto_t += w;
-      late |= kKvHeads * (one - upto_t) + (kKvHeads - 1 + G) * (long long)w > G * (quota + kCut);
+    auto begins_late = [&](long long ahead, int w) { return kKvHeads * ahead + (kKvHeads - 1 + G) * (long long)w > G * (quota + kCut); };
+    if (n_jobs > G && n_tiles <= kSorted) {
+      if (tid < n_tiles) {
+        const int own = (int)mine;
+        int rank = 0, ahead = 0;
+        for (int i = 0; i < n_tiles; i += 4) {
+          const int4 v = *reinterpret_cast<const int4*>(s_weight + i);
+          const int u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (i + j < n_tiles && (u[j] > own || (u[j] == own && i + j > tid))) {
+              ++rank;
+              ahead += u[j];
+            }
+        }
+        s_order[rank] = (uint16_t)tid;
+        late = begins_late(ahead, own);
+      }
+    } else {
+      long long upto_t = before + incl - mine;
+      for (int t = t0; t < t1; ++t) {
+        const int w = job_weight(p.tiles[t].n_tok, p.tiles[t].n_pg);
+        upto_t += w;
+        late |= begins_late(one - upto_t, w);
+      }
     }
     const bool dealt = __syncthreads_or(w + rest > quota + kCut), cut = __syncthreads_or(late) && dealt;
     while (__syncthreads_or(whole > 0 && tid < G && w + kLeast > quota)) {
@@ -707,7 +733,138 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
   const bool idle = (int)blockIdx.x >= G;
 
   // registers: 128 threads x 64 + 256 x 160 + 128 x 128 of the launch's 512 x 128
-  if (warp < 4) {
+  // (the longest loop's code first: 100 tokens 17 us, 18 behind the others')
+  if (warp >= 4 && warp < 12) {
+    regs_inc<160>();
+    // ---------------- softmax: set = (warp - 4) / 4, row = TMEM lane ------------------------------------
+    const int set = (warp - 4) >> 2, quad = warp & 3, lrow = 32 * quad + lane;
+    const uint32_t t_s = tmem + ((uint32_t)(32 * quad) << 16) + kTmemS + 128 * set, t_o = t_s + kTmemO - kTmemS;
+    const uint64_t scale2 = pair64(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
+    uint32_t e = 0, par = 0, segs = 0;  // pages so far, parity of this set's jobs, its segments
+    for (int k = 0;; ++k) {
+      if (!swait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc)) break;
+      const SegRec r = *rec(k);
+      __syncwarp();
+      if (r.n_pg < 0) break;
+      if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
+      if (set == 1 && r.n_tok <= 32) {
+        e += r.n_pg;
+        continue;
+      }
+      const int token = 32 * set + (lrow >> 2);
+      const bool busy = 32 * set + 8 * quad < r.n_tok, mine = token < r.n_tok;
+      // keys that the row sees, counted from the first one of the page
+      int start = 0, end = 0x7FFFFFFF;
+      if (mine) {
+        const int pos = r.pos + token;
+        start = (p.window ? max(0, pos + 1 - p.window) : 0) - r.page0 * kPageTokens;
+        end = (p.ends ? min(max(p.ends[r.q0 + token], 0), r.len) : pos + 1) - r.page0 * kPageTokens;
+      }
+      // (a row that sees nothing is weighed as if it saw all, so that its warp's pages need no masks; its sum is 0)
+      const bool none = end <= start;
+      if (none) {
+        start = 0;
+        end = 0x7FFFFFFF;
+      }
+      float shift = kUnset, l = 0.f;  // kBias less the reference, and the sum of weights
+      bool ok = true;
+      for (const uint32_t e0 = e; e - e0 < (uint32_t)r.n_pg; ++e) {
+        if (!swait(bar(kBSFull + set), par, wc)) {
+          ok = false;
+          break;
+        }
+        par ^= 1;
+        if (busy) {
+          tc_fence_after();
+          const int hi = s_info[e % kInfo] ? end : 0;
+          if (__any_sync(0xffffffffu, start > 0 || hi < kPageTokens)) {  // -inf where the row does not see the token
+#pragma unroll 1
+            for (int c = 0; c < kPageTokens; c += 32) {
+              uint32_t v[32];
+              const uint32_t vis = low_bits(hi - c) & ~low_bits(start - c);
+              if (__all_sync(0xffffffffu, vis == 0xFFFFFFFFu)) continue;
+              tmem_ld32x32b_x32(t_s + c, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int x = 0; x < 32; ++x) v[x] = vis >> x & 1 ? v[x] : 0xFF800000u;
+              tmem_st32(t_s + c, v);
+            }
+            tmem_wait_st();
+          }
+          // Half a page at a time, the next 32 scores loaded under the exponentials of 32.  There is no pass
+          // for the maximum: 64 weights that sum to 49,152 or less have none above it, and others (a
+          // row's first ones: its shift is kUnset) move the reference and are weighed again.
+          uint32_t v[2][32];
+          tmem_ld32x32b_x32(t_s, v[0]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint64_t shift2 = pair64(__float_as_uint(shift), __float_as_uint(shift));
+            uint64_t sums[2] = {0, 0};
+            uint32_t o[32];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              wait_ld32(v[c]);
+              if (h + c < 2) tmem_ld32x32b_x32(t_s + 64 * h + 32 * c + 32, v[(c + 1) & 1]);
+              weigh32(v[c], scale2, shift2, sums, o + 16 * c);
+            }
+            const uint2 sum2 = split64(add_f32x2(sums[0], sums[1]));
+            float sum = __uint_as_float(sum2.x) + __uint_as_float(sum2.y);
+            const bool over = mine && sum > kMost;
+            if (__any_sync(0xffffffffu, over)) {
+              // (S of this half is as it was; the other half's load may be under way)
+              wait_ld32(v[0]);
+              float top = -INFINITY;
+#pragma unroll 1
+              for (int c = 0; c < 64; c += 16) {
+                uint32_t u[16];
+                tmem_ld32x32b_x16(t_s + 64 * h + c, u);
+                tmem_wait_ld();
+#pragma unroll
+                for (int x = 0; x < 16; ++x) top = fmaxf(top, __uint_as_float(u[x]));
+              }
+              float f = 1.f;
+              if (over) {
+                const float next = kBias - top * p.scale_log2;
+                f = fast_exp2(next - shift);  // (0 for the first: shift is kUnset)
+                shift = next;
+                l *= f;
+              }
+              __syncwarp();
+              if (e != e0) scale_acc(t_o, f);  // (the PVs before this S are done)
+              if (h) scale_p(t_s, f);
+              const uint64_t again2 = pair64(__float_as_uint(shift), __float_as_uint(shift));
+              sums[0] = sums[1] = 0;
+#pragma unroll 1
+              for (int c = 0; c < 64; c += 32) {
+                uint32_t u[32], y[16];
+                tmem_ld32x32b_x32(t_s + 64 * h + c, u);
+                tmem_wait_ld();
+                weigh32(u, scale2, again2, sums, y);
+                tmem_st_x16(t_s + 64 * h + c, y);
+              }
+              const uint2 again = split64(add_f32x2(sums[0], sums[1]));
+              sum = __uint_as_float(again.x) + __uint_as_float(again.y);
+            } else {
+              tmem_st_x16(t_s + 64 * h, o);
+              tmem_st_x16(t_s + 64 * h + 32, o + 16);
+            }
+            l += sum;
+          }
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBPFull + set));
+        start -= kPageTokens;
+        if (mine && !none) end -= kPageTokens;
+      }
+      if (!ok) break;
+      reinterpret_cast<float2*>(smem + kOffMl)[256 * set + 128 * (segs & 1) + lrow] = make_float2(kBias - shift, none ? 0.f : l);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBMl + 2 * set + (segs & 1)));
+      ++segs;
+    }
+  } else if (warp < 4) {
     regs_dec<64>();
     if (warp == 0) {
       // ---------------- segment records and page copies -------------------------------------
@@ -789,7 +946,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
             if (!cut) {
               const int job = (int)blockIdx.x + i * G;
               g = whole < 0 ? x % kKvHeads : job / n_tiles;
-              t = whole < 0 ? n_tiles - 1 - x / kKvHeads : job % n_tiles;
+              t = whole >= 0 ? job % n_tiles : kKvHeads * n_tiles > G && n_tiles <= kSorted ? s_order[x / kKvHeads] : n_tiles - 1 - x / kKvHeads;
             }
             const TileRec r = tile(t);
             const int pw = page_weight(r.n_tok);
@@ -949,136 +1106,6 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBQFull + (k & 1)));
       }
-    }
-  } else if (warp < 12) {
-    regs_inc<160>();
-    // ---------------- softmax: set = (warp - 4) / 4, row = TMEM lane ------------------------------------
-    const int set = (warp - 4) >> 2, quad = warp & 3, lrow = 32 * quad + lane;
-    const uint32_t t_s = tmem + ((uint32_t)(32 * quad) << 16) + kTmemS + 128 * set, t_o = t_s + kTmemO - kTmemS;
-    const uint64_t scale2 = pair64(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
-    uint32_t e = 0, par = 0, segs = 0;  // pages so far, parity of this set's jobs, its segments
-    for (int k = 0;; ++k) {
-      if (!swait(bar(kBRecFull + k % kRecs), (k / kRecs) & 1, wc)) break;
-      const SegRec r = *rec(k);
-      __syncwarp();
-      if (r.n_pg < 0) break;
-      if (lane == 0) mbar_arrive(bar(kBRecEmpty + k % kRecs));
-      if (set == 1 && r.n_tok <= 32) {
-        e += r.n_pg;
-        continue;
-      }
-      const int token = 32 * set + (lrow >> 2);
-      const bool busy = 32 * set + 8 * quad < r.n_tok, mine = token < r.n_tok;
-      // keys that the row sees, counted from the first one of the page
-      int start = 0, end = 0x7FFFFFFF;
-      if (mine) {
-        const int pos = r.pos + token;
-        start = (p.window ? max(0, pos + 1 - p.window) : 0) - r.page0 * kPageTokens;
-        end = (p.ends ? min(max(p.ends[r.q0 + token], 0), r.len) : pos + 1) - r.page0 * kPageTokens;
-      }
-      // (a row that sees nothing is weighed as if it saw all, so that its warp's pages need no masks; its sum is 0)
-      const bool none = end <= start;
-      if (none) {
-        start = 0;
-        end = 0x7FFFFFFF;
-      }
-      float shift = kUnset, l = 0.f;  // kBias less the reference, and the sum of weights
-      bool ok = true;
-      for (const uint32_t e0 = e; e - e0 < (uint32_t)r.n_pg; ++e) {
-        if (!swait(bar(kBSFull + set), par, wc)) {
-          ok = false;
-          break;
-        }
-        par ^= 1;
-        if (busy) {
-          tc_fence_after();
-          const int hi = s_info[e % kInfo] ? end : 0;
-          if (__any_sync(0xffffffffu, start > 0 || hi < kPageTokens)) {  // -inf where the row does not see the token
-#pragma unroll 1
-            for (int c = 0; c < kPageTokens; c += 32) {
-              uint32_t v[32];
-              const uint32_t vis = low_bits(hi - c) & ~low_bits(start - c);
-              if (__all_sync(0xffffffffu, vis == 0xFFFFFFFFu)) continue;
-              tmem_ld32x32b_x32(t_s + c, v);
-              tmem_wait_ld();
-#pragma unroll
-              for (int x = 0; x < 32; ++x) v[x] = vis >> x & 1 ? v[x] : 0xFF800000u;
-              tmem_st32(t_s + c, v);
-            }
-            tmem_wait_st();
-          }
-          // Half a page at a time, the next 32 scores loaded under the exponentials of 32.  There is no pass
-          // for the maximum: 64 weights that sum to 49,152 or less have none above it, and others (a
-          // row's first ones: its shift is kUnset) move the reference and are weighed again.
-          uint32_t v[2][32];
-          tmem_ld32x32b_x32(t_s, v[0]);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint64_t shift2 = pair64(__float_as_uint(shift), __float_as_uint(shift));
-            uint64_t sums[2] = {0, 0};
-            uint32_t o[32];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              wait_ld32(v[c]);
-              if (h + c < 2) tmem_ld32x32b_x32(t_s + 64 * h + 32 * c + 32, v[(c + 1) & 1]);
-              weigh32(v[c], scale2, shift2, sums, o + 16 * c);
-            }
-            const uint2 sum2 = split64(add_f32x2(sums[0], sums[1]));
-            float sum = __uint_as_float(sum2.x) + __uint_as_float(sum2.y);
-            const bool over = mine && sum > kMost;
-            if (__any_sync(0xffffffffu, over)) {
-              // (S of this half is as it was; the other half's load may be under way)
-              wait_ld32(v[0]);
-              float top = -INFINITY;
-#pragma unroll 1
-              for (int c = 0; c < 64; c += 16) {
-                uint32_t u[16];
-                tmem_ld32x32b_x16(t_s + 64 * h + c, u);
-                tmem_wait_ld();
-#pragma unroll
-                for (int x = 0; x < 16; ++x) top = fmaxf(top, __uint_as_float(u[x]));
-              }
-              float f = 1.f;
-              if (over) {
-                const float next = kBias - top * p.scale_log2;
-                f = fast_exp2(next - shift);  // (0 for the first: shift is kUnset)
-                shift = next;
-                l *= f;
-              }
-              __syncwarp();
-              if (e != e0) scale_acc(t_o, f);  // (the PVs before this S are done)
-              if (h) scale_p(t_s, f);
-              const uint64_t again2 = pair64(__float_as_uint(shift), __float_as_uint(shift));
-              sums[0] = sums[1] = 0;
-#pragma unroll 1
-              for (int c = 0; c < 64; c += 32) {
-                uint32_t u[32], y[16];
-                tmem_ld32x32b_x32(t_s + 64 * h + c, u);
-                tmem_wait_ld();
-                weigh32(u, scale2, again2, sums, y);
-                tmem_st_x16(t_s + 64 * h + c, y);
-              }
-              const uint2 again = split64(add_f32x2(sums[0], sums[1]));
-              sum = __uint_as_float(again.x) + __uint_as_float(again.y);
-            } else {
-              tmem_st_x16(t_s + 64 * h, o);
-              tmem_st_x16(t_s + 64 * h + 32, o + 16);
-            }
-            l += sum;
-          }
-          tmem_wait_st();
-          tc_fence_before();
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBPFull + set));
-        start -= kPageTokens;
-        if (mine && !none) end -= kPageTokens;
-      }
-      if (!ok) break;
-      reinterpret_cast<float2*>(smem + kOffMl)[256 * set + 128 * (segs & 1) + lrow] = make_float2(kBias - shift, none ? 0.f : l);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBMl + 2 * set + (segs & 1)));
-      ++segs;
     }
   } else {
     // ---------------- outputs: the rows of a finished segment, one set after the other, while the softmax
