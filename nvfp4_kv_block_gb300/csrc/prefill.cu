@@ -652,7 +652,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
       for (int i = 0; i < whole; ++i) w += weight(tid + i * G);
     const int rest = tid < G && tid + whole * G < n_jobs ? weight(tid + whole * G) : 0;
     // None is cut if all of them, dealt like that, leave no CTA with more than an equal share and kCut, or if a
-    // queue of them, heaviest first (or last tile first), does: a job begins when the ones before it, S in all, are out, at S / G or earlier
+    // queue of them, heaviest first (or last tile first), does: a job begins when those before it, S in all, are
+    // out of the queue, at S / G or earlier
     bool late = false;
     auto begins_late = [&](long long ahead, int w) { return kKvHeads * ahead + (kKvHeads - 1 + G) * (long long)w > G * (quota + kCut); };
     if (n_jobs > G && n_tiles <= kSorted) {
