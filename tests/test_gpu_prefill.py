@@ -224,6 +224,17 @@ def test_large_prompts_by_samples_of_rows(ctx, n, window):
         part.same(out[lo: lo + 20], lse[lo: lo + 20], F16, window)
 
 
+def test_sequences_behind_the_workspaces_pages_keep_their_rows_in_a_long_queue():
+    b = Prompts([(90, 64)] * 70, 51)  # two pages each: the last five do not fit
+    bufs = b.buffers(BF16, 130)
+    bufs.out.fill_(3.0)
+    bufs.lse.fill_(5.0)
+    out, lse, cache = b.go(BF16, bufs=bufs)
+    assert cache.read_status() == ops.STATUS_BAD_SEQ
+    b.same(out, lse, BF16, only={0, 1, 33, 63, 64})
+    assert (out[65 * 64:] == 3.0).all() and (lse[65 * 64:] == 5.0).all()
+
+
 def test_parts_of_a_prompt_agree_with_the_whole():
     """A chunk's rows do not depend on what else the call holds, but for the order of their sums."""
     b = Prompts([(0, 1000)], 13)
