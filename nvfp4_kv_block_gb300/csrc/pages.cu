@@ -275,14 +275,38 @@ struct ForkParams {
   const int* dst;
   int n;
   int4* plan;  // [n] workspace: tokens (-1: no fork), page to copy from and to (-1: none), 0
+  int wide;    // the targets' rows were looked at by fork_rows_kernel (plan[x].x: a page is held)
   LayerPools layers;
 };
+// A target is empty if no entry of its row holds a page; a caller may keep one anywhere in it.  Up to one entry a
+// thread of the planning CTA it looks at them itself (with the release behind it, 16 rows of 34 entries: 8.0 us; a wide
+// launch takes the host another 3.5), a wide launch before it at more (256 rows of 34: 13.4 us, 19 by the planning
+// CTA; 128 of 1,024: 15.2 and 85).
+constexpr int kPlanEntries = kPlanThreads;
+__global__ void __launch_bounds__(kCopyThreads) fork_rows_kernel(const __grid_constant__ ForkParams p) {
+  const int x = blockIdx.x;
+  pdl_wait();
+  pdl_trigger();
+  const int dst = p.dst[x];
+  int holds = 0;
+  if (dst >= 0 && dst < p.n_seqs)
+    for (int i = threadIdx.x; i < p.max_pages; i += kCopyThreads) holds |= p.block_table[(size_t)dst * p.max_pages + i] >= 0;
+  holds = __syncthreads_or(holds);
+  if (threadIdx.x == 0) p.plan[x] = make_int4(holds, 0, 0, 0);
+}
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const __grid_constant__ ForkParams p) {
   __shared__ int list[kMaxSeqs], claim[kMaxSeqs], s_warp[32];
+  __shared__ uint32_t held[kPlanEntries / 32];  // pairs whose target's row holds a page
   const int tid = threadIdx.x;
   pdl_wait();
   pdl_trigger();
   for (int i = tid; i < p.n_seqs; i += kPlanThreads) claim[i] = 0x7FFFFFFF;
+  if (tid < kPlanEntries / 32) held[tid] = 0;
+  __syncthreads();
+  if (!p.wide && tid < p.n * p.max_pages) {
+    const int x = tid / p.max_pages, row = p.dst[x];
+    if (row >= 0 && row < p.n_seqs && p.block_table[(size_t)row * p.max_pages + tid % p.max_pages] >= 0) atomicOr(held + x / 32, 1u << x % 32);
+  }
   __syncthreads();
   const int per = (p.n + kPlanThreads - 1) / kPlanThreads;  // pairs per * tid .. of a thread
   int src[kOwnSeqs], dst[kOwnSeqs], len[kOwnSeqs], last[kOwnSeqs], need = 0;
@@ -297,7 +321,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const __grid_co
       len[i] = p.seq_lens[src[i]];
       // the target has to be empty: neither tokens nor pages
       if (len[i] < 0 || len[i] > (long long)p.max_pages * kPageTokens || p.seq_lens[dst[i]] != 0 ||
-          p.block_table[(size_t)dst[i] * p.max_pages] >= 0)
+          (p.wide ? p.plan[x].x != 0 : (held[x / 32] >> x % 32 & 1) != 0))
         len[i] = -1;
       else
         atomicMin(claim + dst[i], x);
@@ -612,7 +636,9 @@ cudaError_t launch_fork(const msa_cache* layers, int n_layers, const msa_page_po
                         cudaStream_t stream) {
   if (n == 0) return cudaSuccess;
   const ForkParams p{pool_of(pool), block_table, max_pages, seq_lens, n_seqs, src, dst, n, static_cast<int4*>(ws),
-                     layer_pools(layers, n_layers)};
+                     (long long)n * max_pages > kPlanEntries, layer_pools(layers, n_layers)};
+  if (p.wide)
+    if (const cudaError_t e = launch_pdl(fork_rows_kernel, dim3(n), dim3(kCopyThreads), 0, stream, p); e != cudaSuccess) return e;
   const cudaError_t e = launch_pdl(fork_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
   if (e != cudaSuccess) return e;
   return launch_pdl(fork_copy_kernel, dim3(n, 1 + n_layers * kParts), dim3(kCopyThreads), 0, stream, p);

@@ -54,7 +54,7 @@ def fork(refs, table, lens, src, dst):
     old_lens, old_table = list(lens), [list(r) for r in table]
     taken = set()
     for a, b in zip(src, dst):
-        if not (0 <= a < len(table) and 0 <= b < len(table)) or old_lens[b] or old_table[b][0] >= 0 or b in taken:
+        if not (0 <= a < len(table) and 0 <= b < len(table)) or old_lens[b] or max(old_table[b]) >= 0 or b in taken:
             status |= BAD_SEQ
             continue
         taken.add(b)

@@ -286,3 +286,49 @@ def test_pages_on_another_stream_and_arguments():
         ops.release_sequences(s.pool, s.d_table.t(), s.d_lens, _dev([0]))
     with pytest.raises(ValueError):
         ops.extend_sequences(s.pool, s.d_table, s.d_lens, _dev([0, 0]), torch.empty(0, dtype=torch.int64, device=DEV))
+
+
+def _held(s, rows):
+    """Pages of a caller's own in the rows: ``rows`` maps a row to {column: page}."""
+    for b, cells in rows.items():
+        for at, page in cells.items():
+            s.table[b][at] = page
+            s.refs[page] += 1
+    s.pool = ops.PagePool.from_refs(_dev(s.refs))
+    s.d_table = _dev(s.table)
+
+
+@pytest.mark.parametrize("rows,cols", [(9, 4), (40, 700)])
+def test_fork_leaves_rows_alone_that_hold_a_page_behind_a_hole(rows, cols):
+    """Few entries and many, a page in the first, a middle and the last column; afterwards every page is dealt once."""
+    caches = _random_caches(1, 64, 21)
+    host = _host(caches)
+    s = State(64, rows, cols)
+    s.extend([200, 128] + [0] * (rows - 2))
+    _held(s, {2: {1: 40}, 3: {cols - 1: 41}, 4: {0: 42}, 5: {cols // 2: 63, cols - 1: 62}})
+    # (a pair that is left out names a row that a later one may have no more than it)
+    src = [0, 0, 1, 0, 0, 1, 0] + [0, 1] * ((rows - 9) // 2)
+    dst = [2, 3, 4, 5, 6, 7, 3] + list(range(8, 8 + len(src) - 7))
+    before = [list(r) for r in s.table[2:6]]
+    s.fork(src, dst, caches, host)
+    assert s.table[2:6] == before and s.lens[2:8] == [0, 0, 0, 0, 200, 128]
+    _same(caches, host)
+    held = [p for r in s.table for p in r if p >= 0]
+    assert s.refs == [held.count(p) for p in range(64)]
+    s.release(list(range(rows)))
+    assert not any(s.refs)
+
+
+@pytest.mark.parametrize("rows,cols,n", [(4096, 5, 4000), (300, 4, 256), (220, 5, 205), (70, 15, 68), (1040, 17, 1024)])
+def test_fork_of_many_rows_some_of_which_hold_pages(rows, cols, n):
+    """More pairs than threads, entries at the number that the planning CTA looks at and beyond it."""
+    caches = _random_caches(1, 5000, 22)
+    host = _host(caches)
+    s = State(5000, rows, cols)
+    s.extend([129] + [0] * (rows - 1))
+    rng = random.Random(cols)
+    _held(s, {b: {rng.randrange(cols): 100 + b} for b in rng.sample(range(1, rows), min(60, rows // 3))})
+    s.fork([0] * n, [1 + (i * 8 + i // (rows - 1)) % (rows - 1) for i in range(n)], caches, host)
+    _same(caches, host)
+    s.release(list(range(rows)))
+    assert not any(s.refs)

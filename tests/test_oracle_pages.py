@@ -159,3 +159,12 @@ def test_page_pool_needs_a_gpu_tensor():
         ops.PagePool.from_refs(torch.zeros(4, dtype=torch.int32))
     with pytest.raises(TypeError):
         ops.PagePool.from_refs(torch.zeros(4))
+
+
+def test_a_fork_leaves_a_row_alone_that_holds_a_page_behind_a_hole():
+    for at in (0, 1, 2):
+        refs, table, lens = [1, 1, 0, 0], [[0, -1, -1], [-1, -1, -1], [-1, -1, -1]], [5, 0, 0]
+        table[1][at] = 1
+        copies, status = pages.fork(refs, table, lens, [0, 0], [1, 2])
+        assert copies == [(0, 2, 5)] and status == pages.BAD_SEQ and lens == [5, 0, 5]
+        assert table[1][at] == 1 and refs == [1, 1, 1, 0]
