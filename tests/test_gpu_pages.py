@@ -332,3 +332,46 @@ def test_fork_of_many_rows_some_of_which_hold_pages(rows, cols, n):
     _same(caches, host)
     s.release(list(range(rows)))
     assert not any(s.refs)
+
+
+def test_fork_from_a_pool_that_runs_dry():
+    """One free page: the first pair that needs one gets it; later ones get none, and those that need none are made."""
+    caches = _random_caches(2, 11, 23)
+    host = _host(caches)
+    s = State(11, 10, 4)
+    s.extend([130, 256, 5, 512, 128, 0, 0, 0, 0, 0])
+    s.release([4])
+    assert sum(n == 0 for n in s.refs) == 2
+    s.extend([0, 0, 0, 0, 3, 0, 0, 0, 0, 0])
+    assert sum(n == 0 for n in s.refs) == 1
+    copies, status = pages.fork(list(s.refs), [list(r) for r in s.table], list(s.lens), [2, 0, 1, 4, 9], [5, 6, 7, 8, 6])
+    assert status & pages.NO_PAGES and len(copies) == 1
+    s.fork([2, 0, 1, 4, 9], [5, 6, 7, 8, 6], caches, host)
+    assert s.lens == [130, 256, 5, 512, 3, 5, 0, 256, 0, 0] and all(s.refs)
+    s.fork([0, 3, 2], [6, 8, 9], caches, host)  # none left at all
+    assert s.lens[6:] == [0, 256, 512, 0]
+    _same(caches, host)
+
+
+def test_random_lives_of_a_pool_that_is_too_small():
+    """Extensions and forks that find too few pages, among those that find them."""
+    rng = random.Random(77)
+    short = {"extend": 0, "fork": 0}
+    copied = 0
+    for n_pages, rows, cols in ((9, 5, 3), (40, 20, 4)):
+        caches = _random_caches(1, n_pages, n_pages)
+        host = _host(caches)
+        s = State(n_pages, rows, cols)
+        for _ in range(40):
+            new = [rng.choice([0, 0, 1, 60, 128]) if n < 300 else 0 for n in s.lens]
+            _, status = pages.extend(list(s.refs), [list(r) for r in s.table], list(s.lens), new, sum(new))
+            short["extend"] += status & pages.NO_PAGES != 0
+            s.extend(new)
+            src, dst = [rng.randrange(rows) for _ in range(4)], [rng.randrange(rows) for _ in range(4)]
+            copies, status = pages.fork(list(s.refs), [list(r) for r in s.table], list(s.lens), src, dst)
+            short["fork"] += status & pages.NO_PAGES != 0
+            copied += len(copies)
+            s.fork(src, dst, caches, host)
+            s.release(rng.sample(range(rows), rng.choice([0, 1, rows // 4])) or [rng.randrange(rows)])
+        _same(caches, host)
+    assert short["extend"] >= 5 and short["fork"] >= 5 and copied >= 5

@@ -168,3 +168,12 @@ def test_a_fork_leaves_a_row_alone_that_holds_a_page_behind_a_hole():
         copies, status = pages.fork(refs, table, lens, [0, 0], [1, 2])
         assert copies == [(0, 2, 5)] and status == pages.BAD_SEQ and lens == [5, 0, 5]
         assert table[1][at] == 1 and refs == [1, 1, 1, 0]
+
+
+def test_a_fork_runs_dry():
+    refs, table, lens = [1, 1, 0, 1, 1], [[0, 1], [3, -1], [4, -1]] + [[-1, -1] for _ in range(5)], [140, 128, 7, 0, 0, 0, 0, 0]
+    # the second pair finds no page any more, nor does the fourth; the third and the fifth need none
+    copies, status = pages.fork(refs, table, lens, [0, 2, 1, 0, 7], [3, 4, 5, 6, 6])
+    assert copies == [(1, 2, 12)] and status & pages.NO_PAGES
+    assert lens == [140, 128, 7, 140, 0, 128, 0, 0] and refs == [2, 1, 1, 2, 1]
+    assert table[3:] == [[0, 2], [-1, -1], [3, -1], [-1, -1], [-1, -1]]
