@@ -29,6 +29,33 @@ __device__ __forceinline__ bool twait(uint32_t bar, uint32_t parity, const WaitC
     }
   }
 }
+// One poll without mbar_try_wait's hint.
+__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Waits as twait does, with a shorter way through when the phase completes: a hand-over between two
+// warps takes about 110 cycles without the time hint and a vote per poll, 170 with them.  A poll answers
+// each lane for itself, so lanes can come apart here: every way out of the polls leads to the one vote, which all
+// of them take part in and which gives all the same answer.
+__device__ __forceinline__ bool swait(uint32_t bar, uint32_t parity, const WaitCtl& w) {
+  bool ok = mbar_poll(bar, parity);
+  if (!ok) {
+    const unsigned long long t0 = globaltimer_ns();
+    do {
+#pragma unroll 1
+      for (int i = 0; i < 64 && !ok; ++i) ok = mbar_poll(bar, parity);
+    } while (!ok && !*w.abort && globaltimer_ns() - t0 <= w.limit_ns);
+  }
+  if (__all_sync(0xffffffffu, ok)) return true;
+  *w.abort = 1;
+  return false;
+}
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"

@@ -352,36 +352,6 @@ __device__ __forceinline__ void st32(void* p, uint32_t a, uint32_t b, uint32_t c
                : "memory");
 }
 
-// Waits as twait does, with a shorter way through when the phase completes: a hand-over between two
-// warps takes about 110 cycles without the time hint and the vote, 170 with them.
-__device__ __forceinline__ bool swait(uint32_t bar, uint32_t parity, const WaitCtl& w) {
-  auto poll = [&] {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-  };
-  bool ok = poll();
-  if (ok) {
-    __syncwarp();
-    return true;
-  }
-  if (!ok) {
-    const unsigned long long t0 = globaltimer_ns();
-    for (;;) {
-#pragma unroll 1
-      for (int i = 0; i < 64 && !ok; ++i) ok = poll();
-      if (ok || *w.abort || globaltimer_ns() - t0 > w.limit_ns) break;
-    }
-  }
-  if (__all_sync(0xffffffffu, ok)) return true;
-  *w.abort = 1;
-  return false;
-}
-
 // Waits for tensor memory loads; the 32 values (one of them) are not touched before.
 __device__ __forceinline__ void wait_ld32(uint32_t (&v)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
