@@ -463,6 +463,7 @@ __device__ __forceinline__ void put_part(const PrefillParams& p, const SegRec& r
 #pragma unroll 1
   for (int c = 0; c < 2; ++c) {  // 64 channels of 32 rows: [16 of 4 channels][32 rows]
     uint32_t v[64];
+    __syncwarp();  // (lane 0 was apart: tensor memory is read by whole warps)
     tmem_ld32x32b_x64(t_o + 64 * c, v);
     tmem_wait_ld();
     if (c) freed();
@@ -1121,6 +1122,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t v[32];
+            __syncwarp();  // (lanes part ways in put32: tensor memory is read by whole warps)
             tmem_ld32x32b_x32(t_o + 32 * c, v);
             wait_ld32(v);
             if (c == 3) freed();
