@@ -81,13 +81,13 @@ constexpr float kMost = 49152.0f;  // largest sum of 64 weights, and so largest 
 constexpr float kUnset = 3e38f;           // shift of a row without a reference
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// Weights of the partition: a page of a tile of up to 32 tokens and of one of up to 64 (one set's chain
+// Weights of the partition: a page, whether a tile has up to 32 tokens or up to 64 (one set's chain
 // takes as long as two sets': 2,330 cycles); the fixed part of a job, records, queries and the rows' way out
 // (16: 8,192 tokens 170 us, 159 with 24, 165 with 40; 14 other calls, geometric mean, 62.3, 59.7, and 20 to 32 alike);
 // the least weight of a job (one of a page or two takes as long as five: the chain of its first scores and of its rows'
 // way out); and the least share of a CTA (a page's weight at least, so that every CTA between a job's first and
 // last has pages of it).
-constexpr int kPage1 = 9, kPage2 = 9, kFixed = 24, kSmall = 45, kLeast = 10;
+constexpr int kPageWeight = 9, kFixed = 24, kSmall = 45, kLeast = 10;
 
 // Jobs stay whole if the CTA with most then has no more than an equal share and kCut: parts cost their rows'
 // way to memory and back, some 16,000 cycles, with nothing under it at a call's end.  The same 14 calls: 59.0 us where
@@ -340,8 +340,7 @@ __global__ void __launch_bounds__(kConvThreads) prefill_convert_kernel(const __g
 __device__ __forceinline__ long long quot(long long a, long long b) {
   return (a | b) >> 31 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
 }
-__device__ __forceinline__ int page_weight(int n_tok) { return n_tok <= 32 ? kPage1 : kPage2; }
-__device__ __forceinline__ int job_weight(int n_tok, int n_pg) { return n_pg > 0 ? max(kFixed + n_pg * page_weight(n_tok), kSmall) : 0; }
+__device__ __forceinline__ int job_weight(int n_pg) { return n_pg > 0 ? max(kFixed + n_pg * kPageWeight, kSmall) : 0; }
 
 // Bits 0 .. n - 1 (n clamped to 0 .. 32).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1; }
@@ -594,7 +593,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
     const int per = (n_tiles + kPrefillThreads - 1) / kPrefillThreads;
     const int t0 = min(tid * per, n_tiles), t1 = min(t0 + per, n_tiles);
     long long mine = 0;
-    for (int t = t0; t < t1; ++t) mine += job_weight(p.tiles[t].n_tok, p.tiles[t].n_pg);
+    for (int t = t0; t < t1; ++t) mine += job_weight(p.tiles[t].n_pg);
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -612,10 +611,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
     const long long total = kKvHeads * one;
     const int n_jobs = kKvHeads * n_tiles, G = (int)min((long long)gridDim.x, max(1ll, quot(total, kLeast)));
     const long long quota = quot(total, G);
-    auto weight = [&](int job) {
-      const TileRec* r = p.tiles + job % n_tiles;
-      return job_weight(r->n_tok, r->n_pg);
-    };
+    auto weight = [&](int job) { return job_weight(p.tiles[job % n_tiles].n_pg); };
     // Whole jobs c, c + G, ... of CTA c: as many rounds as leave every CTA a share of the cut ones
     int whole = total > 0 ? n_jobs / G : 0;
     long long w = 0;
@@ -647,7 +643,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
     } else {
       long long upto_t = before + incl - mine;
       for (int t = t0; t < t1; ++t) {
-        const int w = job_weight(p.tiles[t].n_tok, p.tiles[t].n_pg);
+        const int w = job_weight(p.tiles[t].n_pg);
         upto_t += w;
         late |= begins_late(one - upto_t, w);
       }
@@ -668,7 +664,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
     const int first_g = total > 0 ? whole * G / n_tiles : 0, first_t = total > 0 ? whole * G % n_tiles : 0;
     if (t0 <= first_t && first_t < t1) {
       long long x = first_g * one + before + incl - mine;
-      for (int t = t0; t < first_t; ++t) x += job_weight(p.tiles[t].n_tok, p.tiles[t].n_pg);
+      for (int t = t0; t < first_t; ++t) x += job_weight(p.tiles[t].n_pg);
       s_scan[24] = x;
     }
     __syncthreads();
@@ -690,7 +686,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
         if (mine > 0 && in >= x && in < x + mine) {
           int t = t0;
           for (;; ++t) {
-            const int w = job_weight(p.tiles[t].n_tok, p.tiles[t].n_pg);
+            const int w = job_weight(p.tiles[t].n_pg);
             if (in < x + w) break;
             x += w;
           }
@@ -921,22 +917,21 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_attn_kernel(const 
               t = whole >= 0 ? job % n_tiles : kKvHeads * n_tiles > G && n_tiles <= kSorted ? s_order[x / kKvHeads] : n_tiles - 1 - x / kKvHeads;
             }
             const TileRec r = tile(t);
-            const int pw = page_weight(r.n_tok);
-            // page i starts at weight base + i pw; it belongs to the range that holds its start
+            // page i starts at weight base + i kPageWeight; it belongs to the range that holds its start
             const long long base = off + kFixed;
             auto page_at = [&](long long x) {  // the first page that starts at weight x or behind it
               if (x <= base) return 0;
-              return x - base > (long long)r.n_pg * pw ? r.n_pg : ((int)(x - base) + pw - 1) / pw;
+              return x - base > (long long)r.n_pg * kPageWeight ? r.n_pg : ((int)(x - base) + kPageWeight - 1) / kPageWeight;
             };
             const int a = cut && r.n_pg > 0 ? page_at(lo) : 0, z = cut && r.n_pg > 0 ? page_at(hi) : r.n_pg;
             const bool take = a < z && (pass ? !cut || off != early : z < r.n_pg);
             if (take) {
               if (pass == 0) early = off;
               const int c0 = cut ? owner(base) : (int)blockIdx.x;
-              ok = segment(r, t, g, a, z, c0, cut ? owner(base + (long long)(r.n_pg - 1) * pw) - c0 + 1 : 1);
+              ok = segment(r, t, g, a, z, c0, cut ? owner(base + (long long)(r.n_pg - 1) * kPageWeight) - c0 + 1 : 1);
             }
             if (whole < 0) x = G + __shfl_sync(0xffffffffu, lane == 0 ? atomicAdd(p.next, 1) : 0, 0);
-            off += job_weight(r.n_tok, r.n_pg);
+            off += job_weight(r.n_pg);
             if (++t == n_tiles) {
               t = 0;
               ++g;
