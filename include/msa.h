@@ -597,8 +597,10 @@ typedef struct msa_page_pool {
  *          sequences' order, for msa_rotary_insert and its like; -1 for the tokens of a
  *          sequence that could not grow and for rows behind the last sequence.
  * A sequence that could not grow keeps its length and row: one without enough free
- * pages, one with n < 0, tokens outside [0, n_tokens) or more than max_pages * 128 of
- * them (MSA_STATUS_BAD_SEQ), one whose last tokens have no page (MSA_STATUS_BAD_PAGE).
+ * pages, one with tokens outside [0, n_tokens) or more than max_pages * 128 of them
+ * (MSA_STATUS_BAD_SEQ), one whose last tokens have no page (MSA_STATUS_BAD_PAGE).  Where
+ * n < 0 for some sequence, tokens belong to several of them and none grows
+ * (MSA_STATUS_BAD_SEQ).
  * n_tokens <= 262,144.
  */
 int msa_extend_sequences(const msa_page_pool* pool, int32_t* block_table, int32_t max_pages, int32_t* seq_lens,

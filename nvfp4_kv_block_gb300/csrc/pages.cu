@@ -137,6 +137,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const __grid_const
   // sequences per * tid ..: the entries from first to last get pages; what each is short of (-1: left out)
   const int per = (p.n_seqs + kPlanThreads - 1) / kPlanThreads;
   int need[kOwnSeqs], first[kOwnSeqs], last[kOwnSeqs], mine = 0;
+  bool back = false;
 #pragma unroll
   for (int i = 0; i < kOwnSeqs; ++i) {
     const int b = per * tid + i;
@@ -146,6 +147,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const __grid_const
     if (i < per && b < p.n_seqs) {
       const int start = p.q_start_loc[b], n = p.q_start_loc[b + 1] - start, len = p.seq_lens[b];
       s_start[b] = start;
+      back |= n < 0;
       if (b == p.n_seqs - 1) s_start[b + 1] = start + n;
       bool ok = n >= 0 && start >= 0 && n <= p.n_tokens - start && len >= 0 && (long long)len + n <= (long long)p.max_pages * kPageTokens;
       const int* row = p.block_table + (size_t)b * p.max_pages;
@@ -175,6 +177,17 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(const __grid_const
       if (lane == who) need[i] = count;
     }
     mine += max(need[i], 0);
+  }
+  // Where q_start_loc goes back some tokens are of several sequences, and which slots they and the tokens behind
+  // them had would depend on the threads' order: none grows then.
+  if (__syncthreads_or(back)) {
+    mine = 0;
+#pragma unroll
+    for (int i = 0; i < kOwnSeqs; ++i)
+      if (need[i] >= 0) {
+        need[i] = -1;
+        s_len[per * tid + i] = -1;
+      }
   }
   int want;
   int at = block_scan(mine, s_warp, want);

@@ -837,7 +837,8 @@ def extend_sequences(pool, block_table, seq_lens, q_start_loc, slots):
     """Room for q_start_loc[b + 1] - q_start_loc[b] new tokens of each sequence: pages of
     the pool for the entries of its row that have none (lowest pages first), its length
     grown in place.  ``slots`` (int64 [n_tokens], returned) gets the slot of every new token,
-    or -1 where a sequence could not grow and for rows behind the last sequence."""
+    or -1 where a sequence could not grow and for rows behind the last sequence; none grows
+    where q_start_loc goes back."""
     dev, n_seqs, max_pages, table, lens = _table(pool, block_table, seq_lens)
     n = slots.shape[0]
     _check(lib().msa_extend_sequences(pool.packed(), table, max_pages, lens,

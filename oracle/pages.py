@@ -21,8 +21,8 @@ def _free(refs):
 
 
 def extend(refs, table, lens, new, n_tokens):
-    """Grows sequence b by new[b] tokens; (slots [n_tokens], status)."""
-    status, slots, free, dry = 0, [], _free(refs), False
+    """Grows sequence b by new[b] tokens, or none where one would shrink; (slots [n_tokens], status)."""
+    status, slots, free, dry, back = 0, [], _free(refs), False, min(new, default=0) < 0
     for b, n in enumerate(new):
         row = table[b]
         if n < 0 or lens[b] < 0 or lens[b] + n > len(row) * PAGE:
@@ -32,6 +32,8 @@ def extend(refs, table, lens, new, n_tokens):
         if n and lens[b] % PAGE and row[lens[b] // PAGE] < 0:
             status |= BAD_PAGE
             slots += [-1] * n
+            continue
+        if back:
             continue
         blocks = {p // PAGE for p in range(lens[b], lens[b] + n)} - ({lens[b] // PAGE} if lens[b] % PAGE else set())
         short = [i for i in sorted(blocks) if row[i] < 0]
@@ -45,7 +47,7 @@ def extend(refs, table, lens, new, n_tokens):
             refs[row[i]] = 1
         slots += [row[p // PAGE] * PAGE + p % PAGE for p in range(lens[b], lens[b] + n)]
         lens[b] += n
-    return slots + [-1] * (n_tokens - len(slots)), status
+    return [-1] * n_tokens if back else slots + [-1] * (n_tokens - len(slots)), status
 
 
 def fork(refs, table, lens, src, dst):

@@ -375,3 +375,19 @@ def test_random_lives_of_a_pool_that_is_too_small():
             s.release(rng.sample(range(rows), rng.choice([0, 1, rows // 4])) or [rng.randrange(rows)])
         _same(caches, host)
     assert short["extend"] >= 5 and short["fork"] >= 5 and copied >= 5
+
+
+@pytest.mark.parametrize("scale", [1, 100])
+def test_extend_grows_none_where_starts_go_back(scale):
+    """Tokens that two sequences claim: few, and more than the planning CTA writes.  No slot of a token that is there already is
+    given out, whatever the threads' order."""
+    s = State(400, 4, 130)
+    s.extend([60 * scale, 3, 50 * scale, 0])
+    before = list(s.lens)
+    for new in ([50 * scale, -10 * scale, 50 * scale, 0], [130 * 128, -(130 * 128 - 40 * scale), 50 * scale, 0], [0, 5, -5, 60 * scale]):
+        n = 90 * scale
+        got = ops.extend_sequences(s.pool, s.d_table, s.d_lens, s.starts(new), torch.full((n,), 77, dtype=torch.int64, device=DEV))
+        want, status = pages.extend(s.refs, s.table, s.lens, new, n)
+        assert got.tolist() == want == [-1] * n and status == ops.STATUS_BAD_SEQ and s.lens == before
+        s.check(status)
+    s.extend([50 * scale, 0, 1, 40 * scale])

@@ -177,3 +177,10 @@ def test_a_fork_runs_dry():
     assert copies == [(1, 2, 12)] and status & pages.NO_PAGES
     assert lens == [140, 128, 7, 140, 0, 128, 0, 0] and refs == [2, 1, 1, 2, 1]
     assert table[3:] == [[0, 2], [-1, -1], [3, -1], [-1, -1], [-1, -1]]
+
+
+def test_extend_grows_none_where_starts_go_back():
+    refs, table, lens = [1, 0, 0, 0], [[0, -1], [-1, -1], [-1, -1]], [4, 0, 0]
+    slots, status = pages.extend(refs, table, lens, [30, -20, 9], 30)
+    assert slots == [-1] * 30 and status == pages.BAD_SEQ
+    assert (refs, lens, table) == ([1, 0, 0, 0], [4, 0, 0], [[0, -1], [-1, -1], [-1, -1]])
