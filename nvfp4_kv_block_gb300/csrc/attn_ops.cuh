@@ -39,22 +39,21 @@ __device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Waits as twait does, with a shorter way through when the phase completes: a hand-over between two
-// warps takes about 110 cycles without the time hint and a vote per poll, 170 with them.  A poll answers
-// each lane for itself, so lanes can come apart here: every way out of the polls leads to the one vote, which all
-// of them take part in and which gives all the same answer.
+// Waits as twait does, without the hint: a hand-over between two warps takes 112 cycles, 142 with it.  (A poll
+// answers each lane for itself; a vote at every poll keeps the warp together.  Lanes that poll alone and vote once
+// at the end need 170.)
 __device__ __forceinline__ bool swait(uint32_t bar, uint32_t parity, const WaitCtl& w) {
-  bool ok = mbar_poll(bar, parity);
-  if (!ok) {
-    const unsigned long long t0 = globaltimer_ns();
-    do {
+  if (__all_sync(0xffffffffu, mbar_poll(bar, parity))) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  for (;;) {
 #pragma unroll 1
-      for (int i = 0; i < 64 && !ok; ++i) ok = mbar_poll(bar, parity);
-    } while (!ok && !*w.abort && globaltimer_ns() - t0 <= w.limit_ns);
+    for (int i = 0; i < 64; ++i)
+      if (__all_sync(0xffffffffu, mbar_poll(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, *w.abort || globaltimer_ns() - t0 > w.limit_ns)) {
+      *w.abort = 1;
+      return false;
+    }
   }
-  if (__all_sync(0xffffffffu, ok)) return true;
-  *w.abort = 1;
-  return false;
 }
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
