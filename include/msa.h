@@ -520,14 +520,16 @@ size_t msa_tree_attn_workspace_bytes(int32_t n_q_total);
  *               A token sees the positions start <= t < end; none where end <= start.
  *   n_visited   pages that ws has room for: the sequences' pages from the first that
  *               their first token sees to their last, summed over the call, at most (the
- *               sum of ceil(seq_lens[b] / 128) always will do).  A sequence behind that
- *               many sets MSA_STATUS_BAD_SEQ and keeps its rows.
+ *               sum of ceil(seq_lens[b] / 128) always will do; a page that several
+ *               sequences of the call share counts, and is converted, once for each).
+ *               A sequence behind that many sets MSA_STATUS_BAD_SEQ and keeps its rows.
  *   dtype, out, lse as msa_tree_attn; out on a 32-byte boundary.
  *   ws, ws_bytes scratch of at least msa_prefill_workspace_bytes(n_q_total, n_seqs,
  *               n_visited) bytes, 16-byte aligned, nothing of which is kept between calls.
  *               Calls sharing a workspace must not overlap on the GPU.
  * Rows behind the last sequence, and those of an inconsistent one (MSA_STATUS_BAD_SEQ),
- * are left as they were.  Operands, sums and special values as msa_tree_attn; the weights
+ * are left as they were; rows that several sequences claim (q_start_loc goes back) hold
+ * any of their results.  Operands, sums and special values as msa_tree_attn; the weights
  * are rounded to f16 (2^-11 relative, or 2^-33 of the weight at the row's reference) once,
  * those of the first 64 tokens of a page once more where the page's others move the row's
  * reference.  Rows are summed in an order that depends on the call's sizes and the device's
@@ -615,10 +617,11 @@ int msa_extend_sequences(const msa_page_pool* pool, int32_t* block_table, int32_
  *   layers    HOST array of n_layers caches (1 .. 128), each with pool->n_pages pages
  *             or more.
  *   ws        device scratch of msa_fork_workspace_bytes(n) bytes, 16-byte aligned.
- * A pair outside the table, with a target that has tokens or pages or that an earlier
- * pair of the call names, is left out (MSA_STATUS_BAD_SEQ), so a row that is another
- * pair's target counts as empty; so is one whose last page is outside the pool, and an
- * entry outside it is taken over and flagged (MSA_STATUS_BAD_PAGE).  n <= 4096.
+ * A pair outside the table, with a target that has tokens or holds a page in any entry of
+ * its row, or that an earlier pair which is not left out for these reasons names, is left
+ * out (MSA_STATUS_BAD_SEQ), so a row that is another pair's target counts as empty; so is
+ * one whose last page is outside the pool, and an entry outside it is taken over and
+ * flagged (MSA_STATUS_BAD_PAGE).  n <= 4096.
  */
 int msa_fork_sequences(const msa_cache* layers, int32_t n_layers, const msa_page_pool* pool, int32_t* block_table,
                        int32_t max_pages, int32_t* seq_lens, int32_t n_seqs, const int32_t* src, const int32_t* dst,

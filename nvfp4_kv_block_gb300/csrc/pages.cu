@@ -15,8 +15,8 @@
 //
 // Every kernel is a programmatic dependent of the one before it and lets the next begin
 // launching at once; it touches memory behind pdl_wait only (release, fork and extension of
-// 256 rows, 43.8 us a pass; 49.8 with plain launches).  On the GPU the pass takes 3.4 for
-// the release, 8 for the plan, 28 for the copies (12 layers, 246 MB read and written, 8.8 TB/s: partly
+// 256 rows, 45.4 us a pass; before targets' rows were looked at as a whole 43.8, and 49.8 with plain launches).  On the
+// GPU the pass takes 3.4 for the release, 1.3 for the look at the targets' rows, 8 for the plan, 28 for the copies (12 layers, 246 MB read and written, 8.8 TB/s: partly
 // from L2) and 7.5 for the extension: three chains of a few dependent loads and one launch bound
 // by memory.  A commit of 8 x 8 drafts takes 2.4 us, of 64 x 64 in 12 layers 6 to 7.5 (9.8 MB).
 #include "common.cuh"
@@ -118,7 +118,7 @@ constexpr int kExtendSmem = (kMaxDealt + 2 * (kMaxSeqs + 1) + 32) * sizeof(int);
 // it, 16 rows of 2,048 tokens: 13 us, 18 where a warp takes 9 entries and more; one of 8,192: 9.5, 16 without warps).
 constexpr int kOwnEntries = 20;
 // Tokens whose slots the planning CTA writes, 1,024 at a time; a wide launch behind it those of more
-// (with the release, 4,096 tokens: 7.8 us, 8.5 by a wide launch; 262,144: 324 and 33).
+// (with the release, 4,096 tokens: 6.3 to 7.8 us, 8.5 by a wide launch; 262,144: 324 and 37 to 39).
 constexpr int kPlanTokens = 4096;
 
 __device__ __forceinline__ int64_t slot_at(const int* row, int pos) {

@@ -6,12 +6,17 @@
 //   x_t = (q . k8_t) scale / s_enc_k log2(e),  out = sum_t 2^x_t v8_t / sum_t 2^x_t / s_enc_v,
 // in one pass over the pages with a reference m per row: weights 2^(x_t - m + 8), summed in
 // fp32, multiply V in f16 (a relative 2^-11; an E4M3 weight would lose the bulk of a long
-// context behind one large key).  m moves, to the page's maximum, only when a weight would
-// pass 49,152 (f16 ends at 65,504), so the accumulator is rescaled a few times per row.
+// context behind one large key).  m moves only when the weights of 64 tokens, half a page, would sum to more
+// than 49,152 (f16 ends at 65,504), and to the maximum of those 64: 1.1 (all alike) to 5.3 (one alone) natural units above m and more.  A row's
+// first 64 tokens do it always, later ones where scores spread: then the half's scores are read twice more and the
+// accumulator is rescaled, for 32 rows when one of them needs it.  Scores that deviate by 0.5: 8,192 tokens 161 us,
+// 2,048 over 131,072 1,113; by 1.6: 164 and 1,132; by 3.2: 257 and 1,293, and 255 and 1,504 where keys grow eightfold along
+// the context; by 6.3: 287 and 1,371.
 //
-// Three kernels.  (1) Every page that the call visits is converted once per KV head into the
+// Three kernels.  (1) Every page that a sequence visits is converted once per KV head into the
 // operand tiles of the products, 16 KB of E4M3 keys and 32 KB of f16 values, by a kernel bound
-// by memory; it also writes down the tiles of 64 tokens and their pages.  (2) The attention: a job
+// by memory (a page that several sequences of the call share, once for each of them); it also writes down the tiles of
+// 64 tokens and their pages.  (2) The attention: a job
 // is a tile (256 rows, 4 i + h for token i and head h of the group) and a KV head; the jobs'
 // pages in a row are cut into equal weighted ranges, one per persistent CTA, or, where that is nearly as even, jobs are
 // taken whole from a queue.  A job that was cut
@@ -31,10 +36,10 @@
 // takes about 2,330: a set's chain is its softmax (850 cycles for 128 keys), the hand-over of the weights
 // (290), PV and the next QK into the same columns (820), the hand-over of the scores (400), and the two
 // sets run half a period apart.  Two tiles of scores and two accumulators are all of tensor memory, so there is no
-// third one to fill the gaps.  2,048 tokens over 131,072: 1,095 us, 2.02 PFLOP/s (1.90 is the measured bf16 rate; at
-// that rate for PV and twice it for QK the products alone take 877); 8,192 from the beginning: 160 us, the products 109;
-// 4,096 with a window of 4,096: 97, 55.  Tiles of 64 tokens x 4 heads: a page's 48 KB then feed two products
-// of 128 rows, 21 bytes a cycle and SM from L2.  100 tokens: 17 to 19 us, two launches and a chain of some
+// third one to fill the gaps.  From card to card, 2,048 tokens over 131,072: 1,113 to 1,136 us, 1.95 to 1.99 PFLOP/s (1.90
+// is the measured bf16 rate; at that rate for PV and twice it for QK the products alone take 877); 8,192 from the
+// beginning: 161 to 163 us, the products 109; 4,096 with a window of 4,096: 97 to 98, 55.  Tiles of 64 tokens x 4 heads: a page's 48 KB then feed two products
+// of 128 rows, 21 bytes a cycle and SM from L2.  100 tokens: 18 us, two launches and a chain of some
 // thirty latencies.
 #include <cuda_fp16.h>
 

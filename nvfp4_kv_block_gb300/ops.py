@@ -574,11 +574,12 @@ class RopeAxes:
 
 
 def rope_axes(sections, dealt=False):
-    """RopeAxes of ``sections``: how many pairs turn by each axis (time, height, width, ...;
-    their sum is rot_dim / 2).  The sections follow one another (pairs 0 .. sections[0] - 1
-    are the first axis's), or, when ``dealt``, the axes take the pairs in turn, axis
-    i % n_axes pair i, as long as i < n_axes * sections[i % n_axes]; the pairs that no axis
-    takes so are the first axis's."""
+    """RopeAxes of ``sections``, counts of pairs of each axis (time, height, width, ...; their
+    sum is rot_dim / 2).  The sections follow one another (pairs 0 .. sections[0] - 1 are the
+    first axis's), or, when ``dealt``, the axes take the pairs in turn: pair i is of axis
+    i % n_axes where i < n_axes * sections[i % n_axes], else of the first axis.  So an axis a > 0
+    has the count asked for where its last turn, a + n_axes * (sections[a] - 1), is below the sum,
+    and fewer where the pairs end before it ([3, 5]: 4 and 4)."""
     sections = [int(n) for n in sections]
     if not sections or min(sections) < 0:
         raise ValueError("sections must be counts of pairs")
@@ -721,9 +722,9 @@ def tree_attn(cache, q, block_table, seq_lens, q_start_loc, bufs, tree_mask=None
 class PrefillBuffers:
     """Outputs and scratch of prefill_attn calls with n_q_total query rows (exactly: rows behind
     the last sequence stay as they were), up to n_seqs sequences and n_pages pages of their
-    contexts (the sum of ceil(seq_len / 128), or of those within the window): out [n_q_total,
-    16, 128] in ``dtype`` (bf16 or fp16), lse [n_q_total, 16], and 196,608 bytes of scratch a
-    page.  ``ws``: scratch of other buffers, to share it between layers or steps (calls that
+    contexts (the sum of ceil(seq_len / 128), or of those within the window; a page counts for
+    each sequence that shares it): out [n_q_total, 16, 128] in ``dtype`` (bf16 or fp16), lse
+    [n_q_total, 16], and 196,608 bytes of scratch a page.  ``ws``: scratch of other buffers, to share it between layers or steps (calls that
     share it must not overlap on the GPU)."""
 
     def __init__(self, n_q_total, n_seqs, n_pages, dtype=torch.bfloat16, device="cuda", ws=None):
@@ -848,9 +849,10 @@ def extend_sequences(pool, block_table, seq_lens, q_start_loc, slots):
 
 
 def fork_sequences(layers, pool, block_table, seq_lens, src, dst):
-    """Row dst[i] of the table, which has to be empty, becomes a second copy of row src[i]
-    (int32 [n] each): full pages are shared, the tokens of the last one are copied to a page
-    of its own in every layer (``layers``: CacheLayers, a list of caches or one cache)."""
+    """Row dst[i] of the table, which has to be empty (no tokens, no entry that holds a page),
+    becomes a second copy of row src[i] (int32 [n] each): full pages are shared, the tokens of
+    the last one are copied to a page of its own in every layer (``layers``: CacheLayers, a list
+    of caches or one cache)."""
     layers = CacheLayers.of(layers)
     dev, n_seqs, max_pages, table, lens = _table(pool, block_table, seq_lens)
     _same_device(layers, dev)
